@@ -460,6 +460,87 @@ int vggt3_ttt_read_streamed_ex(const void* Q_host, const float* theta, void* O_h
                                int64_t chunk_tokens, void* stage, size_t stage_bytes, void* workspace,
                                size_t workspace_bytes, void* stream, void* h2d_stream, void* d2h_stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Microscaled 4-bit matrices (element type e2m1, blocks of 32, e8m0 scales):
+ * the form in which a frozen theta* and the tokens it is applied to pass
+ * through the 4-bit matrix unit.
+ *
+ * A matrix [rows][k], contracted over k, is two byte arrays; kp is k rounded up
+ * to 128:
+ *   codes   [rows][kp/2], two values a byte, the even column in the low nibble;
+ *           bit 3 of a code is the sign, bits 0-2 index 0, .5, 1, 1.5, 2, 3, 4, 6.
+ *   scales  one byte s per row and block of 32 columns, worth 2^(s-127) (255:
+ *           the block is NaN), in tiles [ceil(rows/64)][kp/128][64][4]: the byte
+ *           of row 64 R + 16 i + r and block 4 B + g is [R][B][16 g + r][i].
+ * Columns k .. kp-1 hold code 0. Every byte of both arrays is written. At most
+ * 2^20 columns. The sizes are vggt3_mx4_codes_bytes / vggt3_mx4_scales_bytes
+ * (0 for a shape that is refused).
+ */
+enum { VGGT3_MX4 = 2 }; /* as an operand type: 4-bit codes with their scales */
+
+size_t vggt3_mx4_codes_bytes(int64_t rows, int32_t k);
+size_t vggt3_mx4_scales_bytes(int64_t rows, int32_t k);
+
+/*
+ * Quantise X [rows][k] (transposed = 0) or X [k][rows] (transposed != 0: the
+ * blocks run along X's first axis) to codes and scales. Per block of 32:
+ *   e = max(floor(log2 max|x|) - 2, -127),  code = x / 2^e to the nearest code,
+ *   ties to the even one, saturating at 6 (values past 6 lie below 8).
+ * A block that holds an Inf or a NaN becomes NaN as a whole. rows == 0 is a
+ * no-op. X, codes and scales must not overlap.
+ */
+int vggt3_mx4_quantize(const void* X, int32_t transposed, void* codes, void* scales, int64_t rows, int32_t k,
+                       int32_t dtype, void* stream);
+
+/* The values X [rows][k] that codes and scales stand for (exact in both dtypes). */
+int vggt3_mx4_dequantize(const void* codes, const void* scales, void* X, int64_t rows, int32_t k, int32_t dtype,
+                         void* stream);
+
+/*
+ * C [m][n] = A W^T, C[i][j] = sum over k of A[i][k] W[j][k], fp32 accumulation,
+ * one rounding to dtype.
+ *   A         a_type VGGT3_MX4: codes of [m][k], with A_scales; VGGT3_BF16 or
+ *             VGGT3_F32: tokens [m][k] (A_scales NULL), quantised on the way as
+ *             by vggt3_mx4_quantize.
+ *   W_codes, W_scales   a 4-bit matrix [n][k].
+ *   workspace at least vggt3_mx4_matmul_workspace_bytes(m, n, k, a_type) bytes
+ *             (may be NULL when that is 0).
+ * C and the workspace must not overlap anything else. m == 0 is a no-op. A NaN
+ * block of A makes its row of C NaN, one of W its column.
+ */
+size_t vggt3_mx4_matmul_workspace_bytes(int64_t m, int32_t n, int32_t k, int32_t a_type);
+int vggt3_mx4_matmul(const void* A, const void* A_scales, int32_t a_type, const void* W_codes, const void* W_scales,
+                     void* C, int64_t m, int32_t n, int32_t k, int32_t dtype, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * Freeze the full-width (1, 1024, 4096) fast weights in 4 bits: W_g, W_u as
+ * [4096][1024] and W_d as [1024][4096] (each contracted over its second axis),
+ * 6.7 MB for theta's 50 MB. For query mode, where theta* is only read.
+ */
+int vggt3_ttt_freeze_mx4(const float* theta, void* gate_codes, void* gate_scales, void* up_codes, void* up_scales,
+                         void* down_codes, void* down_scales, int32_t n_heads, int32_t d_head, int32_t d_hidden,
+                         void* stream);
+
+/*
+ * vggt3_ttt_read_ex on fast weights frozen in 4 bits ([GRAPH] Eq. 4, query
+ * mode): O = H W_d with H = silu(Q W_g) * (Q W_u); Q and H are quantised on the
+ * way (H from fp32), products accumulate in fp32, O is bf16.
+ *   Q   q_type VGGT3_BF16: [n_tokens][1024] (Q_scales NULL); VGGT3_MX4: its
+ *       codes, with Q_scales.
+ *   workspace  at least vggt3_ttt_read_mx4_workspace_bytes(...) bytes.
+ * Only (1, 1024, 4096): the per-head reads are bound by the traffic of Q and O,
+ * which 4-bit weights do not change. O and the workspace must not overlap
+ * anything else. n_tokens == 0 is a no-op.
+ */
+size_t vggt3_ttt_read_mx4_workspace_bytes(int64_t n_tokens, int32_t n_heads, int32_t d_head, int32_t d_hidden,
+                                          int32_t q_type);
+int vggt3_ttt_read_mx4(const void* Q, const void* Q_scales, int32_t q_type, const void* gate_codes,
+                       const void* gate_scales, const void* up_codes, const void* up_scales, const void* down_codes,
+                       const void* down_scales, void* O, int64_t n_tokens, int32_t n_heads, int32_t d_head,
+                       int32_t d_hidden, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,7 +13,7 @@ without a GPU, calls raise.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+from typing import NamedTuple, Optional, Union
 
 import torch
 
@@ -21,6 +21,7 @@ from . import _lib
 
 BF16 = 0
 F32 = 1
+MX4 = 2
 
 OK, EINVAL, EUNSUPPORTED, EWORKSPACE, EHIP = 0, -1, -2, -3, -4
 
@@ -468,4 +469,193 @@ def ttt_read_streamed(Q_host: torch.Tensor, theta: torch.Tensor, n_heads: int, c
     _call("vggt3_ttt_read_streamed_ex", _ptr(Q_host), _ptr(theta), _ptr(out), n, n_heads, d, m, dt,
           int(chunk_tokens), _ptr(stage), stage.numel() * stage.element_size(), _ptr(workspace), nb, _stream(),
           ctypes.c_void_p(h2d_stream.cuda_stream), ctypes.c_void_p(d2h_stream.cuda_stream))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Microscaled 4-bit matrices: quantisation, products, and the read of fast
+# weights frozen in 4 bits
+# ---------------------------------------------------------------------------
+
+def _on(*ts):
+    """The device context of a call's tensors: they share one GPU, and the call
+    runs on that GPU's current stream, whichever device is current."""
+    devs = {t.device for t in ts if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors live on different devices: {sorted(str(d) for d in devs)}")
+    return torch.cuda.device(devs.pop())
+
+
+class Mx4(NamedTuple):
+    """A 4-bit matrix [rows, k] (include/vggt3.h, "Microscaled 4-bit matrices"):
+    codes uint8 [rows, kp / 2] and scales uint8 [ceil(rows / 64), kp / 128, 64, 4],
+    kp = k rounded up to 128."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    k: int
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+
+class FrozenMx4(NamedTuple):
+    """The full-width fast weights in 4 bits: gate and up [4096, 1024], down [1024, 4096]."""
+
+    gate: Mx4
+    up: Mx4
+    down: Mx4
+
+
+def _mx4_shapes(rows: int, k: int):
+    kp = (k + 127) // 128 * 128
+    return (rows, kp // 2), ((rows + 63) // 64, kp // 128, 64, 4)
+
+
+def _mx4_empty(rows: int, k: int, device) -> Mx4:
+    cs, ss = _mx4_shapes(rows, k)
+    return Mx4(torch.empty(cs, dtype=torch.uint8, device=device), torch.empty(ss, dtype=torch.uint8, device=device), k)
+
+
+def _check_mx4(name: str, a: Mx4, rows: Optional[int] = None, k: Optional[int] = None) -> None:
+    if not isinstance(a, Mx4):
+        raise TypeError(f"{name} must be an Mx4 (codes, scales, k), got {type(a).__name__}")
+    for part, t in (("codes", a.codes), ("scales", a.scales)):
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{name}.{part} must be uint8, got {t.dtype}")
+    if a.codes.dim() != 2 or int(a.k) < 1:
+        raise ValueError(f"{name}: codes are [rows, kp / 2] and k >= 1, got {tuple(a.codes.shape)} and k = {a.k}")
+    if (rows is not None and a.rows != rows) or (k is not None and a.k != k):
+        raise ValueError(f"{name} is [{a.rows}, {a.k}], [{a.rows if rows is None else rows}, {a.k if k is None else k}] expected")
+    cs, ss = _mx4_shapes(a.rows, int(a.k))
+    if tuple(a.codes.shape) != cs or tuple(a.scales.shape) != ss:
+        raise ValueError(f"{name} [{a.rows}, {a.k}] has codes {tuple(a.codes.shape)} and scales "
+                         f"{tuple(a.scales.shape)}, {cs} and {ss} expected")
+
+
+def _type_code(dtype: torch.dtype) -> int:
+    if dtype == torch.bfloat16:
+        return BF16
+    if dtype == torch.float32:
+        return F32
+    raise TypeError(f"unsupported dtype {dtype}; bfloat16 or float32")
+
+
+def _check_out(out: Optional[torch.Tensor], shape, dtype: torch.dtype) -> None:
+    if out is not None and (tuple(out.shape) != tuple(shape) or out.dtype != dtype):
+        raise ValueError(f"out {tuple(out.shape)} {out.dtype}, {tuple(shape)} {dtype} expected")
+
+
+def _ws(workspace: Optional[torch.Tensor], need: int, device):
+    """(workspace, its bytes), allocated where none was given and one is needed."""
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def mx4_quantize(X: torch.Tensor, transpose: bool = False, out: Optional[Mx4] = None) -> Mx4:
+    """X [rows, k] (or, with transpose, X [k, rows]) in 4 bits, blocks of 32 along k."""
+    _check_tokens("X", X)
+    k, rows = X.shape if transpose else (X.shape[1], X.shape[0])
+    if k < 1:
+        raise ValueError("X has no columns to contract over")
+    if out is not None:
+        _check_mx4("out", out, rows, k)
+    else:
+        out = _mx4_empty(rows, k, X.device)
+    _check_dev(X, out.codes, out.scales)
+    with _on(X, out.codes, out.scales):
+        _call("vggt3_mx4_quantize", _ptr(X), int(bool(transpose)), _ptr(out.codes), _ptr(out.scales), rows, k,
+              _dtype_code(X), _stream())
+    return out
+
+
+def mx4_dequantize(A: Mx4, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values [rows, k] that A stands for."""
+    _check_mx4("A", A)
+    dt = _type_code(dtype)
+    _check_out(out, (A.rows, A.k), dtype)
+    if out is None:
+        out = torch.empty((A.rows, A.k), dtype=dtype, device=A.codes.device)
+    _check_dev(A.codes, A.scales, out)
+    with _on(A.codes, A.scales, out):
+        _call("vggt3_mx4_dequantize", _ptr(A.codes), _ptr(A.scales), _ptr(out), A.rows, A.k, dt, _stream())
+    return out
+
+
+def mx4_matmul_workspace_bytes(m: int, n: int, k: int, a_type: int) -> int:
+    return int(lib().vggt3_mx4_matmul_workspace_bytes(m, n, k, a_type))
+
+
+def mx4_matmul(A: Union[Mx4, torch.Tensor], W: Mx4, dtype: torch.dtype = torch.bfloat16,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A W^T [m, n] with W [n, k] in 4 bits; tokens A [m, k] are quantised on the way."""
+    _check_mx4("W", W)
+    if isinstance(A, Mx4):
+        _check_mx4("A", A, k=W.k)
+        m, a_type, data, scales = A.rows, MX4, A.codes, A.scales
+    else:
+        _check_tokens("A", A)
+        if A.shape[1] != W.k:
+            raise ValueError(f"A has {A.shape[1]} columns, W is [{W.rows}, {W.k}]")
+        m, a_type, data, scales = A.shape[0], _dtype_code(A), A, None
+    dt = _type_code(dtype)
+    _check_out(out, (m, W.rows), dtype)
+    if out is None:
+        out = torch.empty((m, W.rows), dtype=dtype, device=data.device)
+    _check_dev(data, scales, W.codes, W.scales, out, workspace)
+    with _on(data, scales, W.codes, W.scales, out, workspace):
+        workspace, nb = _ws(workspace, mx4_matmul_workspace_bytes(m, W.rows, W.k, a_type), data.device)
+        _call("vggt3_mx4_matmul", _ptr(data), _ptr(scales), a_type, _ptr(W.codes), _ptr(W.scales), _ptr(out), m, W.rows,
+              W.k, dt, _ptr(workspace), nb, _stream())
+    return out
+
+
+def ttt_freeze_mx4(theta: torch.Tensor, d_head: int = 1024, d_hidden: int = 4096,
+                   out: Optional[FrozenMx4] = None) -> FrozenMx4:
+    """Freeze the full-width theta* in 4 bits for ttt_read_mx4 (6.7 MB for its 50 MB)."""
+    _check_theta(theta, 1, d_head, d_hidden)
+    shapes = ((d_hidden, d_head), (d_hidden, d_head), (d_head, d_hidden))
+    if out is None:
+        out = FrozenMx4(*(_mx4_empty(r, k, theta.device) for r, k in shapes))
+    parts = []
+    for name, a, (r, k) in zip(FrozenMx4._fields, out, shapes):
+        _check_mx4(name, a, r, k)
+        parts += [a.codes, a.scales]
+    _check_dev(theta, *parts)
+    with _on(theta, *parts):
+        _call("vggt3_ttt_freeze_mx4", _ptr(theta), *(_ptr(p) for p in parts), 1, d_head, d_hidden, _stream())
+    return out
+
+
+def read_mx4_workspace_bytes(n_tokens: int, d_head: int, d_hidden: int, q_type: int) -> int:
+    return int(lib().vggt3_ttt_read_mx4_workspace_bytes(n_tokens, 1, d_head, d_hidden, q_type))
+
+
+def ttt_read_mx4(Q: Union[Mx4, torch.Tensor], frozen: FrozenMx4, out: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """O = T_theta*(Q) with the full-width fast weights frozen in 4 bits (query mode).
+    Q: bf16 tokens [n, 1024], quantised on the way, or an Mx4; O is bf16."""
+    d, m = frozen.down.rows, frozen.gate.rows
+    if isinstance(Q, Mx4):
+        _check_mx4("Q", Q, k=d)
+        n, q_type, data, scales = Q.rows, MX4, Q.codes, Q.scales
+    else:
+        _check_tokens("Q", Q)
+        if Q.shape[1] != d:
+            raise ValueError(f"Q has {Q.shape[1]} channels, the frozen weights {d}")
+        n, q_type, data, scales = Q.shape[0], _dtype_code(Q), Q, None
+    parts = []
+    for name, a, (r, k) in zip(FrozenMx4._fields, frozen, ((m, d), (m, d), (d, m))):
+        _check_mx4(name, a, r, k)
+        parts += [a.codes, a.scales]
+    _check_out(out, (n, d), torch.bfloat16)
+    if out is None:
+        out = torch.empty((n, d), dtype=torch.bfloat16, device=data.device)
+    _check_dev(data, scales, out, workspace, *parts)
+    with _on(data, scales, out, workspace, *parts):
+        workspace, nb = _ws(workspace, read_mx4_workspace_bytes(n, d, m, q_type), data.device)
+        _call("vggt3_ttt_read_mx4", _ptr(data), _ptr(scales), q_type, *(_ptr(p) for p in parts), _ptr(out), n, 1, d, m,
+              _ptr(workspace), nb, _stream())
     return out

@@ -63,6 +63,17 @@ SIGNATURES = {
                                         c_void_p, c_size, c_void_p, c_void_p, c_void_p]),
     "vggt3_ttt_read_streamed_ex": (c_int, [c_void_p, c_void_p, c_void_p, c_i64, c_int, c_int, c_int, c_int, c_i64,
                                            c_void_p, c_size, c_void_p, c_size, c_void_p, c_void_p, c_void_p]),
+    "vggt3_mx4_codes_bytes": (c_size, [c_i64, c_int]),
+    "vggt3_mx4_scales_bytes": (c_size, [c_i64, c_int]),
+    "vggt3_mx4_quantize": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_i64, c_int, c_int, c_void_p]),
+    "vggt3_mx4_dequantize": (c_int, [c_void_p, c_void_p, c_void_p, c_i64, c_int, c_int, c_void_p]),
+    "vggt3_mx4_matmul_workspace_bytes": (c_size, [c_i64, c_int, c_int, c_int]),
+    "vggt3_mx4_matmul": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_i64, c_int, c_int, c_int,
+                                 c_void_p, c_size, c_void_p]),
+    "vggt3_ttt_freeze_mx4": (c_int, [c_void_p] * 7 + [c_int, c_int, c_int, c_void_p]),
+    "vggt3_ttt_read_mx4_workspace_bytes": (c_size, [c_i64, c_int, c_int, c_int, c_int]),
+    "vggt3_ttt_read_mx4": (c_int, [c_void_p, c_void_p, c_int] + [c_void_p] * 7 + [c_i64, c_int, c_int, c_int,
+                                                                                  c_void_p, c_size, c_void_p]),
 }
 
 _lib = None

@@ -1,51 +1,17 @@
 // C ABI of the TTT layer: argument validation and launch sequencing.
 // Every check runs on the host before anything is enqueued.
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <mutex>
-#include <string>
 
 #include "../../include/vggt3.h"
+#include "api_util.hpp"
 #include "kernels.hpp"
 #include "wide.hpp"
 
+using namespace vggt3::api;
+
 namespace {
-
-thread_local std::string g_last_error;
-
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-int fail(int status, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return status;
-}
-
-int ok() {
-  g_last_error.clear();
-  return VGGT3_OK;
-}
-
-int check_hip(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(VGGT3_EHIP, "%s: %s", what, hipGetErrorString(e));
-  return VGGT3_OK;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-  if (a == nullptr || b == nullptr || an == 0 || bn == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + bn && b0 < a0 + an;
-}
-
-bool valid_dtype(int32_t dt) { return dt == VGGT3_BF16 || dt == VGGT3_F32; }
-size_t elem_size(int32_t dt) { return dt == VGGT3_BF16 ? 2 : 4; }
 
 // The pages' full-width MLP: one 1024 -> 4096 -> 1024 SwiGLU (one "head").
 bool is_wide(int32_t d, int32_t m) { return d == vggt3::wide::kD && m == vggt3::wide::kM; }
@@ -94,8 +60,6 @@ int check_mlp(const MlpArgs& a) {
 
 size_t theta_bytes(const MlpArgs& a) { return (size_t)a.H * 3 * a.d * a.m * sizeof(float); }
 size_t token_bytes(const MlpArgs& a) { return (size_t)a.n * a.H * a.d * elem_size(a.dt); }
-
-size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 // Workspace: [per-chunk gradient partials | per-chunk loss partials | one
 // reduced gradient (the Muon step's input)], each 256-byte aligned.
@@ -423,7 +387,7 @@ const char* vggt3_status_str(int status) {
   }
 }
 
-const char* vggt3_last_error(void) { return g_last_error.c_str(); }
+const char* vggt3_last_error(void) { return last_error().c_str(); }
 
 int vggt3_shortconv_ex(const void* V, void* Vp, const float* w, int64_t n_views, int32_t grid_h, int32_t grid_w,
                        int32_t n_special, int32_t channels, int32_t ksize, int32_t dtype, void* stream) {
