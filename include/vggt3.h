@@ -541,6 +541,63 @@ int vggt3_ttt_read_mx4(const void* Q, const void* Q_scales, int32_t q_type, cons
                        const void* down_scales, void* O, int64_t n_tokens, int32_t n_heads, int32_t d_head,
                        int32_t d_hidden, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Block join: the tail of one block and the head of the next in one pass over
+ * the stream. For every token,
+ *
+ *   h = post(f),   r = x + scale * gate * h   (stored),   y = pre(r)
+ *
+ * with f the block's output (the layer's O after its projection), x the
+ * residual stream, and post and pre each VGGT3_NORM_NONE, VGGT3_NORM_RMS
+ * (v / sqrt(mean v^2 + eps) * w + b) or VGGT3_NORM_LAYER (the same of v - mean v).
+ * y is the norm of r as stored, so it equals the norm taken in a call of its own.
+ *
+ *   x, f, r, y  [n_tokens][channels], dtype. r may be x (in place); no other
+ *               output may overlap anything. f NULL (then r, gate, scale NULL and
+ *               post NONE): y = pre(x) alone.
+ *   gate        NULL (1) or [ceil(n_tokens / gate_tokens)][channels], dtype: row
+ *               t / gate_tokens serves token t (1: a gate per token; the tokens
+ *               of a view: a gate per view).
+ *   scale       NULL (1) or float32 [channels], the residual scale.
+ *   post_w, post_b, pre_w, pre_b   NULL (1 / 0) or float32 [channels].
+ *   y, or y_codes and y_scales     with a pre norm, one of them: y itself, or y
+ *               rounded to dtype and then quantised as by vggt3_mx4_quantize
+ *               ([n_tokens][channels]), the operand of vggt3_mx4_matmul and
+ *               vggt3_ttt_read_mx4.
+ * All arithmetic is fp32; r and y are rounded once each. channels at most 8192,
+ * of any count (multiples of 16 bytes are faster). n_tokens == 0 is a no-op.
+ */
+enum { VGGT3_NORM_NONE = 0, VGGT3_NORM_RMS = 1, VGGT3_NORM_LAYER = 2 };
+
+int vggt3_block_join(const void* x, const void* f, const void* gate, int64_t gate_tokens, const float* scale,
+                     int32_t post, const float* post_w, const float* post_b, int32_t pre, const float* pre_w,
+                     const float* pre_b, float eps, void* r, void* y, void* y_codes, void* y_scales, int64_t n_tokens,
+                     int32_t channels, int32_t dtype, void* stream);
+
+/*
+ * Gradient of vggt3_block_join, from the stored r, f and the parameters (no
+ * statistics are kept between the calls; without f, r is the forward's x).
+ *
+ *   dr          gradient of r from the stream's later uses; NULL (0) if there is
+ *               a pre norm.
+ *   dy          gradient of y (pre norm only).
+ *   dx, df, dgate     outputs in dtype, of the shapes of x, f, gate; dx may be
+ *               dr (in place). dgate sums over the tokens that share a row.
+ *   dscale, dpost_w, dpost_b, dpre_w, dpre_b    float32 [channels], summed over
+ *               all tokens in fp32, in a fixed order. (A NULL weight or scale
+ *               counts as 1; its gradient may still be asked for.)
+ * Every output may be NULL (not wanted). post_b enters dscale and dgate.
+ *   workspace   at least vggt3_block_join_grad_workspace_bytes(...) bytes.
+ * n_tokens == 0 writes zeros to the float32 outputs.
+ */
+size_t vggt3_block_join_grad_workspace_bytes(int64_t n_tokens, int32_t channels, int32_t dtype);
+int vggt3_block_join_grad(const void* r, const void* f, const void* gate, int64_t gate_tokens, const float* scale,
+                          int32_t post, const float* post_w, const float* post_b, int32_t pre, const float* pre_w,
+                          float eps, const void* dr, const void* dy, void* dx, void* df, void* dgate, float* dscale,
+                          float* dpost_w, float* dpost_b, float* dpre_w, float* dpre_b, int64_t n_tokens,
+                          int32_t channels, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

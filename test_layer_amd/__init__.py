@@ -659,3 +659,135 @@ def ttt_read_mx4(Q: Union[Mx4, torch.Tensor], frozen: FrozenMx4, out: Optional[t
         _call("vggt3_ttt_read_mx4", _ptr(data), _ptr(scales), q_type, *(_ptr(p) for p in parts), _ptr(out), n, 1, d, m,
               _ptr(workspace), nb, _stream())
     return out
+
+
+# ---------------------------------------------------------------------------
+# Block join: norm after a block, gate, residual scale, residual, norm before
+# the next block; and its gradient
+# ---------------------------------------------------------------------------
+
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+_NORMS = {None: NORM_NONE, "none": NORM_NONE, "rms": NORM_RMS, "layer": NORM_LAYER}
+
+
+def _norm_code(kind) -> int:
+    return _NORMS[kind] if kind is None or isinstance(kind, str) else int(kind)
+
+
+def _check_gate(gate: Optional[torch.Tensor], gate_tokens: int, x: torch.Tensor) -> None:
+    if gate is None:
+        return
+    if int(gate_tokens) < 1:
+        raise ValueError(f"gate_tokens = {gate_tokens} < 1")
+    want = (-(-x.shape[0] // int(gate_tokens)), x.shape[1])
+    if tuple(gate.shape) != want or gate.dtype != x.dtype:
+        raise ValueError(f"gate {tuple(gate.shape)} {gate.dtype}, {want} {x.dtype} expected")
+
+
+def block_join(x: torch.Tensor, f: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+               gate_tokens: int = 1, scale: Optional[torch.Tensor] = None, post=None,
+               post_w: Optional[torch.Tensor] = None, post_b: Optional[torch.Tensor] = None, pre=None,
+               pre_w: Optional[torch.Tensor] = None, pre_b: Optional[torch.Tensor] = None, eps: float = 1e-6,
+               mx4: bool = False, r: Optional[torch.Tensor] = None, y: Union[torch.Tensor, Mx4, None] = None):
+    """(r, y): r = x + scale * gate * post(f), y = pre(r).
+
+    post, pre: None, "rms" or "layer". Without f, y = pre(x) and r is None;
+    without pre, y is None. Row t // gate_tokens of gate serves token t. With
+    mx4, y comes in 4 bits (the operand of mx4_matmul and ttt_read_mx4). r and y
+    may be given as outputs; r may be x (in place)."""
+    _check_tokens("x", x)
+    _check_same("f", f, x, "x")
+    _check_gate(gate, gate_tokens, x)
+    n, C = x.shape
+    for name, p in (("scale", scale), ("post_w", post_w), ("post_b", post_b), ("pre_w", pre_w), ("pre_b", pre_b)):
+        _check_f32(name, p, C)
+    post, pre = _norm_code(post), _norm_code(pre)
+    if f is not None:
+        _check_same("r", r, x, "x")
+        if r is None:
+            r = torch.empty_like(x)
+    elif r is not None:
+        raise ValueError("r goes with a block output f")
+    codes = scales = None
+    if pre == NORM_NONE:
+        if y is not None or mx4:
+            raise ValueError("y goes with a norm before the next block")
+    elif mx4:
+        if y is None:
+            y = _mx4_empty(n, C, x.device)
+        _check_mx4("y", y, n, C)
+        codes, scales = y.codes, y.scales
+    else:
+        if y is None:
+            y = torch.empty_like(x)
+        _check_same("y", y, x, "x")
+    plain = None if mx4 else y
+    ts = (x, f, gate, scale, post_w, post_b, pre_w, pre_b, r, plain, codes, scales)
+    _check_dev(*ts)
+    with _on(*ts):
+        _call("vggt3_block_join", _ptr(x), _ptr(f), _ptr(gate), int(gate_tokens), _ptr(scale), post, _ptr(post_w),
+              _ptr(post_b), pre, _ptr(pre_w), _ptr(pre_b), float(eps), _ptr(r), _ptr(plain), _ptr(codes), _ptr(scales),
+              n, C, _dtype_code(x), _stream())
+    return r, y
+
+
+class BlockJoinGrads(NamedTuple):
+    """Gradients of block_join's inputs; None for those that are absent or not wanted."""
+
+    dx: Optional[torch.Tensor] = None
+    df: Optional[torch.Tensor] = None
+    dgate: Optional[torch.Tensor] = None
+    dscale: Optional[torch.Tensor] = None
+    dpost_w: Optional[torch.Tensor] = None
+    dpost_b: Optional[torch.Tensor] = None
+    dpre_w: Optional[torch.Tensor] = None
+    dpre_b: Optional[torch.Tensor] = None
+
+
+def block_join_grad_workspace_bytes(n_tokens: int, channels: int, dtype_code: int) -> int:
+    return int(lib().vggt3_block_join_grad_workspace_bytes(n_tokens, channels, dtype_code))
+
+
+def block_join_grad(r: torch.Tensor, f: Optional[torch.Tensor] = None, dr: Optional[torch.Tensor] = None,
+                    dy: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, gate_tokens: int = 1,
+                    scale: Optional[torch.Tensor] = None, post=None, post_w: Optional[torch.Tensor] = None,
+                    post_b: Optional[torch.Tensor] = None, pre=None, pre_w: Optional[torch.Tensor] = None,
+                    pre_bias: bool = False, eps: float = 1e-6, out: Optional[BlockJoinGrads] = None,
+                    workspace: Optional[torch.Tensor] = None) -> BlockJoinGrads:
+    """Gradient of block_join at its stored r (without f: its x) and f, from the
+    gradients dr of r and dy of y.
+
+    Gradients of what was given are returned (pre_bias: there was a pre_b, whose
+    value does not enter). With `out`, exactly its tensors are written; out.dx
+    may be dr."""
+    _check_tokens("r", r)
+    for name, t in (("f", f), ("dr", dr), ("dy", dy)):
+        _check_same(name, t, r, "r")
+    _check_gate(gate, gate_tokens, r)
+    n, C = r.shape
+    for name, p in (("scale", scale), ("post_w", post_w), ("post_b", post_b), ("pre_w", pre_w)):
+        _check_f32(name, p, C)
+    post, pre = _norm_code(post), _norm_code(pre)
+    if out is None:
+        def vec(p):
+            return torch.empty(C, dtype=torch.float32, device=r.device) if p is not None and p is not False else None
+
+        out = BlockJoinGrads(torch.empty_like(r), None if f is None else torch.empty_like(f),
+                             None if gate is None else torch.empty_like(gate), vec(scale), vec(post_w), vec(post_b),
+                             vec(pre_w), vec(pre_bias))
+    else:
+        _check_same("dx", out.dx, r, "r")
+        _check_same("df", out.df, r, "r")
+        if out.dgate is not None and gate is None:
+            raise ValueError("dgate without a gate")
+        _check_same("dgate", out.dgate, gate, "gate")
+        for name in BlockJoinGrads._fields[3:]:
+            _check_f32(name, getattr(out, name), C)
+    ts = (r, f, dr, dy, gate, scale, post_w, post_b, pre_w, workspace) + tuple(out)
+    _check_dev(*ts)
+    with _on(*ts):
+        workspace, nb = _ws(workspace, block_join_grad_workspace_bytes(n, C, _dtype_code(r)), r.device)
+        _call("vggt3_block_join_grad", _ptr(r), _ptr(f), _ptr(gate), int(gate_tokens), _ptr(scale), post, _ptr(post_w),
+              _ptr(post_b), pre, _ptr(pre_w), float(eps), _ptr(dr), _ptr(dy), *(_ptr(t) for t in out), n, C,
+              _dtype_code(r), _ptr(workspace), nb, _stream())
+    return out

@@ -74,6 +74,12 @@ SIGNATURES = {
     "vggt3_ttt_read_mx4_workspace_bytes": (c_size, [c_i64, c_int, c_int, c_int, c_int]),
     "vggt3_ttt_read_mx4": (c_int, [c_void_p, c_void_p, c_int] + [c_void_p] * 7 + [c_i64, c_int, c_int, c_int,
                                                                                   c_void_p, c_size, c_void_p]),
+    "vggt3_block_join": (c_int, [c_void_p, c_void_p, c_void_p, c_i64, c_void_p, c_int, c_void_p, c_void_p, c_int,
+                                 c_void_p, c_void_p, c_float] + [c_void_p] * 4 + [c_i64, c_int, c_int, c_void_p]),
+    "vggt3_block_join_grad_workspace_bytes": (c_size, [c_i64, c_int, c_int]),
+    "vggt3_block_join_grad": (c_int, [c_void_p, c_void_p, c_void_p, c_i64, c_void_p, c_int, c_void_p, c_void_p, c_int,
+                                      c_void_p, c_float] + [c_void_p] * 10 + [c_i64, c_int, c_int, c_void_p, c_size,
+                                                                              c_void_p]),
 }
 
 _lib = None

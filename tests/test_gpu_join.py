@@ -1,0 +1,315 @@
+"""Block join and its gradient against the float64 oracle on the GPU.
+
+Tolerances, derived before the first run, in u = 2^-24 (an fp32 rounding) and half a step of the output type
+(2^-8 relative for bf16, u for fp32):
+- A row sum adds at most 16 values a thread, 6 butterfly steps and 8 waves: 30 roundings, so a mean is off by
+  30 u mean|v| and, with the few operations round it, a norm by 40 u (|v| + mean|v|) rstd |w|.
+- A gradient row goes through two such sums one after the other (80 u), and the norm after the block through two
+  more (160 u); sums over tokens add at most (rows a unit + 4 + blocks / 16 + 4) < 60 roundings at these sizes.
+  All are bounded by 256 u times the same formula with every term's magnitude in place of the term.
+"""
+import numpy as np
+import pytest
+import torch
+
+import test_layer_amd as tla
+from gpu_util import to64
+from oracle import join, mx4
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+def _case(n, C, dtype, post, pre, gate, per, scale, bias, seed=0):
+    g = np.random.default_rng(seed)
+
+    def t(*shape, std=1.0, mean=0.0, dt=torch.float32):
+        return torch.tensor(g.standard_normal(shape) * std + mean, dtype=torch.float32).to(dt).cuda()
+
+    dt = DT[dtype]
+    c = dict(x=t(n, C, std=1.5, dt=dt), f=t(n, C, std=0.7, mean=0.3, dt=dt), post=post, pre=pre, per=per,
+             gate=t(-(-n // per), C, std=0.5, mean=1.0, dt=dt) if gate else None, scale=t(C, std=0.2, mean=0.3) if scale else None,
+             post_w=t(C, std=0.2, mean=1.0) if post != "none" else None, pre_w=t(C, std=0.2, mean=1.0) if pre != "none" else None,
+             post_b=t(C, std=0.3) if post != "none" and bias else None, pre_b=t(C, std=0.3) if pre != "none" and bias else None,
+             dr=t(n, C, dt=dt), dy=t(n, C, dt=dt) if pre != "none" else None)
+    return c
+
+
+def _o(c, *names):
+    return [None if c[k] is None else to64(c[k]) for k in names]
+
+
+def _args(c):
+    return dict(gate=c["gate"], gate_tokens=c["per"], scale=c["scale"], post=c["post"], post_w=c["post_w"], post_b=c["post_b"],
+                pre=c["pre"], pre_w=c["pre_w"])
+
+
+def _norm_mag(v, kind, w, b):
+    """Magnitude of a norm's terms: |w| rstd (|v| + mean|v|) + |b|, and rstd."""
+    if kind == "none":
+        return np.abs(v)
+    rstd = join.norm(v, kind)[2]
+    m = rstd * (np.abs(v) + np.abs(v).mean(1, keepdims=True)) * (1.0 if w is None else np.abs(w))
+    return m if b is None else m + np.abs(b)
+
+
+def _check_forward(c, dtype, mx=False):
+    r, y = tla.block_join(c["x"], c["f"], pre_b=c["pre_b"], mx4=mx, **_args(c))
+    x, f, gate, scale, pw, pb, w, b = _o(c, "x", "f", "gate", "scale", "post_w", "post_b", "pre_w", "pre_b")
+    want = join.join(x, f, gate, c["per"], scale, c["post"], pw, pb)
+    sg = np.abs((1.0 if scale is None else scale) * join.spread(gate, c["per"], len(x)))
+    tol = 40 * U * (sg * _norm_mag(f, c["post"], pw, pb) + np.abs(x)) + HALF[dtype] * np.abs(want)
+    assert (np.abs(to64(r) - want) <= tol).all()
+    if c["pre"] == "none":
+        assert y is None
+        return r, y
+    r64 = to64(r)  # the norm is that of the stored stream
+    want = join.norm(r64, c["pre"], w, b)[0]
+    if not mx:
+        tol = 40 * U * _norm_mag(r64, c["pre"], w, b) + HALF[dtype] * np.abs(want)
+        assert (np.abs(to64(y) - want) <= tol).all()
+    return r, y
+
+
+MODES = [("none", "none", False, 1, True, False), ("none", "rms", True, 1, False, False), ("rms", "none", True, 3, True, True),
+         ("layer", "layer", True, 7, True, True), ("rms", "rms", False, 1, True, False), ("none", "layer", False, 1, False, True),
+         ("layer", "rms", True, 1000, False, False), ("layer", "layer", True, 1, True, False)]
+SHAPES = [(1, 1), (1, 1024), (2, 33), (5, 64), (37, 100), (64, 512), (65, 513), (130, 1024), (40, 1025), (23, 2048), (9, 4096),
+          (6, 5000), (3, 8192), (700, 24)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("mode", MODES, ids=lambda m: "-".join(map(str, m)))
+@pytest.mark.parametrize("n,C", SHAPES)
+def test_forward(n, C, mode, dtype):
+    post, pre, gate, per, scale, bias = mode
+    _check_forward(_case(n, C, dtype, post, pre, gate, per, scale, bias, n + C), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,C", SHAPES)
+def test_y_in_4_bits_is_y_quantised(n, C, dtype):
+    c = _case(n, C, dtype, "rms", "layer", True, 2, True, True, n)
+    if n > 3:
+        c["x"][2, C // 2] = float("nan")
+    r, y = tla.block_join(c["x"], c["f"], pre_b=c["pre_b"], **_args(c))
+    r4, y4 = tla.block_join(c["x"], c["f"], pre_b=c["pre_b"], mx4=True, **_args(c))
+    want = tla.mx4_quantize(y)
+    assert torch.equal(r.view(torch.int16), r4.view(torch.int16))
+    assert torch.equal(y4.codes, want.codes) and torch.equal(y4.scales, want.scales)
+
+
+@pytest.mark.parametrize("pre", ["rms", "layer"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_alone(pre, dtype):
+    c = _case(50, 200, dtype, "none", pre, False, 1, False, True)
+    r, y = tla.block_join(c["x"], pre=pre, pre_w=c["pre_w"], pre_b=c["pre_b"])
+    assert r is None
+    x, w, b = _o(c, "x", "pre_w", "pre_b")
+    want = join.norm(x, pre, w, b)[0]
+    assert (np.abs(to64(y) - want) <= 40 * U * _norm_mag(x, pre, w, b) + HALF[dtype] * np.abs(want)).all()
+    # and it is the y of a join that gives the same stream
+    zero = torch.zeros_like(c["x"])
+    r2, y2 = tla.block_join(c["x"], zero, pre=pre, pre_w=c["pre_w"], pre_b=c["pre_b"])
+    assert torch.equal(r2, c["x"]) and torch.equal(y2, y)
+
+
+def test_in_place_and_given_outputs():
+    c = _case(300, 1024, "bf16", "layer", "rms", True, 50, True, True)
+    r, y = tla.block_join(c["x"], c["f"], pre_b=c["pre_b"], **_args(c))
+    x, y2 = c["x"].clone(), torch.empty_like(y)
+    r3, y3 = tla.block_join(x, c["f"], pre_b=c["pre_b"], r=x, y=y2, **_args(c))
+    assert r3 is x and y3 is y2 and torch.equal(x, r) and torch.equal(y2, y)
+    got = tla.block_join_grad(r, c["f"], c["dr"], c["dy"], pre_bias=True, **_args(c))
+    dr = c["dr"].clone()
+    out = got._replace(**{k: torch.empty_like(v) for k, v in got._asdict().items()})._replace(dx=dr)
+    tla.block_join_grad(r, c["f"], dr, c["dy"], out=out, **_args(c))
+    for k, v in got._asdict().items():
+        assert torch.equal(getattr(out, k), v), k
+
+
+def test_rows_far_from_zero_mean_and_constant_rows():
+    # a mean 1000 times the deviation: the two-pass variance keeps its digits; a constant row has deviation 0
+    x = torch.randn(20, 512, generator=torch.Generator().manual_seed(0)) + 1000
+    x[3] = 5.0
+    x[4] = 0.0
+    x = x.cuda()
+    _, y = tla.block_join(x, pre="layer")
+    want = join.norm(to64(x), "layer")[0]
+    # the centred values are off by 40 u (|v| + mean|v|) = 80 u 1000, over a deviation of 1 (or sqrt(eps))
+    rstd = join.norm(to64(x), "layer")[2]
+    assert (np.abs(to64(y) - want) <= 80 * U * np.abs(to64(x)) * rstd + 40 * U * np.abs(want)).all()
+    assert (to64(y)[4] == 0).all()
+
+
+def test_non_finite_rows_stay_alone():
+    c = _case(9, 256, "f32", "layer", "rms", True, 1, True, True)
+    c["f"][2, 5] = float("inf")
+    c["x"][7, 0] = float("nan")
+    r, y = tla.block_join(c["x"], c["f"], pre_b=c["pre_b"], **_args(c))
+    bad = torch.isnan(y).all(1)
+    assert bad.tolist() == [i in (2, 7) for i in range(9)]
+    assert torch.isfinite(r[[0, 1, 3, 4, 5, 6, 8]]).all() and torch.isfinite(y[~bad]).all()
+
+
+def _magnitudes(c):
+    """join.grads with every term's magnitude in place of the term."""
+    r, f, dr, dy, gate, scale, pw, pb, w = _o(c, "x", "f", "dr", "dy", "gate", "scale", "post_w", "post_b", "pre_w")
+    n, C = r.shape
+
+    def hat_mag(v, kind):
+        return np.abs(v) if kind == "none" else _norm_mag(v, kind, None, None)
+
+    def back_mag(d, v, kind):
+        if kind == "none":
+            return d
+        h, rstd = hat_mag(v, kind), join.norm(v, kind)[2]
+        return rstd * (d + h * (d * h).mean(1, keepdims=True) + d.mean(1, keepdims=True))
+
+    out = {}
+    d = np.abs(dr)
+    if c["pre"] != "none":
+        h = hat_mag(r, c["pre"])
+        out["dpre_w"], out["dpre_b"] = (np.abs(dy) * h).sum(0), np.abs(dy).sum(0)
+        d = d + back_mag(np.abs(dy) * np.abs(w), r, c["pre"])
+    out["dx"] = d
+    h = _norm_mag(f, c["post"], pw, pb)
+    g, s = np.abs(join.spread(gate, c["per"], n)), 1.0 if scale is None else np.abs(scale)
+    out["dscale"] = (d * g * h).sum(0)
+    groups = -(-n // c["per"])
+    p = np.zeros((groups * c["per"], C))
+    p[:n] = d * s * h
+    out["dgate"] = p.reshape(groups, c["per"], C).sum(1)
+    dh = d * g * s
+    out["dpost_w"], out["dpost_b"] = (dh * hat_mag(f, c["post"])).sum(0), dh.sum(0)
+    out["df"] = back_mag(dh * (1.0 if pw is None else np.abs(pw)), f, c["post"])
+    return out
+
+
+def _check_grad(c, dtype):
+    got = tla.block_join_grad(c["x"], c["f"], c["dr"], c["dy"], pre_bias=c["pre_b"] is not None, **_args(c))
+    r, f, dr, dy, gate, scale, pw, pb, w = _o(c, "x", "f", "dr", "dy", "gate", "scale", "post_w", "post_b", "pre_w")
+    want = join.grads(r, f, dr, dy, gate, c["per"], scale, c["post"], pw, pb, c["pre"], w)
+    mag = _magnitudes(c)
+    given = {"dx": True, "df": True, "dgate": c["gate"], "dscale": c["scale"], "dpost_w": c["post_w"], "dpost_b": c["post_b"],
+             "dpre_w": c["pre_w"], "dpre_b": c["pre_b"]}
+    for k, v in got._asdict().items():
+        assert (v is None) == (given[k] is None), k
+        if v is None:
+            continue
+        half = HALF[dtype] if k in ("dx", "df", "dgate") else U
+        err = np.abs(to64(v) - want[k])
+        tol = 256 * U * mag[k] + half * np.abs(want[k])
+        assert (err <= tol).all(), (k, float((err / np.maximum(tol, 1e-300)).max()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("mode", MODES, ids=lambda m: "-".join(map(str, m)))
+@pytest.mark.parametrize("n,C", SHAPES)
+def test_grad(n, C, mode, dtype):
+    post, pre, gate, per, scale, bias = mode
+    _check_grad(_case(n, C, dtype, post, pre, gate, per, scale, bias, n + C), dtype)
+
+
+@pytest.mark.parametrize("per", [1, 2, 3, 50, 137, 1374, 2999, 3000, 10 ** 6])
+def test_gate_groups_across_units(per):
+    # groups inside a unit's rows, ending with them, spanning two and many, and one longer than the tokens
+    _check_grad(_case(3000, 40, "f32", "rms", "layer", True, per, True, True, per), "f32")
+
+
+def test_grad_at_more_rows_than_one_a_unit():
+    c = _case(20011, 1024, "bf16", "layer", "layer", True, 1374, True, True)
+    got = tla.block_join_grad(c["x"], c["f"], c["dr"], c["dy"], pre_bias=True, **_args(c))
+    again = tla.block_join_grad(c["x"], c["f"], c["dr"], c["dy"], pre_bias=True, **_args(c))
+    r, f, dr, dy, gate, scale, pw, pb, w = _o(c, "x", "f", "dr", "dy", "gate", "scale", "post_w", "post_b", "pre_w")
+    want = join.grads(r, f, dr, dy, gate, 1374, scale, "layer", pw, pb, "layer", w)
+    for k, v in got._asdict().items():
+        assert torch.equal(v, getattr(again, k)), k
+        half = 2.0 ** -8 if k in ("dx", "df", "dgate") else U
+        e = np.linalg.norm(to64(v) - want[k]) / np.linalg.norm(want[k])
+        assert e <= half + 256 * U, (k, e)
+
+
+def test_grad_of_the_norm_alone():
+    c = _case(77, 300, "f32", "none", "layer", False, 1, False, True)
+    got = tla.block_join_grad(c["x"], dy=c["dy"], pre="layer", pre_w=c["pre_w"], pre_bias=True)
+    r, dy, w = _o(c, "x", "dy", "pre_w")
+    want = join.grads(r, None, None, dy, pre="layer", pre_w=w)
+    zero = dict(c, dr=torch.zeros_like(c["dr"]))
+    mag = _magnitudes(zero)
+    assert got.df is None and got.dscale is None and got.dgate is None
+    for k in ("dx", "dpre_w", "dpre_b"):
+        assert (np.abs(to64(getattr(got, k)) - want[k]) <= 256 * U * mag[k] + U * np.abs(want[k])).all(), k
+
+
+def test_unwanted_gradients_are_left_alone():
+    c = _case(60, 128, "f32", "rms", "rms", True, 4, True, False)
+    full = tla.block_join_grad(c["x"], c["f"], c["dr"], c["dy"], **_args(c))
+    only = tla.block_join_grad(c["x"], c["f"], c["dr"], c["dy"], out=tla.BlockJoinGrads(df=torch.empty_like(c["f"])), **_args(c))
+    assert torch.equal(only.df, full.df) and only.dx is None and only.dgate is None and only.dscale is None
+
+
+def test_no_tokens():
+    x = torch.empty(0, 64, device="cuda")
+    w = torch.ones(64, device="cuda")
+    r, y = tla.block_join(x, x.clone(), pre="rms", pre_w=w)
+    assert r.shape == y.shape == (0, 64)
+    _, y4 = tla.block_join(x, x.clone(), pre="rms", pre_w=w, mx4=True)
+    assert y4.codes.shape == (0, 64)
+    got = tla.block_join_grad(x, x.clone(), x.clone(), x.clone(), pre="rms", pre_w=w, scale=w)
+    assert got.dx.shape == (0, 64) and (got.dscale == 0).all() and (got.dpre_w == 0).all()
+
+
+def test_streams_and_graph_replay():
+    c = _case(500, 1024, "bf16", "layer", "layer", True, 100, True, True)
+
+    def both(**kw):
+        return (tla.block_join(c["x"], c["f"], pre_b=c["pre_b"], **_args(c), **{k: v for k, v in kw.items() if k in "ry"}),
+                tla.block_join_grad(c["x"], c["f"], c["dr"], c["dy"], pre_bias=True, **_args(c),
+                                    **{k: v for k, v in kw.items() if k not in "ry"}))
+
+    (r, y), grads = both()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        (r2, y2), grads2 = both()
+    s.synchronize()
+    assert torch.equal(r, r2) and torch.equal(y, y2) and all(torch.equal(a, b) for a, b in zip(grads, grads2))
+    ws = torch.empty(tla.block_join_grad_workspace_bytes(500, 1024, tla.BF16), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        both(r=r2, y=y2, out=grads2, workspace=ws)
+    for seed in (1, 2, 3):
+        new = _case(500, 1024, "bf16", "layer", "layer", True, 100, True, True, seed)
+        for k in ("x", "f", "gate", "dr", "dy", "scale", "post_w"):
+            c[k].copy_(new[k])
+        for t in (r2, y2, *grads2):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        (r, y), grads = both()
+        assert torch.equal(r, r2) and torch.equal(y, y2) and all(torch.equal(a, b) for a, b in zip(grads, grads2))
+
+
+def test_block_on_frozen_weights_end_to_end():
+    """The operators as a served block uses them: norm -> 4 bits -> frozen MLP -> join -> norm -> 4 bits -> product."""
+    n, per = 300, 100
+    g = torch.Generator().manual_seed(2)
+    theta = torch.randn(1, 3 * 1024 * 4096, generator=g) / 32
+    c = _case(n, 1024, "bf16", "layer", "rms", True, per, True, True)
+    frozen = tla.ttt_freeze_mx4(theta.cuda())
+    head = tla.mx4_quantize((torch.randn(77, 1024, generator=g) / 32).cuda())
+    _, q = tla.block_join(c["x"], pre="layer", mx4=True)
+    o = tla.ttt_read_mx4(q, frozen)
+    r, y = tla.block_join(c["x"], o, pre_b=c["pre_b"], mx4=True, **_args(c))
+    z = tla.mx4_matmul(y, head, torch.float32)
+    # each step against the oracle on the step's own inputs
+    qv = to64(tla.mx4_dequantize(q, torch.float32))
+    plain = to64(tla.block_join(c["x"], pre="layer")[1])
+    assert np.array_equal(qv, mx4.roundtrip(plain))
+    assert torch.equal(o, tla.ttt_read_mx4(torch.tensor(plain).to(torch.bfloat16).cuda(), frozen))
+    _check_forward(dict(c, f=o), "bf16", mx=True)
+    yv, hv = to64(tla.mx4_dequantize(y, torch.float32)), to64(tla.mx4_dequantize(head, torch.float32))
+    assert (np.abs(to64(z) - yv @ hv.T) <= 1024 * U * (np.abs(yv) @ np.abs(hv).T)).all()
