@@ -477,13 +477,41 @@ def ttt_read_streamed(Q_host: torch.Tensor, theta: torch.Tensor, n_heads: int, c
 # weights frozen in 4 bits
 # ---------------------------------------------------------------------------
 
-def _on(*ts):
-    """The device context of a call's tensors: they share one GPU, and the call
-    runs on that GPU's current stream, whichever device is current."""
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors live on different devices: {sorted(str(d) for d in devs)}")
-    return torch.cuda.device(devs.pop())
+def _device_of(ts) -> int:
+    """The one GPU that a call's tensors share; they are contiguous."""
+    dev = -1
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must live on the GPU (HIP device memory)")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        d = t.get_device()
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"tensors live on different devices: cuda:{dev} and cuda:{d}")
+    return dev
+
+
+# The current stream of a GPU as the address that the C calls take, without the
+# Stream object round it (which costs as much host time as a launch).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _run(name: str, dev: int, *args) -> None:
+    """Call `name` on GPU `dev`'s current stream, whichever device is current.
+    Tensors among the arguments pass as their addresses."""
+    fn = getattr(_lib.load(), name)
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
+    if rc != OK:
+        raise Vggt3Error(name, rc)
 
 
 class Mx4(NamedTuple):
@@ -509,8 +537,8 @@ class FrozenMx4(NamedTuple):
 
 
 def _mx4_shapes(rows: int, k: int):
-    kp = (k + 127) // 128 * 128
-    return (rows, kp // 2), ((rows + 63) // 64, kp // 128, 64, 4)
+    nb = (k + 127) // 128
+    return (rows, nb * 64), ((rows + 63) // 64, nb, 64, 4)
 
 
 def _mx4_empty(rows: int, k: int, device) -> Mx4:
@@ -521,17 +549,18 @@ def _mx4_empty(rows: int, k: int, device) -> Mx4:
 def _check_mx4(name: str, a: Mx4, rows: Optional[int] = None, k: Optional[int] = None) -> None:
     if not isinstance(a, Mx4):
         raise TypeError(f"{name} must be an Mx4 (codes, scales, k), got {type(a).__name__}")
-    for part, t in (("codes", a.codes), ("scales", a.scales)):
-        if t.dtype != torch.uint8:
-            raise TypeError(f"{name}.{part} must be uint8, got {t.dtype}")
-    if a.codes.dim() != 2 or int(a.k) < 1:
-        raise ValueError(f"{name}: codes are [rows, kp / 2] and k >= 1, got {tuple(a.codes.shape)} and k = {a.k}")
-    if (rows is not None and a.rows != rows) or (k is not None and a.k != k):
-        raise ValueError(f"{name} is [{a.rows}, {a.k}], [{a.rows if rows is None else rows}, {a.k if k is None else k}] expected")
-    cs, ss = _mx4_shapes(a.rows, int(a.k))
-    if tuple(a.codes.shape) != cs or tuple(a.scales.shape) != ss:
-        raise ValueError(f"{name} [{a.rows}, {a.k}] has codes {tuple(a.codes.shape)} and scales "
-                         f"{tuple(a.scales.shape)}, {cs} and {ss} expected")
+    codes, scales, ak = a
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError(f"{name}: codes and scales must be uint8, got {codes.dtype} and {scales.dtype}")
+    if codes.dim() != 2 or ak < 1:
+        raise ValueError(f"{name}: codes are [rows, kp / 2] and k >= 1, got {tuple(codes.shape)} and k = {ak}")
+    n = codes.shape[0]
+    if (rows is not None and n != rows) or (k is not None and ak != k):
+        raise ValueError(f"{name} is [{n}, {ak}], [{n if rows is None else rows}, {ak if k is None else k}] expected")
+    cs, ss = _mx4_shapes(n, ak)
+    if codes.shape != cs or scales.shape != ss:
+        raise ValueError(f"{name} [{n}, {ak}] has codes {tuple(codes.shape)} and scales {tuple(scales.shape)}, "
+                         f"{cs} and {ss} expected")
 
 
 def _type_code(dtype: torch.dtype) -> int:
@@ -564,10 +593,8 @@ def mx4_quantize(X: torch.Tensor, transpose: bool = False, out: Optional[Mx4] = 
         _check_mx4("out", out, rows, k)
     else:
         out = _mx4_empty(rows, k, X.device)
-    _check_dev(X, out.codes, out.scales)
-    with _on(X, out.codes, out.scales):
-        _call("vggt3_mx4_quantize", _ptr(X), int(bool(transpose)), _ptr(out.codes), _ptr(out.scales), rows, k,
-              _dtype_code(X), _stream())
+    dev = _device_of((X, out.codes, out.scales))
+    _run("vggt3_mx4_quantize", dev, X, int(bool(transpose)), out.codes, out.scales, rows, k, _dtype_code(X))
     return out
 
 
@@ -578,9 +605,8 @@ def mx4_dequantize(A: Mx4, dtype: torch.dtype = torch.bfloat16, out: Optional[to
     _check_out(out, (A.rows, A.k), dtype)
     if out is None:
         out = torch.empty((A.rows, A.k), dtype=dtype, device=A.codes.device)
-    _check_dev(A.codes, A.scales, out)
-    with _on(A.codes, A.scales, out):
-        _call("vggt3_mx4_dequantize", _ptr(A.codes), _ptr(A.scales), _ptr(out), A.rows, A.k, dt, _stream())
+    dev = _device_of((A.codes, A.scales, out))
+    _run("vggt3_mx4_dequantize", dev, A.codes, A.scales, out, A.rows, A.k, dt)
     return out
 
 
@@ -604,11 +630,9 @@ def mx4_matmul(A: Union[Mx4, torch.Tensor], W: Mx4, dtype: torch.dtype = torch.b
     _check_out(out, (m, W.rows), dtype)
     if out is None:
         out = torch.empty((m, W.rows), dtype=dtype, device=data.device)
-    _check_dev(data, scales, W.codes, W.scales, out, workspace)
-    with _on(data, scales, W.codes, W.scales, out, workspace):
-        workspace, nb = _ws(workspace, mx4_matmul_workspace_bytes(m, W.rows, W.k, a_type), data.device)
-        _call("vggt3_mx4_matmul", _ptr(data), _ptr(scales), a_type, _ptr(W.codes), _ptr(W.scales), _ptr(out), m, W.rows,
-              W.k, dt, _ptr(workspace), nb, _stream())
+    workspace, nb = _ws(workspace, mx4_matmul_workspace_bytes(m, W.rows, W.k, a_type), data.device)
+    dev = _device_of((data, scales, W.codes, W.scales, out, workspace))
+    _run("vggt3_mx4_matmul", dev, data, scales, a_type, W.codes, W.scales, out, m, W.rows, W.k, dt, workspace, nb)
     return out
 
 
@@ -623,9 +647,7 @@ def ttt_freeze_mx4(theta: torch.Tensor, d_head: int = 1024, d_hidden: int = 4096
     for name, a, (r, k) in zip(FrozenMx4._fields, out, shapes):
         _check_mx4(name, a, r, k)
         parts += [a.codes, a.scales]
-    _check_dev(theta, *parts)
-    with _on(theta, *parts):
-        _call("vggt3_ttt_freeze_mx4", _ptr(theta), *(_ptr(p) for p in parts), 1, d_head, d_hidden, _stream())
+    _run("vggt3_ttt_freeze_mx4", _device_of((theta, *parts)), theta, *parts, 1, d_head, d_hidden)
     return out
 
 
@@ -653,11 +675,9 @@ def ttt_read_mx4(Q: Union[Mx4, torch.Tensor], frozen: FrozenMx4, out: Optional[t
     _check_out(out, (n, d), torch.bfloat16)
     if out is None:
         out = torch.empty((n, d), dtype=torch.bfloat16, device=data.device)
-    _check_dev(data, scales, out, workspace, *parts)
-    with _on(data, scales, out, workspace, *parts):
-        workspace, nb = _ws(workspace, read_mx4_workspace_bytes(n, d, m, q_type), data.device)
-        _call("vggt3_ttt_read_mx4", _ptr(data), _ptr(scales), q_type, *(_ptr(p) for p in parts), _ptr(out), n, 1, d, m,
-              _ptr(workspace), nb, _stream())
+    workspace, nb = _ws(workspace, read_mx4_workspace_bytes(n, d, m, q_type), data.device)
+    dev = _device_of((data, scales, out, workspace, *parts))
+    _run("vggt3_ttt_read_mx4", dev, data, scales, q_type, *parts, out, n, 1, d, m, workspace, nb)
     return out
 
 
@@ -723,11 +743,8 @@ def block_join(x: torch.Tensor, f: Optional[torch.Tensor] = None, gate: Optional
         _check_same("y", y, x, "x")
     plain = None if mx4 else y
     ts = (x, f, gate, scale, post_w, post_b, pre_w, pre_b, r, plain, codes, scales)
-    _check_dev(*ts)
-    with _on(*ts):
-        _call("vggt3_block_join", _ptr(x), _ptr(f), _ptr(gate), int(gate_tokens), _ptr(scale), post, _ptr(post_w),
-              _ptr(post_b), pre, _ptr(pre_w), _ptr(pre_b), float(eps), _ptr(r), _ptr(plain), _ptr(codes), _ptr(scales),
-              n, C, _dtype_code(x), _stream())
+    _run("vggt3_block_join", _device_of(ts), x, f, gate, int(gate_tokens), scale, post, post_w, post_b, pre, pre_w,
+         pre_b, float(eps), r, plain, codes, scales, n, C, _dtype_code(x))
     return r, y
 
 
@@ -769,12 +786,12 @@ def block_join_grad(r: torch.Tensor, f: Optional[torch.Tensor] = None, dr: Optio
         _check_f32(name, p, C)
     post, pre = _norm_code(post), _norm_code(pre)
     if out is None:
-        def vec(p):
-            return torch.empty(C, dtype=torch.float32, device=r.device) if p is not None and p is not False else None
-
+        # the channel vectors are rows of one allocation, 16-byte aligned
+        wanted = [scale is not None, post_w is not None, post_b is not None, pre_w is not None, bool(pre_bias)]
+        rows = iter(torch.empty((sum(wanted), (C + 3) // 4 * 4), dtype=torch.float32, device=r.device).unbind(0))
+        vecs = [(next(rows) if C % 4 == 0 else next(rows)[:C]) if w else None for w in wanted]
         out = BlockJoinGrads(torch.empty_like(r), None if f is None else torch.empty_like(f),
-                             None if gate is None else torch.empty_like(gate), vec(scale), vec(post_w), vec(post_b),
-                             vec(pre_w), vec(pre_bias))
+                             None if gate is None else torch.empty_like(gate), *vecs)
     else:
         _check_same("dx", out.dx, r, "r")
         _check_same("df", out.df, r, "r")
@@ -783,11 +800,8 @@ def block_join_grad(r: torch.Tensor, f: Optional[torch.Tensor] = None, dr: Optio
         _check_same("dgate", out.dgate, gate, "gate")
         for name in BlockJoinGrads._fields[3:]:
             _check_f32(name, getattr(out, name), C)
-    ts = (r, f, dr, dy, gate, scale, post_w, post_b, pre_w, workspace) + tuple(out)
-    _check_dev(*ts)
-    with _on(*ts):
-        workspace, nb = _ws(workspace, block_join_grad_workspace_bytes(n, C, _dtype_code(r)), r.device)
-        _call("vggt3_block_join_grad", _ptr(r), _ptr(f), _ptr(gate), int(gate_tokens), _ptr(scale), post, _ptr(post_w),
-              _ptr(post_b), pre, _ptr(pre_w), float(eps), _ptr(dr), _ptr(dy), *(_ptr(t) for t in out), n, C,
-              _dtype_code(r), _ptr(workspace), nb, _stream())
+    workspace, nb = _ws(workspace, block_join_grad_workspace_bytes(n, C, _dtype_code(r)), r.device)
+    dev = _device_of((r, f, dr, dy, gate, scale, post_w, post_b, pre_w, workspace, *out))
+    _run("vggt3_block_join_grad", dev, r, f, gate, int(gate_tokens), scale, post, post_w, post_b, pre, pre_w, float(eps),
+         dr, dy, *out, n, C, _dtype_code(r), workspace, nb)
     return out

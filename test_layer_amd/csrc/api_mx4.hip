@@ -53,22 +53,17 @@ size_t tokens_bytes(int64_t rows, int64_t k, int32_t type) {
   return type == VGGT3_MX4 ? cbytes(rows, k) : (size_t)rows * k * elem_size(type);
 }
 
-// Workspace of a product: [codes | scales] of A when it comes as tokens, then
-// the fp32 partials of a split contraction.
+// Workspace of a product: [codes | scales] of A, when it comes as more tokens
+// than the product quantises itself.
 struct MatmulWs {
-  size_t scales, part, total;
+  size_t scales, total;
 };
-MatmulWs matmul_ws(int64_t m, int64_t n, int64_t k, int32_t a_type) {
+MatmulWs matmul_ws(int64_t m, int64_t k, int32_t a_type) {
   MatmulWs l{};
-  size_t o = 0;
-  if (a_type != VGGT3_MX4) {
+  if (a_type != VGGT3_MX4 && !mx4::takes_tokens(m, (int)k)) {
     l.scales = round256(cbytes(m, k));
-    o = l.scales + round256(sbytes(m, k));
+    l.total = l.scales + round256(sbytes(m, k));
   }
-  l.part = o;
-  const int s = mx4::gemm_splits(m, (int)n, (int)mx4::padded_k(k));
-  if (s > 1) o += round256((size_t)s * m * n * sizeof(float));
-  l.total = o;
   return l;
 }
 
@@ -83,33 +78,22 @@ int check_matmul_shape(int64_t m, int64_t n, int64_t k, int32_t a_type) {
 }
 
 // Workspace of the 4-bit read of the full-width MLP, for chunks of at most
-// wide::kChunk tokens: Q in 4 bits (when it comes as tokens), H in 4 bits and
-// the second product's partials.
+// wide::kChunk tokens: H in 4 bits, then Q (when it comes as more tokens than
+// the product quantises itself).
 struct ReadWs {
   int64_t ct;
-  size_t qs, hc, hs, part, total;
+  size_t hs, qc, qs, total;
 };
 ReadWs read_ws(int64_t n, int32_t q_type) {
   namespace w = vggt3::wide;
   ReadWs l{};
   l.ct = n < w::kChunk ? n : w::kChunk;
-  size_t o = 0;
-  if (q_type != VGGT3_MX4) {
-    l.qs = round256(cbytes(l.ct, w::kD));
-    o = l.qs + round256(sbytes(l.ct, w::kD));
+  l.hs = round256(cbytes(l.ct, w::kM));
+  l.qc = l.total = l.hs + round256(sbytes(l.ct, w::kM));
+  if (q_type != VGGT3_MX4 && !mx4::takes_tokens(l.ct, w::kD)) {
+    l.qs = l.qc + round256(cbytes(l.ct, w::kD));
+    l.total = l.qs + round256(sbytes(l.ct, w::kD));
   }
-  l.hc = o;
-  l.hs = o + round256(cbytes(l.ct, w::kM));
-  l.part = l.hs + round256(sbytes(l.ct, w::kM));
-  // the last chunk may be shorter and split more often
-  const int64_t tail = l.ct > 0 && n % l.ct ? n % l.ct : l.ct;
-  size_t p = 0;
-  for (int64_t c : {l.ct, tail}) {
-    const int s = mx4::gemm_splits(c, w::kD, w::kM);
-    const size_t b = s > 1 ? (size_t)s * c * w::kD * sizeof(float) : 0;
-    p = b > p ? b : p;
-  }
-  l.total = l.part + round256(p);
   return l;
 }
 
@@ -171,7 +155,7 @@ int vggt3_mx4_dequantize(const void* codes, const void* scales, void* X, int64_t
 }
 
 size_t vggt3_mx4_matmul_workspace_bytes(int64_t m, int32_t n, int32_t k, int32_t a_type) {
-  return check_matmul_shape(m, n, k, a_type) == VGGT3_OK && m > 0 ? matmul_ws(m, n, k, a_type).total : 0;
+  return check_matmul_shape(m, n, k, a_type) == VGGT3_OK && m > 0 ? matmul_ws(m, k, a_type).total : 0;
 }
 
 int vggt3_mx4_matmul(const void* A, const void* A_scales, int32_t a_type, const void* W_codes, const void* W_scales,
@@ -181,7 +165,7 @@ int vggt3_mx4_matmul(const void* A, const void* A_scales, int32_t a_type, const 
   int rc = check_matmul_shape(m, n, k, a_type);
   if (rc) return rc;
   if (m == 0) return ok();
-  const MatmulWs l = matmul_ws(m, n, k, a_type);
+  const MatmulWs l = matmul_ws(m, k, a_type);
   const bool quantized = a_type == VGGT3_MX4;
   if (!quantized && A_scales != nullptr) return fail(VGGT3_EINVAL, "A_scales goes with a VGGT3_MX4 A only");
   if (l.total > 0 && (workspace == nullptr || workspace_bytes < l.total))
@@ -195,16 +179,20 @@ int vggt3_mx4_matmul(const void* A, const void* A_scales, int32_t a_type, const 
                       {"workspace", workspace, l.total, true}});
   if (rc) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const mx4::Matrix w{static_cast<const uint8_t*>(W_codes), static_cast<const uint8_t*>(W_scales)};
+  const bool bf16 = dtype == VGGT3_BF16;
+  if (!quantized && l.total == 0) {
+    rc = check_hip(mx4::launch_gemm_tokens(A, a_type == VGGT3_BF16, w, C, bf16, m, n, k, s), "4-bit product launch");
+    return rc ? rc : ok();
+  }
   mx4::Matrix a{static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(A_scales)};
   if (!quantized) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     a = mx4::Matrix{ws, ws + l.scales};
     rc = check_hip(mx4::launch_quantize(A, false, a_type == VGGT3_BF16, ws, ws + l.scales, m, k, s), "quantize launch");
     if (rc) return rc;
   }
-  const mx4::Matrix w{static_cast<const uint8_t*>(W_codes), static_cast<const uint8_t*>(W_scales)};
-  rc = check_hip(mx4::launch_gemm(a, w, C, dtype == VGGT3_BF16, m, n, (int)mx4::padded_k(k),
-                                  reinterpret_cast<float*>(ws + l.part), s),
+  rc = check_hip(mx4::launch_gemm(a, w, C, bf16, m, n, k, s),
                  "4-bit product launch");
   return rc ? rc : ok();
 }
@@ -273,24 +261,29 @@ int vggt3_ttt_read_mx4(const void* Q, const void* Q_scales, int32_t q_type, cons
   };
   const mx4::Matrix wg = mat(gate_codes, gate_scales), wu = mat(up_codes, up_scales),
                     wd = mat(down_codes, down_scales);
+  const mx4::Matrix h = mat(ws, ws + l.hs);
   for (int64_t t0 = 0; t0 < n_tokens; t0 += l.ct) {
     const int64_t nc = n_tokens - t0 < l.ct ? n_tokens - t0 : l.ct;
-    mx4::Matrix q;
-    if (quantized) {
-      // chunks are whole scale tiles, so a chunk's tiles follow those before it
-      q = mat(static_cast<const uint8_t*>(Q) + cbytes(t0, d), static_cast<const uint8_t*>(Q_scales) + sbytes(t0, d));
+    const uint16_t* tokens = static_cast<const uint16_t*>(Q) + t0 * d;
+    if (!quantized && mx4::takes_tokens(nc, d_head)) {
+      rc = check_hip(mx4::launch_gemm_swiglu_tokens(tokens, wg, wu, ws, ws + l.hs, nc, d_hidden, d_head, s),
+                     "4-bit SwiGLU launch");
     } else {
-      rc = check_hip(mx4::launch_quantize(static_cast<const uint16_t*>(Q) + t0 * d, false, true, ws, ws + l.qs, nc,
-                                          d_head, s),
-                     "quantize launch");
-      if (rc) return rc;
-      q = mat(ws, ws + l.qs);
+      mx4::Matrix q;
+      if (quantized) {
+        // chunks are whole scale tiles, so a chunk's tiles follow those before it
+        q = mat(static_cast<const uint8_t*>(Q) + cbytes(t0, d), static_cast<const uint8_t*>(Q_scales) + sbytes(t0, d));
+      } else {
+        rc = check_hip(mx4::launch_quantize(tokens, false, true, ws + l.qc, ws + l.qs, nc, d_head, s),
+                       "quantize launch");
+        if (rc) return rc;
+        q = mat(ws + l.qc, ws + l.qs);
+      }
+      rc = check_hip(mx4::launch_gemm_swiglu(q, wg, wu, ws, ws + l.hs, nc, d_hidden, d_head, s),
+                     "4-bit SwiGLU launch");
     }
-    rc = check_hip(mx4::launch_gemm_swiglu(q, wg, wu, ws + l.hc, ws + l.hs, nc, d_hidden, d_head, s),
-                   "4-bit SwiGLU launch");
     if (rc) return rc;
-    rc = check_hip(mx4::launch_gemm(mat(ws + l.hc, ws + l.hs), wd, static_cast<uint16_t*>(O) + t0 * d, true, nc, d_head,
-                                    d_hidden, reinterpret_cast<float*>(ws + l.part), s),
+    rc = check_hip(mx4::launch_gemm(h, wd, static_cast<uint16_t*>(O) + t0 * d, true, nc, d_head, d_hidden, s),
                    "4-bit product launch");
     if (rc) return rc;
   }

@@ -43,14 +43,19 @@ hipError_t launch_quantize(const void* X, bool transposed, bool bf16, uint8_t* c
 hipError_t launch_dequantize(const uint8_t* codes, const uint8_t* scales, void* X, bool bf16, int64_t rows, int k,
                              hipStream_t stream);
 
-// C[m][n] = sum_k A[i][k] W[j][k], fp32 accumulation, C bf16 or fp32.
-// `part` holds gemm_splits(...) fp32 copies of C when that is over 1.
-int gemm_splits(int64_t m, int n, int kp);
-hipError_t launch_gemm(const Matrix& A, const Matrix& W, void* C, bool bf16, int64_t m, int n, int kp, float* part,
+// C[i][j] = sum_k A[i][k] W[j][k], fp32 accumulation, C [m][n] bf16 or fp32.
+hipError_t launch_gemm(const Matrix& A, const Matrix& W, void* C, bool bf16, int64_t m, int n, int k,
                        hipStream_t stream);
 // H = quantised(silu(A Wg^T) * (A Wu^T)), n hidden units (a multiple of 128).
 hipError_t launch_gemm_swiglu(const Matrix& A, const Matrix& Wg, const Matrix& Wu, uint8_t* h_codes,
-                              uint8_t* h_scales, int64_t m, int n, int kp, hipStream_t stream);
+                              uint8_t* h_scales, int64_t m, int n, int k, hipStream_t stream);
+// The same for a few tokens A [m][k], quantised inside the product; only where
+// takes_tokens says so.
+bool takes_tokens(int64_t m, int k);
+hipError_t launch_gemm_tokens(const void* A, bool a_bf16, const Matrix& W, void* C, bool bf16, int64_t m, int n, int k,
+                              hipStream_t stream);
+hipError_t launch_gemm_swiglu_tokens(const void* A, const Matrix& Wg, const Matrix& Wu, uint8_t* h_codes,
+                                     uint8_t* h_scales, int64_t m, int n, int k, hipStream_t stream);
 
 }  // namespace mx4
 }  // namespace vggt3

@@ -39,13 +39,63 @@ __device__ __forceinline__ f32x4 mfma4(const i32x4& a, const i32x4& b, const f32
 
 struct Args {
   Matrix A, W, W2;  // token rows, weight rows (W2: the up matrix of the SwiGLU)
+  const void* tokens;  // A as tokens [m][k] (direct_kernel)
   int64_t m;
-  int n, nb, splits;  // nb = kp / 128
-  void* out;          // C, fp32 partials, or the codes of H
+  int n, k, nb;  // nb = kp / 128
+  void* out;     // C, or the codes of H
   uint8_t* h_scales;
 };
 
-enum Epi { EPI_BF16, EPI_F32, EPI_PART, EPI_SWIGLU };
+enum Epi { EPI_BF16, EPI_F32, EPI_SWIGLU };
+
+// Four neighbouring columns of one row of C.
+template <int EPI>
+__device__ __forceinline__ void store_tile(const Args& g, const f32x4& v, int64_t row, int64_t col) {
+  if (row >= g.m) return;
+  if constexpr (EPI == EPI_BF16) {
+    uint16_t* o = (uint16_t*)g.out + row * g.n + col;
+    if (g.n % 4 == 0 && col < g.n) {
+      st8(o, u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (col + r < g.n) o[r] = f32_to_bf16_bits(v[r]);
+    }
+  } else {
+    float* o = (float*)g.out + row * g.n + col;
+    if (g.n % 4 == 0 && col < g.n) {
+      *(f32x4*)o = v;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (col + r < g.n) o[r] = v[r];
+    }
+  }
+}
+
+// One block of H: a lane's 8 of 32 gate and up sums of one row (units 4 (l/16)
+// ..+3 and 16 more), the other 24 in the lanes 16, 32 and 48 further.
+// Quantised from fp32; the lane's codes are two 16-bit halves, 8 bytes apart.
+__device__ __forceinline__ uint32_t swiglu_codes(const f32x4 (&gate)[2], const f32x4 (&up)[2], uint32_t& s) {
+  float h[8];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float v = gate[i][r] * sigmoid_fast(gate[i][r]) * up[i][r];
+      h[4 * i + r] = v;
+      const uint32_t a = __float_as_uint(v) & 0x7fffffffu;
+      amax = a > amax ? a : amax;
+    }
+#pragma unroll
+  for (int off = 16; off <= 32; off <<= 1) {
+    const uint32_t o = __shfl_xor(amax, off, 64);
+    amax = o > amax ? o : amax;
+  }
+  s = scale_byte(amax);
+  return s == 255u ? 0u : encode8(h, scale_value(s));
+}
 
 // LDS tiles: [rows][128 bytes] (256 columns), 16-byte piece c of a row kept at
 // position c ^ ((row / 2) % 8): the 16 lanes of an operand read (16 rows, one
@@ -70,14 +120,10 @@ __global__ __launch_bounds__(64 * WN * WM) void gemm_kernel(Args g) {
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
   const int wn = wid % WN, wm = wid / WN;
   const int64_t tiles_n = (g.n + (EPI == EPI_SWIGLU ? BN / 2 : BN) - 1) / (EPI == EPI_SWIGLU ? BN / 2 : BN);
-  const int64_t tiles_m = (g.m + BM - 1) / BM;
   const int64_t b = xcd_remap(blockIdx.x, gridDim.x);
-  const int slice = (int)(b / (tiles_n * tiles_m));
-  const int64_t t = b % (tiles_n * tiles_m);
-  const int64_t n0 = (t % tiles_n) * (EPI == EPI_SWIGLU ? BN / 2 : BN), m0 = (t / tiles_n) * BM;
+  const int64_t n0 = (b % tiles_n) * (EPI == EPI_SWIGLU ? BN / 2 : BN), m0 = (b / tiles_n) * BM;
 
   const int nst = (g.nb + 1) / 2;
-  const int st0 = (int)((int64_t)nst * slice / g.splits), st1 = (int)((int64_t)nst * (slice + 1) / g.splits);
   const int64_t ld = (int64_t)g.nb * 64;
 
   // Rows past the end read the last one: they give values of C that are not stored.
@@ -174,22 +220,20 @@ __global__ __launch_bounds__(64 * WN * WM) void gemm_kernel(Args g) {
     }
   };
 
-  if (st0 < st1) {
-    issue(st0, 0);
-    load_scales(sn[0], sm[0], st0);
-  }
+  issue(0, 0);
+  load_scales(sn[0], sm[0], 0);
   wait_loads();
   __syncthreads();
-  for (int st = st0; st < st1; st += 2) {
-    if (st + 1 < st1) {
+  for (int st = 0; st < nst; st += 2) {
+    if (st + 1 < nst) {
       issue(st + 1, 1);
       load_scales(sn[1], sm[1], st + 1);
     }
     compute(st, 0, sn[0], sm[0]);
     wait_loads();
     __syncthreads();
-    if (st + 1 >= st1) break;
-    if (st + 2 < st1) {
+    if (st + 1 >= nst) break;
+    if (st + 2 < nst) {
       issue(st + 2, 0);
       load_scales(sn[0], sm[0], st + 2);
     }
@@ -207,26 +251,10 @@ __global__ __launch_bounds__(64 * WN * WM) void gemm_kernel(Args g) {
     static_assert(EPI != EPI_SWIGLU || (TN == 4 && WN == 4), "a tile is 128 units: one scale tile wide");
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      float h[8];
-      uint32_t amax = 0;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float gg = acc[i][j][r];
-          const float v = gg * sigmoid_fast(gg) * acc[i + 2][j][r];
-          h[4 * i + r] = v;
-          const uint32_t a = __float_as_uint(v) & 0x7fffffffu;
-          amax = a > amax ? a : amax;
-        }
-#pragma unroll
-      for (int off = 16; off <= 32; off <<= 1) {
-        const uint32_t o = __shfl_xor(amax, off, 64);
-        amax = o > amax ? o : amax;
-      }
       const int row = (wm * TM + j) * 16 + i16;
-      uint32_t s = scale_byte(amax);
-      const uint32_t q = s == 255u ? 0u : encode8(h, scale_value(s));
+      const f32x4 c0[2] = {acc[0][j], acc[1][j]}, c1[2] = {acc[2][j], acc[3][j]};
+      uint32_t s;
+      const uint32_t q = swiglu_codes(c0, c1, s);
       if (m0 + row >= g.m) s = 0;
       lu8* const d = hc + row * HB + wn * 16 + 2 * g4;
       *(__attribute__((address_space(3))) uint16_t*)d = (uint16_t)q;
@@ -250,90 +278,220 @@ __global__ __launch_bounds__(64 * WN * WM) void gemm_kernel(Args g) {
     return;
   }
 
-  const bool quad = g.n % 4 == 0;
 #pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int64_t row = m0 + (wm * TM + j) * 16 + i16;
-    if (row >= g.m) continue;
+  for (int j = 0; j < TM; ++j)
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const int64_t col = n0 + (wn * TN + i) * 16 + 4 * g4;
-      const f32x4 v = acc[i][j];
-      if (EPI == EPI_BF16) {
-        uint16_t* o = (uint16_t*)g.out + row * g.n + col;
-        if (quad && col < g.n) {
-          st8(o, u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (col + r < g.n) o[r] = f32_to_bf16_bits(v[r]);
-        }
-      } else {
-        float* o = (float*)g.out + (EPI == EPI_PART ? (int64_t)slice * g.m * g.n : 0) + row * g.n + col;
-        if (quad && col < g.n) {
-          *(f32x4*)o = v;
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (col + r < g.n) o[r] = v[r];
-        }
-      }
-    }
-  }
+    for (int i = 0; i < TN; ++i)
+      store_tile<EPI>(g, acc[i][j], m0 + (wm * TM + j) * 16 + i16, n0 + (wn * TN + i) * 16 + 4 * g4);
 }
 
-// C = the sum over the k slices, in slice order.
-template <bool BF16>
-__global__ __launch_bounds__(256) void sum_slices_kernel(const float* part, int splits, int64_t count, void* out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= count) return;
-  float v = part[i];
-  for (int s = 1; s < splits; ++s) v += part[s * count + i];
-  if (BF16)
-    ((uint16_t*)out)[i] = f32_to_bf16_bits(v);
-  else
-    ((float*)out)[i] = v;
+// Products with few tiles: a tile of 16 TN x 16 TM per workgroup, its KW waves
+// splitting k between them, operands straight from global memory to registers
+// (nothing is shared between the waves), the waves' sums joined in LDS in wave
+// order. TOK: A comes as tokens (at most 16 rows), which every workgroup
+// quantises for itself into LDS: one launch instead of two.
+enum Tok { TOK_NONE, TOK_BF16, TOK_F32 };
+
+template <int TN, int TM, int KW, int EPI, int TOK>
+__global__ __launch_bounds__(64 * KW) void direct_kernel(Args g) {
+  static_assert(4 % TN == 0 && 4 % TM == 0, "a tile's rows lie in one scale tile");
+  static_assert(EPI != EPI_SWIGLU || TN == 4, "two gate tiles, two up tiles");
+  static_assert(TOK == TOK_NONE || TM == 1, "tokens: one row tile");
+  constexpr int NT = TN * TM;
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  __shared__ __attribute__((aligned(16))) float red[KW > 1 ? KW * NT * 256 : 4];
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  const int i16 = lane & 15, g4 = lane >> 4;
+  constexpr int BN = EPI == EPI_SWIGLU ? 32 : 16 * TN;
+  const int tiles_n = (g.n + BN - 1) / BN;
+  const int64_t b = xcd_remap(blockIdx.x, gridDim.x);
+  const int64_t n0 = (b % tiles_n) * BN, m0 = b / tiles_n * (16 * TM);
+  const int64_t ld = (int64_t)g.nb * 64;
+
+  // Quantised tokens in LDS: rows of nb * 64 + 16 bytes (the 16 spread the rows
+  // over the banks), then the scale bytes, rows of nb * 4.
+  const int qld = g.nb * 64 + 16;  // (tokens only)
+  uint8_t* const qs = dyn + (TOK == TOK_NONE ? 0 : (int)g.m * qld);
+  if constexpr (TOK != TOK_NONE) {
+    const int kb = g.nb * 4;
+    for (int i = threadIdx.x; i < (int)g.m * kb; i += 64 * KW) {
+      const int row = i / kb, blk = i % kb;
+      float v[32];
+      if (g.k % (TOK == TOK_BF16 ? 8 : 4) == 0)
+        load_block<TOK == TOK_BF16, true>(g.tokens, row, blk * 32, g.k, v);
+      else
+        load_block<TOK == TOK_BF16, false>(g.tokens, row, blk * 32, g.k, v);
+      u32x4 o;
+      const uint32_t s = quantize_block(v, o);
+      st16(dyn + row * qld + blk * 16, o);
+      qs[row * kb + blk] = (uint8_t)s;
+    }
+    __syncthreads();
+  }
+
+  const uint8_t* wrow[TN];
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    if (EPI == EPI_SWIGLU) {
+      wrow[i] = (i < 2 ? g.W.codes : g.W2.codes) + (n0 + 16 * (i & 1) + i16) * ld + 16 * g4;
+    } else {
+      const int64_t row = n0 + 16 * i + i16;
+      wrow[i] = g.W.codes + (row < g.n ? row : g.n - 1) * ld + 16 * g4;
+    }
+  }
+  const uint8_t* arow[TM];
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int64_t row = m0 + 16 * j + i16;
+    arow[j] = TOK == TOK_NONE ? g.A.codes + (row < g.m ? row : g.m - 1) * ld + 16 * g4
+                              : dyn + (row < g.m ? row : g.m - 1) * qld + 16 * g4;
+  }
+  const uint32_t* const ws = (const uint32_t*)g.W.scales + (n0 >> 6) * g.nb * 64 + lane;
+  const uint32_t* const ws2 = (const uint32_t*)g.W2.scales + (n0 >> 6) * g.nb * 64 + lane;
+  const uint32_t* const as = (const uint32_t*)g.A.scales + (m0 >> 6) * g.nb * 64 + lane;
+  const int wsh = 8 * (int)((n0 >> 4) & 3), ash = 8 * (int)((m0 >> 4) & 3);
+
+  struct Frag {
+    i32x4 p[TN], q[TM];
+    uint32_t sp, sq;
+  };
+  auto load = [&](Frag& f, int blk) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i) f.p[i] = *(const i32x4*)(wrow[i] + blk * 64);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) f.q[j] = *(const i32x4*)(arow[j] + blk * 64);
+    f.sp = ws[blk * 64] >> wsh;
+    if constexpr (EPI == EPI_SWIGLU) f.sp = (f.sp & 0xffffu) | (ws2[blk * 64] >> wsh << 16);
+    if constexpr (TOK == TOK_NONE)
+      f.sq = as[blk * 64] >> ash;
+    else
+      f.sq = qs[(i16 < g.m ? i16 : g.m - 1) * (g.nb * 4) + blk * 4 + g4];
+  };
+  f32x4 acc[TN][TM];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto mma = [&](const Frag& f) {
+    unrolled(std::make_integer_sequence<int, TM>{}, [&](auto J) {
+      constexpr int j = decltype(J)::value;
+      unrolled(std::make_integer_sequence<int, TN>{}, [&](auto I) {
+        constexpr int i = decltype(I)::value;
+        acc[i][j] = mfma4<i, j>(f.p[i], f.q[j], acc[i][j], f.sp, f.sq);
+      });
+    });
+  };
+  const int b0 = g.nb * wid / KW, b1 = g.nb * (wid + 1) / KW;
+  if (b0 < b1) {
+    Frag f0, f1;
+    load(f0, b0);
+    for (int blk = b0; blk < b1; blk += 2) {
+      if (blk + 1 < b1) load(f1, blk + 1);
+      mma(f0);
+      if (blk + 1 >= b1) break;
+      if (blk + 2 < b1) load(f0, blk + 2);
+      mma(f1);
+    }
+  }
+  if constexpr (KW > 1) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) *(f32x4*)(red + ((wid * NT + j * TN + i) * 64 + lane) * 4) = acc[i][j];
+    __syncthreads();
+  }
+  auto joined = [&](int t) {  // tile t = j * TN + i, summed over the waves
+    f32x4 v = *(const f32x4*)(red + (t * 64 + lane) * 4);
+    for (int w = 1; w < KW; ++w) v += *(const f32x4*)(red + ((w * NT + t) * 64 + lane) * 4);
+    return v;
+  };
+
+  if constexpr (EPI == EPI_SWIGLU) {
+    const int hnb = g.n / 128;
+    for (int j = wid; j < TM; j += KW) {
+      f32x4 a[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = joined(j * 4 + i);
+      const f32x4 c0[2] = {a[0], a[1]}, c1[2] = {a[2], a[3]};
+      uint32_t s;
+      const uint32_t q = swiglu_codes(c0, c1, s);
+      const int64_t row = m0 + 16 * j + i16;
+      if (row < g.m) {
+        uint8_t* d = (uint8_t*)g.out + row * (int64_t)(hnb * 64) + n0 / 2 + 2 * g4;
+        *(uint16_t*)d = (uint16_t)q;
+        *(uint16_t*)(d + 8) = (uint16_t)(q >> 16);
+      }
+      if (g4 == 0) g.h_scales[scale_at(row, (int)(n0 >> 5), hnb)] = row < g.m ? (uint8_t)s : 0;
+    }
+  } else {
+    for (int t = wid; t < NT; t += KW)
+      store_tile<EPI>(g, joined(t), m0 + 16 * (t / TN) + i16, n0 + 16 * (t % TN) + 4 * g4);
+  }
 }
 
 template <int TN, int TM, int WN, int WM, int EPI>
 hipError_t go(const Args& g, hipStream_t stream) {
   constexpr int BN = 16 * TN * WN / (EPI == EPI_SWIGLU ? 2 : 1), BM = 16 * TM * WM;
   const int64_t tiles = ((g.n + BN - 1) / BN) * ((g.m + BM - 1) / BM);
-  gemm_kernel<TN, TM, WN, WM, EPI><<<dim3((unsigned)(tiles * g.splits)), dim3(64 * WN * WM), 0, stream>>>(g);
+  gemm_kernel<TN, TM, WN, WM, EPI><<<dim3((unsigned)tiles), dim3(64 * WN * WM), 0, stream>>>(g);
   return hipGetLastError();
+}
+
+template <int TN, int TM, int KW, int EPI, int TOK = TOK_NONE>
+hipError_t go_direct(const Args& g, hipStream_t stream) {
+  constexpr int BN = EPI == EPI_SWIGLU ? 32 : 16 * TN, BM = 16 * TM;
+  const int64_t tiles = ((g.n + BN - 1) / BN) * ((g.m + BM - 1) / BM);
+  const size_t lds = TOK == TOK_NONE ? 0 : (size_t)g.m * (g.nb * 68 + 16);  // at most 16384 values: 9 KB
+  direct_kernel<TN, TM, KW, EPI, TOK><<<dim3((unsigned)tiles), dim3(64 * KW), lds, stream>>>(g);
+  return hipGetLastError();
+}
+
+template <int EPI>
+hipError_t product(const Args& g, hipStream_t stream) {
+  const int64_t big = ((g.n + 127) / 128) * ((g.m + 127) / 128);
+  if (g.m <= 16) return go_direct<1, 1, 8, EPI>(g, stream);
+  if (g.m <= 64) return go_direct<1, 4, 4, EPI>(g, stream);
+  if (big < 256) return go_direct<4, 4, 4, EPI>(g, stream);
+  return go<4, 4, 2, 2, EPI>(g, stream);
 }
 
 }  // namespace
 
-int gemm_splits(int64_t m, int n, int kp) {
-  (void)m; (void)n; (void)kp;
-  return 1;
-}
+bool takes_tokens(int64_t m, int k) { return m >= 1 && m <= 16 && m * padded_k(k) <= 16384; }
 
-hipError_t launch_gemm(const Matrix& A, const Matrix& W, void* C, bool bf16, int64_t m, int n, int kp, float* part,
+hipError_t launch_gemm(const Matrix& A, const Matrix& W, void* C, bool bf16, int64_t m, int n, int k,
                        hipStream_t stream) {
   if (m == 0) return hipSuccess;
   Args g{};
-  g.A = A; g.W = W; g.m = m; g.n = n; g.nb = kp / kPad; g.out = C;
-  g.splits = gemm_splits(m, n, kp);
-  if (g.splits == 1) return bf16 ? go<4, 4, 2, 2, EPI_BF16>(g, stream) : go<4, 4, 2, 2, EPI_F32>(g, stream);
-  g.out = part;
-  const hipError_t e = go<4, 4, 2, 2, EPI_PART>(g, stream);
-  if (e != hipSuccess) return e;
-  const int64_t count = m * n;
-  const dim3 grid((unsigned)((count + 255) / 256));
-  if (bf16) sum_slices_kernel<true><<<grid, 256, 0, stream>>>(part, g.splits, count, C);
-  else sum_slices_kernel<false><<<grid, 256, 0, stream>>>(part, g.splits, count, C);
-  return hipGetLastError();
+  g.A = A; g.W = W; g.m = m; g.n = n; g.k = k; g.nb = (int)(padded_k(k) / kPad); g.out = C;
+  return bf16 ? product<EPI_BF16>(g, stream) : product<EPI_F32>(g, stream);
+}
+
+hipError_t launch_gemm_tokens(const void* A, bool a_bf16, const Matrix& W, void* C, bool bf16, int64_t m, int n, int k,
+                              hipStream_t stream) {
+  Args g{};
+  g.tokens = A; g.W = W; g.m = m; g.n = n; g.k = k; g.nb = (int)(padded_k(k) / kPad); g.out = C;
+  if (a_bf16) return bf16 ? go_direct<1, 1, 8, EPI_BF16, TOK_BF16>(g, stream) : go_direct<1, 1, 8, EPI_F32, TOK_BF16>(g, stream);
+  return bf16 ? go_direct<1, 1, 8, EPI_BF16, TOK_F32>(g, stream) : go_direct<1, 1, 8, EPI_F32, TOK_F32>(g, stream);
 }
 
 hipError_t launch_gemm_swiglu(const Matrix& A, const Matrix& Wg, const Matrix& Wu, uint8_t* h_codes,
-                              uint8_t* h_scales, int64_t m, int n, int kp, hipStream_t stream) {
+                              uint8_t* h_scales, int64_t m, int n, int k, hipStream_t stream) {
   if (m == 0) return hipSuccess;
   Args g{};
-  g.A = A; g.W = Wg; g.W2 = Wu; g.m = m; g.n = n; g.nb = kp / kPad; g.splits = 1;
+  g.A = A; g.W = Wg; g.W2 = Wu; g.m = m; g.n = n; g.k = k; g.nb = (int)(padded_k(k) / kPad);
   g.out = h_codes; g.h_scales = h_scales;
+  if (m <= 16) return go_direct<4, 1, 8, EPI_SWIGLU>(g, stream);
+  if (m <= 256) return go_direct<4, 4, 4, EPI_SWIGLU>(g, stream);
   return go<4, 4, 4, 2, EPI_SWIGLU>(g, stream);
+}
+
+hipError_t launch_gemm_swiglu_tokens(const void* A, const Matrix& Wg, const Matrix& Wu, uint8_t* h_codes,
+                                     uint8_t* h_scales, int64_t m, int n, int k, hipStream_t stream) {
+  Args g{};
+  g.tokens = A; g.W = Wg; g.W2 = Wu; g.m = m; g.n = n; g.k = k; g.nb = (int)(padded_k(k) / kPad);
+  g.out = h_codes; g.h_scales = h_scales;
+  return go_direct<4, 1, 8, EPI_SWIGLU, TOK_BF16>(g, stream);
 }
 
 }  // namespace mx4

@@ -37,49 +37,15 @@ __global__ __launch_bounds__(NTHR) void quantize_kernel(const void* X, uint8_t* 
   const int k0 = B * 128 + g * 32;
   const bool live = row < rows;
   float v[32];
+  if constexpr (TRANS) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-  if (live) {
-    if (VEC && !TRANS) {
-      constexpr int E = BF16 ? 8 : 4;  // values per 16-byte load
-      const char* p = (const char*)X + (row * (int64_t)k + k0) * (BF16 ? 2 : 4);
-#pragma unroll
-      for (int c = 0; c < 32 / E; ++c) {
-        if (k0 + c * E < k) {
-          const u32x4 q = ld16(p + 16 * c);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (BF16) {
-              v[c * E + 2 * j] = bf16_lo(q[j]);
-              v[c * E + 2 * j + 1] = bf16_hi(q[j]);
-            } else {
-              v[c * E + j] = __uint_as_float(q[j]);
-            }
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (k0 + j < k) v[j] = load1<BF16>(X, TRANS ? (int64_t)(k0 + j) * rows + row : row * (int64_t)k + k0 + j);
-    }
+    for (int j = 0; j < 32; ++j) v[j] = live && k0 + j < k ? load1<BF16>(X, (int64_t)(k0 + j) * rows + row) : 0.0f;
+  } else {
+    load_block<BF16, VEC>(X, live ? row : 0, k0, live ? k : 0, v);
   }
-  uint32_t amax = 0;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const uint32_t a = __float_as_uint(v[j]) & 0x7fffffffu;
-    amax = a > amax ? a : amax;
-  }
-  const uint32_t s = scale_byte(amax);
-  if (live) {
-    u32x4 o = {0u, 0u, 0u, 0u};
-    if (s != 255u) {
-      const float f = scale_value(s);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) o[c] = encode8(v + 8 * c, f);
-    }
-    st16(codes + row * (int64_t)(nb * 64) + B * 64 + g * 16, o);
-  }
+  u32x4 o;
+  const uint32_t s = quantize_block(v, o);
+  if (live) st16(codes + row * (int64_t)(nb * 64) + B * 64 + g * 16, o);
   ((uint8_t*)sc)[(g * 16 + (rr & 15)) * 4 + (rr >> 4)] = (uint8_t)s;
   __syncthreads();
   if (t < 64) ((uint32_t*)scales)[(R * nb + B) * 64 + t] = sc[t];

@@ -51,6 +51,9 @@ def test_matmul_refusals(lib):
     assert ws > 0
     assert lib.vggt3_mx4_matmul_workspace_bytes(100, 64, 256, 5) == 0
     assert lib.vggt3_mx4_matmul_workspace_bytes(0, 64, 256, tla.BF16) == 0
+    # 4-bit operands and a few tokens need none
+    assert lib.vggt3_mx4_matmul_workspace_bytes(100, 64, 256, tla.MX4) == 0
+    assert lib.vggt3_mx4_matmul_workspace_bytes(1, 64, 256, tla.BF16) == 0
 
     def call(A=P[0], As=None, at=tla.BF16, W=P[1], Ws=P[2], C=P[3], m=100, n=64, k=256, dt=tla.BF16, w=P[4], nb=1 << 20):
         return lib.vggt3_mx4_matmul(A, As, at, W, Ws, C, m, n, k, dt, w, nb, None)
@@ -75,11 +78,11 @@ def test_freeze_and_read_refusals(lib):
     assert freeze(d=64, m=128) == tla.EUNSUPPORTED and freeze(H=2) == tla.EUNSUPPORTED and freeze(d=0) == tla.EINVAL
     assert freeze(theta=None) == tla.EINVAL and freeze(parts=[P[1], P[2], P[1], P[4], P[5], P[6]]) == tla.EINVAL
 
-    need = lib.vggt3_ttt_read_mx4_workspace_bytes(10, 1, 1024, 4096, tla.BF16)
-    assert need > lib.vggt3_ttt_read_mx4_workspace_bytes(10, 1, 1024, 4096, tla.MX4) > 0
+    need = lib.vggt3_ttt_read_mx4_workspace_bytes(100, 1, 1024, 4096, tla.BF16)
+    assert need > lib.vggt3_ttt_read_mx4_workspace_bytes(100, 1, 1024, 4096, tla.MX4) > 0
     assert lib.vggt3_ttt_read_mx4_workspace_bytes(10, 1, 1024, 4096, tla.F32) == 0
 
-    def read(Q=P[0], Qs=None, qt=tla.BF16, parts=P[1:7], O=P[7], n=10, H=1, d=1024, m=4096, w=P[8], nb=1 << 28):
+    def read(Q=P[0], Qs=None, qt=tla.BF16, parts=P[1:7], O=P[7], n=100, H=1, d=1024, m=4096, w=P[8], nb=1 << 28):
         return lib.vggt3_ttt_read_mx4(Q, Qs, qt, *parts, O, n, H, d, m, w, nb, None)
 
     assert read(n=0) == tla.OK
