@@ -141,7 +141,7 @@ int vggt3_block_join_grad(const void* r, const void* f, const void* gate, int64_
   if (post == VGGT3_NORM_NONE && (dpost_w || dpost_b)) return fail(VGGT3_EINVAL, "dpost_w / dpost_b without a norm");
   if (pre == VGGT3_NORM_NONE && (dpre_w || dpre_b || dy)) return fail(VGGT3_EINVAL, "dy / dpre_w / dpre_b without a norm");
   hipStream_t s = static_cast<hipStream_t>(stream);
-  float* outs[join::kVecs];
+  float* outs[join::kOuts];
   outs[join::kDScale] = dscale;
   outs[join::kDPostW] = dpost_w;
   outs[join::kDPostB] = dpost_b;

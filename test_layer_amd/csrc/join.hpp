@@ -38,8 +38,10 @@ struct Args {
   float eps;
 };
 
-// Vectors of the per-workgroup sums, in this order.
-enum Vec { kDScale, kDPostW, kDPostB, kDPreW, kDPreB, kVecs };
+// The per-workgroup sums (see block_join.hip), and the channel gradients made of
+// them.
+enum Sum { kA, kB, kSumPreW, kSumPreB, kVecs };
+enum Out { kDScale, kDPostW, kDPostB, kDPreW, kDPreB, kOuts };
 
 hipError_t launch_forward(const Args& a, bool bf16, hipStream_t stream);
 
