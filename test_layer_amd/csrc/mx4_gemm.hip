@@ -20,6 +20,8 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t lu8;
 typedef __attribute__((address_space(3))) i32x4 li32x4;
+typedef __attribute__((address_space(3))) uint32_t lu32;
+typedef __attribute__((address_space(3))) uint16_t lu16;
 typedef __attribute__((address_space(3))) void lvoid;
 
 template <int... I, class F>
@@ -77,212 +79,368 @@ __device__ __forceinline__ void store_tile(const Args& g, const f32x4& v, int64_
 // ..+3 and 16 more), the other 24 in the lanes 16, 32 and 48 further.
 // Quantised from fp32; the lane's codes are two 16-bit halves, 8 bytes apart.
 __device__ __forceinline__ uint32_t swiglu_codes(const f32x4 (&gate)[2], const f32x4 (&up)[2], uint32_t& s) {
-  float h[8];
-  uint32_t amax = 0;
+  float h[8], top = 0.0f;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float v = gate[i][r] * sigmoid_fast(gate[i][r]) * up[i][r];
-      h[4 * i + r] = v;
-      const uint32_t a = __float_as_uint(v) & 0x7fffffffu;
-      amax = a > amax ? a : amax;
+      h[4 * i + r] = gate[i][r] * up[i][r] * sigmoid_fast(gate[i][r]);
+      top = __builtin_elementwise_maximum(top, __builtin_fabsf(h[4 * i + r]));  // a NaN stays
     }
 #pragma unroll
-  for (int off = 16; off <= 32; off <<= 1) {
-    const uint32_t o = __shfl_xor(amax, off, 64);
-    amax = o > amax ? o : amax;
-  }
+  for (int off = 16; off <= 32; off <<= 1) top = __builtin_elementwise_maximum(top, __shfl_xor(top, off, 64));
+  const uint32_t amax = __float_as_uint(top);
   s = scale_byte(amax);
   return s == 255u ? 0u : encode8(h, scale_value(s));
 }
 
-// LDS tiles: [rows][128 bytes] (256 columns), 16-byte piece c of a row kept at
-// position c ^ ((row / 2) % 8): the 16 lanes of an operand read (16 rows, one
-// piece) then touch every bank equally often.
-constexpr int BKB = 128;
-__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
+// ------------------------------------------------------------ tiled products
+// A workgroup of WN x WM waves works through BN x BM tiles of C^T, TN x TM tiles of
+// 16x16 a wave, in steps of 128 columns (one MFMA deep). LDS holds a ring of RING
+// steps, each [BN + BM rows][64 bytes] of codes and the scale tiles of those rows,
+// filled by direct global-to-LDS loads RING - 1 steps ahead. The steps of all the
+// workgroup's tiles are one stream: while a tile's last steps are worked on and its
+// results stored, the next tile's first steps are under way. (At k = 1024 a tile
+// has 8 steps, 3.6 us of MFMAs; as a workgroup of its own it would spend more than
+// that on its first loads and its stores.)
+//
+// A 16-byte piece c of row r is kept at position c ^ ((r / 4) % 4): the 16 lanes
+// of an operand read (16 rows, one piece) then touch every bank once.
+constexpr int STEP = 64;  // bytes of a row and step
+__device__ __forceinline__ int swz(int row) { return (row >> 2) & 3; }
 
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Wait until at most N of this wave's global loads, or none of its LDS reads, are
+// under way. (Builtins: the compiler then knows, and adds no waits of its own.)
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | 0x0f70);
+}
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }
 
-// BN x BM tile of C^T per workgroup of WN x WM waves, each TN x TM tiles of
-// 16x16; k stages of 256 columns (two MFMA steps) in a double-buffered LDS,
-// filled by direct global-to-LDS loads. The scales go straight to registers.
-template <int TN, int TM, int WN, int WM, int EPI>
-__global__ __launch_bounds__(64 * WN * WM) void gemm_kernel(Args g) {
-  constexpr int NW = WN * WM, NTHR = 64 * NW;
+// A choice between values (of variables, ?: would choose between their places, and
+// so keep them in memory).
+template <class T>
+__device__ __forceinline__ T pick(bool c, T a, T b) {
+  return c ? a : b;
+}
+// Lambdas that stay calls would keep what they refer to in memory.
+#define INLINE __attribute__((always_inline))
+
+// 16 or 4 bytes a lane from memory to LDS, the lanes of a wave side by side from dst
+// on. (As buffer loads: a scalar base and offset, a 32-bit lane offset. Their
+// global_load form also counts as a possible LDS access of the wave's own, which
+// makes the compiler wait for every LDS read in front of each use of one.)
+__device__ __forceinline__ void to_lds16(const uint8_t* p, uint32_t lane_off, uint32_t off, lu8* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7fffffff, 0x00027000),
+                                           (lvoid*)dst, 16, lane_off, off, 0, 0);
+}
+__device__ __forceinline__ void to_lds4(const uint8_t* p, uint32_t lane_off, uint32_t off, lu8* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7fffffff, 0x00027000),
+                                           (lvoid*)dst, 4, lane_off, off, 0, 0);
+}
+// Barrier for LDS alone: loads and stores under way stay so.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+__device__ __forceinline__ void swap_rows(uint32_t& a, uint32_t& b) {
+  // odd 16-lane rows of a <-> even rows of b
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
+template <int TN, int TM, int WN, int WM, int RING, int EPI>
+__global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2))) void gemm_kernel(Args g) {
+  constexpr int NW = WN * WM;
   constexpr int BN = 16 * TN * WN, BM = 16 * TM * WM;
   static_assert(TN % 4 == 0 && TM % 4 == 0, "a wave's rows are whole scale tiles");
   constexpr int SN = TN / 4, SM = TM / 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (BN + BM) * BKB];
+  constexpr int CODES = (BN + BM) * STEP, STAGE = CODES + (BN + BM) * 4;
+  constexpr int DN = BN / 16 / NW, DM = BM / 16 / NW, DS = ((BN + BM) / 64 + NW - 1) / NW;  // loads a wave and step
+  static_assert(DN * NW * 16 == BN && DM * NW * 16 == BM, "whole loads");
+  constexpr int LOADS = DN + DM + DS;
+  // Stores (at least) a wave makes of a tile that lies inside C.
+  constexpr int STORES = EPI == EPI_SWIGLU ? BM * (BN / 4) / 16 / (64 * NW) : EPI == EPI_BF16 ? TN * TM / 2 : TN * TM;
+  static_assert(RING >= 3 && (RING - 3) * LOADS + STORES < 64, "vmcnt");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   lu8* const lds = (lu8*)smem;
 
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wid % WN, wm = wid / WN;
-  const int64_t tiles_n = (g.n + (EPI == EPI_SWIGLU ? BN / 2 : BN) - 1) / (EPI == EPI_SWIGLU ? BN / 2 : BN);
-  const int64_t b = xcd_remap(blockIdx.x, gridDim.x);
-  const int64_t n0 = (b % tiles_n) * (EPI == EPI_SWIGLU ? BN / 2 : BN), m0 = (b / tiles_n) * BM;
-
-  const int nst = (g.nb + 1) / 2;
+  constexpr int CN = EPI == EPI_SWIGLU ? BN / 2 : BN;  // columns (hidden units) a tile
+  const uint32_t tiles_n = (g.n + CN - 1) / CN, tiles_m = (uint32_t)((g.m + BM - 1) / BM);
+  const int steps = g.nb;
   const int64_t ld = (int64_t)g.nb * 64;
 
-  // Rows past the end read the last one: they give values of C that are not stored.
-  auto dma = [&](lu8* tile, const uint8_t* src, int64_t r0, int64_t rows, int R, int st) {
-    const uint8_t* base = src + r0 * ld + (int64_t)st * BKB;
-    const int rmax = (int)(rows - r0 - 1);
-    const bool half = 2 * st + 1 >= g.nb;  // the last stage of an odd nb: 64 bytes a row
-    for (int i = 0; i < R * 8 / NTHR; ++i) {
-      const int p = (NW * i + wid) * 64 + lane;
-      const int row = p >> 3;
-      int c = (p & 7) ^ swz(row);
-      if (half) c &= 3;
-      __builtin_amdgcn_global_load_lds(base + (int64_t)(row < rmax ? row : rmax) * ld + 16 * c,
-                                       (lvoid*)(tile + (NW * i + wid) * 1024), 16, 0, 0);
+  // This workgroup's tiles: the XCD it runs on (number % 8) has a contiguous range,
+  // which its workgroups go through side by side.
+  uint32_t tile, tile_end, stride;
+  {
+    const uint32_t x = blockIdx.x % kNumXcd, q = gridDim.x / kNumXcd, r = gridDim.x % kNumXcd;
+    const uint32_t before = x * q + (x < r ? x : r);
+    const uint64_t tiles = (uint64_t)tiles_n * tiles_m;
+    stride = q + (x < r ? 1 : 0);
+    tile = __builtin_amdgcn_readfirstlane((uint32_t)(tiles * before / gridDim.x) + blockIdx.x / kNumXcd);
+    tile_end = __builtin_amdgcn_readfirstlane((uint32_t)(tiles * (before + stride) / gridDim.x));
+  }
+  if (tile >= tile_end) return;
+  // Tiles in groups of GM row tiles x all column tiles, row-fastest, so that those
+  // side by side share rows of both operands.
+  auto place = [&](uint32_t t, int64_t& n0, int64_t& m0) INLINE {
+    constexpr uint32_t GM = 4;
+    const uint32_t first = t / (GM * tiles_n) * GM, in = t % (GM * tiles_n);
+    const uint32_t rows = tiles_m - first < GM ? tiles_m - first : GM;
+    // (the divisions go through vector registers)
+    m0 = (int64_t)__builtin_amdgcn_readfirstlane(first + in % rows) * BM;
+    n0 = (int64_t)__builtin_amdgcn_readfirstlane(in / rows) * CN;
+  };
+
+  // The stream of loads: the tile and step it has come to, where that tile's rows
+  // are, and this lane's places in them. Rows and scale tiles past the end read the
+  // last ones: they give values of C that are not stored.
+  const uint8_t *wp, *up, *ap, *wsp, *usp, *asp;
+  int wtiles, atiles;
+  uint32_t off_n[DN], off_m[DM];
+  const uint32_t tile_bytes = (uint32_t)g.nb * 256;
+  auto aim = [&](uint32_t t) INLINE {
+    int64_t n0, m0;
+    place(t, n0, m0);
+    wp = g.W.codes + n0 * ld;
+    up = EPI == EPI_SWIGLU ? g.W2.codes + n0 * ld : wp;
+    ap = g.A.codes + m0 * ld;
+    wsp = g.W.scales + (n0 >> 6) * tile_bytes;
+    usp = EPI == EPI_SWIGLU ? g.W2.scales + (n0 >> 6) * tile_bytes : wsp;
+    asp = g.A.scales + (m0 >> 6) * tile_bytes;
+    const int64_t wt = row_tiles(g.n) - (n0 >> 6), at = row_tiles(g.m) - (m0 >> 6);
+    wtiles = wt < 64 ? (int)wt : 64;
+    atiles = at < 64 ? (int)at : 64;
+    const int nmost = (int)(g.n - n0 < BN ? g.n - n0 : BN) - 1, mmost = (int)(g.m - m0 < BM ? g.m - m0 : BM) - 1;
+    const int row = lane >> 2;
+    const uint32_t piece = 16 * ((lane & 3) ^ swz(row));
+#pragma unroll
+    for (int i = 0; i < DN; ++i) {
+      const int r = (NW * i + wid) * 16 + row;
+      // SwiGLU: rows are [32 gate units | the same 32 up units] in turn
+      const int from = EPI == EPI_SWIGLU ? (r >> 6) * 32 + (r & 31) : r < nmost ? r : nmost;
+      off_n[i] = (uint32_t)from * (uint32_t)ld + piece;
+    }
+#pragma unroll
+    for (int i = 0; i < DM; ++i) {
+      const int r = (NW * i + wid) * 16 + row;
+      off_m[i] = (uint32_t)(r < mmost ? r : mmost) * (uint32_t)ld + piece;
     }
   };
-  // SwiGLU: tile rows are [32 gate units | the same 32 up units] in turn.
-  auto dma_gu = [&](lu8* tile, int st) {
-    const bool half = 2 * st + 1 >= g.nb;
-    for (int i = 0; i < BN * 8 / NTHR; ++i) {
-      const int p = (NW * i + wid) * 64 + lane;
-      const int row = p >> 3;
-      int c = (p & 7) ^ swz(row);
-      if (half) c &= 3;
-      const uint8_t* src = (row & 32) ? g.W2.codes : g.W.codes;
-      const int64_t unit = n0 + (row >> 6) * 32 + (row & 31);
-      __builtin_amdgcn_global_load_lds(src + unit * ld + (int64_t)st * BKB + 16 * c,
-                                       (lvoid*)(tile + (NW * i + wid) * 1024), 16, 0, 0);
+  auto issue = [&](int step, lu8* stage) INLINE {
+#pragma unroll
+    for (int i = 0; i < DN; ++i) {
+      // a load covers 16 rows, so it lies in one of gate and up
+      to_lds16(EPI == EPI_SWIGLU ? pick((NW * i + wid) & 2, up, wp) : +wp, off_n[i], step * STEP, stage + (NW * i + wid) * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < DM; ++i) to_lds16(ap, off_m[i], step * STEP, stage + BN * STEP + (NW * i + wid) * 1024);
+#pragma unroll
+    for (int i = 0; i < DS; ++i) {
+      // the scale tiles of W (of gate, then of up), then of A; where there are fewer
+      // than loads, several waves load the last one
+      const int want = NW * i + wid, slot = want < (BN + BM) / 64 ? want : (BN + BM) / 64 - 1;
+      const bool of_a = slot >= BN / 64, of_up = EPI == EPI_SWIGLU && slot >= BN / 128;
+      const int t = of_a ? slot - BN / 64 : of_up ? slot - BN / 128 : slot;
+      const int most = pick(of_a, atiles, wtiles) - 1;
+      const uint8_t* p = pick(of_a, asp, pick(of_up, usp, wsp));
+      to_lds4(p, lane * 4, (uint32_t)(t < most ? t : most) * tile_bytes + step * 256, stage + CODES + slot * 256);
     }
   };
-  const int64_t nrt = row_tiles(g.n), mrt = row_tiles(g.m);
-  auto scale_word = [&](const uint8_t* s, int64_t rt, int blk) {
-    return ((const uint32_t*)s)[(rt * g.nb + (blk < g.nb ? blk : g.nb - 1)) * 64 + lane];
-  };
-  auto load_scales = [&](uint32_t (&sn)[2][SN], uint32_t (&sm)[2][SM], int st) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (EPI == EPI_SWIGLU) {
-        const int64_t unit = n0 + 32 * wn;
-        const int sh = (unit & 32) ? 16 : 0;  // the lower or upper 32 rows of a scale tile
-        const uint32_t a = scale_word(g.W.scales, unit >> 6, 2 * st + u) >> sh;
-        const uint32_t c = scale_word(g.W2.scales, unit >> 6, 2 * st + u) >> sh;
-        sn[u][0] = (a & 0xffffu) | (c << 16);
-      } else {
-#pragma unroll
-        for (int i = 0; i < SN; ++i) {
-          const int64_t rt = (n0 >> 6) + wn * SN + i;
-          sn[u][i] = scale_word(g.W.scales, rt < nrt ? rt : nrt - 1, 2 * st + u);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < SM; ++i) {
-        const int64_t rt = (m0 >> 6) + wm * SM + i;
-        sm[u][i] = scale_word(g.A.scales, rt < mrt ? rt : mrt - 1, 2 * st + u);
-      }
+  // The step after the one just issued. Behind the last one it stays where it is:
+  // the loads beyond the end are copies that nothing uses, so that every round is
+  // the same.
+  uint32_t at = tile;
+  int at_step = 0;
+  auto load_on = [&]() INLINE {
+    if (at_step + 1 < steps) {
+      ++at_step;
+    } else if (stride < tile_end - at) {
+      at_step = 0;
+      at += stride;
+      aim(at);
     }
   };
 
-  f32x4 acc[TN][TM];
-#pragma unroll
-  for (int i = 0; i < TN; ++i)
-#pragma unroll
-    for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  uint32_t sn[2][2][SN], sm[2][2][SM];
-  auto issue = [&](int st, int s) {
-    lu8* const P = lds + s * (BN + BM) * BKB;
-    if (EPI == EPI_SWIGLU)
-      dma_gu(P, st);
-    else
-      dma(P, g.W.codes, n0, g.n, BN, st);
-    dma(P + BN * BKB, g.A.codes, m0, g.m, BM, st);
-  };
   const int i16 = lane & 15, g4 = lane >> 4;
-  auto compute = [&](int st, int s, const uint32_t (&ssn)[2][SN], const uint32_t (&ssm)[2][SM]) {
-    const lu8* const P = lds + s * (BN + BM) * BKB;
-    const lu8* const Q = P + BN * BKB;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (u == 1 && 2 * st + 1 >= g.nb) break;
-      const int off = i16 * BKB + 16 * ((4 * u + g4) ^ swz(i16));
-      i32x4 p[TN], q[TM];
-#pragma unroll
-      for (int i = 0; i < TN; ++i) p[i] = *(const li32x4*)(P + (wn * TN + i) * 16 * BKB + off);
-#pragma unroll
-      for (int j = 0; j < TM; ++j) q[j] = *(const li32x4*)(Q + (wm * TM + j) * 16 * BKB + off);
-      unrolled(std::make_integer_sequence<int, TM>{}, [&](auto J) {
-        constexpr int j = decltype(J)::value;
-        unrolled(std::make_integer_sequence<int, TN>{}, [&](auto I) {
-          constexpr int i = decltype(I)::value;
-          acc[i][j] = mfma4<i & 3, j & 3>(p[i], q[j], acc[i][j], ssn[u][i >> 2], ssm[u][j >> 2]);
-        });
-      });
-    }
+  const int foff = i16 * STEP + 16 * (g4 ^ swz(i16));
+  struct Cols {               // one step's token rows, and all scales
+    i32x4 q[TM];
+    uint32_t sp[SN], sq[SM];
+    uint32_t su[EPI == EPI_SWIGLU ? SN : 1];  // (sp: gate's scales, su: up's)
   };
-
-  issue(0, 0);
-  load_scales(sn[0], sm[0], 0);
-  wait_loads();
-  __syncthreads();
-  for (int st = 0; st < nst; st += 2) {
-    if (st + 1 < nst) {
-      issue(st + 1, 1);
-      load_scales(sn[1], sm[1], st + 1);
-    }
-    compute(st, 0, sn[0], sm[0]);
-    wait_loads();
-    __syncthreads();
-    if (st + 1 >= nst) break;
-    if (st + 2 < nst) {
-      issue(st + 2, 0);
-      load_scales(sn[0], sm[0], st + 2);
-    }
-    compute(st + 1, 1, sn[1], sm[1]);
-    wait_loads();
-    __syncthreads();
-  }
-
-  if constexpr (EPI == EPI_SWIGLU) {
-    // Each wave holds gate (tiles 0, 1) and up (tiles 2, 3) of the same 32
-    // units: one block of H per row. Codes and scales are gathered in LDS.
-    constexpr int HB = BN / 4;  // bytes of codes per row of this tile
-    lu8* const hc = lds;                 // [BM][HB]
-    lu8* const hs = lds + BM * HB;       // [BM / 64][64][4], the scale tiles
-    static_assert(EPI != EPI_SWIGLU || (TN == 4 && WN == 4), "a tile is 128 units: one scale tile wide");
+  auto fetch_row = [&](int i, const lu8* stage) INLINE {
+    return *(const li32x4*)(stage + (wn * TN + i) * 16 * STEP + foff);
+  };
+  auto fetch_cols = [&](Cols& f, const lu8* stage) INLINE {
+    const lu8* const Q = stage + BN * STEP + wm * TM * 16 * STEP + foff;
+    const lu8* const S = stage + CODES + lane * 4;
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const int row = (wm * TM + j) * 16 + i16;
-      const f32x4 c0[2] = {acc[0][j], acc[1][j]}, c1[2] = {acc[2][j], acc[3][j]};
-      uint32_t s;
-      const uint32_t q = swiglu_codes(c0, c1, s);
-      if (m0 + row >= g.m) s = 0;
-      lu8* const d = hc + row * HB + wn * 16 + 2 * g4;
-      *(__attribute__((address_space(3))) uint16_t*)d = (uint16_t)q;
-      *(__attribute__((address_space(3))) uint16_t*)(d + 8) = (uint16_t)(q >> 16);
-      if (g4 == 0) hs[(row >> 6) * 256 + (wn * 16 + i16) * 4 + ((row >> 4) & 3)] = (uint8_t)s;
+    for (int i = 0; i < SN; ++i) {
+      if (EPI == EPI_SWIGLU) {
+        const int t = (wn * SN + i) >> 1;
+        f.sp[i] = *(const lu32*)(S + t * 256);
+        f.su[i] = *(const lu32*)(S + (BN / 128 + t) * 256);
+      } else {
+        f.sp[i] = *(const lu32*)(S + (wn * SN + i) * 256);
+      }
     }
-    __syncthreads();
-    const int hnb = g.n / 128;  // scale tiles across H
-    for (int p = threadIdx.x; p < BM * HB / 16; p += NTHR) {
-      const int row = p / (HB / 16), c = p % (HB / 16);
-      if (m0 + row < g.m)
-        *(i32x4*)((uint8_t*)g.out + (m0 + row) * (int64_t)(hnb * 64) + n0 / 2 + 16 * c) =
-            *(const li32x4*)(hc + row * HB + 16 * c);
-    }
-    for (int p = threadIdx.x; p < BM; p += NTHR) {
-      const int64_t rt = (m0 >> 6) + (p >> 6);
-      if (rt < mrt)
-        ((uint32_t*)g.h_scales)[(rt * hnb + n0 / 128) * 64 + (p & 63)] =
-            *(__attribute__((address_space(3))) uint32_t*)(hs + p * 4);
-    }
-    return;
-  }
-
 #pragma unroll
-  for (int j = 0; j < TM; ++j)
+    for (int j = 0; j < SM; ++j) f.sq[j] = *(const lu32*)(S + (BN / 64 + wm * SM + j) * 256);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) f.q[j] = *(const li32x4*)(Q + j * 16 * STEP);
+  };
+  f32x4 acc[TN][TM];
+  auto clear = [&]() INLINE {
 #pragma unroll
     for (int i = 0; i < TN; ++i)
-      store_tile<EPI>(g, acc[i][j], m0 + (wm * TM + j) * 16 + i16, n0 + (wn * TN + i) * 16 + 4 * g4);
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  // The MFMAs of weight row tile i (p) with all token rows.
+  auto mma = [&](auto I, const i32x4& p, const Cols& c) INLINE {
+    constexpr int i = decltype(I)::value;
+    // SwiGLU: the wave's 32 of a tile's 64 gate units, and the same up units
+    const int sh = 16 * ((wn * SN + i / 4) & 1);
+    const uint32_t sp =
+        EPI == EPI_SWIGLU ? (c.sp[i / 4] >> sh & 0xffffu) | (c.su[EPI == EPI_SWIGLU ? i / 4 : 0] >> sh << 16) : c.sp[i / 4];
+    unrolled(std::make_integer_sequence<int, TM>{}, [&](auto J) INLINE {
+      constexpr int j = decltype(J)::value;
+      acc[i][j] = mfma4<i & 3, j & 3>(p, c.q[j], acc[i][j], sp, c.sq[j >> 2]);
+    });
+  };
+
+  aim(tile);
+  issue(0, lds);
+  for (int i = 1; i < RING - 1; ++i) {
+    load_on();
+    issue(at_step, lds + i * STAGE);
+  }
+  wait_loads<0>();
+  __builtin_amdgcn_s_barrier();
+  i32x4 rows[TN];
+  Cols cols, next;
+  fetch_cols(cols, lds);
+#pragma unroll
+  for (int i = 0; i < TN; ++i) rows[i] = fetch_row(i, lds);
+  clear();
+  int ring = 0;  // place of the present step
+  for (;; tile += stride) {
+    // Work on the present step, in registers, and read the next one, each part as
+    // the registers of its predecessor fall free. The next step's loads are waited
+    // for; those of RING - 3 later steps may be under way and, in the first RING - 2
+    // rounds, whose loads were issued ahead of them (or are done), the stores of the
+    // tile before. The reads of the step before this one have been used, so behind
+    // the barrier its place takes the step RING - 1 ahead. The scheduling fences keep
+    // the reads ahead of the MFMAs that hide them.
+    // The questions come first: between the reads and the MFMAs on one side and
+    // the end of the round on the other there is no branch for them to cross.
+    for (int s = 0; s < steps; ++s) {
+      load_on();
+      if (s < RING - 2)
+        wait_loads<(RING - 3) * LOADS + STORES>();
+      else
+        wait_loads<(RING - 3) * LOADS>();
+      __builtin_amdgcn_s_barrier();
+      issue(at_step, lds + (ring == 0 ? RING - 1 : ring - 1) * STAGE);
+      ring = ring + 1 == RING ? 0 : ring + 1;
+      const lu8* const stage = lds + ring * STAGE;
+      // (The compiler takes the loads to LDS for LDS accesses of this wave's and would
+      // wait for all reads at the first use of one; so the wait is here, where the
+      // last reads were asked for a barrier ago, and none follows.)
+      wait_lds();
+      fetch_cols(next, stage);
+      __builtin_amdgcn_sched_barrier(0);
+      unrolled(std::make_integer_sequence<int, TN>{}, [&](auto I) INLINE {
+        constexpr int i = decltype(I)::value;
+        mma(I, rows[i], cols);
+        __builtin_amdgcn_sched_barrier(0);
+        rows[i] = fetch_row(i, stage);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      cols = next;
+    }
+
+    int64_t n0, m0;
+    place(tile, n0, m0);
+    const bool inside = m0 + BM <= g.m && n0 + CN <= g.n && (EPI == EPI_SWIGLU || g.n % 8 == 0);
+    if constexpr (EPI == EPI_SWIGLU) {
+      // Each wave holds gate (tiles 0, 1 of four) and up (tiles 2, 3) of the same
+      // 32 units: one block of H per row. Codes and scales are gathered in LDS.
+      constexpr int HB = BN / 4;  // bytes of codes per row of this tile
+      static_assert(EPI != EPI_SWIGLU || BN == 256, "a tile is 128 units: one scale tile wide");
+      lu8* const hc = lds + RING * STAGE;  // [BM][HB]
+      lu8* const hs = hc + BM * HB;        // [BM / 64][64][4], the scale tiles
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+#pragma unroll
+        for (int q = 0; q < SN; ++q) {
+          const int row = (wm * TM + j) * 16 + i16, blk = wn * SN + q;
+          const f32x4 gate[2] = {acc[4 * q][j], acc[4 * q + 1][j]}, upv[2] = {acc[4 * q + 2][j], acc[4 * q + 3][j]};
+          uint32_t sc;
+          const uint32_t code = swiglu_codes(gate, upv, sc);
+          if (m0 + row >= g.m) sc = 0;
+          lu8* const d = hc + row * HB + blk * 16 + 2 * g4;
+          *(lu16*)d = (uint16_t)code;
+          *(lu16*)(d + 8) = (uint16_t)(code >> 16);
+          if (g4 == 0) hs[(row >> 6) * 256 + (blk * 16 + i16) * 4 + ((row >> 4) & 3)] = (uint8_t)sc;
+        }
+      lds_barrier();
+      const int hnb = g.n / 128;  // scale tiles across H
+      for (int p = threadIdx.x; p < BM * HB / 16; p += 64 * NW) {
+        const int row = p / (HB / 16), c = p % (HB / 16);
+        if (m0 + row < g.m)
+          *(i32x4*)((uint8_t*)g.out + (m0 + row) * (int64_t)(hnb * 64) + n0 / 2 + 16 * c) =
+              *(const li32x4*)(hc + row * HB + 16 * c);
+      }
+      const int64_t mrt = row_tiles(g.m);
+      for (int p = threadIdx.x; p < BM; p += 64 * NW) {
+        const int64_t rt = (m0 >> 6) + (p >> 6);
+        if (rt < mrt) ((uint32_t*)g.h_scales)[(rt * hnb + n0 / 128) * 64 + (p & 63)] = *(const lu32*)(hs + p * 4);
+      }
+    } else {
+      const int64_t row0 = m0 + wm * TM * 16 + i16, col0 = n0 + wn * TN * 16;
+      if (!inside) {
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+#pragma unroll
+          for (int i = 0; i < TN; ++i) store_tile<EPI>(g, acc[i][j], row0 + 16 * j, col0 + 16 * i + 4 * g4);
+      } else if constexpr (EPI == EPI_BF16) {
+        // Lanes of odd 16-lane rows trade one column tile for its neighbour's, so
+        // that each lane has 8 neighbouring columns: 16-byte stores, 64 bytes a row, and
+        // past the caches' keeping, where the operands are wanted again (68,700 x 1024 x
+        // 4096: 222 us, 232 with ordinary stores; in fp32 it is 388 against 342).
+        uint16_t* const o = (uint16_t*)g.out + row0 * g.n + col0 + 16 * (g4 & 1) + 4 * (g4 & 2);
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+#pragma unroll
+          for (int i = 0; i < TN; i += 2) {
+            const f32x4 a = acc[i][j], b = acc[i + 1][j];
+            uint32_t a0 = pack_bf16x2(a[0], a[1]), a1 = pack_bf16x2(a[2], a[3]);
+            uint32_t b0 = pack_bf16x2(b[0], b[1]), b1 = pack_bf16x2(b[2], b[3]);
+            swap_rows(a0, b0);
+            swap_rows(a1, b1);
+            __builtin_nontemporal_store(u32x4{a0, a1, b0, b1}, (u32x4*)(o + (int64_t)(16 * j) * g.n + 16 * i));
+          }
+      } else {
+        float* const o = (float*)g.out + row0 * g.n + col0 + 4 * g4;
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+#pragma unroll
+          for (int i = 0; i < TN; ++i) *(f32x4*)(o + (int64_t)(16 * j) * g.n + 16 * i) = acc[i][j];
+      }
+    }
+    if (stride >= tile_end - tile) break;
+    clear();
+    // A tile over the edge makes fewer stores than the waits above allow for.
+    if (!inside) wait_loads<0>();
+  }
 }
 
 // Products with few tiles: a tile of 16 TN x 16 TM per workgroup, its KW waves
@@ -429,11 +587,16 @@ __global__ __launch_bounds__(64 * KW) void direct_kernel(Args g) {
   }
 }
 
-template <int TN, int TM, int WN, int WM, int EPI>
+template <int TN, int TM, int WN, int WM, int RING, int EPI>
 hipError_t go(const Args& g, hipStream_t stream) {
-  constexpr int BN = 16 * TN * WN / (EPI == EPI_SWIGLU ? 2 : 1), BM = 16 * TM * WM;
-  const int64_t tiles = ((g.n + BN - 1) / BN) * ((g.m + BM - 1) / BM);
-  gemm_kernel<TN, TM, WN, WM, EPI><<<dim3((unsigned)tiles), dim3(64 * WN * WM), 0, stream>>>(g);
+  constexpr int BN = 16 * TN * WN, BM = 16 * TM * WM, CN = EPI == EPI_SWIGLU ? BN / 2 : BN;
+  constexpr size_t lds = (size_t)RING * (BN + BM) * (STEP + 4) + (EPI == EPI_SWIGLU ? BM * (BN / 4 + 4) : 0);
+  static_assert(lds <= 160 * 1024, "LDS of one workgroup");
+  // as many workgroups as 256 compute units hold at once
+  const int64_t most = 256 * (160 * 1024 / lds < 8 / (WN * WM) ? 160 * 1024 / lds : 8 / (WN * WM));
+  const int64_t tiles = ((g.n + CN - 1) / CN) * ((g.m + BM - 1) / BM);
+  gemm_kernel<TN, TM, WN, WM, RING, EPI>
+      <<<dim3((unsigned)(tiles < most ? tiles : most)), dim3(64 * WN * WM), lds, stream>>>(g);
   return hipGetLastError();
 }
 
@@ -446,13 +609,28 @@ hipError_t go_direct(const Args& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Which kernel (measured at n x k = 4096 x 1024 and 1024 x 4096, us):
+//  up to 16 rows    16 x 16 tiles, 8 waves splitting k;
+//  up to 64 rows    16 columns x 64 rows (64 rows: 3.8, 6.8; 64 x 64 tiles: 5.7, 10.7);
+//  64 x 64 tiles    while the 256 compute units hold them all (200 rows: 6.0, 10.8;
+//                   128 x 128: 6.5, 14.0; at 300 rows, 4096 columns: 10.3 and 6.6);
+//  128 x 128, 2 workgroups a unit, or 256 x 256, one: by the rounds that either
+//                   needs. A round of 256 x 256 takes as long as two at k = 1024 (the
+//                   stores' time; it hides them from the third round on) and one and
+//                   a half at 4096 (1374 rows: 10.4, 14.5 and 13.6, 28.5; 2748: 13.8
+//                   and 15.7; 10,992: 45.1, 38.9 and 45.4, 35.4; 68,700: 259, 202 and
+//                   222, 175).
 template <int EPI>
 hipError_t product(const Args& g, hipStream_t stream) {
-  const int64_t big = ((g.n + 127) / 128) * ((g.m + 127) / 128);
   if (g.m <= 16) return go_direct<1, 1, 8, EPI>(g, stream);
   if (g.m <= 64) return go_direct<1, 4, 4, EPI>(g, stream);
-  if (big < 256) return go_direct<4, 4, 4, EPI>(g, stream);
-  return go<4, 4, 2, 2, EPI>(g, stream);
+  auto tiles = [&](int edge) { return ceil_div(g.n, edge) * ceil_div(g.m, edge); };
+  if (tiles(64) <= 256) return go_direct<4, 4, 4, EPI>(g, stream);
+  const int64_t small = ceil_div(tiles(128), 512), large = ceil_div(tiles(256), 256);
+  const bool use_large = g.nb >= 16 ? 3 * large <= 2 * small : large >= 3 && 2 * large <= small;
+  return use_large ? go<8, 4, 2, 4, 4, EPI>(g, stream) : go<4, 4, 2, 2, 4, EPI>(g, stream);
 }
 
 }  // namespace
@@ -481,9 +659,11 @@ hipError_t launch_gemm_swiglu(const Matrix& A, const Matrix& Wg, const Matrix& W
   Args g{};
   g.A = A; g.W = Wg; g.W2 = Wu; g.m = m; g.n = n; g.k = k; g.nb = (int)(padded_k(k) / kPad);
   g.out = h_codes; g.h_scales = h_scales;
+  // as above (8192 x 1024: 256 rows 11.4 us in 64 x 64 tiles, 12.3 in 256 x 256; 300 rows
+  // 15.7 and 13.3)
   if (m <= 16) return go_direct<4, 1, 8, EPI_SWIGLU>(g, stream);
-  if (m <= 256) return go_direct<4, 4, 4, EPI_SWIGLU>(g, stream);
-  return go<4, 4, 4, 2, EPI_SWIGLU>(g, stream);
+  if (ceil_div(2 * (int64_t)n, 64) * ceil_div(m, 64) <= 512) return go_direct<4, 4, 4, EPI_SWIGLU>(g, stream);
+  return go<8, 4, 2, 4, 4, EPI_SWIGLU>(g, stream);
 }
 
 hipError_t launch_gemm_swiglu_tokens(const void* A, const Matrix& Wg, const Matrix& Wu, uint8_t* h_codes,
