@@ -477,22 +477,24 @@ def ttt_read_streamed(Q_host: torch.Tensor, theta: torch.Tensor, n_heads: int, c
 # weights frozen in 4 bits
 # ---------------------------------------------------------------------------
 
-def _device_of(ts) -> int:
-    """The one GPU that a call's tensors share; they are contiguous."""
-    dev = -1
+def _pointers(*ts):
+    """The GPU that a call's tensors (contiguous, None where absent) share, and their addresses."""
+    dev, out = None, []
     for t in ts:
         if t is None:
+            out.append(None)
             continue
-        if not t.is_cuda:
-            raise ValueError("tensors must live on the GPU (HIP device memory)")
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError("tensors must live on the GPU (HIP device memory)")
+            if dev is not None:
+                raise ValueError(f"tensors live on different devices: cuda:{dev} and cuda:{d}")
+            dev = d
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
-        d = t.get_device()
-        if dev < 0:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"tensors live on different devices: cuda:{dev} and cuda:{d}")
-    return dev
+        out.append(t.data_ptr())
+    return dev, out
 
 
 # The current stream of a GPU as the address that the C calls take, without the
@@ -501,10 +503,8 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _run(name: str, dev: int, *args) -> None:
-    """Call `name` on GPU `dev`'s current stream, whichever device is current.
-    Tensors among the arguments pass as their addresses."""
+    """Call `name` on GPU `dev`'s current stream, whichever device is current."""
     fn = getattr(_lib.load(), name)
-    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
     if dev == torch._C._cuda_getDevice():
         rc = fn(*args, _raw_stream(dev))
     else:
@@ -593,8 +593,8 @@ def mx4_quantize(X: torch.Tensor, transpose: bool = False, out: Optional[Mx4] = 
         _check_mx4("out", out, rows, k)
     else:
         out = _mx4_empty(rows, k, X.device)
-    dev = _device_of((X, out.codes, out.scales))
-    _run("vggt3_mx4_quantize", dev, X, int(bool(transpose)), out.codes, out.scales, rows, k, _dtype_code(X))
+    dev, (x, c, s) = _pointers(X, out.codes, out.scales)
+    _run("vggt3_mx4_quantize", dev, x, int(bool(transpose)), c, s, rows, k, _dtype_code(X))
     return out
 
 
@@ -605,8 +605,8 @@ def mx4_dequantize(A: Mx4, dtype: torch.dtype = torch.bfloat16, out: Optional[to
     _check_out(out, (A.rows, A.k), dtype)
     if out is None:
         out = torch.empty((A.rows, A.k), dtype=dtype, device=A.codes.device)
-    dev = _device_of((A.codes, A.scales, out))
-    _run("vggt3_mx4_dequantize", dev, A.codes, A.scales, out, A.rows, A.k, dt)
+    dev, (c, s, o) = _pointers(A.codes, A.scales, out)
+    _run("vggt3_mx4_dequantize", dev, c, s, o, A.rows, A.k, dt)
     return out
 
 
@@ -631,8 +631,8 @@ def mx4_matmul(A: Union[Mx4, torch.Tensor], W: Mx4, dtype: torch.dtype = torch.b
     if out is None:
         out = torch.empty((m, W.rows), dtype=dtype, device=data.device)
     workspace, nb = _ws(workspace, mx4_matmul_workspace_bytes(m, W.rows, W.k, a_type), data.device)
-    dev = _device_of((data, scales, W.codes, W.scales, out, workspace))
-    _run("vggt3_mx4_matmul", dev, data, scales, a_type, W.codes, W.scales, out, m, W.rows, W.k, dt, workspace, nb)
+    dev, (a, a_s, w, w_s, o, ws) = _pointers(data, scales, W.codes, W.scales, out, workspace)
+    _run("vggt3_mx4_matmul", dev, a, a_s, a_type, w, w_s, o, m, W.rows, W.k, dt, ws, nb)
     return out
 
 
@@ -647,7 +647,8 @@ def ttt_freeze_mx4(theta: torch.Tensor, d_head: int = 1024, d_hidden: int = 4096
     for name, a, (r, k) in zip(FrozenMx4._fields, out, shapes):
         _check_mx4(name, a, r, k)
         parts += [a.codes, a.scales]
-    _run("vggt3_ttt_freeze_mx4", _device_of((theta, *parts)), theta, *parts, 1, d_head, d_hidden)
+    dev, ptrs = _pointers(theta, *parts)
+    _run("vggt3_ttt_freeze_mx4", dev, *ptrs, 1, d_head, d_hidden)
     return out
 
 
@@ -676,8 +677,8 @@ def ttt_read_mx4(Q: Union[Mx4, torch.Tensor], frozen: FrozenMx4, out: Optional[t
     if out is None:
         out = torch.empty((n, d), dtype=torch.bfloat16, device=data.device)
     workspace, nb = _ws(workspace, read_mx4_workspace_bytes(n, d, m, q_type), data.device)
-    dev = _device_of((data, scales, out, workspace, *parts))
-    _run("vggt3_ttt_read_mx4", dev, data, scales, q_type, *parts, out, n, 1, d, m, workspace, nb)
+    dev, (q, q_s, *weights, o, ws) = _pointers(data, scales, *parts, out, workspace)
+    _run("vggt3_ttt_read_mx4", dev, q, q_s, q_type, *weights, o, n, 1, d, m, ws, nb)
     return out
 
 
@@ -704,6 +705,12 @@ def _check_gate(gate: Optional[torch.Tensor], gate_tokens: int, x: torch.Tensor)
         raise ValueError(f"gate {tuple(gate.shape)} {gate.dtype}, {want} {x.dtype} expected")
 
 
+def _check_channels(C: int, **params) -> None:
+    for name, p in params.items():
+        if p is not None and (p.dtype != torch.float32 or p.numel() != C):
+            _check_f32(name, p, C)
+
+
 def block_join(x: torch.Tensor, f: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
                gate_tokens: int = 1, scale: Optional[torch.Tensor] = None, post=None,
                post_w: Optional[torch.Tensor] = None, post_b: Optional[torch.Tensor] = None, pre=None,
@@ -719,8 +726,7 @@ def block_join(x: torch.Tensor, f: Optional[torch.Tensor] = None, gate: Optional
     _check_same("f", f, x, "x")
     _check_gate(gate, gate_tokens, x)
     n, C = x.shape
-    for name, p in (("scale", scale), ("post_w", post_w), ("post_b", post_b), ("pre_w", pre_w), ("pre_b", pre_b)):
-        _check_f32(name, p, C)
+    _check_channels(C, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w, pre_b=pre_b)
     post, pre = _norm_code(post), _norm_code(pre)
     if f is not None:
         _check_same("r", r, x, "x")
@@ -742,9 +748,10 @@ def block_join(x: torch.Tensor, f: Optional[torch.Tensor] = None, gate: Optional
             y = torch.empty_like(x)
         _check_same("y", y, x, "x")
     plain = None if mx4 else y
-    ts = (x, f, gate, scale, post_w, post_b, pre_w, pre_b, r, plain, codes, scales)
-    _run("vggt3_block_join", _device_of(ts), x, f, gate, int(gate_tokens), scale, post, post_w, post_b, pre, pre_w,
-         pre_b, float(eps), r, plain, codes, scales, n, C, _dtype_code(x))
+    dev, (px, pf, pg, ps, *norms, pr, py, pc, psc) = _pointers(x, f, gate, scale, post_w, post_b, pre_w, pre_b, r,
+                                                               plain, codes, scales)
+    _run("vggt3_block_join", dev, px, pf, pg, int(gate_tokens), ps, post, norms[0], norms[1], pre, norms[2], norms[3],
+         float(eps), pr, py, pc, psc, n, C, _dtype_code(x))
     return r, y
 
 
@@ -782,8 +789,7 @@ def block_join_grad(r: torch.Tensor, f: Optional[torch.Tensor] = None, dr: Optio
         _check_same(name, t, r, "r")
     _check_gate(gate, gate_tokens, r)
     n, C = r.shape
-    for name, p in (("scale", scale), ("post_w", post_w), ("post_b", post_b), ("pre_w", pre_w)):
-        _check_f32(name, p, C)
+    _check_channels(C, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w)
     post, pre = _norm_code(post), _norm_code(pre)
     if out is None:
         # the channel vectors are rows of one allocation, 16-byte aligned
@@ -801,7 +807,8 @@ def block_join_grad(r: torch.Tensor, f: Optional[torch.Tensor] = None, dr: Optio
         for name in BlockJoinGrads._fields[3:]:
             _check_f32(name, getattr(out, name), C)
     workspace, nb = _ws(workspace, block_join_grad_workspace_bytes(n, C, _dtype_code(r)), r.device)
-    dev = _device_of((r, f, dr, dy, gate, scale, post_w, post_b, pre_w, workspace, *out))
-    _run("vggt3_block_join_grad", dev, r, f, gate, int(gate_tokens), scale, post, post_w, post_b, pre, pre_w, float(eps),
-         dr, dy, *out, n, C, _dtype_code(r), workspace, nb)
+    dev, (pr, pf, pg, ps, pw, pb, w, ws, *grads) = _pointers(r, f, gate, scale, post_w, post_b, pre_w, workspace, dr, dy,
+                                                             *out)
+    _run("vggt3_block_join_grad", dev, pr, pf, pg, int(gate_tokens), ps, post, pw, pb, pre, w, float(eps), *grads, n, C,
+         _dtype_code(r), ws, nb)
     return out

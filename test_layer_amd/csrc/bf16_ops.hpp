@@ -11,6 +11,16 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 __device__ __forceinline__ u32x4 ld16(const void* p) { return *reinterpret_cast<const u32x4*>(p); }
 __device__ __forceinline__ void st16(void* p, const u32x4& v) { *reinterpret_cast<u32x4*>(p) = v; }
+// 16 bytes of a result; STREAM: past the caches' keeping, for results that they could not hold in any case (streams()). A stream of
+// such stores alone reaches 6.1 TB/s, where ordinary ones reach 5.1.
+template <bool STREAM>
+__device__ __forceinline__ void st16(void* p, const u32x4& v) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+  else
+    *reinterpret_cast<u32x4*>(p) = v;
+}
+inline bool streams(int64_t bytes) { return bytes >= (int64_t)128 << 20; }
 __device__ __forceinline__ u32x2 ld8(const void* p) { return *reinterpret_cast<const u32x2*>(p); }
 __device__ __forceinline__ void st8(void* p, const u32x2& v) { *reinterpret_cast<u32x2*>(p) = v; }
 

@@ -48,13 +48,14 @@ struct Args {
   uint8_t* h_scales;
 };
 
-enum Epi { EPI_BF16, EPI_F32, EPI_SWIGLU };
+enum Epi { EPI_BF16, EPI_BF16_STREAM, EPI_F32, EPI_SWIGLU };
+constexpr bool to_bf16(int epi) { return epi == EPI_BF16 || epi == EPI_BF16_STREAM; }
 
 // Four neighbouring columns of one row of C.
 template <int EPI>
 __device__ __forceinline__ void store_tile(const Args& g, const f32x4& v, int64_t row, int64_t col) {
   if (row >= g.m) return;
-  if constexpr (EPI == EPI_BF16) {
+  if constexpr (to_bf16(EPI)) {
     uint16_t* o = (uint16_t*)g.out + row * g.n + col;
     if (g.n % 4 == 0 && col < g.n) {
       st8(o, u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
@@ -163,7 +164,7 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2)
   static_assert(DN * NW * 16 == BN && DM * NW * 16 == BM, "whole loads");
   constexpr int LOADS = DN + DM + DS;
   // Stores (at least) a wave makes of a tile that lies inside C.
-  constexpr int STORES = EPI == EPI_SWIGLU ? BM * (BN / 4) / 16 / (64 * NW) : EPI == EPI_BF16 ? TN * TM / 2 : TN * TM;
+  constexpr int STORES = EPI == EPI_SWIGLU ? BM * (BN / 4) / 16 / (64 * NW) : to_bf16(EPI) ? TN * TM / 2 : TN * TM;
   static_assert(RING >= 3 && (RING - 3) * LOADS + STORES < 64, "vmcnt");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   lu8* const lds = (lu8*)smem;
@@ -411,11 +412,11 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2)
         for (int j = 0; j < TM; ++j)
 #pragma unroll
           for (int i = 0; i < TN; ++i) store_tile<EPI>(g, acc[i][j], row0 + 16 * j, col0 + 16 * i + 4 * g4);
-      } else if constexpr (EPI == EPI_BF16) {
+      } else if constexpr (to_bf16(EPI)) {
         // Lanes of odd 16-lane rows trade one column tile for its neighbour's, so
-        // that each lane has 8 neighbouring columns: 16-byte stores, 64 bytes a row, and
-        // past the caches' keeping, where the operands are wanted again (68,700 x 1024 x
-        // 4096: 222 us, 232 with ordinary stores; in fp32 it is 388 against 342).
+        // that each lane has 8 neighbouring columns: 16-byte stores, 64 bytes a row,
+        // streamed when C is large (68,700 x 1024 x 4096: 222 us, 232 with ordinary
+        // stores; in fp32, whose stores are 64 bytes a row too, 388 against 342).
         uint16_t* const o = (uint16_t*)g.out + row0 * g.n + col0 + 16 * (g4 & 1) + 4 * (g4 & 2);
 #pragma unroll
         for (int j = 0; j < TM; ++j)
@@ -426,7 +427,7 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2)
             uint32_t b0 = pack_bf16x2(b[0], b[1]), b1 = pack_bf16x2(b[2], b[3]);
             swap_rows(a0, b0);
             swap_rows(a1, b1);
-            __builtin_nontemporal_store(u32x4{a0, a1, b0, b1}, (u32x4*)(o + (int64_t)(16 * j) * g.n + 16 * i));
+            st16<EPI == EPI_BF16_STREAM>(o + (int64_t)(16 * j) * g.n + 16 * i, u32x4{a0, a1, b0, b1});
           }
       } else {
         float* const o = (float*)g.out + row0 * g.n + col0 + 4 * g4;
@@ -630,7 +631,9 @@ hipError_t product(const Args& g, hipStream_t stream) {
   if (tiles(64) <= 256) return go_direct<4, 4, 4, EPI>(g, stream);
   const int64_t small = ceil_div(tiles(128), 512), large = ceil_div(tiles(256), 256);
   const bool use_large = g.nb >= 16 ? 3 * large <= 2 * small : large >= 3 && 2 * large <= small;
-  return use_large ? go<8, 4, 2, 4, 4, EPI>(g, stream) : go<4, 4, 2, 2, 4, EPI>(g, stream);
+  if (!use_large) return go<4, 4, 2, 2, 4, EPI>(g, stream);
+  if (EPI == EPI_BF16 && streams(g.m * g.n * 2)) return go<8, 4, 2, 4, 4, EPI_BF16_STREAM>(g, stream);
+  return go<8, 4, 2, 4, 4, EPI>(g, stream);
 }
 
 }  // namespace

@@ -19,30 +19,94 @@ __device__ __forceinline__ float load1(const void* X, int64_t i) {
   return ((const float*)X)[i];
 }
 
-// One workgroup per 64 rows x 128 columns, one thread per (row, block): the
-// maximum needs no exchange between lanes, and the 256 scale bytes of the
-// workgroup are one whole scale tile, put together in LDS. VEC: rows start at
-// 16-byte boundaries and k is a multiple of a 16-byte load.
-template <bool BF16, bool TRANS, bool VEC>
+// Both directions are bound by memory; a workgroup takes 64 rows x 128 columns, one
+// scale tile. Row-major: thread t has 8 columns (16 neighbouring threads a row: 256
+// or 512 consecutive bytes) of the rows t / 16 + 16 i, i = 0..3, so that the 4 scale
+// bytes of one block column that it is part of are one dword of the tile, and a
+// block is 4 neighbouring lanes. (One thread per block of 32 needs no exchange
+// between lanes, but its loads step 64 bytes from lane to lane: 137,400 x 1024 bf16
+// took 90 us that way.)
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load8(const void* X, int64_t row, int k0, int k, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  if constexpr (VEC && BF16) {
+    if (k0 >= k) return;
+    const u32x4 q = ld16((const uint16_t*)X + row * k + k0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo(q[j]);
+      v[2 * j + 1] = bf16_hi(q[j]);
+    }
+  } else if constexpr (VEC) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (k0 + 4 * h >= k) continue;
+      const f32x4 q = *(const f32x4*)((const float*)X + row * k + k0 + 4 * h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * h + j] = q[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k0 + j < k) v[j] = load1<BF16>(X, row * (int64_t)k + k0 + j);
+  }
+}
+
+// Largest of 4 neighbouring lanes, by DPP.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, false);  // lane ^ 1
+  v = o > v ? o : v;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, false);  // lane ^ 2
+  return o > v ? o : v;
+}
+
+template <bool BF16, bool VEC>
 __global__ __launch_bounds__(NTHR) void quantize_kernel(const void* X, uint8_t* codes, uint8_t* scales, int64_t rows,
                                                         int k, int nb) {
+  const int t = threadIdx.x, piece = t & 15, r = t >> 4;
+  const int64_t R = blockIdx.x / (uint32_t)nb;
+  const int B = (int)(blockIdx.x % (uint32_t)nb);
+  const int k0 = B * 128 + piece * 8;
+  float v[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = R * 64 + 16 * i + r;
+    load8<BF16, VEC>(X, row, k0, row < rows ? k : 0, v[i]);
+  }
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t a = __float_as_uint(v[i][j]) & 0x7fffffffu;
+      amax = a > amax ? a : amax;
+    }
+    const uint32_t s = scale_byte(quad_max(amax));
+    word |= s << (8 * i);
+    const int64_t row = R * 64 + 16 * i + r;
+    if (row < rows)
+      ((uint32_t*)(codes + row * (int64_t)(nb * 64) + B * 64))[piece] =
+          s == 255u ? 0u : encode8(v[i], scale_value(s));
+  }
+  if ((piece & 3) == 0) ((uint32_t*)scales)[(R * nb + B) * 64 + 16 * (piece >> 2) + r] = word;
+}
+
+// X [k][rows]: a wave takes 64 neighbouring rows of one block, a thread one block.
+template <bool BF16>
+__global__ __launch_bounds__(NTHR) void quantize_transposed_kernel(const void* X, uint8_t* codes, uint8_t* scales,
+                                                                   int64_t rows, int k, int nb) {
   __shared__ uint32_t sc[64];
-  const int t = threadIdx.x;
-  const int64_t R = blockIdx.x / nb;
-  const int B = (int)(blockIdx.x % nb);
-  // Row-major: 4 neighbouring threads share a row (256 or 512 consecutive
-  // bytes); transposed: a wave takes 64 neighbouring rows of one block.
-  const int rr = TRANS ? (t & 63) : (t >> 2), g = TRANS ? (t >> 6) : (t & 3);
+  const int t = threadIdx.x, rr = t & 63, g = t >> 6;
+  const int64_t R = blockIdx.x / (uint32_t)nb;
+  const int B = (int)(blockIdx.x % (uint32_t)nb);
   const int64_t row = R * 64 + rr;
   const int k0 = B * 128 + g * 32;
   const bool live = row < rows;
   float v[32];
-  if constexpr (TRANS) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = live && k0 + j < k ? load1<BF16>(X, (int64_t)(k0 + j) * rows + row) : 0.0f;
-  } else {
-    load_block<BF16, VEC>(X, live ? row : 0, k0, live ? k : 0, v);
-  }
+  for (int j = 0; j < 32; ++j) v[j] = live && k0 + j < k ? load1<BF16>(X, (int64_t)(k0 + j) * rows + row) : 0.0f;
   u32x4 o;
   const uint32_t s = quantize_block(v, o);
   if (live) st16(codes + row * (int64_t)(nb * 64) + B * 64 + g * 16, o);
@@ -51,42 +115,62 @@ __global__ __launch_bounds__(NTHR) void quantize_kernel(const void* X, uint8_t* 
   if (t < 64) ((uint32_t*)scales)[(R * nb + B) * 64 + t] = sc[t];
 }
 
-// One thread per 8 columns of a row.
-template <bool BF16, bool VEC>
+// Thread t has V columns, 16 bytes of X (8 of bf16, 4 of fp32), of the rows
+// t / (128 / V) + (2 V) i: stores of a wave lie side by side (with 8 columns of fp32
+// a thread they step 32 bytes: 178 us instead of
+// 125 for 137,400 x 1024, or 104 streamed).
+template <bool BF16, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NTHR) void dequantize_kernel(const uint8_t* codes, const uint8_t* scales, void* X,
                                                           int64_t rows, int k, int nb) {
-  const int groups = (k + 7) / 8;
-  const int64_t i = (int64_t)blockIdx.x * NTHR + threadIdx.x;
-  if (i >= rows * groups) return;
-  const int64_t row = i / groups;
-  const int c = (int)(i % groups);
-  const uint32_t q = ((const uint32_t*)(codes + row * (int64_t)(nb * 64)))[c];
-  const uint32_t s = scales[scale_at(row, c >> 2, nb)];
-  const float f = s == 255u ? __uint_as_float(0x7fc00000u) : scale_value(s);
-  float v[8];
+  constexpr int V = BF16 ? 8 : 4, LANES = 128 / V, PASS = NTHR / LANES, N = 64 / PASS;
+  constexpr int WORDS = PASS < 16 ? 16 / PASS : 1;  // scale dwords: the rows of a pass modulo 16
+  const int t = threadIdx.x, piece = t % LANES, r = t / LANES;
+  const int64_t R = blockIdx.x / (uint32_t)nb;
+  const int B = (int)(blockIdx.x % (uint32_t)nb);
+  const int k0 = B * 128 + piece * V;
+  if (k0 >= k) return;
+  uint32_t word[WORDS], q[N];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t code = (q >> (4 * j)) & 15u, m = code & 7u;
-    // {0, .5, 1, 1.5, 2, 3, 4, 6}: .5 m below 2, else (1 + .5 (m & 1)) 2^(m / 2 - 1)
-    const float a = m < 4u ? 0.5f * (float)m : (float)(2u + (m & 1u)) * (m < 6u ? 1.0f : 2.0f);
-    v[j] = (code & 8u ? -a : a) * f;
+  for (int w = 0; w < WORDS; ++w)
+    word[w] = ((const uint32_t*)scales)[(R * nb + B) * 64 + 16 * (piece * V / 32) + r + PASS * w];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t row = R * 64 + PASS * i + r;
+    const uint8_t* p = codes + row * (int64_t)(nb * 64) + B * 64 + piece * V / 2;
+    q[i] = row < rows ? (V == 8 ? *(const uint32_t*)p : *(const uint16_t*)p) : 0u;
   }
-  if (VEC) {
-    if (BF16) {
-      st16((uint16_t*)X + row * k + 8 * c, as_u32x4(pack8(v)));
-    } else {
-      float* p = (float*)X + row * k + 8 * c;
-      *(f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
-      *(f32x4*)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    }
-  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (8 * c + j >= k) continue;
-      if (BF16)
-        ((uint16_t*)X)[row * k + 8 * c + j] = f32_to_bf16_bits(v[j]);
+  for (int i = 0; i < N; ++i) {
+    const int64_t row = R * 64 + PASS * i + r;
+    if (row >= rows) continue;
+    const uint32_t s = word[i % WORDS] >> (8 * (i / WORDS)) & 255u;
+    const float f = scale_value(s);
+    float v[8];
+#define PAIR(j)                                                                   \
+  {                                                                               \
+    const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], f, j);          \
+    v[2 * j] = s == 255u ? __uint_as_float(0x7fc00000u) : p[0];                   \
+    v[2 * j + 1] = s == 255u ? __uint_as_float(0x7fc00000u) : p[1];               \
+  }
+    PAIR(0) PAIR(1)
+    if constexpr (V == 8) {
+      PAIR(2) PAIR(3)
+    }
+#undef PAIR
+    if constexpr (VEC) {
+      if constexpr (BF16)
+        st16<STREAM>((uint16_t*)X + row * k + k0, as_u32x4(pack8(v)));
       else
-        ((float*)X)[row * k + 8 * c + j] = v[j];
+        st16<STREAM>((float*)X + row * k + k0, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (k0 + j >= k) continue;
+        if constexpr (BF16)
+          ((uint16_t*)X)[row * k + k0 + j] = f32_to_bf16_bits(v[j]);
+        else
+          ((float*)X)[row * k + k0 + j] = v[j];
+      }
     }
   }
 }
@@ -99,15 +183,16 @@ hipError_t launch_quantize(const void* X, bool transposed, bool bf16, uint8_t* c
   const int nb = (int)(padded_k(k) / kPad);
   const dim3 grid((unsigned)(row_tiles(rows) * nb)), block(NTHR);
   const bool vec = k % (bf16 ? 8 : 4) == 0;
-#define GO(B, T, V) quantize_kernel<B, T, V><<<grid, block, 0, stream>>>(X, codes, scales, rows, k, nb)
-  if (bf16) {
-    if (transposed) GO(true, true, false);
-    else if (vec) GO(true, false, true);
-    else GO(true, false, false);
+#define GO(KERNEL) KERNEL<<<grid, block, 0, stream>>>(X, codes, scales, rows, k, nb)
+  if (transposed) {
+    if (bf16) GO(quantize_transposed_kernel<true>);
+    else GO(quantize_transposed_kernel<false>);
+  } else if (bf16) {
+    if (vec) GO((quantize_kernel<true, true>));
+    else GO((quantize_kernel<true, false>));
   } else {
-    if (transposed) GO(false, true, false);
-    else if (vec) GO(false, false, true);
-    else GO(false, false, false);
+    if (vec) GO((quantize_kernel<false, true>));
+    else GO((quantize_kernel<false, false>));
   }
 #undef GO
   return hipGetLastError();
@@ -117,15 +202,18 @@ hipError_t launch_dequantize(const uint8_t* codes, const uint8_t* scales, void* 
                              hipStream_t stream) {
   if (rows == 0) return hipSuccess;
   const int nb = (int)(padded_k(k) / kPad);
-  const dim3 grid((unsigned)((rows * ((k + 7) / 8) + NTHR - 1) / NTHR)), block(NTHR);
-  const bool vec = k % 8 == 0;
-#define GO(B, V) dequantize_kernel<B, V><<<grid, block, 0, stream>>>(codes, scales, X, rows, k, nb)
+  const dim3 grid((unsigned)(row_tiles(rows) * nb)), block(NTHR);
+  const bool vec = k % (bf16 ? 8 : 4) == 0;
+  const bool past = vec && streams(rows * k * (bf16 ? 2 : 4));
+#define GO(B, V, S) dequantize_kernel<B, V, S><<<grid, block, 0, stream>>>(codes, scales, X, rows, k, nb)
   if (bf16) {
-    if (vec) GO(true, true);
-    else GO(true, false);
+    if (past) GO(true, true, true);
+    else if (vec) GO(true, true, false);
+    else GO(true, false, false);
   } else {
-    if (vec) GO(false, true);
-    else GO(false, false);
+    if (past) GO(false, true, true);
+    else if (vec) GO(false, true, false);
+    else GO(false, false, false);
   }
 #undef GO
   return hipGetLastError();
