@@ -57,8 +57,8 @@ __device__ __forceinline__ void store_tile(const Args& g, const f32x4& v, int64_
   if (row >= g.m) return;
   if constexpr (to_bf16(EPI)) {
     uint16_t* o = (uint16_t*)g.out + row * g.n + col;
-    if (g.n % 4 == 0 && col < g.n) {
-      st8(o, u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+    if (col + 4 <= g.n) {
+      *(u32x2_any*)o = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -66,8 +66,8 @@ __device__ __forceinline__ void store_tile(const Args& g, const f32x4& v, int64_
     }
   } else {
     float* o = (float*)g.out + row * g.n + col;
-    if (g.n % 4 == 0 && col < g.n) {
-      *(f32x4*)o = v;
+    if (col + 4 <= g.n) {
+      *(f32x4_any*)o = v;
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -370,14 +370,16 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2)
 
     int64_t n0, m0;
     place(tile, n0, m0);
-    const bool inside = m0 + BM <= g.m && n0 + CN <= g.n && (EPI == EPI_SWIGLU || g.n % 8 == 0);
+    const bool inside = m0 + BM <= g.m && n0 + CN <= g.n;
     if constexpr (EPI == EPI_SWIGLU) {
       // Each wave holds gate (tiles 0, 1 of four) and up (tiles 2, 3) of the same
       // 32 units: one block of H per row. Codes and scales are gathered in LDS.
       constexpr int HB = BN / 4;  // bytes of codes per row of this tile
       static_assert(EPI != EPI_SWIGLU || BN == 256, "a tile is 128 units: one scale tile wide");
-      lu8* const hc = lds + RING * STAGE;  // [BM][HB]
-      lu8* const hs = hc + BM * HB;        // [BM / 64][64][4], the scale tiles
+      // (In the place of the step just done: free from there to the next barrier.)
+      static_assert(BM * (HB + 4) <= STAGE, "staging");
+      lu8* const hc = lds + (ring == 0 ? RING - 1 : ring - 1) * STAGE;  // [BM][HB]
+      lu8* const hs = hc + BM * HB;                                    // [BM / 64][64][4], the scale tiles
 #pragma unroll
       for (int j = 0; j < TM; ++j)
 #pragma unroll
@@ -427,14 +429,18 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2)
             uint32_t b0 = pack_bf16x2(b[0], b[1]), b1 = pack_bf16x2(b[2], b[3]);
             swap_rows(a0, b0);
             swap_rows(a1, b1);
-            st16<EPI == EPI_BF16_STREAM>(o + (int64_t)(16 * j) * g.n + 16 * i, u32x4{a0, a1, b0, b1});
+            uint16_t* const at = o + (int64_t)(16 * j) * g.n + 16 * i;
+            if constexpr (EPI == EPI_BF16_STREAM)
+              st16<true>(at, u32x4{a0, a1, b0, b1});
+            else
+              st16_any(at, u32x4{a0, a1, b0, b1});
           }
       } else {
         float* const o = (float*)g.out + row0 * g.n + col0 + 4 * g4;
 #pragma unroll
         for (int j = 0; j < TM; ++j)
 #pragma unroll
-          for (int i = 0; i < TN; ++i) *(f32x4*)(o + (int64_t)(16 * j) * g.n + 16 * i) = acc[i][j];
+          for (int i = 0; i < TN; ++i) *(f32x4_any*)(o + (int64_t)(16 * j) * g.n + 16 * i) = acc[i][j];
       }
     }
     if (stride >= tile_end - tile) break;
@@ -591,7 +597,7 @@ __global__ __launch_bounds__(64 * KW) void direct_kernel(Args g) {
 template <int TN, int TM, int WN, int WM, int RING, int EPI>
 hipError_t go(const Args& g, hipStream_t stream) {
   constexpr int BN = 16 * TN * WN, BM = 16 * TM * WM, CN = EPI == EPI_SWIGLU ? BN / 2 : BN;
-  constexpr size_t lds = (size_t)RING * (BN + BM) * (STEP + 4) + (EPI == EPI_SWIGLU ? BM * (BN / 4 + 4) : 0);
+  constexpr size_t lds = (size_t)RING * (BN + BM) * (STEP + 4);
   static_assert(lds <= 160 * 1024, "LDS of one workgroup");
   // as many workgroups as 256 compute units hold at once
   const int64_t most = 256 * (160 * 1024 / lds < 8 / (WN * WM) ? 160 * 1024 / lds : 8 / (WN * WM));
@@ -632,7 +638,7 @@ hipError_t product(const Args& g, hipStream_t stream) {
   const int64_t small = ceil_div(tiles(128), 512), large = ceil_div(tiles(256), 256);
   const bool use_large = g.nb >= 16 ? 3 * large <= 2 * small : large >= 3 && 2 * large <= small;
   if (!use_large) return go<4, 4, 2, 2, 4, EPI>(g, stream);
-  if (EPI == EPI_BF16 && streams(g.m * g.n * 2)) return go<8, 4, 2, 4, 4, EPI_BF16_STREAM>(g, stream);
+  if (EPI == EPI_BF16 && g.n % 8 == 0 && streams(g.m * g.n * 2)) return go<8, 4, 2, 4, 4, EPI_BF16_STREAM>(g, stream);
   return go<8, 4, 2, 4, 4, EPI>(g, stream);
 }
 

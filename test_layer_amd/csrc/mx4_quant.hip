@@ -46,6 +46,23 @@ __device__ __forceinline__ void load8(const void* X, int64_t row, int k0, int k,
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[4 * h + j] = q[j];
     }
+  } else if (k0 + 8 <= k) {
+    if constexpr (BF16) {
+      const u32x4 q = ld16_any((const uint16_t*)X + row * k + k0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16_lo(q[j]);
+        v[2 * j + 1] = bf16_hi(q[j]);
+      }
+    } else {
+      const float* p = (const float*)X + row * k + k0;
+      const f32x4 a = *(const f32x4_any*)p, b = *(const f32x4_any*)(p + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = a[j];
+        v[4 + j] = b[j];
+      }
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -162,6 +179,11 @@ __global__ __launch_bounds__(NTHR) void dequantize_kernel(const uint8_t* codes, 
         st16<STREAM>((uint16_t*)X + row * k + k0, as_u32x4(pack8(v)));
       else
         st16<STREAM>((float*)X + row * k + k0, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
+    } else if (k0 + V <= k) {
+      if constexpr (BF16)
+        st16_any((uint16_t*)X + row * k + k0, as_u32x4(pack8(v)));
+      else
+        st16_any((float*)X + row * k + k0, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) {

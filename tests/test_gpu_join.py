@@ -78,7 +78,7 @@ MODES = [("none", "none", False, 1, True, False), ("none", "rms", True, 1, False
          ("layer", "rms", True, 1000, False, False), ("layer", "layer", True, 1, True, False)]
 SHAPES = [(1, 1), (1, 1024), (2, 33), (5, 64), (37, 100), (64, 512), (65, 513), (130, 1024), (40, 1025), (23, 2048), (9, 4096),
           (6, 5000), (3, 8192), (700, 24), (33, 128), (21, 256),
-          (19, 200)]
+          (19, 200), (50, 7), (31, 515), (12, 1999), (5, 4095), (3, 8191)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
