@@ -24,7 +24,7 @@ def norm(v, kind, w=None, b=None, eps=1e-6):
 
 
 def spread(gate, per, n):
-    return 1.0 if gate is None else np.repeat(np.asarray(gate, np.float64), per, axis=0)[:n]
+    return 1.0 if gate is None else np.repeat(np.asarray(gate, np.float64), min(per, n), axis=0)[:n]
 
 
 def join(x, f, gate=None, per=1, scale=None, post="none", post_w=None, post_b=None, eps=1e-6):
@@ -59,6 +59,7 @@ def grads(r, f, dr, dy, gate=None, per=1, scale=None, post="none", post_w=None, 
     h, hat, rstd = norm(f, post, post_w, post_b, eps)
     g, s = spread(gate, per, n), 1.0 if scale is None else scale
     out["dscale"] = (d * g * h).sum(0)
+    per = min(per, n)
     groups = -(-n // per)
     p = np.zeros((groups * per, C))
     p[:n] = d * s * h

@@ -660,6 +660,8 @@ def ttt_read_mx4(Q: Union[Mx4, torch.Tensor], frozen: FrozenMx4, out: Optional[t
                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """O = T_theta*(Q) with the full-width fast weights frozen in 4 bits (query mode).
     Q: bf16 tokens [n, 1024], quantised on the way, or an Mx4; O is bf16."""
+    if not isinstance(frozen, FrozenMx4):
+        raise TypeError(f"frozen must be a FrozenMx4 (ttt_freeze_mx4), got {type(frozen).__name__}")
     d, m = frozen.down.rows, frozen.gate.rows
     if isinstance(Q, Mx4):
         _check_mx4("Q", Q, k=d)

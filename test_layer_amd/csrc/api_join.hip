@@ -59,6 +59,10 @@ int check_regions(const Region* rs, int count, int a, int b) {
   return VGGT3_OK;
 }
 
+// Tokens that share a gate row: at most all of them.
+int64_t tokens_per_gate(const void* gate, int64_t gate_tokens, int64_t n) {
+  return gate == nullptr ? 1 : gate_tokens < n ? gate_tokens : n > 0 ? n : 1;
+}
 int64_t gate_rows(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
 // Workspace of the gradient: [per-workgroup sums | shared gate groups' parts].
@@ -91,13 +95,14 @@ int vggt3_block_join(const void* x, const void* f, const void* gate, int64_t gat
     return fail(VGGT3_EINVAL, pre == VGGT3_NORM_NONE ? "y without a norm before the next block"
                                                      : "give y or (y_codes, y_scales), one of them");
   if (n_tokens == 0) return ok();
+  const int64_t per = tokens_per_gate(gate, gate_tokens, n_tokens);
   if (x == nullptr) return fail(VGGT3_EINVAL, "x is NULL");
   if (f && r == nullptr) return fail(VGGT3_EINVAL, "r is NULL");
   if (!f && r) return fail(VGGT3_EINVAL, "r goes with a block output f");
   const size_t tb = (size_t)n_tokens * channels * elem_size(dtype), vb = (size_t)channels * sizeof(float);
   const Region rs[] = {{"x", x, tb, false},
                        {"f", f, tb, false},
-                       {"gate", gate, gate ? (size_t)gate_rows(n_tokens, gate_tokens) * channels * elem_size(dtype) : 0, false},
+                       {"gate", gate, gate ? (size_t)gate_rows(n_tokens, per) * channels * elem_size(dtype) : 0, false},
                        {"scale", scale, vb, false},
                        {"post_w", post_w, vb, false},
                        {"post_b", post_b, vb, false},
@@ -114,7 +119,7 @@ int vggt3_block_join(const void* x, const void* f, const void* gate, int64_t gat
   a.post_w = post_w; a.post_b = post_b; a.pre_w = pre_w; a.pre_b = pre_b;
   a.r = r; a.y = y;
   a.y_codes = static_cast<uint8_t*>(y_codes); a.y_scales = static_cast<uint8_t*>(y_scales);
-  a.n = n_tokens; a.per = gate ? gate_tokens : 1; a.C = channels; a.post = post; a.pre = pre; a.eps = eps;
+  a.n = n_tokens; a.per = per; a.C = channels; a.post = post; a.pre = pre; a.eps = eps;
   rc = check_hip(join::launch_forward(a, dtype == VGGT3_BF16, static_cast<hipStream_t>(stream)), "block join launch");
   return rc ? rc : ok();
 }
@@ -158,7 +163,8 @@ int vggt3_block_join_grad(const void* r, const void* f, const void* gate, int64_
       return fail(VGGT3_EWORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : (size_t)0, l.total);
   }
   const size_t tb = (size_t)n_tokens * channels * elem_size(dtype);
-  const size_t gb = gate ? (size_t)gate_rows(n_tokens, gate_tokens) * channels * elem_size(dtype) : 0;
+  const int64_t per = tokens_per_gate(gate, gate_tokens, n_tokens);
+  const size_t gb = gate ? (size_t)gate_rows(n_tokens, per) * channels * elem_size(dtype) : 0;
   const Region rs[] = {{"r", r, tb, false},           {"f", f, tb, false},
                        {"gate", gate, gb, false},     {"scale", scale, vb, false},
                        {"post_w", post_w, vb, false}, {"post_b", post_b, vb, false},
@@ -176,7 +182,7 @@ int vggt3_block_join_grad(const void* r, const void* f, const void* gate, int64_
   a.dr = dr; a.dy = dy; a.dx = dx; a.df = df; a.dgate = dgate;
   a.part = static_cast<float*>(workspace);
   a.edge = reinterpret_cast<float*>(static_cast<char*>(workspace) + l.edge);
-  a.n = n_tokens; a.per = gate ? gate_tokens : 1; a.C = channels; a.post = post; a.pre = pre; a.eps = eps;
+  a.n = n_tokens; a.per = per; a.C = channels; a.post = post; a.pre = pre; a.eps = eps;
   rc = check_hip(join::launch_grad(a, p, outs, dtype == VGGT3_BF16, s), "block join gradient launch");
   return rc ? rc : ok();
 }

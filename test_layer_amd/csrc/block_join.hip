@@ -757,10 +757,10 @@ GradPlan grad_plan(int64_t n, int C, bool bf16) {
   // kernels of up to 168 registers, 8 of the others.
   const int64_t waves = bf16 && row_mode(C, bf16) != SCALAR && T >= 64 && T <= 256 ? 12 : 8;
   const int64_t most = 256 * waves * 64 / T;
-  // Few rows: up to 4 a unit, for a unit's start costs as much as three rows and
-  // its sums as many bytes as one (1374 x 1024 fp32: 25, 23, 22, 24, 27 us for 1, 2,
-  // 3, 4, 6 rows a unit; bf16: 55, 35, 31, 31, 32).
-  const int64_t least = (n + 255) / 256 < 4 ? (n + 255) / 256 : 4;
+  // Few rows: up to 3 a unit, for a unit's start costs as much as a row or two and
+  // its sums as many bytes as one (1374 x 1024: 19.8, 19.7, 20.4, 22.3 us for 1, 2, 3, 4
+  // rows a unit in fp32, and 41, 32, 28, 28 in bf16 with one gate for all).
+  const int64_t least = (n + 255) / 256 < 3 ? (n + 255) / 256 : 3;
   GradPlan p;
   p.rows_per_unit = (n + most - 1) / most;
   if (p.rows_per_unit < least) p.rows_per_unit = least;

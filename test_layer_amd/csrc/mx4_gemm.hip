@@ -376,7 +376,9 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2)
       // 32 units: one block of H per row. Codes and scales are gathered in LDS.
       constexpr int HB = BN / 4;  // bytes of codes per row of this tile
       static_assert(EPI != EPI_SWIGLU || BN == 256, "a tile is 128 units: one scale tile wide");
-      // (In the place of the step just done: free from there to the next barrier.)
+      // In the place of the step just done, which takes no loads before the next
+      // round's barrier; behind this one every wave has its reads of it.
+      lds_barrier();
       static_assert(BM * (HB + 4) <= STAGE, "staging");
       lu8* const hc = lds + (ring == 0 ? RING - 1 : ring - 1) * STAGE;  // [BM][HB]
       lu8* const hs = hc + BM * HB;                                    // [BM / 64][64][4], the scale tiles
@@ -448,6 +450,7 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2)
     // A tile over the edge makes fewer stores than the waits above allow for.
     if (!inside) wait_loads<0>();
   }
+  wait_loads<0>();  // the copies beyond the end still go to this workgroup's LDS
 }
 
 // Products with few tiles: a tile of 16 TN x 16 TM per workgroup, its KW waves

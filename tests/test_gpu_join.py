@@ -179,10 +179,11 @@ def _magnitudes(c):
     h = _norm_mag(f, c["post"], pw, pb)
     g, s = np.abs(join.spread(gate, c["per"], n)), 1.0 if scale is None else np.abs(scale)
     out["dscale"] = (d * g * h).sum(0)
-    groups = -(-n // c["per"])
-    p = np.zeros((groups * c["per"], C))
+    per = min(c["per"], n)
+    groups = -(-n // per)
+    p = np.zeros((groups * per, C))
     p[:n] = d * s * h
-    out["dgate"] = p.reshape(groups, c["per"], C).sum(1)
+    out["dgate"] = p.reshape(groups, per, C).sum(1)
     dh = d * g * s
     out["dpost_w"], out["dpost_b"] = (dh * hat_mag(f, c["post"])).sum(0), dh.sum(0)
     out["df"] = back_mag(dh * (1.0 if pw is None else np.abs(pw)), f, c["post"])
@@ -214,10 +215,12 @@ def test_grad(n, C, mode, dtype):
     _check_grad(_case(n, C, dtype, post, pre, gate, per, scale, bias, n + C), dtype)
 
 
-@pytest.mark.parametrize("per", [1, 2, 3, 50, 137, 1374, 2999, 3000, 10 ** 6])
+@pytest.mark.parametrize("per", [1, 2, 3, 50, 137, 1374, 2999, 3000, 10 ** 6, 2 ** 32, 2 ** 63 - 1])
 def test_gate_groups_across_units(per):
     # groups inside a unit's rows, ending with them, spanning two and many, and one longer than the tokens
-    _check_grad(_case(3000, 40, "f32", "rms", "layer", True, per, True, True, per), "f32")
+    c = _case(3000, 40, "f32", "rms", "layer", True, per, True, True, per % 1000)
+    _check_forward(c, "f32")
+    _check_grad(c, "f32")
 
 
 def test_grad_at_more_rows_than_one_a_unit():

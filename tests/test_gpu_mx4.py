@@ -122,6 +122,33 @@ def test_matmul(m, n, k, out):
     _check_product(tla.mx4_matmul(a, w, DT[out]), _vals(a), _vals(w), out)
 
 
+def _check_product_on_gpu(m, n, k, out):
+    """A product too large for numpy: float64 on the GPU, on the values the operands stand for."""
+    g = torch.Generator("cuda").manual_seed(k)
+    a = tla.mx4_quantize(torch.randn(m, k, generator=g, device="cuda") * torch.randn(m, 1, generator=g, device="cuda"))
+    w = tla.mx4_quantize(torch.randn(n, k, generator=g, device="cuda"))
+    c = tla.mx4_matmul(a, w, DT[out])
+    av, wv = tla.mx4_dequantize(a, torch.float32).double(), tla.mx4_dequantize(w, torch.float32).double()
+    kp = -(-k // 128) * 128
+    for r in range(0, m, 8192):
+        want = av[r:r + 8192] @ wv.t()
+        tol = kp * 2.0 ** -24 * (av[r:r + 8192].abs() @ wv.abs().t()) + (2.0 ** -8 if out == "bf16" else 2.0 ** -24) * want.abs()
+        assert bool(((c[r:r + 8192].double() - want).abs() <= tol).all()), r
+
+
+# each kernel with more tiles than workgroups, ragged edges, and from one step of 128 columns on
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [40, 256, 384, 500, 640, 1100])
+@pytest.mark.parametrize("m,n", [(9001, 2500), (9000, 2501), (68701, 4096), (70000, 4001)])
+def test_matmul_of_many_tiles(m, n, k, out):
+    _check_product_on_gpu(m, n, k, out)
+
+
+@pytest.mark.parametrize("m,n,k", [(11000, 1024, 4096), (22001, 1000, 2100), (300, 60000, 256), (5, 70000, 300)])
+def test_matmul_of_long_sides(m, n, k):
+    _check_product_on_gpu(m, n, k, "bf16")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 1024, 1024), (3, 100, 1000), (8, 64, 8192), (16, 999, 1000), (17, 64, 256),
                                    (200, 300, 333)])
@@ -199,6 +226,17 @@ def test_read_frozen(frozen, n):
     assert np.linalg.norm(o - want) <= 2.0 ** -8 * np.linalg.norm(want)
     # tokens in 4 bits already give the same bits
     assert torch.equal(tla.ttt_read_mx4(tla.mx4_quantize(q), f).cpu(), torch.tensor(o).to(torch.bfloat16))
+
+
+def test_read_of_many_tokens_agrees_with_that_of_a_few(frozen):
+    # other kernels, the same numbers up to the order of fp32 sums (and an H value here and there that this moves
+    # over a rounding border): far below the half step of bf16 that both are rounded by
+    _, f = frozen
+    q = torch.randn(9003, 1024, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    o = tla.ttt_read_mx4(q, f)
+    for r in (0, 250, 4096, 8987):
+        few = to64(tla.ttt_read_mx4(q[r:r + 16], f))
+        assert np.linalg.norm(to64(o[r:r + 16]) - few) <= 2.0 ** -9 * np.linalg.norm(few), r
 
 
 def test_read_chunks_agree_with_their_parts(frozen):

@@ -118,5 +118,7 @@ def test_binding_refusals():
         tla.mx4_matmul(torch.zeros(4, 32), a)
     with pytest.raises(ValueError):
         tla.mx4_matmul(a, a, out=torch.zeros(4, 5))
+    with pytest.raises(TypeError, match="FrozenMx4"):
+        tla.ttt_read_mx4(x.bfloat16(), (a, a, a))
     with pytest.raises(ValueError):
         tla.mx4_quantize(x, out=a._replace(k=63))
