@@ -99,7 +99,7 @@ __device__ __forceinline__ uint32_t swiglu_codes(const f32x4 (&gate)[2], const f
 // A workgroup of WN x WM waves works through BN x BM tiles of C^T, TN x TM tiles of
 // 16x16 a wave, in steps of 128 columns (one MFMA deep). LDS holds a ring of RING
 // steps, each [BN + BM rows][64 bytes] of codes and the scale tiles of those rows,
-// filled by direct global-to-LDS loads RING - 1 steps ahead. The steps of all the
+// filled by direct global-to-LDS loads RING steps ahead. The steps of all the
 // workgroup's tiles are one stream: while a tile's last steps are worked on and its
 // results stored, the next tile's first steps are under way. (At k = 1024 a tile
 // has 8 steps, 3.6 us of MFMAs; as a workgroup of its own it would spend more than
@@ -139,16 +139,16 @@ __device__ __forceinline__ void to_lds4(const uint8_t* p, uint32_t lane_off, uin
   __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7fffffff, 0x00027000),
                                            (lvoid*)dst, 4, lane_off, off, 0, 0);
 }
-// Barrier for LDS alone: loads and stores under way stay so.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 __device__ __forceinline__ void swap_rows(uint32_t& a, uint32_t& b) {
   // odd 16-lane rows of a <-> even rows of b
   const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+  // upper 32 lanes of a <-> lower 32 lanes of b
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
   a = r[0];
   b = r[1];
 }
@@ -164,8 +164,8 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2)
   static_assert(DN * NW * 16 == BN && DM * NW * 16 == BM, "whole loads");
   constexpr int LOADS = DN + DM + DS;
   // Stores (at least) a wave makes of a tile that lies inside C.
-  constexpr int STORES = EPI == EPI_SWIGLU ? BM * (BN / 4) / 16 / (64 * NW) : to_bf16(EPI) ? TN * TM / 2 : TN * TM;
-  static_assert(RING >= 3 && (RING - 3) * LOADS + STORES < 64, "vmcnt");
+  constexpr int STORES = EPI == EPI_SWIGLU ? 2 * SN : to_bf16(EPI) ? TN * TM / 2 : TN * TM;
+  static_assert(RING >= 2 && (RING - 2) * LOADS + STORES < 64, "vmcnt");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   lu8* const lds = (lu8*)smem;
 
@@ -319,7 +319,7 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2)
 
   aim(tile);
   issue(0, lds);
-  for (int i = 1; i < RING - 1; ++i) {
+  for (int i = 1; i < RING; ++i) {
     load_on();
     issue(at_step, lds + i * STAGE);
   }
@@ -335,27 +335,28 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2)
   for (;; tile += stride) {
     // Work on the present step, in registers, and read the next one, each part as
     // the registers of its predecessor fall free. The next step's loads are waited
-    // for; those of RING - 3 later steps may be under way and, in the first RING - 2
+    // for; those of RING - 2 later steps may be under way and, in the first RING - 1
     // rounds, whose loads were issued ahead of them (or are done), the stores of the
-    // tile before. The reads of the step before this one have been used, so behind
-    // the barrier its place takes the step RING - 1 ahead. The scheduling fences keep
-    // the reads ahead of the MFMAs that hide them.
-    // The questions come first: between the reads and the MFMAs on one side and
-    // the end of the round on the other there is no branch for them to cross.
+    // tile before. The reads of this step are waited for too, so behind the barrier
+    // every wave has them and their place takes the step RING ahead (68,700 rows
+    // through a frozen read: 531 us; 543 with the reads' wait behind the barrier and
+    // the loads one step less ahead). The scheduling fences keep the reads ahead of the
+    // MFMAs that hide them. The questions come first: between the reads and the MFMAs
+    // on one side and the end of the round on the other there is no branch for them to
+    // cross.
     for (int s = 0; s < steps; ++s) {
       load_on();
-      if (s < RING - 2)
-        wait_loads<(RING - 3) * LOADS + STORES>();
+      if (s < RING - 1)
+        wait_loads<(RING - 2) * LOADS + STORES>();
       else
-        wait_loads<(RING - 3) * LOADS>();
+        wait_loads<(RING - 2) * LOADS>();
+      // (The compiler takes the loads to LDS for LDS accesses of this wave's and would
+      // wait for all reads at the first use of one; with this wait there is none.)
+      wait_lds();
       __builtin_amdgcn_s_barrier();
-      issue(at_step, lds + (ring == 0 ? RING - 1 : ring - 1) * STAGE);
+      issue(at_step, lds + ring * STAGE);
       ring = ring + 1 == RING ? 0 : ring + 1;
       const lu8* const stage = lds + ring * STAGE;
-      // (The compiler takes the loads to LDS for LDS accesses of this wave's and would
-      // wait for all reads at the first use of one; so the wait is here, where the
-      // last reads were asked for a barrier ago, and none follows.)
-      wait_lds();
       fetch_cols(next, stage);
       __builtin_amdgcn_sched_barrier(0);
       unrolled(std::make_integer_sequence<int, TN>{}, [&](auto I) INLINE {
@@ -372,42 +373,34 @@ __global__ __launch_bounds__(64 * WN * WM) __attribute__((amdgpu_waves_per_eu(2)
     place(tile, n0, m0);
     const bool inside = m0 + BM <= g.m && n0 + CN <= g.n;
     if constexpr (EPI == EPI_SWIGLU) {
-      // Each wave holds gate (tiles 0, 1 of four) and up (tiles 2, 3) of the same
-      // 32 units: one block of H per row. Codes and scales are gathered in LDS.
-      constexpr int HB = BN / 4;  // bytes of codes per row of this tile
-      static_assert(EPI != EPI_SWIGLU || BN == 256, "a tile is 128 units: one scale tile wide");
-      // In the place of the step just done, which takes no loads before the next
-      // round's barrier; behind this one every wave has its reads of it.
-      lds_barrier();
-      static_assert(BM * (HB + 4) <= STAGE, "staging");
-      lu8* const hc = lds + (ring == 0 ? RING - 1 : ring - 1) * STAGE;  // [BM][HB]
-      lu8* const hs = hc + BM * HB;                                    // [BM / 64][64][4], the scale tiles
+      // Each wave holds gate (tiles 0, 1 of four) and up (tiles 2, 3) of the same 32
+      // units: one block of H per row, whose 16 bytes of codes lie in 4 lanes, 4 each.
+      // A transposition over 4 row tiles and the 4 16-lane rows brings a block
+      // together: lane 16 j + r gets that of row 16 j + r, to store in one piece.
+      static_assert(EPI != EPI_SWIGLU || (TM == 4 && BN == 256), "64 rows a wave, 128 units a tile");
+      const int hnb = g.n / 128;  // scale tiles across H
+      const int64_t row0 = m0 + wm * 64;
 #pragma unroll
-      for (int j = 0; j < TM; ++j)
+      for (int q = 0; q < SN; ++q) {
+        const int blk = wn * SN + q;  // of the tile's four
+        uint32_t d[4], word = 0;
 #pragma unroll
-        for (int q = 0; q < SN; ++q) {
-          const int row = (wm * TM + j) * 16 + i16, blk = wn * SN + q;
+        for (int j = 0; j < 4; ++j) {
           const f32x4 gate[2] = {acc[4 * q][j], acc[4 * q + 1][j]}, upv[2] = {acc[4 * q + 2][j], acc[4 * q + 3][j]};
           uint32_t sc;
-          const uint32_t code = swiglu_codes(gate, upv, sc);
-          if (m0 + row >= g.m) sc = 0;
-          lu8* const d = hc + row * HB + blk * 16 + 2 * g4;
-          *(lu16*)d = (uint16_t)code;
-          *(lu16*)(d + 8) = (uint16_t)(code >> 16);
-          if (g4 == 0) hs[(row >> 6) * 256 + (blk * 16 + i16) * 4 + ((row >> 4) & 3)] = (uint8_t)sc;
+          d[j] = swiglu_codes(gate, upv, sc);
+          if (row0 + 16 * j + i16 < g.m) word |= sc << (8 * j);
         }
-      lds_barrier();
-      const int hnb = g.n / 128;  // scale tiles across H
-      for (int p = threadIdx.x; p < BM * HB / 16; p += 64 * NW) {
-        const int row = p / (HB / 16), c = p % (HB / 16);
-        if (m0 + row < g.m)
-          *(i32x4*)((uint8_t*)g.out + (m0 + row) * (int64_t)(hnb * 64) + n0 / 2 + 16 * c) =
-              *(const li32x4*)(hc + row * HB + 16 * c);
-      }
-      const int64_t mrt = row_tiles(g.m);
-      for (int p = threadIdx.x; p < BM; p += 64 * NW) {
-        const int64_t rt = (m0 >> 6) + (p >> 6);
-        if (rt < mrt) ((uint32_t*)g.h_scales)[(rt * hnb + n0 / 128) * 64 + (p & 63)] = *(const lu32*)(hs + p * 4);
+        swap_halves(d[0], d[2]);
+        swap_halves(d[1], d[3]);
+        swap_rows(d[0], d[1]);
+        swap_rows(d[2], d[3]);
+        const u32x4 codes = {(d[0] & 0xffffu) | d[1] << 16, (d[2] & 0xffffu) | d[3] << 16,
+                             d[0] >> 16 | (d[1] & 0xffff0000u), d[2] >> 16 | (d[3] & 0xffff0000u)};
+        const int64_t row = row0 + lane;
+        if (row < g.m) st16((uint8_t*)g.out + row * (int64_t)(hnb * 64) + n0 / 2 + 16 * blk, codes);
+        if (g4 == 0 && row0 < g.m)
+          ((uint32_t*)g.h_scales)[((row0 >> 6) * hnb + n0 / 128) * 64 + 16 * blk + i16] = word;
       }
     } else {
       const int64_t row0 = m0 + wm * TM * 16 + i16, col0 = n0 + wn * TN * 16;
