@@ -165,6 +165,27 @@ __device__ __forceinline__ float rounded(float v) {
   return BF16 ? bf16_bits_to_f32(f32_to_bf16_bits(v)) : v;
 }
 
+// Largest of N = 4, 8 or 32 neighbouring lanes, the same in each.
+template <int N>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  static_assert(N == 4 || N == 8 || N == 32, "parts of DPP rows, or two rows");
+#define VGGT3_DPP(ctrl)                                                                      \
+  {                                                                                          \
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xf, 0xf, false); \
+    v = o > v ? o : v;                                                                       \
+  }
+  VGGT3_DPP(0xb1)                         // quad_perm 1,0,3,2
+  VGGT3_DPP(0x4e)                         // quad_perm 2,3,0,1
+  if constexpr (N >= 8) VGGT3_DPP(0x141)  // row_half_mirror
+  if constexpr (N == 32) {
+    VGGT3_DPP(0x140)  // row_mirror
+    const uint32_t o = __shfl_xor(v, 16, 64);
+    v = o > v ? o : v;
+  }
+#undef VGGT3_DPP
+  return v;
+}
+
 #define VGGT3_DPP(v, ctrl, rows) \
   __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, false))
 // Sum over T = 16, 32 or 64 neighbouring lanes, the same in each, by DPP (no LDS
@@ -229,7 +250,6 @@ __device__ __forceinline__ int unit_of_thread() {
   return T >= 64 ? __builtin_amdgcn_readfirstlane(u) : u;
 }
 
-
 // Centre v for a layer norm and return 1/sqrt(mean square + eps); past C, v stays 0.
 template <class R, int T, int E>
 __device__ __forceinline__ float center(float (&v)[E], int kind, int C, float inv_c, float eps, float* red, int tid) {
@@ -265,18 +285,13 @@ __device__ __forceinline__ void store_mx4(const float (&y)[E], int64_t row, int 
       const uint32_t a = __float_as_uint(value(c, j)) & 0x7fffffffu;
       amax = a > amax ? a : amax;
     }
-#pragma unroll
-    for (int off = 1; off < 32 / R::VL; off <<= 1) {
-      const uint32_t o = __shfl_xor(amax, off, 64);
-      amax = o > amax ? o : amax;
-    }
-    const uint32_t s = mx4::scale_byte(amax);
+    const uint32_t s = mx4::scale_byte(lanes_max<32 / R::VL>(amax));
     const int k = R::col(c, tid);
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = j < R::VL ? value(c, j < R::VL ? j : 0) : 0.0f;
     uint32_t q = s == 255u ? 0u : mx4::encode8(v, mx4::scale_value(s));
-    if constexpr (R::VL == 1) q |= (uint32_t)__shfl_xor((int)q, 1, 64) << 4;
+    if constexpr (R::VL == 1) q |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)q, 0xb1, 0xf, 0xf, false) << 4;
     if (k >= nb * 128) continue;
     uint8_t* p = codes + row * (int64_t)(nb * 64) + k / 2;
     if constexpr (R::VL == 8)
@@ -651,8 +666,12 @@ __global__ __launch_bounds__(1024) void sum_parts_kernel(Args a, int64_t blocks,
 // Gate groups that several units share, each by the unit that it starts in.
 template <bool BF16, bool BY_UNIT>
 __global__ __launch_bounds__(BY_UNIT ? 256 : 1024) void sum_edges_kernel(Args a) {
-  // One workgroup per group or, where units are fewer (BY_UNIT: so that a group has
-  // few of them), per unit for its last group.
+  // One workgroup per group, its units shared out to 16 runs, or (BY_UNIT), where a
+  // group has fewer units than that, one per unit for its last group. (1024 bf16
+  // channels, the whole gradient in us, by group and by unit: 65,952 tokens in groups
+  // of 2: 1004, 231; of 30: 289, 214; of 100, 2.3 units: 224, 201; of 1374, 32 units:
+  // 202, 206. 1374 tokens in groups of 5: 36, 27; of 30, 10 units: 27, 27; of 100: 26, 29;
+  // of 1374: 28, 71.)
   int64_t group = blockIdx.x;
   if (BY_UNIT) {
     const int64_t t1 = (group + 1) * a.rows_per_unit;
@@ -684,8 +703,12 @@ Mode row_mode(int C, bool bf16) {
   return C >= 128 && (C & (C - 1)) == 0 ? FULL : C % (bf16 ? 8 : 4) == 0 ? PIECES : SCALAR;
 }
 
-
-// Threads per row for C channels: forward, gradient.
+// Threads per row for C channels: forward, gradient. Rows of up to 256 channels
+// share a wave: a unit's reductions take as long for few channels as for many (a
+// wave a row against this, 65,952 bf16 rows: forward 34 and 14 us at 128 channels, 38
+// and 25 at 256; gradient 74 and 37, 75 and 54). The gradient has 8 values a thread for
+// the registers of its sums (1024 channels as 16 values x 64 threads: 293 us, 245 as
+// 8 x 128).
 int unit_threads(int C, bool narrow) {
   return narrow && C <= 256 ? 16 : C <= 1024 ? 64 : C <= 2048 ? 128 : C <= 4096 ? 256 : 512;
 }
@@ -787,7 +810,7 @@ hipError_t launch_grad(const Args& args, const GradPlan& p, float* const* out, b
   if (e != hipSuccess) return e;
   if (a.n > 0 && a.dgate && a.per > 1) {
     const int64_t groups = (a.n + a.per - 1) / a.per;
-    const bool by_unit = groups > p.units;
+    const bool by_unit = 16 * groups > p.units;
     const dim3 grid((unsigned)(by_unit ? p.units : groups), (a.C + (by_unit ? 255 : 63)) / (by_unit ? 256 : 64));
     if (by_unit) {
       if (bf16) sum_edges_kernel<true, true><<<grid, dim3(256), 0, stream>>>(a);
