@@ -474,7 +474,7 @@ int vggt3_ttt_read_streamed_ex(const void* Q_host, const float* theta, void* O_h
  *           the block is NaN), in tiles [ceil(rows/64)][kp/128][64][4]: the byte
  *           of row 64 R + 16 i + r and block 4 B + g is [R][B][16 g + r][i].
  * Columns k .. kp-1 hold code 0. Every byte of both arrays is written. At most
- * 2^20 columns. The sizes are vggt3_mx4_codes_bytes / vggt3_mx4_scales_bytes
+ * 2^20 columns and fewer than 2^24 scale tiles (2^30 rows of up to 128 columns). The sizes are vggt3_mx4_codes_bytes / vggt3_mx4_scales_bytes
  * (0 for a shape that is refused).
  */
 enum { VGGT3_MX4 = 2 }; /* as an operand type: 4-bit codes with their scales */

@@ -12,7 +12,10 @@ namespace mx4 = vggt3::mx4;
 namespace {
 
 constexpr int64_t kMaxCols = (int64_t)1 << 20;   // columns of a 4-bit matrix
-constexpr int64_t kMaxBlocks = (int64_t)1 << 31;  // workgroups of one launch
+// Scale tiles of a matrix: the quantiser's workgroups of 256 threads, of which a
+// launch may have fewer than 2^32 in all.
+constexpr int64_t kMaxTiles = (int64_t)1 << 24;
+constexpr int64_t kMaxProductTiles = (int64_t)1 << 31;  // 16 x 16, of C
 
 struct Region {
   const char* name;
@@ -39,7 +42,7 @@ int check_matrix(const char* what, int64_t rows, int64_t k) {
   if (k < 1) return fail(VGGT3_EINVAL, "%s has %lld columns", what, (long long)k);
   if (k > kMaxCols) return fail(VGGT3_EUNSUPPORTED, "%s has %lld columns, at most %lld", what, (long long)k,
                                 (long long)kMaxCols);
-  if (rows > (int64_t)1 << 40 || mx4::row_tiles(rows) * (mx4::padded_k(k) / mx4::kPad) >= kMaxBlocks)
+  if (rows > (int64_t)1 << 40 || mx4::row_tiles(rows) * (mx4::padded_k(k) / mx4::kPad) >= kMaxTiles)
     return fail(VGGT3_EUNSUPPORTED, "%s is too large (%lld x %lld)", what, (long long)rows, (long long)k);
   return VGGT3_OK;
 }
@@ -73,7 +76,7 @@ int check_matmul_shape(int64_t m, int64_t n, int64_t k, int32_t a_type) {
   if (rc) return rc;
   if (n < 1) return fail(VGGT3_EINVAL, "n = %lld < 1", (long long)n);
   if (n > kMaxCols) return fail(VGGT3_EUNSUPPORTED, "n = %lld, at most %lld", (long long)n, (long long)kMaxCols);
-  if (((m + 15) / 16) * ((n + 15) / 16) >= kMaxBlocks) return fail(VGGT3_EUNSUPPORTED, "m x n is too large");
+  if (((m + 15) / 16) * ((n + 15) / 16) >= kMaxProductTiles) return fail(VGGT3_EUNSUPPORTED, "m x n is too large");
   return VGGT3_OK;
 }
 

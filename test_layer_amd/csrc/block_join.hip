@@ -279,6 +279,7 @@ __device__ __forceinline__ void store_mx4(const float (&y)[E], int64_t row, int 
   auto value = [&](int c, int j) { return R::inside(R::col(c, tid) + j, C) ? y[c * R::VL + j] : 0.0f; };
 #pragma unroll
   for (int c = 0; c < R::NC; ++c) {
+    if (R::VL == 1 && R::col(c, 0) >= nb * 128) continue;
     uint32_t amax = 0;
 #pragma unroll
     for (int j = 0; j < R::VL; ++j) {
@@ -287,11 +288,18 @@ __device__ __forceinline__ void store_mx4(const float (&y)[E], int64_t row, int 
     }
     const uint32_t s = mx4::scale_byte(lanes_max<32 / R::VL>(amax));
     const int k = R::col(c, tid);
-    float v[8];
+    uint32_t q = 0;
+    if constexpr (R::VL == 1) {  // two lanes' values a byte
+      const float v = value(c, 0);
+      const float o = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xb1, 0xf, 0xf, false));
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v, o, mx4::scale_value(s), 0);
+      if (s == 255u) q = 0;
+    } else {
+      float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < R::VL ? value(c, j < R::VL ? j : 0) : 0.0f;
-    uint32_t q = s == 255u ? 0u : mx4::encode8(v, mx4::scale_value(s));
-    if constexpr (R::VL == 1) q |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)q, 0xb1, 0xf, 0xf, false) << 4;
+      for (int j = 0; j < 8; ++j) v[j] = j < R::VL ? value(c, j < R::VL ? j : 0) : 0.0f;
+      q = s == 255u ? 0u : mx4::encode8(v, mx4::scale_value(s));
+    }
     if (k >= nb * 128) continue;
     uint8_t* p = codes + row * (int64_t)(nb * 64) + k / 2;
     if constexpr (R::VL == 8)

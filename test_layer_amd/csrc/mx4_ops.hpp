@@ -32,36 +32,77 @@ __device__ __forceinline__ uint32_t encode8(const float* v, float scale) {
   return o;
 }
 
-// The 32 values of a row [k] from column k0 on, 0 past k. VEC: 16-byte loads
-// (rows start at 16-byte boundaries, k is a whole number of them).
+template <bool BF16>
+__device__ __forceinline__ float load1(const void* X, int64_t i) {
+  if (BF16) return bf16_bits_to_f32(((const uint16_t*)X)[i]);
+  return ((const float*)X)[i];
+}
+
+// The 8 values of a row [k] from column k0 on, 0 past k. VEC: 16-byte loads (rows
+// start at 16-byte boundaries, k is a whole number of them).
 template <bool BF16, bool VEC>
-__device__ __forceinline__ void load_block(const void* X, int64_t row, int k0, int k, float (&v)[32]) {
+__device__ __forceinline__ void load8(const void* X, int64_t row, int k0, int k, float (&v)[8]) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-  if constexpr (VEC) {
-    constexpr int E = BF16 ? 8 : 4;
-    const char* p = (const char*)X + (row * (int64_t)k + k0) * (BF16 ? 2 : 4);
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  if constexpr (VEC && BF16) {
+    if (k0 >= k) return;
+    const u32x4 q = ld16((const uint16_t*)X + row * k + k0);
 #pragma unroll
-    for (int c = 0; c < 32 / E; ++c) {
-      if (k0 + c * E >= k) continue;
-      const u32x4 q = ld16(p + 16 * c);
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo(q[j]);
+      v[2 * j + 1] = bf16_hi(q[j]);
+    }
+  } else if constexpr (VEC) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (k0 + 4 * h >= k) continue;
+      const f32x4 q = *(const f32x4*)((const float*)X + row * k + k0 + 4 * h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * h + j] = q[j];
+    }
+  } else if (k0 + 8 <= k) {
+    if constexpr (BF16) {
+      const u32x4 q = ld16_any((const uint16_t*)X + row * k + k0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (BF16) {
-          v[c * E + 2 * j] = bf16_lo(q[j]);
-          v[c * E + 2 * j + 1] = bf16_hi(q[j]);
-        } else {
-          v[c * E + j] = __uint_as_float(q[j]);
-        }
+        v[2 * j] = bf16_lo(q[j]);
+        v[2 * j + 1] = bf16_hi(q[j]);
+      }
+    } else {
+      const float* p = (const float*)X + row * k + k0;
+      const f32x4 a = *(const f32x4_any*)p, b = *(const f32x4_any*)(p + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = a[j];
+        v[4 + j] = b[j];
       }
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int64_t i = row * (int64_t)k + k0 + j;
-      if (k0 + j < k) v[j] = BF16 ? bf16_bits_to_f32(((const uint16_t*)X)[i]) : ((const float*)X)[i];
-    }
+    for (int j = 0; j < 8; ++j)
+      if (k0 + j < k) v[j] = load1<BF16>(X, row * (int64_t)k + k0 + j);
   }
+}
+
+// Largest of 4 neighbouring lanes, by DPP.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, false);  // lane ^ 1
+  v = o > v ? o : v;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, false);  // lane ^ 2
+  return o > v ? o : v;
+}
+
+// A quarter of a block, its other 24 values in the 3 neighbours of a group of 4
+// lanes: the block's scale byte and the lane's codes.
+__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t& s) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t a = __float_as_uint(v[j]) & 0x7fffffffu;
+    amax = a > amax ? a : amax;
+  }
+  s = scale_byte(quad_max(amax));
+  return s == 255u ? 0u : encode8(v, scale_value(s));
 }
 
 // A block's scale byte and its 32 codes.

@@ -13,12 +13,6 @@ namespace {
 
 constexpr int NTHR = 256;
 
-template <bool BF16>
-__device__ __forceinline__ float load1(const void* X, int64_t i) {
-  if (BF16) return bf16_bits_to_f32(((const uint16_t*)X)[i]);
-  return ((const float*)X)[i];
-}
-
 // Both directions are bound by memory; a workgroup takes 64 rows x 128 columns, one
 // scale tile. Row-major: thread t has 8 columns (16 neighbouring threads a row: 256
 // or 512 consecutive bytes) of the rows t / 16 + 16 i, i = 0..3, so that the 4 scale
@@ -26,58 +20,6 @@ __device__ __forceinline__ float load1(const void* X, int64_t i) {
 // block is 4 neighbouring lanes. (One thread per block of 32 needs no exchange
 // between lanes, but its loads step 64 bytes from lane to lane: 137,400 x 1024 bf16
 // took 90 us that way.)
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void load8(const void* X, int64_t row, int k0, int k, float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-  if constexpr (VEC && BF16) {
-    if (k0 >= k) return;
-    const u32x4 q = ld16((const uint16_t*)X + row * k + k0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = bf16_lo(q[j]);
-      v[2 * j + 1] = bf16_hi(q[j]);
-    }
-  } else if constexpr (VEC) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (k0 + 4 * h >= k) continue;
-      const f32x4 q = *(const f32x4*)((const float*)X + row * k + k0 + 4 * h);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[4 * h + j] = q[j];
-    }
-  } else if (k0 + 8 <= k) {
-    if constexpr (BF16) {
-      const u32x4 q = ld16_any((const uint16_t*)X + row * k + k0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = bf16_lo(q[j]);
-        v[2 * j + 1] = bf16_hi(q[j]);
-      }
-    } else {
-      const float* p = (const float*)X + row * k + k0;
-      const f32x4 a = *(const f32x4_any*)p, b = *(const f32x4_any*)(p + 4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = a[j];
-        v[4 + j] = b[j];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (k0 + j < k) v[j] = load1<BF16>(X, row * (int64_t)k + k0 + j);
-  }
-}
-
-// Largest of 4 neighbouring lanes, by DPP.
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, false);  // lane ^ 1
-  v = o > v ? o : v;
-  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, false);  // lane ^ 2
-  return o > v ? o : v;
-}
-
 template <bool BF16, bool VEC>
 __global__ __launch_bounds__(NTHR) void quantize_kernel(const void* X, uint8_t* codes, uint8_t* scales, int64_t rows,
                                                         int k, int nb) {
@@ -94,18 +36,11 @@ __global__ __launch_bounds__(NTHR) void quantize_kernel(const void* X, uint8_t* 
   uint32_t word = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t amax = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t a = __float_as_uint(v[i][j]) & 0x7fffffffu;
-      amax = a > amax ? a : amax;
-    }
-    const uint32_t s = scale_byte(quad_max(amax));
+    uint32_t s;
+    const uint32_t q = quantize8(v[i], s);
     word |= s << (8 * i);
     const int64_t row = R * 64 + 16 * i + r;
-    if (row < rows)
-      ((uint32_t*)(codes + row * (int64_t)(nb * 64) + B * 64))[piece] =
-          s == 255u ? 0u : encode8(v[i], scale_value(s));
+    if (row < rows) ((uint32_t*)(codes + row * (int64_t)(nb * 64) + B * 64))[piece] = q;
   }
   if ((piece & 3) == 0) ((uint32_t*)scales)[(R * nb + B) * 64 + 16 * (piece >> 2) + r] = word;
 }

@@ -122,3 +122,15 @@ def test_binding_refusals():
         tla.ttt_read_mx4(x.bfloat16(), (a, a, a))
     with pytest.raises(ValueError):
         tla.mx4_quantize(x, out=a._replace(k=63))
+
+
+def test_matrices_of_more_tiles_than_a_launch_takes(lib):
+    # a launch has fewer than 2^32 threads in all: 2^24 workgroups of 256, one a scale tile of 64 x 128
+    most = ((1 << 24) - 1) * 64
+    assert lib.vggt3_mx4_scales_bytes(most, 1) == most * 4 and lib.vggt3_mx4_scales_bytes(most + 1, 1) == 0
+    two = ((1 << 23) - 1) * 64  # rows of two tiles
+    assert lib.vggt3_mx4_codes_bytes(two, 256) == two * 128 and lib.vggt3_mx4_codes_bytes(two + 1, 129) == 0
+    far = [ctypes.c_void_p(1 << 44), ctypes.c_void_p(1 << 45), ctypes.c_void_p(1 << 46)]
+    assert lib.vggt3_mx4_quantize(far[0], 0, far[1], far[2], most + 1, 1, tla.BF16, None) == tla.EUNSUPPORTED
+    assert lib.vggt3_mx4_dequantize(far[0], far[1], far[2], most + 1, 1, tla.BF16, None) == tla.EUNSUPPORTED
+    assert lib.vggt3_mx4_matmul_workspace_bytes(most + 1, 1, 1, tla.BF16) == 0
