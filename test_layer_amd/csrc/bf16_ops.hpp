@@ -18,8 +18,9 @@ typedef u32x2 __attribute__((aligned(2))) u32x2_any;
 typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 __device__ __forceinline__ u32x4 ld16_any(const void* p) { return *reinterpret_cast<const u32x4_any*>(p); }
 __device__ __forceinline__ void st16_any(void* p, const u32x4& v) { *reinterpret_cast<u32x4_any*>(p) = v; }
-// 16 bytes of a result; STREAM: past the caches' keeping, for results that they could not hold in any case (streams()). A stream of
-// such stores alone reaches 6.1 TB/s, where ordinary ones reach 5.1.
+// 16 bytes of a result; STREAM: past the caches' keeping, for results that they
+// could not hold in any case (streams()). A stream of such stores alone reaches
+// 6.1 TB/s, where ordinary ones reach 5.1.
 template <bool STREAM>
 __device__ __forceinline__ void st16(void* p, const u32x4& v) {
   if constexpr (STREAM)

@@ -623,7 +623,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //                   stores' time; it hides them from the third round on) and one and
 //                   a half at 4096 (1374 rows: 10.4, 14.5 and 13.6, 28.5; 2748: 13.8
 //                   and 15.7; 10,992: 45.1, 38.9 and 45.4, 35.4; 68,700: 259, 202 and
-//                   222, 175).
+//                   219, 170).
 template <int EPI>
 hipError_t product(const Args& g, hipStream_t stream) {
   if (g.m <= 16) return go_direct<1, 1, 8, EPI>(g, stream);
