@@ -165,10 +165,10 @@ __device__ __forceinline__ float rounded(float v) {
   return BF16 ? bf16_bits_to_f32(f32_to_bf16_bits(v)) : v;
 }
 
-// Largest of N = 4, 8 or 32 neighbouring lanes, the same in each.
+// Largest of N = 4, 8, 16 or 32 neighbouring lanes, the same in each.
 template <int N>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
-  static_assert(N == 4 || N == 8 || N == 32, "parts of DPP rows, or two rows");
+  static_assert(N == 4 || N == 8 || N == 16 || N == 32, "parts of a DPP row, one, or two");
 #define VGGT3_DPP(ctrl)                                                                      \
   {                                                                                          \
     const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xf, 0xf, false); \
@@ -177,8 +177,8 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   VGGT3_DPP(0xb1)                         // quad_perm 1,0,3,2
   VGGT3_DPP(0x4e)                         // quad_perm 2,3,0,1
   if constexpr (N >= 8) VGGT3_DPP(0x141)  // row_half_mirror
+  if constexpr (N >= 16) VGGT3_DPP(0x140)  // row_mirror
   if constexpr (N == 32) {
-    VGGT3_DPP(0x140)  // row_mirror
     const uint32_t o = __shfl_xor(v, 16, 64);
     v = o > v ? o : v;
   }
@@ -269,46 +269,53 @@ __device__ __forceinline__ float center(float (&v)[E], int kind, int C, float in
   return rsqrtf(q[0] * inv_c + eps);
 }
 
-// One row of y in 4 bits (values already rounded to the token type): blocks of
-// 32 columns lie in 32 / VL neighbouring threads.
+// One row of y in 4 bits (values already rounded to the token type): a block of 32
+// columns lies in 32 / VL neighbouring threads, or in G column chunks of a unit of
+// 16 threads with single values.
 template <class R, int T, int E>
 __device__ __forceinline__ void store_mx4(const float (&y)[E], int64_t row, int C, uint8_t* codes, uint8_t* scales,
                                           int tid) {
+  constexpr int G = 32 / R::VL > T ? 32 / R::VL / T : 1;
   const int nb = (C + 127) / 128;
   // past C the value is 0 whatever the row holds (a NaN row has NaN there too)
   auto value = [&](int c, int j) { return R::inside(R::col(c, tid) + j, C) ? y[c * R::VL + j] : 0.0f; };
 #pragma unroll
-  for (int c = 0; c < R::NC; ++c) {
-    if (R::VL == 1 && R::col(c, 0) >= nb * 128) continue;
+  for (int c0 = 0; c0 < R::NC; c0 += G) {
+    if (R::VL == 1 && R::col(c0, 0) >= nb * 128) continue;
     uint32_t amax = 0;
 #pragma unroll
-    for (int j = 0; j < R::VL; ++j) {
-      const uint32_t a = __float_as_uint(value(c, j)) & 0x7fffffffu;
-      amax = a > amax ? a : amax;
-    }
-    const uint32_t s = mx4::scale_byte(lanes_max<32 / R::VL>(amax));
-    const int k = R::col(c, tid);
-    uint32_t q = 0;
-    if constexpr (R::VL == 1) {  // two lanes' values a byte
-      const float v = value(c, 0);
-      const float o = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xb1, 0xf, 0xf, false));
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v, o, mx4::scale_value(s), 0);
-      if (s == 255u) q = 0;
-    } else {
-      float v[8];
+    for (int c = c0; c < c0 + G; ++c)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < R::VL ? value(c, j < R::VL ? j : 0) : 0.0f;
-      q = s == 255u ? 0u : mx4::encode8(v, mx4::scale_value(s));
+      for (int j = 0; j < R::VL; ++j) {
+        const uint32_t a = __float_as_uint(value(c, j)) & 0x7fffffffu;
+        amax = a > amax ? a : amax;
+      }
+    const uint32_t s = mx4::scale_byte(lanes_max<32 / R::VL / G>(amax));
+#pragma unroll
+    for (int c = c0; c < c0 + G; ++c) {
+      const int k = R::col(c, tid);
+      uint32_t q = 0;
+      if constexpr (R::VL == 1) {  // two lanes' values a byte
+        const float v = value(c, 0);
+        const float o = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xb1, 0xf, 0xf, false));
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v, o, mx4::scale_value(s), 0);
+        if (s == 255u) q = 0;
+      } else {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < R::VL ? value(c, j < R::VL ? j : 0) : 0.0f;
+        q = s == 255u ? 0u : mx4::encode8(v, mx4::scale_value(s));
+      }
+      if (k >= nb * 128) continue;
+      uint8_t* p = codes + row * (int64_t)(nb * 64) + k / 2;
+      if constexpr (R::VL == 8)
+        *(uint32_t*)p = q;
+      else if constexpr (R::VL == 4)
+        *(uint16_t*)p = (uint16_t)q;
+      else if ((tid & 1) == 0)
+        *p = (uint8_t)q;
+      if ((k & 31) == 0) scales[mx4::scale_at(row, k >> 5, nb)] = (uint8_t)s;
     }
-    if (k >= nb * 128) continue;
-    uint8_t* p = codes + row * (int64_t)(nb * 64) + k / 2;
-    if constexpr (R::VL == 8)
-      *(uint32_t*)p = q;
-    else if constexpr (R::VL == 4)
-      *(uint16_t*)p = (uint16_t)q;
-    else if ((tid & 1) == 0)
-      *p = (uint8_t)q;
-    if ((k & 31) == 0) scales[mx4::scale_at(row, k >> 5, nb)] = (uint8_t)s;
   }
 }
 
@@ -717,8 +724,8 @@ Mode row_mode(int C, bool bf16) {
 // and 25 at 256; gradient 74 and 37, 75 and 54). The gradient has 8 values a thread for
 // the registers of its sums (1024 channels as 16 values x 64 threads: 293 us, 245 as
 // 8 x 128).
-int unit_threads(int C, bool narrow) {
-  return narrow && C <= 256 ? 16 : C <= 1024 ? 64 : C <= 2048 ? 128 : C <= 4096 ? 256 : 512;
+int unit_threads(int C) {
+  return C <= 256 ? 16 : C <= 1024 ? 64 : C <= 2048 ? 128 : C <= 4096 ? 256 : 512;
 }
 int grad_threads(int C) { return C <= 128 ? 16 : C <= 256 ? 32 : C <= 512 ? 64 : C <= 1024 ? 128 : C <= 2048 ? 256 : 512; }
 
@@ -745,8 +752,8 @@ constexpr size_t lds_bytes(int T, int E) {
 static_assert(lds_bytes(512, 16) + 2 * 8 * sizeof(float) <= 160 * 1024, "LDS of one workgroup");
 #define VGGT3_JOIN_FORWARD(B, V)                                                                                 \
   do {                                                                                                           \
-    if (narrow && a.C <= 128) VGGT3_JOIN_GO((join_kernel<B, V, 16, 8>), 16, 8);                                  \
-    else if (narrow && a.C <= 256) VGGT3_JOIN_GO((join_kernel<B, V, 16, 16>), 16, 16);                           \
+    if (a.C <= 128) VGGT3_JOIN_GO((join_kernel<B, V, 16, 8>), 16, 8);                                            \
+    else if (a.C <= 256) VGGT3_JOIN_GO((join_kernel<B, V, 16, 16>), 16, 16);                                     \
     else if (a.C <= 512) VGGT3_JOIN_GO((join_kernel<B, V, 64, 8>), 64, 8);                                       \
     else if (a.C <= 1024) VGGT3_JOIN_GO((join_kernel<B, V, 64, 16>), 64, 16);                                    \
     else if (a.C <= 2048) VGGT3_JOIN_GO((join_kernel<B, V, 128, 16>), 128, 16);                                  \
@@ -769,10 +776,7 @@ static_assert(lds_bytes(512, 16) + 2 * 8 * sizeof(float) <= 160 * 1024, "LDS of 
 hipError_t launch_forward(const Args& args, bool bf16, hipStream_t stream) {
   Args a = args;
   if (a.n == 0) return hipSuccess;
-  // Narrow rows, four to a wave. (In 4 bits with single values a thread a block
-  // of 32 needs 32 lanes.)
-  const bool narrow = !a.y_codes || row_mode(a.C, bf16) != SCALAR;
-  const int T = unit_threads(a.C, narrow), U = block_threads(T) / T;
+  const int T = unit_threads(a.C), U = block_threads(T) / T;
   const int64_t rows = a.y_codes ? mx4::row_tiles(a.n) * mx4::kTileRows : a.n;
   const int64_t most = 8192 * 64 / T;  // units
   a.rows_per_unit = (rows + most - 1) / most;

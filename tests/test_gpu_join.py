@@ -317,3 +317,29 @@ def test_block_on_frozen_weights_end_to_end():
     _check_forward(dict(c, f=o), "bf16", mx=True)
     yv, hv = to64(tla.mx4_dequantize(y, torch.float32)), to64(tla.mx4_dequantize(head, torch.float32))
     assert (np.abs(to64(z) - yv @ hv.T) <= 1024 * U * (np.abs(yv) @ np.abs(hv).T)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,C,per", [(1000, 300, 5), (1001, 130, 20), (1374, 1024, 30), (3000, 257, 40), (2999, 512, 47),
+                                     (2999, 512, 49)])
+def test_gate_groups_of_a_few_units(n, C, per, dtype):
+    # groups that 2 to 17 units share, the last one short
+    _check_grad(_case(n, C, dtype, "layer", "rms", True, per, True, True, per), dtype)
+
+
+@pytest.mark.parametrize("C", [1, 33, 99, 127, 129, 500, 999, 2050])
+def test_odd_rows_in_4_bits_on_two_streams_at_once(C):
+    # a row of odd width ends inside a unit's columns; two calls on streams of their own, outputs of their own
+    a, b = (_case(301, C, d, "rms", "layer", True, 7, True, True, C + i) for i, d in enumerate(("bf16", "f32")))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    torch.cuda.synchronize()
+    for c, s in zip((a, b), streams):
+        with torch.cuda.stream(s):
+            got.append(tla.block_join(c["x"], c["f"], pre_b=c["pre_b"], mx4=True, **_args(c)))
+    torch.cuda.synchronize()
+    for c, (r, y4) in zip((a, b), got):
+        r1, y1 = tla.block_join(c["x"], c["f"], pre_b=c["pre_b"], **_args(c))
+        assert torch.equal(r, r1)
+        want = tla.mx4_quantize(y1)
+        assert torch.equal(y4.codes, want.codes) and torch.equal(y4.scales, want.scales)
