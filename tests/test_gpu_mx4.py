@@ -288,3 +288,37 @@ def test_other_stream_and_graph_replay(m):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, tla.mx4_matmul(x, w))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(1, 40, 31), (2, 100, 37), (4, 64, 1001), (4, 4096, 4096), (7, 33, 129), (16, 70, 1024),
+                                   (1, 17, 16384), (1, 17, 16385), (15, 16, 999)])
+def test_tokens_quantised_in_the_product(m, n, k, dtype):
+    x, w = _x(m, k, k, dtype), tla.mx4_quantize(_w(n, k, n))
+    x[m - 1, k // 2] = float("inf")  # one block of the last row
+    c = tla.mx4_matmul(x, w, torch.float32)
+    want = tla.mx4_matmul(tla.mx4_quantize(x), w, torch.float32)
+    assert torch.isnan(c[m - 1]).all() and torch.isnan(want[m - 1]).all()
+    assert torch.equal(c[:m - 1], want[:m - 1])
+
+
+def test_two_products_at_once_and_two_captured_graphs():
+    w = tla.mx4_quantize(_w(1024, 1024, 2))
+    xs = [_x(3000, 1024, s, "bf16") for s in (1, 2)]
+    want = [tla.mx4_matmul(x, w) for x in xs]
+    outs, graphs = [torch.empty_like(c) for c in want], []
+    need = tla.mx4_matmul_workspace_bytes(3000, 1024, 1024, tla.BF16)
+    for x, out in zip(xs, outs):
+        g, ws = torch.cuda.CUDAGraph(), torch.empty(need, dtype=torch.uint8, device="cuda")
+        with torch.cuda.graph(g):
+            tla.mx4_matmul(x, w, out=out, workspace=ws)
+        graphs.append((g, ws))
+    for _ in range(3):
+        for out in outs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for g, _ in graphs:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, c) for o, c in zip(outs, want))
