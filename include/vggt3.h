@@ -565,7 +565,8 @@ int vggt3_ttt_read_mx4(const void* Q, const void* Q_scales, int32_t q_type, cons
  *               rounded to dtype and then quantised as by vggt3_mx4_quantize
  *               ([n_tokens][channels]), the operand of vggt3_mx4_matmul and
  *               vggt3_ttt_read_mx4.
- * All arithmetic is fp32; r and y are rounded once each. channels at most 8192,
+ * All arithmetic is fp32; r and y are rounded once each. (In 4 bits the last bit
+ * of an fp32 y at a boundary between two codes decides which it is.) channels at most 8192,
  * of any count (multiples of 16 bytes are faster). n_tokens == 0 is a no-op.
  */
 enum { VGGT3_NORM_NONE = 0, VGGT3_NORM_RMS = 1, VGGT3_NORM_LAYER = 2 };
