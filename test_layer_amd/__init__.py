@@ -697,14 +697,18 @@ def _norm_code(kind) -> int:
     return _NORMS[kind] if kind is None or isinstance(kind, str) else int(kind)
 
 
-def _check_gate(gate: Optional[torch.Tensor], gate_tokens: int, x: torch.Tensor) -> None:
+def _check_gate(gate: Optional[torch.Tensor], gate_tokens: int, x: torch.Tensor) -> int:
+    """Tokens that share a gate row, at most all of them (so that the count fits the C call's 64 bits)."""
     if gate is None:
-        return
-    if int(gate_tokens) < 1:
+        return 1
+    per = int(gate_tokens)
+    if per < 1:
         raise ValueError(f"gate_tokens = {gate_tokens} < 1")
-    want = (-(-x.shape[0] // int(gate_tokens)), x.shape[1])
+    n = x.shape[0]
+    want = (-(-n // per), x.shape[1])
     if tuple(gate.shape) != want or gate.dtype != x.dtype:
         raise ValueError(f"gate {tuple(gate.shape)} {gate.dtype}, {want} {x.dtype} expected")
+    return min(per, max(n, 1))
 
 
 def _check_channels(C: int, **params) -> None:
@@ -726,7 +730,7 @@ def block_join(x: torch.Tensor, f: Optional[torch.Tensor] = None, gate: Optional
     may be given as outputs; r may be x (in place)."""
     _check_tokens("x", x)
     _check_same("f", f, x, "x")
-    _check_gate(gate, gate_tokens, x)
+    per = _check_gate(gate, gate_tokens, x)
     n, C = x.shape
     _check_channels(C, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w, pre_b=pre_b)
     post, pre = _norm_code(post), _norm_code(pre)
@@ -752,7 +756,7 @@ def block_join(x: torch.Tensor, f: Optional[torch.Tensor] = None, gate: Optional
     plain = None if mx4 else y
     dev, (px, pf, pg, ps, *norms, pr, py, pc, psc) = _pointers(x, f, gate, scale, post_w, post_b, pre_w, pre_b, r,
                                                                plain, codes, scales)
-    _run("vggt3_block_join", dev, px, pf, pg, int(gate_tokens), ps, post, norms[0], norms[1], pre, norms[2], norms[3],
+    _run("vggt3_block_join", dev, px, pf, pg, per, ps, post, norms[0], norms[1], pre, norms[2], norms[3],
          float(eps), pr, py, pc, psc, n, C, _dtype_code(x))
     return r, y
 
@@ -789,7 +793,7 @@ def block_join_grad(r: torch.Tensor, f: Optional[torch.Tensor] = None, dr: Optio
     _check_tokens("r", r)
     for name, t in (("f", f), ("dr", dr), ("dy", dy)):
         _check_same(name, t, r, "r")
-    _check_gate(gate, gate_tokens, r)
+    per = _check_gate(gate, gate_tokens, r)
     n, C = r.shape
     _check_channels(C, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w)
     post, pre = _norm_code(post), _norm_code(pre)
@@ -811,6 +815,6 @@ def block_join_grad(r: torch.Tensor, f: Optional[torch.Tensor] = None, dr: Optio
     workspace, nb = _ws(workspace, block_join_grad_workspace_bytes(n, C, _dtype_code(r)), r.device)
     dev, (pr, pf, pg, ps, pw, pb, w, ws, *grads) = _pointers(r, f, gate, scale, post_w, post_b, pre_w, workspace, dr, dy,
                                                              *out)
-    _run("vggt3_block_join_grad", dev, pr, pf, pg, int(gate_tokens), ps, post, pw, pb, pre, w, float(eps), *grads, n, C,
+    _run("vggt3_block_join_grad", dev, pr, pf, pg, per, ps, post, pw, pb, pre, w, float(eps), *grads, n, C,
          _dtype_code(r), ws, nb)
     return out

@@ -110,3 +110,18 @@ def test_binding_refusals():
         tla.block_join_grad(x, f, dr=f[:3])
     with pytest.raises(ValueError, match="dgate"):
         tla.block_join_grad(x, f, dr=f, out=tla.BlockJoinGrads(dgate=x))
+
+
+@pytest.mark.parametrize("per", [2 ** 31, 2 ** 63 - 1, 2 ** 63, 2 ** 64 + 1, 2 ** 64 + 2])
+def test_gate_group_longer_than_any_run_of_tokens(per, monkeypatch):
+    # one gate row serves all tokens; the count that the C call sees must not wrap to a small one, which would have it
+    # read gate rows that are not there
+    seen = []
+    monkeypatch.setattr(tla, "_pointers", lambda *ts: (0, [None if t is None else 0x10000 for t in ts]))
+    monkeypatch.setattr(tla, "_run", lambda name, dev, *args: seen.append(args[3]))
+    x, gate = torch.zeros(6, 32), torch.zeros(1, 32)
+    tla.block_join(x, x.clone(), gate, per)
+    tla.block_join_grad(x, x.clone(), x.clone(), gate=gate, gate_tokens=per)
+    assert len(seen) == 2
+    for v in seen:
+        assert ctypes.c_int64(v).value >= 6
