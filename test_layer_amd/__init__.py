@@ -536,6 +536,11 @@ class FrozenMx4(NamedTuple):
     down: Mx4
 
 
+def _check_width(name: str, k: int) -> None:
+    if k > 0x7FFFFFFF:  # ctypes would pass on its low 32 bits
+        raise ValueError(f"{name} has {k} columns, which do not fit 32 bits")
+
+
 def _mx4_shapes(rows: int, k: int):
     nb = (k + 127) // 128
     return (rows, nb * 64), ((rows + 63) // 64, nb, 64, 4)
@@ -554,6 +559,7 @@ def _check_mx4(name: str, a: Mx4, rows: Optional[int] = None, k: Optional[int] =
         raise TypeError(f"{name}: codes and scales must be uint8, got {codes.dtype} and {scales.dtype}")
     if codes.dim() != 2 or ak < 1:
         raise ValueError(f"{name}: codes are [rows, kp / 2] and k >= 1, got {tuple(codes.shape)} and k = {ak}")
+    _check_width(name, ak)
     n = codes.shape[0]
     if (rows is not None and n != rows) or (k is not None and ak != k):
         raise ValueError(f"{name} is [{n}, {ak}], [{n if rows is None else rows}, {ak if k is None else k}] expected")
@@ -589,6 +595,7 @@ def mx4_quantize(X: torch.Tensor, transpose: bool = False, out: Optional[Mx4] = 
     k, rows = X.shape if transpose else (X.shape[1], X.shape[0])
     if k < 1:
         raise ValueError("X has no columns to contract over")
+    _check_width("X", k)
     if out is not None:
         _check_mx4("out", out, rows, k)
     else:
@@ -732,6 +739,7 @@ def block_join(x: torch.Tensor, f: Optional[torch.Tensor] = None, gate: Optional
     _check_same("f", f, x, "x")
     per = _check_gate(gate, gate_tokens, x)
     n, C = x.shape
+    _check_width("x", C)
     _check_channels(C, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w, pre_b=pre_b)
     post, pre = _norm_code(post), _norm_code(pre)
     if f is not None:
@@ -795,6 +803,7 @@ def block_join_grad(r: torch.Tensor, f: Optional[torch.Tensor] = None, dr: Optio
         _check_same(name, t, r, "r")
     per = _check_gate(gate, gate_tokens, r)
     n, C = r.shape
+    _check_width("r", C)
     _check_channels(C, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w)
     post, pre = _norm_code(post), _norm_code(pre)
     if out is None:

@@ -134,3 +134,24 @@ def test_matrices_of_more_tiles_than_a_launch_takes(lib):
     assert lib.vggt3_mx4_quantize(far[0], 0, far[1], far[2], most + 1, 1, tla.BF16, None) == tla.EUNSUPPORTED
     assert lib.vggt3_mx4_dequantize(far[0], far[1], far[2], most + 1, 1, tla.BF16, None) == tla.EUNSUPPORTED
     assert lib.vggt3_mx4_matmul_workspace_bytes(most + 1, 1, 1, tla.BF16) == 0
+
+
+@pytest.mark.parametrize("k", [2 ** 31, 2 ** 32 + 64])
+def test_widths_that_do_not_fit_32_bits(k):
+    # the C calls take widths as int32, where 2^32 + 64 would pass as 64 and leave the rest of the result unwritten
+    x = torch.empty((2, k), dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="columns"):
+        tla.mx4_quantize(x)
+    with pytest.raises(ValueError, match="columns"):
+        tla.mx4_quantize(x.t(), transpose=True)
+    kp = (k + 127) // 128 * 128
+    a = tla.Mx4(torch.empty((2, kp // 2), dtype=torch.uint8, device="meta"),
+                torch.empty((1, kp // 128, 64, 4), dtype=torch.uint8, device="meta"), k)
+    with pytest.raises(ValueError, match="columns"):
+        tla.mx4_dequantize(a)
+    with pytest.raises(ValueError, match="columns"):
+        tla.mx4_matmul(a, a)
+    with pytest.raises(ValueError, match="columns"):
+        tla.block_join(x, x, pre="rms")
+    with pytest.raises(ValueError, match="columns"):
+        tla.block_join_grad(x, x, x, x, pre="rms")
