@@ -498,14 +498,23 @@ def _pointers(*ts):
 
 
 # The current stream of a GPU as the address that the C calls take, without the
-# Stream object round it (which costs as much host time as a launch).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# Stream object round it (which costs as much host time as a launch), and the
+# current GPU. Both are private to torch, so a build without them takes the
+# public calls.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_gpu = getattr(torch._C, "_cuda_getDevice", None)
+if _raw_stream is None or _current_gpu is None:
+    def _raw_stream(dev: int) -> int:
+        return torch.cuda.current_stream(dev).cuda_stream
+
+    def _current_gpu() -> int:
+        return torch.cuda.current_device()
 
 
 def _run(name: str, dev: int, *args) -> None:
     """Call `name` on GPU `dev`'s current stream, whichever device is current."""
     fn = getattr(_lib.load(), name)
-    if dev == torch._C._cuda_getDevice():
+    if dev == _current_gpu():
         rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):

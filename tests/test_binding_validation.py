@@ -4,6 +4,10 @@ checks run before the device check, so host tensors with bad shapes exercise
 them without a GPU."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -103,3 +107,27 @@ def test_well_formed_host_tensors_reach_the_device_check():
         tla.ttt_write(_tok(), _tok(), _theta(), 0.1, 2, H, loss_out=torch.zeros(2 * H))
     with pytest.raises(ValueError, match="GPU"):
         tla.ttt_read(_tok(), _theta(), H, out=_tok())
+
+
+def test_import_and_stream_without_torchs_private_names():
+    # a torch build may lack the private short cuts to the current stream and device: the import still works, and the
+    # public calls stand in for them
+    code = ("import torch\n"
+            "for name in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, name):\n"
+            "        delattr(torch._C, name)\n"
+            "import test_layer_amd as tla\n"
+            "class S:\n"
+            "    cuda_stream = 77\n"
+            "torch.cuda.current_stream = lambda dev=None: S()\n"
+            "torch.cuda.current_device = lambda: 3\n"
+            "seen = []\n"
+            "class L:\n"
+            "    def __getattr__(self, name):\n"
+            "        return lambda *args: seen.append(args) or 0\n"
+            "tla._lib.load = lambda: L()\n"
+            "tla._run('anything', 3, 1, 2)\n"
+            "assert seen == [(1, 2, 77)], seen\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
