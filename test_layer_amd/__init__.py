@@ -769,6 +769,8 @@ def block_join(x: torch.Tensor, f: Optional[torch.Tensor] = None, gate: Optional
     else:
         if y is None:
             y = torch.empty_like(x)
+        elif isinstance(y, Mx4):
+            raise TypeError("y is an Mx4, which goes with mx4=True")
         _check_same("y", y, x, "x")
     plain = None if mx4 else y
     dev, (px, pf, pg, ps, *norms, pr, py, pc, psc) = _pointers(x, f, gate, scale, post_w, post_b, pre_w, pre_b, r,

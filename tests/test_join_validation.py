@@ -125,3 +125,12 @@ def test_gate_group_longer_than_any_run_of_tokens(per, monkeypatch):
     assert len(seen) == 2
     for v in seen:
         assert ctypes.c_int64(v).value >= 6
+
+
+def test_y_of_the_other_form_is_refused():
+    x = torch.zeros(4, 64)
+    y4 = tla.Mx4(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(1, 1, 64, 4, dtype=torch.uint8), 64)
+    with pytest.raises(TypeError, match="mx4"):
+        tla.block_join(x, x.clone(), pre="rms", y=y4)
+    with pytest.raises(TypeError, match="Mx4"):
+        tla.block_join(x, x.clone(), pre="rms", y=x.clone(), mx4=True)
