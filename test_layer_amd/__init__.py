@@ -710,7 +710,11 @@ _NORMS = {None: NORM_NONE, "none": NORM_NONE, "rms": NORM_RMS, "layer": NORM_LAY
 
 
 def _norm_code(kind) -> int:
-    return _NORMS[kind] if kind is None or isinstance(kind, str) else int(kind)
+    if kind is not None and not isinstance(kind, str):
+        return int(kind)
+    if kind not in _NORMS:
+        raise KeyError(f"unknown norm {kind!r}; None, 'none', 'rms' or 'layer'")
+    return _NORMS[kind]
 
 
 def _check_gate(gate: Optional[torch.Tensor], gate_tokens: int, x: torch.Tensor) -> int:

@@ -134,3 +134,12 @@ def test_y_of_the_other_form_is_refused():
         tla.block_join(x, x.clone(), pre="rms", y=y4)
     with pytest.raises(TypeError, match="Mx4"):
         tla.block_join(x, x.clone(), pre="rms", y=x.clone(), mx4=True)
+
+
+@pytest.mark.parametrize("where", ["post", "pre"])
+def test_unknown_norm_says_which_there_are(where):
+    x = torch.zeros(4, 64)
+    with pytest.raises(KeyError, match="batch.*rms.*layer"):
+        tla.block_join(x, x.clone(), **{where: "batch"})
+    with pytest.raises(KeyError, match="batch.*rms.*layer"):
+        tla.block_join_grad(x, x.clone(), x.clone(), **{where: "batch"})
