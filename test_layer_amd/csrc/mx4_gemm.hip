@@ -79,13 +79,15 @@ __device__ __forceinline__ void store_tile(const Args& g, const f32x4& v, int64_
 // One block of H: a lane's 8 of 32 gate and up sums of one row (units 4 (l/16)
 // ..+3 and 16 more), the other 24 in the lanes 16, 32 and 48 further.
 // Quantised from fp32; the lane's codes are two 16-bit halves, 8 bytes apart.
+// (The sigmoid goes to the gate first: gate * up may pass fp32 where silu(gate) * up
+// does not, and Inf * 0 would make the block NaN.)
 __device__ __forceinline__ uint32_t swiglu_codes(const f32x4 (&gate)[2], const f32x4 (&up)[2], uint32_t& s) {
   float h[8], top = 0.0f;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      h[4 * i + r] = gate[i][r] * up[i][r] * sigmoid_fast(gate[i][r]);
+      h[4 * i + r] = gate[i][r] * sigmoid_fast(gate[i][r]) * up[i][r];
       top = __builtin_elementwise_maximum(top, __builtin_fabsf(h[4 * i + r]));  // a NaN stays
     }
 #pragma unroll

@@ -322,3 +322,26 @@ def test_two_products_at_once_and_two_captured_graphs():
                 g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, c) for o, c in zip(outs, want))
+
+
+@pytest.mark.parametrize("n", [5, 40, 200, 700])
+def test_read_where_gate_times_up_passes_fp32(n):
+    # Unit 5: gate = -2^40 q0, up = 2^40 q0. q0 = 2^35 in one row, so gate * up is past fp32 there, but silu(gate) * up
+    # is 0, as in the other rows (q0 = 1): the same bits as with up = 0. By 16 rows, by 64 rows, by 64 x 64 tiles and
+    # by 256 x 256 tiles, from tokens and from 4 bits.
+    g = torch.Generator().manual_seed(n)
+    theta = torch.randn(3, 1024 * 4096, generator=g) / 32
+    gate, up = theta[0].view(1024, 4096), theta[1].view(1024, 4096)
+    gate[0], up[0] = 0.0, 0.0
+    gate[0, 5] = -2.0 ** 40
+    zero = tla.ttt_freeze_mx4(theta.view(1, -1).cuda())
+    up[0, 5] = 2.0 ** 40
+    f = tla.ttt_freeze_mx4(theta.view(1, -1).cuda())
+    q = torch.randn(n, 1024, generator=g)
+    q[:, 0] = 1.0
+    q[3, 0] = 2.0 ** 35
+    q = q.to(torch.bfloat16).cuda()
+    o = tla.ttt_read_mx4(q, f)
+    assert torch.isfinite(o).all()
+    assert torch.equal(o, tla.ttt_read_mx4(q, zero))
+    assert torch.equal(o, tla.ttt_read_mx4(tla.mx4_quantize(q), f))
