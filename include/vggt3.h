@@ -559,7 +559,9 @@ int vggt3_ttt_read_mx4(const void* Q, const void* Q_scales, int32_t q_type, cons
  *   gate        NULL (1) or [ceil(n_tokens / gate_tokens)][channels], dtype: row
  *               t / gate_tokens serves token t (1: a gate per token; the tokens
  *               of a view: a gate per view).
- *   scale       NULL (1) or float32 [channels], the residual scale.
+ *   scale       NULL (1) or float32 [channels], the residual scale. (It is
+ *               multiplied into post's weight and bias: with a post_b, an
+ *               infinite scale gives NaN where their terms differ in sign.)
  *   post_w, post_b, pre_w, pre_b   NULL (1 / 0) or float32 [channels].
  *   y, or y_codes and y_scales     with a pre norm, one of them: y itself, or y
  *               rounded to dtype and then quantised as by vggt3_mx4_quantize

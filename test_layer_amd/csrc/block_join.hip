@@ -368,7 +368,7 @@ __global__ __launch_bounds__(block_threads(T)) void join_kernel(Args a) {
 #pragma unroll
     for (size_t i = 0; i < sizeof(pw.v) / sizeof(f32x4); ++i) {
       pw.v[i] *= sc.v[i];
-      pb.v[i] *= sc.v[i];
+      if (a.post_b) pb.v[i] *= sc.v[i];  // no bias stays 0 where the scale is Inf
     }
     R::stage_param(params + PW * T * E, pw, tid, uid);
     R::stage_param(params + PB * T * E, pb, tid, uid);

@@ -343,3 +343,18 @@ def test_odd_rows_in_4_bits_on_two_streams_at_once(C):
         assert torch.equal(r, r1)
         want = tla.mx4_quantize(y1)
         assert torch.equal(y4.codes, want.codes) and torch.equal(y4.scales, want.scales)
+
+
+# ------------------------------------------------------------------------------------------------- values past fp32
+
+@pytest.mark.parametrize("post", ["none", "rms", "layer"])
+@pytest.mark.parametrize("C", [64, 99])
+def test_infinite_scale_without_a_bias(C, post):
+    # scale = Inf: r = x + Inf h, an Inf of h's sign; the other channels as they were
+    c = _case(30, C, "f32", post, "none", True, 1, True, False)
+    r, _ = tla.block_join(c["x"], c["f"], **_args(c))
+    h = to64(r) - to64(c["x"])
+    c["scale"][3] = float("inf")
+    got = to64(tla.block_join(c["x"], c["f"], **_args(c))[0])
+    assert np.array_equal(got[:, 3], np.sign(h[:, 3]) * np.inf)
+    assert np.array_equal(np.delete(got, 3, 1), np.delete(to64(r), 3, 1))
