@@ -669,7 +669,7 @@ __global__ __launch_bounds__(1024) void sum_parts_kernel(Args a, int64_t blocks,
   if (v0 == kA) {
     const float sc = a.scale ? a.scale[c] : 1.0f;
     if (out.v[kDScale])
-      out.v[kDScale][c] = (a.post_w ? a.post_w[c] : 1.0f) * s0 + (a.post_b ? a.post_b[c] : 0.0f) * s1;
+      out.v[kDScale][c] = (a.post_w ? a.post_w[c] * s0 : s0) + (a.post_b ? a.post_b[c] * s1 : 0.0f);
     if (out.v[kDPostW]) out.v[kDPostW][c] = sc * s0;
     if (out.v[kDPostB]) out.v[kDPostB][c] = sc * s1;
   } else {

@@ -358,3 +358,15 @@ def test_infinite_scale_without_a_bias(C, post):
     got = to64(tla.block_join(c["x"], c["f"], **_args(c))[0])
     assert np.array_equal(got[:, 3], np.sign(h[:, 3]) * np.inf)
     assert np.array_equal(np.delete(got, 3, 1), np.delete(to64(r), 3, 1))
+
+
+@pytest.mark.parametrize("post", ["none", "rms"])
+def test_infinite_gradient_without_a_bias(post):
+    # dr = Inf at one token and channel: dscale there is an Inf of h's sign
+    c = _case(30, 64, "f32", post, "none", False, 1, True, False)
+    c["dr"][5, 3] = float("inf")
+    got = tla.block_join_grad(c["x"], c["f"], c["dr"], **_args(c))
+    f = to64(c["f"])
+    h = join.norm(f, post, None if c["post_w"] is None else to64(c["post_w"]))[0]
+    assert got.dscale[3].item() == np.sign(h[5, 3]) * np.inf
+    assert torch.isfinite(got.dscale[:3]).all() and torch.isfinite(got.dscale[4:]).all()
