@@ -814,6 +814,7 @@ hipError_t launch_grad(const Args& args, const GradPlan& p, float* const* out, b
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  if (a.n == 0) a.scale = a.post_w = a.post_b = nullptr;  // zeros, whatever the vectors hold
   Outs o;
   bool any = false;
   for (int v = 0; v < kOuts; ++v) any |= (o.v[v] = out[v]) != nullptr;

@@ -370,3 +370,10 @@ def test_infinite_gradient_without_a_bias(post):
     h = join.norm(f, post, None if c["post_w"] is None else to64(c["post_w"]))[0]
     assert got.dscale[3].item() == np.sign(h[5, 3]) * np.inf
     assert torch.isfinite(got.dscale[:3]).all() and torch.isfinite(got.dscale[4:]).all()
+
+
+def test_zeros_of_no_tokens_whatever_the_weights():
+    x, w = torch.empty(0, 64, device="cuda"), torch.full((64,), float("inf"), device="cuda")
+    got = tla.block_join_grad(x, x.clone(), x.clone(), x.clone(), post="rms", post_w=w, post_b=w.clone(), pre="rms",
+                              pre_w=w.clone(), scale=w.clone())
+    assert all((v == 0).all() for v in (got.dscale, got.dpost_w, got.dpost_b, got.dpre_w))
