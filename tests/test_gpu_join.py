@@ -345,6 +345,76 @@ def test_odd_rows_in_4_bits_on_two_streams_at_once(C):
         assert torch.equal(y4.codes, want.codes) and torch.equal(y4.scales, want.scales)
 
 
+# -------------------------------------------------------------------------------------- many rows a unit of threads
+# The kernels' units take one row each up to 524,288 / threads rows (forward) and 256 (gradient), and a range of rows
+# beyond. The shapes below give 2 or more rows a unit to each unit size (forward: 16, 64, 128, 256, 512 threads;
+# gradient: 16, 32, 64, 128, 256, 512 and 512 x 16 values), with rows of whole pieces and of odd width.
+
+LONG_FORWARD = [(70001, 40), (66001, 99), (65600, 128), (66001, 200), (20011, 500), (20011, 1024), (17003, 999), (9001, 2048),
+                (9001, 1999), (4500, 4096), (4201, 4095), (2500, 5000), (2500, 8191), (2101, 8192)]
+
+
+@pytest.mark.parametrize("per,dtype", [(1, "bf16"), (3, "f32"), (1009, "bf16"), (1009, "f32")])
+@pytest.mark.parametrize("n,C", LONG_FORWARD)
+def test_forward_of_many_rows_a_unit_is_that_of_slices(n, C, per, dtype):
+    # Slices small enough for one row a unit, with the gate's rows repeated for their tokens: the same arithmetic on
+    # each row, so the same bits. In place too, and into 4 bits, whose last scale tile is cut.
+    g = torch.Generator("cuda").manual_seed(n + per)
+
+    def t(*shape, std=1.0, mean=0.0, dt=torch.float32):
+        return (torch.randn(shape, generator=g, device="cuda") * std + mean).to(dt)
+
+    dt = DT[dtype]
+    x, f, gate = t(n, C, std=1.5, dt=dt), t(n, C, std=0.7, mean=0.3, dt=dt), t(-(-n // per), C, std=0.5, mean=1.0, dt=dt)
+    kw = dict(scale=t(C, std=0.2, mean=0.3), post="rms", post_w=t(C, std=0.2, mean=1.0), post_b=t(C, std=0.3), pre="layer",
+              pre_w=t(C, std=0.2, mean=1.0), pre_b=t(C, std=0.3))
+    r, y = tla.block_join(x, f, gate, per, **kw)
+    r4, y4 = tla.block_join(x, f, gate, per, mx4=True, **kw)
+    assert torch.equal(r4, r)
+    want = tla.mx4_quantize(y)
+    assert torch.equal(y4.codes, want.codes) and torch.equal(y4.scales, want.scales)
+    threads = 16 if C <= 256 else 64 if C <= 1024 else 128 if C <= 2048 else 256 if C <= 4096 else 512
+    step = 524288 // threads
+    assert n > step
+    rows = gate if per == 1 else gate.repeat_interleave(per, 0)[:n]
+    for a in range(0, n, step):
+        s = slice(a, min(n, a + step))
+        r1, y1 = tla.block_join(x[s].clone(), f[s].clone(), rows[s].clone(), 1, **kw)
+        assert torch.equal(r[s], r1) and torch.equal(y[s], y1), a
+    r5, y5 = tla.block_join(x, f, gate, per, r=x, **kw)
+    assert r5 is x and torch.equal(x, r) and torch.equal(y5, y)
+
+
+@pytest.mark.parametrize("post,pre", [("none", "none"), ("layer", "rms"), ("none", "layer")])
+@pytest.mark.parametrize("n,C,dtype", [(33000, 24, "bf16"), (33001, 99, "f32"), (9000, 999, "bf16"), (8300, 1024, "f32"),
+                                       (4200, 2048, "bf16"), (2100, 4100, "f32")])
+def test_forward_of_many_rows_a_unit(n, C, dtype, post, pre):
+    _check_forward(_case(n, C, dtype, post, pre, post == "layer", 250, True, post != "none", n), dtype)
+
+
+# A channel sum adds the rows of a unit (at most 14 here), the up to 16 units of a workgroup, the workgroups' parts in
+# 64 runs of at most 23 and then 6 levels of a tree: at most 14 + 15 + 23 + 6 roundings. A shared gate group adds its
+# rows in a unit, then at most 16 units in turn, or its units in 16 runs and 4 levels: fewer. With the 160 of a row that
+# the head of this file counts, all stay below the 256 u of _check_grad.
+@pytest.mark.parametrize("n,C,dtype", [(40000, 40, "bf16"), (33001, 99, "f32"), (20000, 200, "f32"), (20001, 257, "bf16"),
+                                       (9000, 500, "bf16"), (5000, 1024, "f32"), (6000, 999, "bf16"), (2600, 2048, "bf16"),
+                                       (1500, 1999, "f32"), (900, 4096, "bf16"), (900, 4095, "f32"), (1100, 5000, "bf16"),
+                                       (900, 8192, "bf16"), (900, 8192, "f32"), (600, 8191, "f32"), (900, 8191, "bf16")])
+@pytest.mark.parametrize("per", [1, 3, 400])
+def test_grad_of_many_rows_a_unit(n, C, dtype, per):
+    _check_grad(_case(n, C, dtype, "layer", "rms" if per % 2 else "layer", True, per, True, True, n + per), dtype)
+
+
+@pytest.mark.parametrize("post,pre", [("none", "rms"), ("rms", "none"), ("rms", "rms")])
+@pytest.mark.parametrize("n,C,dtype", [(9000, 40, "f32"), (2000, 1024, "bf16"), (1500, 2048, "f32"), (700, 6000, "bf16")])
+def test_grad_of_many_rows_a_unit_without_a_shared_gate(n, C, dtype, post, pre):
+    _check_grad(_case(n, C, dtype, post, pre, False, 1, post == "rms", False, n), dtype)
+
+
+def test_grad_of_a_scene_value_by_value():
+    _check_grad(_case(20011, 1024, "bf16", "layer", "layer", True, 1374, True, True), "bf16")
+
+
 # ------------------------------------------------------------------------------------------------- values past fp32
 
 @pytest.mark.parametrize("post", ["none", "rms", "layer"])
@@ -377,3 +447,61 @@ def test_zeros_of_no_tokens_whatever_the_weights():
     got = tla.block_join_grad(x, x.clone(), x.clone(), x.clone(), post="rms", post_w=w, post_b=w.clone(), pre="rms",
                               pre_w=w.clone(), scale=w.clone())
     assert all((v == 0).all() for v in (got.dscale, got.dpost_w, got.dpost_b, got.dpre_w))
+
+
+# ------------------------------------------------------------------------------------------ calls that are left over
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("C", [40, 99, 1024])
+def test_vectors_left_out_and_their_gradients(C, kind, dtype):
+    # no weights, no scale, biases alone; their gradients asked for all the same, those of the rest not
+    n, per = 77, 5
+    c = _case(n, C, dtype, kind, kind, True, per, False, True, C)
+    c["post_w"] = c["pre_w"] = None
+    _check_forward(c, dtype)
+    f32 = [torch.full((C,), 7.0, device="cuda") for _ in range(5)]
+    out = tla.BlockJoinGrads(None, torch.empty_like(c["f"]), None, *f32)
+    got = tla.block_join_grad(c["x"], c["f"], c["dr"], c["dy"], out=out, **_args(c))
+    assert got is out
+    ones = dict(c, post_w=torch.ones(C, device="cuda"), pre_w=torch.ones(C, device="cuda"), scale=torch.ones(C, device="cuda"))
+    want = tla.block_join_grad(c["x"], c["f"], c["dr"], c["dy"], pre_bias=True, **_args(ones))
+    for k in ("df", "dscale", "dpost_w", "dpost_b", "dpre_w", "dpre_b"):
+        assert torch.equal(getattr(got, k), getattr(want, k)), k
+    _check_grad(ones, dtype)
+
+
+@pytest.mark.parametrize("n,C", [(1, 40), (500, 99), (1000, 1024), (300, 5000)])
+def test_grad_without_dr_is_that_of_zeros(n, C):
+    c = _case(n, C, "bf16", "layer", "rms", True, 3, True, False, n)
+    want = tla.block_join_grad(c["x"], c["f"], torch.zeros_like(c["dr"]), c["dy"], **_args(c))
+    got = tla.block_join_grad(c["x"], c["f"], None, c["dy"], **_args(c))
+    for k, v in want._asdict().items():
+        assert (v is None) == (getattr(got, k) is None) and (v is None or torch.equal(getattr(got, k), v)), k
+
+
+def test_more_than_2_31_values():
+    n, C, per = 2_200_001, 1024, 1374
+    g = torch.Generator("cuda").manual_seed(3)
+    x, f, dr, dy = (torch.randn(n, C, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(4))
+    gate = torch.randn(-(-n // per), C, generator=g, device="cuda", dtype=torch.bfloat16)
+    kw = dict(scale=torch.randn(C, generator=g, device="cuda"), post="rms", pre="layer")
+    r, y = tla.block_join(x, f, gate, per, **kw)
+    y4 = tla.block_join(x, f, gate, per, mx4=True, **kw)[1]
+    got = tla.block_join_grad(r, f, dr, dy, gate, per, pre_bias=True, **kw)
+    rows = n // 64 * 64 - 640  # a whole scale tile's first row
+    own = gate[torch.arange(rows, n, device="cuda") // per].contiguous()
+    s = slice(rows, n)
+    tail = [t[s].clone() for t in (x, f, dr, dy)]
+    r1, y1 = tla.block_join(*tail[:2], own, 1, **kw)
+    assert torch.equal(r[s], r1) and torch.equal(y[s], y1)
+    want = tla.mx4_quantize(y1)
+    assert torch.equal(y4.codes[s], want.codes) and torch.equal(y4.scales[rows // 64:], want.scales)
+    few = tla.block_join_grad(r1, *tail[1:], own, 1, **kw)
+    assert torch.equal(got.dx[s], few.dx) and torch.equal(got.df[s], few.df)
+    # sum of dy: at most 1433 rows in a unit, 23 + 6 joins
+    total, mag = torch.zeros(C, dtype=torch.float64, device="cuda"), torch.zeros(C, dtype=torch.float64, device="cuda")
+    for part in dy.split(200_000):
+        total += part.double().sum(0)
+        mag += part.double().abs().sum(0)
+    assert bool(((got.dpre_b.double() - total).abs() <= 1500 * U * mag).all())

@@ -345,3 +345,26 @@ def test_read_where_gate_times_up_passes_fp32(n):
     assert torch.isfinite(o).all()
     assert torch.equal(o, tla.ttt_read_mx4(q, zero))
     assert torch.equal(o, tla.ttt_read_mx4(tla.mx4_quantize(q), f))
+
+
+def test_more_than_2_31_values():
+    rows, k, n = 2_200_001, 1024, 1000
+    g = torch.Generator("cuda").manual_seed(6)
+    x = torch.randn(rows, k, generator=g, device="cuda", dtype=torch.bfloat16)
+    a = tla.mx4_quantize(x)
+    at = rows // 64 * 64 - 640  # a whole scale tile's first row
+    few = tla.mx4_quantize(x[at:].clone())
+    assert torch.equal(a.codes[at:], few.codes) and torch.equal(a.scales[at // 64:], few.scales)
+    back = tla.mx4_dequantize(a)
+    assert torch.equal(back[at:], tla.mx4_dequantize(few))
+    w = tla.mx4_quantize(torch.randn(n, k, generator=g, device="cuda"))
+    c = tla.mx4_matmul(a, w)  # 2.2e9 values
+    want = back[at:].double() @ tla.mx4_dequantize(w, torch.float32).double().t()
+    mag = back[at:].double().abs() @ tla.mx4_dequantize(w, torch.float32).double().abs().t()
+    assert bool(((c[at:].double() - want).abs() <= k * 2.0 ** -24 * mag + 2.0 ** -8 * want.abs()).all())
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 20, 1 << 20), (40, 100, (1 << 20) - 5), (1100, 1100, 1 << 18), (70, 1 << 20, 200),
+                                   (1, 1 << 20, 33)])
+def test_matmul_of_the_longest_sides(m, n, k):
+    _check_product_on_gpu(m, n, k, "f32")
