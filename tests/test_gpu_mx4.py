@@ -368,3 +368,51 @@ def test_more_than_2_31_values():
                                    (1, 1 << 20, 33)])
 def test_matmul_of_the_longest_sides(m, n, k):
     _check_product_on_gpu(m, n, k, "f32")
+
+
+@pytest.mark.parametrize("n", [5, 40, 200, 700])
+def test_read_of_a_non_finite_token_leaves_the_others(frozen, n):
+    _, f = frozen
+    q = torch.randn(n, 1024, generator=torch.Generator().manual_seed(n)).to(torch.bfloat16).cuda()
+    want = tla.ttt_read_mx4(q, f)
+    q[3, 1000], q[n - 2, 0] = float("nan"), float("-inf")
+    for o in (tla.ttt_read_mx4(q, f), tla.ttt_read_mx4(tla.mx4_quantize(q), f)):
+        assert torch.isnan(o[[3, n - 2]]).all()
+        o[[3, n - 2]] = want[[3, n - 2]]
+        assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("n", [1, 100, 700])
+def test_read_on_another_stream_and_in_graphs(frozen, n):
+    # quantise, read and quantise back as one captured pass, replayed on new tokens between eager passes
+    _, f = frozen
+    q = torch.randn(n, 1024, generator=torch.Generator().manual_seed(n)).to(torch.bfloat16).cuda()
+
+    def both(a, o, back, ws):
+        tla.mx4_quantize(q, out=a)
+        tla.ttt_read_mx4(a, f, out=o, workspace=ws)
+        tla.mx4_dequantize(a, out=back)
+
+    def fresh():
+        return (tla.mx4_quantize(torch.zeros_like(q)), torch.empty_like(q), torch.empty_like(q),
+                torch.empty(tla.read_mx4_workspace_bytes(n, 1024, 4096, tla.MX4), dtype=torch.uint8, device="cuda"))
+
+    eager, other, caught = fresh(), fresh(), fresh()
+    both(*eager)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        both(*other)
+    s.synchronize()
+    assert torch.equal(other[1], eager[1]) and torch.equal(other[2], eager[2])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        both(*caught)
+    for seed in (1, 2, 3):
+        q.copy_(torch.randn(n, 1024, generator=torch.Generator().manual_seed(seed)))
+        caught[1].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        both(*eager)
+        assert torch.equal(caught[1], eager[1]) and torch.equal(caught[2], eager[2])
+        assert torch.equal(caught[0].codes, eager[0].codes) and torch.equal(caught[0].scales, eager[0].scales)
