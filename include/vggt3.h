@@ -601,6 +601,122 @@ int vggt3_block_join_grad(const void* r, const void* f, const void* gate, int64_
                           float* dpost_w, float* dpost_b, float* dpre_w, float* dpre_b, int64_t n_tokens,
                           int32_t channels, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Queries and keys before the layer: a norm of every head ([GRAPH] "LayerNorm
+ * removal": L2; RMS and layer norm with weight and bias as well) and the rotation of
+ * its channels by the token's position on up to 4 axes (time, row, column), in one
+ * pass. With x a head's d_head channels,
+ *
+ *   h = norm(x):  VGGT3_NORM_NONE x;  VGGT3_NORM_L2 x / max(|x|, eps);  VGGT3_NORM_RMS
+ *       x / sqrt(mean x^2 + eps) * w + b;  VGGT3_NORM_LAYER the same of x - mean x
+ *   for every rotated pair of channels (a, b), t = position * base^(-j / size):
+ *   (a, b) <- (a cos t - b sin t, b cos t + a sin t)
+ *
+ *   q, k        [n_tokens][n_heads][d_head], [n_tokens][n_heads_k][d_head], dtype, rows
+ *               q_stride and k_stride values apart (slices of one projection);
+ *               n_heads_k = 0: no keys. q_out, k_out have no gaps; q_out may be q
+ *               and k_out k (in place) where these have none either.
+ *   q_w .. k_b  NULL (1 / 0) or float32 [d_head] (RMS and layer norm).
+ *   pos         int32 [n_tokens][n_axes], any values (angles are formed in 64 bits).
+ *   sections    HOST int32 [n_axes]: pairs that each axis rotates, 1 or more; twice
+ *               their sum at most d_head. Channels behind them are not rotated. 0
+ *               axes: no rotation (pos and sections may be NULL).
+ *   per_axis    != 0: axis i has the 2 * sections[i] channels behind those of the
+ *               axes before it, and its pair j turns by base^(-j / sections[i]) a
+ *               step. 0: all pairs form one ladder base^(-j / sum of sections) over the
+ *               first 2 * sum channels, pairs to axes in their order.
+ *   interleaved != 0: pair j is channels 2j and 2j + 1 (of its axis's channels, or of
+ *               all); 0: channels j and size + j.
+ * All arithmetic but the angles is fp32; every output is rounded once. d_head at most 512, of any
+ * count (sections and heads that are multiples of 4 channels are faster).
+ * n_tokens == 0 is a no-op.
+ */
+enum { VGGT3_NORM_L2 = 3 };
+
+int vggt3_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int32_t norm,
+                       const float* q_w, const float* q_b, const float* k_w, const float* k_b, float eps,
+                       const int32_t* pos, const int32_t* sections, int32_t n_axes, double base, int32_t per_axis,
+                       int32_t interleaved, void* q_out, void* k_out, int64_t n_tokens, int32_t n_heads,
+                       int32_t n_heads_k, int32_t d_head, int32_t dtype, void* stream);
+
+/*
+ * Gradient of vggt3_qk_norm_rope, from its inputs (no statistics are kept between
+ * the calls) and the gradients dq_out, dk_out of its outputs (without gaps).
+ *
+ *   dq, dk       gradients of q and k, without gaps; dq may be dq_out, dk dk_out.
+ *   dq_w .. dk_b float32 [d_head], summed over all tokens and heads in fp32, in a fixed
+ *                order (a NULL weight counts as 1; its gradient may still be asked
+ *                for). A bias's value does not enter.
+ * Every output may be NULL (not wanted). An L2 norm of a head shorter than eps passes
+ * dy / eps on.
+ *   workspace    for dq_w .. dk_b: at least vggt3_qk_norm_rope_grad_workspace_bytes
+ *                bytes.
+ * n_tokens == 0 writes zeros to the float32 outputs.
+ */
+size_t vggt3_qk_norm_rope_grad_workspace_bytes(int64_t n_tokens, int32_t d_head);
+int vggt3_qk_norm_rope_grad(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* dq_out,
+                            const void* dk_out, int32_t norm, const float* q_w, const float* k_w, float eps,
+                            const int32_t* pos, const int32_t* sections, int32_t n_axes, double base,
+                            int32_t per_axis, int32_t interleaved, void* dq, void* dk, float* dq_w, float* dq_b,
+                            float* dk_w, float* dk_b, int64_t n_tokens, int32_t n_heads, int32_t n_heads_k,
+                            int32_t d_head, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The gated delta rule: the write and read of the layer for a linear T, online. Each
+ * value head's fast weights S [d_k][d_v] take one step a token on the squared error
+ * of S^T k against v, after a decay exp(g), and answer the query (tokens in order, so
+ * that streamed views can be read as they come):
+ *
+ *   p_t = e^{g_t} S_{t-1}^T k_t,   u_t = beta_t (v_t - p_t),
+ *   S_t = e^{g_t} S_{t-1} + k_t u_t^T,   o_t = scale S_t^T q_t
+ *
+ *   q, k         [n_tokens][n_heads][d_k], dtype; value head h uses key head
+ *                h / (n_heads_v / n_heads).
+ *   v, o         [n_tokens][n_heads_v][d_v], dtype.
+ *   g, beta      float32 [n_tokens][n_heads_v]; g NULL: 0 (no decay); -Inf empties S.
+ *   cu_seqlens   NULL (one sequence) or DEVICE int32 [n_seqs + 1]: sequence b is rows
+ *                cu[b] .. cu[b + 1] - 1, empty ones included. Rows of no sequence are
+ *                neither read nor written. (Boundaries outside 0 .. n_tokens count as
+ *                the nearer of the two, a sequence that ends before it begins as empty; sequences
+ *                must not share rows.)
+ *   max_seqlen   the longest sequence's length, or 0 if unknown. Only how the work is
+ *                cut depends on it: a wrong one costs time, not results beyond rounding.
+ *   state, state_out   float32 [n_seqs][n_heads_v][d_k][d_v]: S before each
+ *                sequence (NULL: 0) and after it (NULL: not wanted). state_out may be
+ *                state.
+ *   workspace    at least vggt3_gated_delta_workspace_bytes(...) bytes (may be NULL when
+ *                that is 0).
+ * Computed by chunks of 32 tokens (the same values by matrix products): S, decays,
+ * sums and the chunk's triangular inverse are fp32 (bf16 dtype: products of bf16 pairs,
+ * 2^-17 relative), o is rounded once. A value that is not finite makes its sequence's
+ * results not finite from its chunk on, other sequences' not at all. Heads of 64 or
+ * 128 each way. The results are the same bits each time. Outputs and the workspace must
+ * not overlap anything else. n_tokens == 0 copies state to state_out.
+ */
+size_t vggt3_gated_delta_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int64_t max_seqlen, int32_t n_heads,
+                                         int32_t n_heads_v, int32_t d_k, int32_t d_v, int32_t dtype);
+int vggt3_gated_delta(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                      const int32_t* cu_seqlens, int64_t max_seqlen, const float* state, float scale, void* o,
+                      float* state_out, int64_t n_tokens, int32_t n_seqs, int32_t n_heads, int32_t n_heads_v,
+                      int32_t d_k, int32_t d_v, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token of each of several streams by the same rule, on states in a cache.
+ *
+ *   q, k, v, g, beta, o   as above, a row a token.
+ *   state        float32 [n_slots][n_heads_v][d_k][d_v], updated.
+ *   slots        NULL (row r uses state r) or DEVICE int32 [n_rows]: row r's state.
+ *                Rows of one slot are taken in their order, as that stream's next
+ *                tokens. A slot outside 0 .. n_slots - 1 marks a row of a padded batch:
+ *                its o is 0 and no state changes.
+ * fp32 throughout, o rounded once. n_rows == 0 is a no-op.
+ */
+int vggt3_gated_delta_step(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                           float* state, int64_t n_slots, const int32_t* slots, float scale, void* o, int64_t n_rows,
+                           int32_t n_heads, int32_t n_heads_v, int32_t d_k, int32_t d_v, int32_t dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -842,3 +842,252 @@ def block_join_grad(r: torch.Tensor, f: Optional[torch.Tensor] = None, dr: Optio
     _run("vggt3_block_join_grad", dev, pr, pf, pg, per, ps, post, pw, pb, pre, w, float(eps), *grads, n, C,
          _dtype_code(r), ws, nb)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Queries and keys: a norm of every head and the rotation by position; its gradient
+# ---------------------------------------------------------------------------
+
+NORM_L2 = 3
+
+
+def _qk_norm_code(kind) -> int:
+    return NORM_L2 if kind == "l2" else _norm_code(kind)
+
+
+def _heads_of(name: str, t: torch.Tensor, heads: int, d: Optional[int] = None) -> int:
+    """The channels of a head of t [tokens, heads * d]."""
+    if heads < 1 or t.shape[1] % heads or t.shape[1] == 0:
+        raise ValueError(f"{name} has {t.shape[1]} channels, which {heads} heads do not divide")
+    if d is not None and t.shape[1] != heads * d:
+        raise ValueError(f"{name} has {t.shape[1]} channels, {heads} heads of {d} expected")
+    return t.shape[1] // heads
+
+
+def _rows_of(name: str, t: Optional[torch.Tensor]):
+    """(t's address, how far its rows are apart): rows may be slices of longer ones."""
+    if t is None:
+        return None, 0
+    if t.get_device() < 0:
+        raise ValueError("tensors must live on the GPU (HIP device memory)")
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name}: the channels of a row must be neighbours and rows apart, strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _qk_inputs(q, k, n_heads, n_heads_k, pos, sections, weights):
+    _check_tokens("q", q)
+    d = _heads_of("q", q, n_heads)
+    hk = 0
+    if k is not None:
+        _check_tokens("k", k)
+        hk = n_heads if n_heads_k is None else n_heads_k
+        if k.shape[0] != q.shape[0] or k.dtype != q.dtype:
+            raise ValueError(f"k {tuple(k.shape)} {k.dtype} does not match q {tuple(q.shape)} {q.dtype}")
+        _heads_of("k", k, hk, d)
+    sections = tuple(int(c) for c in sections)
+    if bool(sections) != (pos is not None):
+        raise ValueError("pos and sections go together")
+    if pos is not None and (pos.dtype != torch.int32 or tuple(pos.shape) != (q.shape[0], len(sections))):
+        raise ValueError(f"pos {tuple(pos.shape)} {pos.dtype}, {(q.shape[0], len(sections))} int32 expected")
+    for name, w in weights.items():
+        _check_f32(name, w, d)
+        if w is not None and k is None and name.startswith("k"):
+            raise ValueError(f"{name} without k")
+    return d, hk, sections
+
+
+def _sections_ptr(sections):
+    return (ctypes.c_int32 * len(sections))(*sections) if sections else None
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], n_heads: int, n_heads_k: Optional[int] = None, norm="l2",
+                 q_w: Optional[torch.Tensor] = None, q_b: Optional[torch.Tensor] = None,
+                 k_w: Optional[torch.Tensor] = None, k_b: Optional[torch.Tensor] = None, eps: float = 1e-12,
+                 pos: Optional[torch.Tensor] = None, sections=(), base: float = 100.0, per_axis: bool = True,
+                 interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None):
+    """(q', k'): every head normed (None, "l2", "rms" or "layer") and rotated by its
+    token's positions, in one pass.
+
+    q [n, n_heads * d], k [n, n_heads_k * d] or None; rows may be slices of a wider
+    projection. pos int32 [n, axes] and sections, the pairs of channels that each
+    axis turns: with per_axis each axis has channels and a ladder of frequencies
+    base^(-j / section) of its own, without it all pairs share one. Pairs are a half apart,
+    or neighbours (interleaved). q_out may be q and k_out k."""
+    d, hk, sections = _qk_inputs(q, k, n_heads, n_heads_k, pos, sections, dict(q_w=q_w, q_b=q_b, k_w=k_w, k_b=k_b))
+    n = q.shape[0]
+    if q_out is None:
+        q_out = torch.empty((n, n_heads * d), dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty((n, hk * d), dtype=k.dtype, device=k.device)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    _check_same("q_out", q_out, q, "q")
+    _check_same("k_out", k_out, k, "k")
+    pq, sq = _rows_of("q", q)
+    pk, sk = _rows_of("k", k)
+    dev, (_, _, qw, qb, kw, kb, pp, po, ko) = _pointers(q[:0], None if k is None else k[:0], q_w, q_b, k_w, k_b, pos, q_out,
+                                                        k_out)
+    _run("vggt3_qk_norm_rope", dev, pq, sq, pk, sk, _qk_norm_code(norm), qw, qb, kw, kb, float(eps), pp,
+         _sections_ptr(sections), len(sections), float(base), int(bool(per_axis)), int(bool(interleaved)), po, ko, n,
+         n_heads, hk, d, _dtype_code(q))
+    return q_out, k_out
+
+
+class QkNormRopeGrads(NamedTuple):
+    """Gradients of qk_norm_rope's inputs; None for those that are absent or not wanted."""
+
+    dq: Optional[torch.Tensor] = None
+    dk: Optional[torch.Tensor] = None
+    dq_w: Optional[torch.Tensor] = None
+    dq_b: Optional[torch.Tensor] = None
+    dk_w: Optional[torch.Tensor] = None
+    dk_b: Optional[torch.Tensor] = None
+
+
+def qk_norm_rope_grad_workspace_bytes(n_tokens: int, d_head: int) -> int:
+    return int(lib().vggt3_qk_norm_rope_grad_workspace_bytes(n_tokens, d_head))
+
+
+def qk_norm_rope_grad(q: torch.Tensor, k: Optional[torch.Tensor], dq_out: torch.Tensor,
+                      dk_out: Optional[torch.Tensor], n_heads: int, n_heads_k: Optional[int] = None, norm="l2",
+                      q_w: Optional[torch.Tensor] = None, k_w: Optional[torch.Tensor] = None, bias: bool = False,
+                      eps: float = 1e-12, pos: Optional[torch.Tensor] = None, sections=(), base: float = 100.0,
+                      per_axis: bool = True, interleaved: bool = False, out: Optional[QkNormRopeGrads] = None,
+                      workspace: Optional[torch.Tensor] = None) -> QkNormRopeGrads:
+    """Gradient of qk_norm_rope at its inputs q, k from the gradients dq_out, dk_out of
+    its outputs.
+
+    Gradients of what was given are returned (bias: there were biases, whose values
+    do not enter). With `out`, exactly its tensors are written; out.dq may be
+    dq_out and out.dk dk_out."""
+    d, hk, sections = _qk_inputs(q, k, n_heads, n_heads_k, pos, sections, dict(q_w=q_w, k_w=k_w))
+    n = q.shape[0]
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out go together")
+    _check_same("dq_out", dq_out, q, "q")
+    _check_same("dk_out", dk_out, k, "k")
+    if out is None:
+        wanted = [q_w is not None, bool(bias), k_w is not None, bool(bias) and k is not None]
+        rows = iter(torch.empty((sum(wanted), d), dtype=torch.float32, device=q.device).unbind(0))
+        out = QkNormRopeGrads(torch.empty((n, n_heads * d), dtype=q.dtype, device=q.device),
+                              None if k is None else torch.empty((n, hk * d), dtype=q.dtype, device=q.device),
+                              *[next(rows) if w else None for w in wanted])
+    else:
+        if k is None and (out.dk is not None or out.dk_w is not None or out.dk_b is not None):
+            raise ValueError("gradients of k without k")
+        _check_same("dq", out.dq, q, "q")
+        _check_same("dk", out.dk, k, "k")
+        for name in QkNormRopeGrads._fields[2:]:
+            _check_f32(name, getattr(out, name), d)
+    need = qk_norm_rope_grad_workspace_bytes(n, d) if any(t is not None for t in out[2:]) else 0
+    workspace, nb = _ws(workspace, need, q.device)
+    pq, sq = _rows_of("q", q)
+    pk, sk = _rows_of("k", k)
+    dev, (_, _, dqo, dko, qw, kw, pp, ws, *grads) = _pointers(q[:0], None if k is None else k[:0], dq_out, dk_out, q_w, k_w,
+                                                              pos, workspace, *out)
+    _run("vggt3_qk_norm_rope_grad", dev, pq, sq, pk, sk, dqo, dko, _qk_norm_code(norm), qw, kw, float(eps), pp,
+         _sections_ptr(sections), len(sections), float(base), int(bool(per_axis)), int(bool(interleaved)), *grads, n, n_heads,
+         hk, d, _dtype_code(q), ws, nb)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# The gated delta rule: over whole sequences, its gradient, and a token at a time
+# ---------------------------------------------------------------------------
+
+def _delta_inputs(q, k, v, g, beta, n_heads):
+    """(n, value heads, d_k, d_v)"""
+    _check_tokens("q", q)
+    _check_same("k", k, q, "q")
+    _check_tokens("v", v)
+    n, dk = q.shape[0], _heads_of("q", q, n_heads)
+    if v.shape[0] != n or v.dtype != q.dtype:
+        raise ValueError(f"v {tuple(v.shape)} {v.dtype} does not match q {tuple(q.shape)} {q.dtype}")
+    if beta.dim() != 2 or beta.shape[0] != n or beta.dtype != torch.float32:
+        raise ValueError(f"beta {tuple(beta.shape)} {beta.dtype}, [{n}, value heads] float32 expected")
+    hv = beta.shape[1]
+    dv = _heads_of("v", v, hv)
+    if hv % n_heads:
+        raise ValueError(f"{hv} value heads are not a multiple of {n_heads} key heads")
+    _check_same("g", g, beta, "beta")
+    return n, hv, dk, dv
+
+
+def _delta_seqs(cu_seqlens, max_seqlen):
+    """(sequences, the longest one's length or 0)"""
+    if cu_seqlens is not None and (cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
+        raise ValueError(f"cu_seqlens {tuple(cu_seqlens.shape)} {cu_seqlens.dtype}, int32 [sequences + 1] expected")
+    longest = 0 if max_seqlen is None else int(max_seqlen)
+    if longest < 0:
+        raise ValueError(f"max_seqlen = {max_seqlen} < 0")
+    return 1 if cu_seqlens is None else cu_seqlens.numel() - 1, longest
+
+
+def _check_state(name: str, t: Optional[torch.Tensor], shape) -> None:
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != torch.float32):
+        raise ValueError(f"{name} {tuple(t.shape)} {t.dtype}, {tuple(shape)} float32 expected")
+
+
+def gated_delta_workspace_bytes(n_tokens: int, n_seqs: int, max_seqlen: int, n_heads: int, n_heads_v: int, d_k: int,
+                                d_v: int, dtype_code: int) -> int:
+    return int(lib().vggt3_gated_delta_workspace_bytes(n_tokens, n_seqs, max_seqlen, n_heads, n_heads_v, d_k, d_v,
+                                                       dtype_code))
+
+
+def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor], beta: torch.Tensor,
+                n_heads: int, scale: float = 1.0, state: Optional[torch.Tensor] = None,
+                cu_seqlens: Optional[torch.Tensor] = None, max_seqlen: Optional[int] = None,
+                out: Optional[torch.Tensor] = None, state_out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None):
+    """(o, state_out) of the gated delta rule: S <- e^g S + k (beta (v - e^g S^T k))^T,
+    o = scale S^T q, token by token for each value head.
+
+    q, k [n, n_heads * d_k]; v [n, value heads * d_v]; g (None: no decay) and beta
+    fp32 [n, value heads]; state fp32 [sequences, value heads, d_k, d_v] (None: zeros). Sequence
+    b is rows cu_seqlens[b] .. cu_seqlens[b + 1] (None: all rows are one); rows of no
+    sequence are left as they are. max_seqlen, where it is known, saves work.
+    state_out may be state."""
+    n, hv, dk, dv = _delta_inputs(q, k, v, g, beta, n_heads)
+    nseq, longest = _delta_seqs(cu_seqlens, max_seqlen)
+    shape = (nseq, hv, dk, dv)
+    _check_state("state", state, shape)
+    _check_state("state_out", state_out, shape)
+    _check_same("out", out, v, "v")
+    if out is None:
+        out = torch.empty_like(v)
+    if state_out is None:
+        state_out = torch.empty(shape, dtype=torch.float32, device=v.device)
+    dt = _dtype_code(q)
+    workspace, nb = _ws(workspace, gated_delta_workspace_bytes(n, nseq, longest, n_heads, hv, dk, dv, dt), v.device)
+    dev, (pq, pk, pv, pg, pb, cu, s, o, so, ws) = _pointers(q, k, v, g, beta, cu_seqlens, state, out, state_out, workspace)
+    _run("vggt3_gated_delta", dev, pq, pk, pv, pg, pb, cu, longest, s, float(scale), o, so, n, nseq, n_heads, hv, dk, dv,
+         dt, ws, nb)
+    return out, state_out
+
+
+def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor], beta: torch.Tensor,
+                     n_heads: int, state: torch.Tensor, slots: Optional[torch.Tensor] = None, scale: float = 1.0,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """o of one token of each of several streams by the gated delta rule; their states
+    (fp32 [slots, value heads, d_k, d_v]) are updated in place.
+
+    Row r uses state slots[r] (None: state r). Rows of one slot are that stream's next
+    tokens in order; a slot that does not exist marks a row to be left out (o = 0)."""
+    n, hv, dk, dv = _delta_inputs(q, k, v, g, beta, n_heads)
+    if state.dim() != 4:
+        raise ValueError(f"state {tuple(state.shape)}, [slots, {hv}, {dk}, {dv}] expected")
+    _check_state("state", state, (state.shape[0], hv, dk, dv))
+    if slots is None:
+        if n > state.shape[0]:
+            raise ValueError(f"{n} rows without slots, {state.shape[0]} states")
+    elif slots.dtype != torch.int32 or tuple(slots.shape) != (n,):
+        raise ValueError(f"slots {tuple(slots.shape)} {slots.dtype}, ({n},) int32 expected")
+    _check_same("out", out, v, "v")
+    if out is None:
+        out = torch.empty_like(v)
+    dev, (pq, pk, pv, pg, pb, st, sl, o) = _pointers(q, k, v, g, beta, state, slots, out)
+    _run("vggt3_gated_delta_step", dev, pq, pk, pv, pg, pb, st, state.shape[0], sl, float(scale), o, n, n_heads, hv, dk,
+         dv, _dtype_code(q))
+    return out

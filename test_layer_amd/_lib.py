@@ -16,6 +16,7 @@ c_int = ctypes.c_int32
 c_i64 = ctypes.c_int64
 c_size = ctypes.c_size_t
 c_float = ctypes.c_float
+c_double = ctypes.c_double
 
 # name -> (restype, argtypes), mirroring include/vggt3.h
 SIGNATURES = {
@@ -80,6 +81,18 @@ SIGNATURES = {
     "vggt3_block_join_grad": (c_int, [c_void_p, c_void_p, c_void_p, c_i64, c_void_p, c_int, c_void_p, c_void_p, c_int,
                                       c_void_p, c_float] + [c_void_p] * 10 + [c_i64, c_int, c_int, c_void_p, c_size,
                                                                               c_void_p]),
+    "vggt3_qk_norm_rope": (c_int, [c_void_p, c_i64, c_void_p, c_i64, c_int] + [c_void_p] * 4 + [c_float]
+                           + [c_void_p] * 2 + [c_int, c_double, c_int, c_int] + [c_void_p] * 2
+                           + [c_i64, c_int, c_int, c_int, c_int, c_void_p]),
+    "vggt3_qk_norm_rope_grad_workspace_bytes": (c_size, [c_i64, c_int]),
+    "vggt3_qk_norm_rope_grad": (c_int, [c_void_p, c_i64, c_void_p, c_i64, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                        c_float, c_void_p, c_void_p, c_int, c_double, c_int, c_int] + [c_void_p] * 6
+                                + [c_i64, c_int, c_int, c_int, c_int, c_void_p, c_size, c_void_p]),
+    "vggt3_gated_delta_workspace_bytes": (c_size, [c_i64, c_int, c_i64, c_int, c_int, c_int, c_int, c_int]),
+    "vggt3_gated_delta": (c_int, [c_void_p] * 6 + [c_i64, c_void_p, c_float, c_void_p, c_void_p, c_i64]
+                          + [c_int] * 6 + [c_void_p, c_size, c_void_p]),
+    "vggt3_gated_delta_step": (c_int, [c_void_p] * 6 + [c_i64, c_void_p, c_float, c_void_p, c_i64] + [c_int] * 5
+                               + [c_void_p]),
 }
 
 _lib = None

@@ -36,29 +36,6 @@ int check_join(bool has_f, const void* gate, int64_t gate_tokens, const float* s
   return VGGT3_OK;
 }
 
-struct Region {
-  const char* name;
-  const void* p;
-  size_t bytes;
-  bool written;
-};
-
-// Non-null where needed is the caller's check. 16-byte aligned, and no written
-// region overlapping another one, but for regions `a` and `b`, which may be one
-// and the same (a row is read whole before it is written).
-int check_regions(const Region* rs, int count, int a, int b) {
-  for (int i = 0; i < count; ++i)
-    if (rs[i].p && !aligned16(rs[i].p)) return fail(VGGT3_EINVAL, "%s is not 16-byte aligned", rs[i].name);
-  for (int i = 0; i < count; ++i)
-    for (int j = i + 1; j < count; ++j) {
-      if (!(rs[i].written || rs[j].written)) continue;
-      if (i == a && j == b && rs[i].p == rs[j].p) continue;
-      if (overlap(rs[i].p, rs[i].bytes, rs[j].p, rs[j].bytes))
-        return fail(VGGT3_EINVAL, "%s and %s overlap", rs[i].name, rs[j].name);
-    }
-  return VGGT3_OK;
-}
-
 // Tokens that share a gate row: at most all of them.
 int64_t tokens_per_gate(const void* gate, int64_t gate_tokens, int64_t n) {
   return gate == nullptr ? 1 : gate_tokens < n ? gate_tokens : n > 0 ? n : 1;
@@ -112,7 +89,7 @@ int vggt3_block_join(const void* x, const void* f, const void* gate, int64_t gat
                        {"y", y, tb, true},
                        {"y_codes", y_codes, (size_t)mx4::code_bytes(n_tokens, channels), true},
                        {"y_scales", y_scales, (size_t)mx4::scale_bytes(n_tokens, channels), true}};
-  rc = check_regions(rs, 12, 0, 8);  // in place: r may be x
+  rc = check_regions(rs, 12, {{0, 8}});  // in place: r may be x
   if (rc) return rc;
   join::Args a{};
   a.x = x; a.f = f; a.gate = gate; a.scale = scale;
@@ -174,7 +151,7 @@ int vggt3_block_join_grad(const void* r, const void* f, const void* gate, int64_
                        {"dscale", dscale, vb, true},  {"dpost_w", dpost_w, vb, true},
                        {"dpost_b", dpost_b, vb, true}, {"dpre_w", dpre_w, vb, true},
                        {"dpre_b", dpre_b, vb, true},  {"workspace", n_tokens > 0 ? workspace : nullptr, l.total, true}};
-  rc = check_regions(rs, 18, 7, 9);  // in place: dx may be dr
+  rc = check_regions(rs, 18, {{7, 9}});  // in place: dx may be dr
   if (rc) return rc;
   join::Args a{};
   a.x = r; a.f = f; a.gate = gate; a.scale = scale;

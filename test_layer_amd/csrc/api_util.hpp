@@ -7,7 +7,9 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <string>
+#include <utility>
 
 #include "../../include/vggt3.h"
 
@@ -46,6 +48,33 @@ inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   if (a == nullptr || b == nullptr || an == 0 || bn == 0) return false;
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
   return a0 < b0 + bn && b0 < a0 + an;
+}
+
+// A tensor of a call: its bytes, whether they are written, and the alignment asked of it.
+struct Region {
+  const char* name;
+  const void* p;
+  size_t bytes;
+  bool written;
+  size_t align = 16;
+};
+
+// Non-null where needed is the caller's check. Aligned, and no written region
+// overlapping another one, but for the pairs `same`, which may be one and the same
+// (a row is read whole before it is written).
+inline int check_regions(const Region* rs, int count, std::initializer_list<std::pair<int, int>> same) {
+  for (int i = 0; i < count; ++i)
+    if (rs[i].p && (reinterpret_cast<uintptr_t>(rs[i].p) & (rs[i].align - 1)))
+      return fail(VGGT3_EINVAL, "%s is not %zu-byte aligned", rs[i].name, rs[i].align);
+  for (int i = 0; i < count; ++i)
+    for (int j = i + 1; j < count; ++j) {
+      if (!(rs[i].written || rs[j].written)) continue;
+      bool may = false;
+      for (const auto& s : same) may = may || (i == s.first && j == s.second && rs[i].p == rs[j].p);
+      if (!may && overlap(rs[i].p, rs[i].bytes, rs[j].p, rs[j].bytes))
+        return fail(VGGT3_EINVAL, "%s and %s overlap", rs[i].name, rs[j].name);
+    }
+  return VGGT3_OK;
 }
 
 inline bool valid_dtype(int32_t dt) { return dt == VGGT3_BF16 || dt == VGGT3_F32; }

@@ -1,0 +1,54 @@
+// Launchers of the gated delta rule's kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace vggt3 {
+namespace delta {
+
+struct Args {
+  const void* q;  // [n][hk dk]
+  const void* k;
+  const void* v;      // [n][hv dv]
+  const float* g;     // NULL or [n][hv]
+  const float* beta;  // [n][hv]
+  const int32_t* cu;  // NULL (one sequence) or [nseq + 1]
+  const float* state; // NULL (zeros) or [nseq][hv][dk][dv]
+  void* o;
+  float* state_out;
+  // pieces (segments) of a sequence that are worked on at once
+  float* seg_n;  // [pieces][hv][dk][dv]: a piece's last state from none; then its first state
+  float* seg_m;  // [pieces][hv][dk][dk]: what it makes of its first state
+  int64_t n, per;  // per: tokens of a piece
+  int nseq, hk, hv, dk, dv;
+  float scale;
+};
+
+// How a call's sequences are cut: pieces of `per` tokens, at most `pieces` in all;
+// split: whether a sequence may have more than one.
+struct Plan {
+  int64_t per, pieces;
+  bool split;
+};
+Plan plan(int64_t n, int nseq, int64_t longest, int hv, int dk, int dv);
+
+struct StepArgs {
+  const void* q;  // [rows][hk dk]
+  const void* k;
+  const void* v;         // [rows][hv dv]
+  const float* g;        // NULL or [rows][hv]
+  const float* beta;     // [rows][hv]
+  float* state;          // [n_slots][hv][dk][dv], updated
+  const int32_t* slots;  // NULL (row r: slot r) or [rows]
+  void* o;
+  int64_t n_slots;
+  int rows, hk, hv, dk, dv;
+  float scale;
+};
+
+hipError_t launch_step(const StepArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_forward(const Args& a, const Plan& p, bool bf16, hipStream_t stream);
+
+}  // namespace delta
+}  // namespace vggt3

@@ -1,0 +1,289 @@
+// Device helpers of the gated delta rule's kernels: products of 16 x 16 tiles in
+// fp32 or in split bf16, a chunk's decays, and the inverse of its unit triangle.
+//
+// Tiles are held as the matrix unit leaves them: lane (c = l % 16, q = l / 16)
+// has rows 4q .. 4q+3 of column c. Two tiles one above the other are, register
+// for register, the right operand of a product over their 32 rows, if the left
+// operand takes its 32 columns in the same order: element j of lane quarter q is
+// column 16 (j / 4) + 4q + j % 4. So a product's result goes into the next product
+// without leaving the wave's registers.
+#pragma once
+
+#include "bf16_ops.hpp"
+
+namespace vggt3 {
+namespace delta {
+
+// Tokens of a chunk: one 32-deep product. (A chunk of 64 costs as many products a
+// token at 128-wide heads and more at 64-wide ones, since the triangle's share
+// grows with the chunk.)
+constexpr int kChunk = 32;
+
+// Operand of a 32-deep product. bf16: hi + lo, 16 bits of the value (hi alone where
+// the value is bf16 already); fp32: the value.
+template <class T>
+struct Frag;
+template <>
+struct Frag<uint16_t> {
+  bf16x8 hi, lo;
+};
+template <>
+struct Frag<float> {
+  f32x4 a, b;
+};
+
+// c += A B. NA, NB: parts of A and B that count (bf16). Two values of two parts
+// each differ from fp32 ones by the product of their second parts and by what the
+// second parts leave out, 2^-17 relative at most each.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mm(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x4 c) {
+  if constexpr (NB == 2) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.hi, b.lo, c, 0, 0, 0);
+  if constexpr (NA == 2) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.lo, b.hi, c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.hi, b.hi, c, 0, 0, 0);
+}
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mm(const Frag<float>& a, const Frag<float>& b, f32x4 c) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[e], b.a[e], c, 0, 0, 0);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.b[e], b.b[e], c, 0, 0, 0);
+  return c;
+}
+// c += A B over 16: one tile each, in fp32.
+__device__ __forceinline__ f32x4 mm16(const f32x4& a, const f32x4& b, f32x4 c) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+  return c;
+}
+
+__device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+
+// Two tiles as an operand.
+__device__ __forceinline__ void make(Frag<float>& f, const f32x4& x, const f32x4& y) {
+  f.a = x;
+  f.b = y;
+}
+__device__ __forceinline__ void make(Frag<uint16_t>& f, const f32x4& x, const f32x4& y) {
+  u32x4 h, l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float p = i < 2 ? x[2 * i] : y[2 * i - 4], q = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
+    h[i] = pack_bf16x2(p, q);
+    l[i] = pack_bf16x2(p - bf16_lo(h[i]), q - bf16_hi(h[i]));
+  }
+  f.hi = as_bf16x8(h);
+  f.lo = as_bf16x8(l);
+}
+
+// Operands through LDS: 2 KB each, 16 bytes a lane twice.
+__device__ __forceinline__ void put(u32x4* at, const Frag<uint16_t>& f, int lane) {
+  at[lane] = as_u32x4(f.hi);
+  at[64 + lane] = as_u32x4(f.lo);
+}
+__device__ __forceinline__ void put(u32x4* at, const Frag<float>& f, int lane) {
+  at[lane] = __builtin_bit_cast(u32x4, f.a);
+  at[64 + lane] = __builtin_bit_cast(u32x4, f.b);
+}
+__device__ __forceinline__ void get(Frag<uint16_t>& f, const u32x4* at, int lane) {
+  f.hi = as_bf16x8(at[lane]);
+  f.lo = as_bf16x8(at[64 + lane]);
+}
+__device__ __forceinline__ void get(Frag<float>& f, const u32x4* at, int lane) {
+  f.a = __builtin_bit_cast(f32x4, at[lane]);
+  f.b = __builtin_bit_cast(f32x4, at[64 + lane]);
+}
+
+// 8 values of a row, at a 16-byte boundary.
+__device__ __forceinline__ void row8(Frag<uint16_t>& f, const uint16_t* p) { f.hi = ld_op(p); }
+__device__ __forceinline__ void row8(Frag<float>& f, const float* p) {
+  f.a = *reinterpret_cast<const f32x4*>(p);
+  f.b = *reinterpret_cast<const f32x4*>(p + 4);
+}
+__device__ __forceinline__ void clear(Frag<uint16_t>& f) { f.hi = as_bf16x8(u32x4{0, 0, 0, 0}); }
+__device__ __forceinline__ void clear(Frag<float>& f) { f.a = f.b = zero4(); }
+
+// A head's channels are the rows of its state's tiles in an order in which 8
+// neighbours are an operand's 8 elements: row p of tile t is channel
+// 32 (t / 2) + 8 (p / 4) + 4 (t % 2) + p % 4.
+__device__ __forceinline__ int channel(int tile, int row) {
+  return 32 * (tile / 2) + 8 * (row / 4) + 4 * (tile % 2) + row % 4;
+}
+
+// Left operand X^T for tile t of X's channels, over the chunk's tokens, from X
+// [kChunk][pitch] in LDS. bf16: transposing reads, each lane of 16 giving the
+// address of 4 neighbouring channels of one token.
+template <int PITCH>
+__device__ __forceinline__ void columns(Frag<uint16_t>& f, const uint16_t* x, int tile, int lane) {
+  const int s = lane % 16, q = lane / 16;
+  const uint16_t* p = x + (4 * q + s / 4) * PITCH + 32 * (tile / 2) + 8 * (s % 4) + 4 * (tile % 2);
+  f.hi = tr_op(p, p + 16 * PITCH);
+}
+template <int PITCH>
+__device__ __forceinline__ void columns(Frag<float>& f, const float* x, int tile, int lane) {
+  const int q = lane / 16;
+  const float* p = x + 4 * q * PITCH + channel(tile, lane % 16);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    f.a[r] = p[r * PITCH];
+    f.b[r] = p[(16 + r) * PITCH];
+  }
+}
+
+// N neighbouring values <-> fp32 (N = 1, 2 or 4, aligned to N values).
+template <int N>
+__device__ __forceinline__ void load_n(float* o, const uint16_t* p) {
+  if constexpr (N == 1) {
+    o[0] = bf16_bits_to_f32(*p);
+  } else if constexpr (N == 2) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    o[0] = bf16_lo(w);
+    o[1] = bf16_hi(w);
+  } else {
+    const u32x2 w = ld8(p);
+    o[0] = bf16_lo(w[0]);
+    o[1] = bf16_hi(w[0]);
+    o[2] = bf16_lo(w[1]);
+    o[3] = bf16_hi(w[1]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_n(float* o, const float* p) {
+  typedef float vec __attribute__((ext_vector_type(N)));
+  if constexpr (N == 1) {
+    o[0] = *p;
+  } else {
+    const vec w = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = w[i];
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_n(uint16_t* p, const float* v) {
+  if constexpr (N == 1) {
+    *p = f32_to_bf16_bits(v[0]);
+  } else if constexpr (N == 2) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0], v[1]);
+  } else {
+    st8(p, u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_n(float* p, const float* v) {
+  typedef float vec __attribute__((ext_vector_type(N)));
+  if constexpr (N == 1) {
+    *p = v[0];
+  } else {
+    vec w;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = v[i];
+    *reinterpret_cast<vec*>(p) = w;
+  }
+}
+
+// Between a wave's writes to LDS and its reads of what other lanes wrote: LDS
+// operations of one wave are carried out in order, so only the compiler has to
+// keep it.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// x + w * (x of lane M of the lane's 16)
+template <int M>
+__device__ __forceinline__ float add_from(float x, float w) {
+  const float y = __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x150 + M, 0xf, 0xf, true));
+  return __builtin_fmaf(w, y, x);
+}
+template <int M>
+__device__ __forceinline__ void eliminate(f32x4& x, f32x4& y, const float* nx, const float* ny) {
+  if constexpr (M < 15) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      x[r] = add_from<M>(x[r], -nx[M]);
+      y[r] = add_from<M>(y[r], -ny[M]);
+    }
+    eliminate<M + 1>(x, y, nx, ny);
+  }
+}
+
+// A strictly lower triangle N [32][32] as left-operand tiles (lane (i, q) holds
+// columns 4q .. 4q+3 of row i): n00, n11 its diagonal tiles, n10 the one below.
+// t00, t10, t11: (I + N)^-1 in the same form. Row by row in the diagonal tiles
+// (forward substitution, stable for any N; repeated squaring of N loses digits
+// where keys repeat), then t10 = -t11 n10 t00. scratch: 2 x 16 x 20 floats of LDS.
+__device__ __forceinline__ void unit_inverse(const f32x4& n00, const f32x4& n10, const f32x4& n11, f32x4& t00,
+                                             f32x4& t10, f32x4& t11, float* scratch, int lane) {
+  const int i = lane % 16, q = lane / 16;
+  float* a = scratch + i * 20;
+  float* b = scratch + (16 + i) * 20;
+  *reinterpret_cast<f32x4*>(a + 4 * q) = n00;
+  *reinterpret_cast<f32x4*>(b + 4 * q) = n11;
+  wave_lds_order();
+  float nx[16], ny[16];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const f32x4 u = *reinterpret_cast<const f32x4*>(a + 4 * s), w = *reinterpret_cast<const f32x4*>(b + 4 * s);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      nx[4 * s + r] = u[r];
+      ny[4 * s + r] = w[r];
+    }
+  }
+  wave_lds_order();
+  f32x4 one;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) one[r] = 4 * q + r == i ? 1.0f : 0.0f;
+  t00 = t11 = one;
+  eliminate<0>(t00, t11, nx, ny);
+  const f32x4 c00 = mm16(t00, one, zero4());  // t00 as a result tile: its transpose as an operand
+  const f32x4 p = mm16(n10, c00, zero4());
+  t10 = mm16(p, t11, zero4());
+#pragma unroll
+  for (int r = 0; r < 4; ++r) t10[r] = -t10[r];
+}
+
+// A sequence's piece: rows first .. first + len - 1, piece `seg` of `segs` of
+// sequence b. Rows and sequence boundaries are held inside [0, n], whatever cu
+// says.
+struct Piece {
+  int64_t first;   // row of its first token
+  int64_t begin;   // row of its sequence's first token
+  int len;         // tokens
+  int b, seg, segs;
+};
+
+__device__ __forceinline__ int64_t bound(const int32_t* cu, int64_t i, int64_t n) {
+  if (cu == nullptr) return i == 0 ? 0 : n;
+  const int64_t v = cu[i];
+  return v < 0 ? 0 : v > n ? n : v;
+}
+
+// Piece `sid`: sequence b's pieces of `per` tokens are numbered from
+// cu[b] / per + b on, which leaves room for each sequence's last, shorter piece (an
+// empty sequence has one piece of no tokens). A 64-ary search by the wave.
+__device__ __forceinline__ Piece find_piece(const int32_t* cu, int nseq, int64_t n, int64_t per, int64_t sid, int lane) {
+  int64_t lo = 0, size = nseq;
+  while (size > 1) {
+    const int64_t stride = (size + 63) / 64, at = lo + lane * stride;
+    const bool before = lane * stride < size && bound(cu, at, n) / per + at <= sid;
+    const int64_t found = __popcll(__ballot(before));
+    lo += (found > 0 ? found - 1 : 0) * stride;
+    size = size < stride ? size : stride;
+    if (lo + size > nseq) size = nseq - lo;
+  }
+  Piece p;
+  p.b = __builtin_amdgcn_readfirstlane((int)lo);
+  p.begin = bound(cu, p.b, n);
+  const int64_t end = bound(cu, p.b + 1, n), len = end > p.begin ? end - p.begin : 0;
+  p.seg = (int)(sid - (p.begin / per + p.b));
+  p.segs = len > 0 ? (int)((len + per - 1) / per) : 1;
+  p.first = p.begin + p.seg * per;
+  const int64_t left = len - p.seg * per;
+  p.len = (int)(left < 0 ? 0 : left < per ? left : per);
+  if (p.seg < 0 || p.seg >= p.segs) p.seg = -1;
+  return p;
+}
+
+}  // namespace delta
+}  // namespace vggt3
