@@ -689,8 +689,8 @@ int vggt3_qk_norm_rope_grad(const void* q, int64_t q_stride, const void* k, int6
  *   workspace    at least vggt3_gated_delta_workspace_bytes(...) bytes (may be NULL when
  *                that is 0).
  * Computed by chunks of 32 tokens (the same values by matrix products): S, decays,
- * sums and the chunk's triangular inverse are fp32 (bf16 dtype: products of bf16 pairs,
- * 2^-17 relative), o is rounded once. A value that is not finite makes its sequence's
+ * sums and the chunk's triangular inverse are fp32 (bf16 dtype: products of fp32 values
+ * in three bf16 parts; two for o), o is rounded once. A value that is not finite makes its sequence's
  * results not finite from its chunk on, other sequences' not at all. Heads of 64 or
  * 128 each way. The results are the same bits each time. Outputs and the workspace must
  * not overlap anything else. n_tokens == 0 copies state to state_out.
@@ -701,6 +701,30 @@ int vggt3_gated_delta(const void* q, const void* k, const void* v, const float* 
                       const int32_t* cu_seqlens, int64_t max_seqlen, const float* state, float scale, void* o,
                       float* state_out, int64_t n_tokens, int32_t n_seqs, int32_t n_heads, int32_t n_heads_v,
                       int32_t d_k, int32_t d_v, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of vggt3_gated_delta, from its inputs (nothing is kept between the calls).
+ *
+ *   d_o          gradient of o, [n_tokens][n_heads_v][d_v], dtype.
+ *   dstate_out   gradient of state_out; NULL: 0.
+ *   dq, dk, dv   in dtype, of the shapes of q, k, v (those of a key head summed over its
+ *                value heads); dg, dbeta float32 [n_tokens][n_heads_v] (dg with g only);
+ *                dstate float32, of state (may be dstate_out; may be asked for without a
+ *                state). Each may be NULL (not wanted). Rows of no sequence are left as
+ *                they are.
+ *   workspace    at least vggt3_gated_delta_grad_workspace_bytes(...) bytes: the state
+ *                before, and the gradient of the state after, every 32 tokens.
+ * Rounding as in the forward; no atomics, the same bits each time. n_tokens == 0 copies
+ * dstate_out to dstate.
+ */
+size_t vggt3_gated_delta_grad_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int64_t max_seqlen, int32_t n_heads,
+                                              int32_t n_heads_v, int32_t d_k, int32_t d_v, int32_t dtype);
+int vggt3_gated_delta_grad(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                           const int32_t* cu_seqlens, int64_t max_seqlen, const float* state, float scale,
+                           const void* d_o, const float* dstate_out, void* dq, void* dk, void* dv, float* dg,
+                           float* dbeta, float* dstate, int64_t n_tokens, int32_t n_seqs, int32_t n_heads,
+                           int32_t n_heads_v, int32_t d_k, int32_t d_v, int32_t dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 /*
  * One token of each of several streams by the same rule, on states in a cache.

@@ -1067,6 +1067,59 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[t
     return out, state_out
 
 
+class GatedDeltaGrads(NamedTuple):
+    """Gradients of gated_delta's inputs; None for those that are absent or not wanted."""
+
+    dq: Optional[torch.Tensor] = None
+    dk: Optional[torch.Tensor] = None
+    dv: Optional[torch.Tensor] = None
+    dg: Optional[torch.Tensor] = None
+    dbeta: Optional[torch.Tensor] = None
+    dstate: Optional[torch.Tensor] = None
+
+
+def gated_delta_grad_workspace_bytes(n_tokens: int, n_seqs: int, max_seqlen: int, n_heads: int, n_heads_v: int, d_k: int,
+                                     d_v: int, dtype_code: int) -> int:
+    return int(lib().vggt3_gated_delta_grad_workspace_bytes(n_tokens, n_seqs, max_seqlen, n_heads, n_heads_v, d_k, d_v,
+                                                            dtype_code))
+
+
+def gated_delta_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor], beta: torch.Tensor,
+                     d_o: torch.Tensor, n_heads: int, dstate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                     state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                     max_seqlen: Optional[int] = None, out: Optional[GatedDeltaGrads] = None,
+                     workspace: Optional[torch.Tensor] = None) -> GatedDeltaGrads:
+    """Gradient of gated_delta at its inputs from the gradients d_o of o and dstate of
+    state_out (None: zeros).
+
+    Gradients of what was given are returned. With `out`, exactly its tensors are
+    written; out.dstate may be dstate. Rows of no sequence are left as they are."""
+    n, hv, dk, dv = _delta_inputs(q, k, v, g, beta, n_heads)
+    nseq, longest = _delta_seqs(cu_seqlens, max_seqlen)
+    shape = (nseq, hv, dk, dv)
+    _check_state("state", state, shape)
+    _check_state("dstate", dstate, shape)
+    _check_same("d_o", d_o, v, "v")
+    if out is None:
+        out = GatedDeltaGrads(torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
+                              None if g is None else torch.empty_like(g), torch.empty_like(beta),
+                              None if state is None else torch.empty_like(state))
+    else:
+        if out.dg is not None and g is None:
+            raise ValueError("dg without g")
+        for name, t, ref, what in (("dq", out.dq, q, "q"), ("dk", out.dk, k, "k"), ("dv", out.dv, v, "v"),
+                                   ("dg", out.dg, g, "g"), ("dbeta", out.dbeta, beta, "beta")):
+            _check_same(name, t, ref, what)
+        _check_state("out.dstate", out.dstate, shape)
+    dt = _dtype_code(q)
+    workspace, nb = _ws(workspace, gated_delta_grad_workspace_bytes(n, nseq, longest, n_heads, hv, dk, dv, dt), v.device)
+    dev, (pq, pk, pv, pg, pb, cu, s, do, ds, ws, *grads) = _pointers(q, k, v, g, beta, cu_seqlens, state, d_o, dstate,
+                                                                     workspace, *out)
+    _run("vggt3_gated_delta_grad", dev, pq, pk, pv, pg, pb, cu, longest, s, float(scale), do, ds, *grads, n, nseq,
+         n_heads, hv, dk, dv, dt, ws, nb)
+    return out
+
+
 def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor], beta: torch.Tensor,
                      n_heads: int, state: torch.Tensor, slots: Optional[torch.Tensor] = None, scale: float = 1.0,
                      out: Optional[torch.Tensor] = None) -> torch.Tensor:

@@ -91,6 +91,9 @@ SIGNATURES = {
     "vggt3_gated_delta_workspace_bytes": (c_size, [c_i64, c_int, c_i64, c_int, c_int, c_int, c_int, c_int]),
     "vggt3_gated_delta": (c_int, [c_void_p] * 6 + [c_i64, c_void_p, c_float, c_void_p, c_void_p, c_i64]
                           + [c_int] * 6 + [c_void_p, c_size, c_void_p]),
+    "vggt3_gated_delta_grad_workspace_bytes": (c_size, [c_i64, c_int, c_i64, c_int, c_int, c_int, c_int, c_int]),
+    "vggt3_gated_delta_grad": (c_int, [c_void_p] * 6 + [c_i64, c_void_p, c_float] + [c_void_p] * 8 + [c_i64]
+                               + [c_int] * 6 + [c_void_p, c_size, c_void_p]),
     "vggt3_gated_delta_step": (c_int, [c_void_p] * 6 + [c_i64, c_void_p, c_float, c_void_p, c_i64] + [c_int] * 5
                                + [c_void_p]),
 }

@@ -24,7 +24,7 @@ ARCH = "gfx950"
 SOURCES = ["api.hip", "shortconv.hip", "ttt_write_bf16.hip", "ttt_read_bf16.hip", "ttt_f32.hip", "reduce.hip",
            "muon.hip", "wide_mlp.hip", "wide_muon.hip", "api_mx4.hip", "mx4_quant.hip", "mx4_gemm.hip",
            "api_join.hip", "block_join.hip", "api_qk.hip", "qk_rope.hip", "api_delta.hip", "delta_scan.hip",
-           "delta_step.hip"]
+           "delta_grad.hip", "delta_step.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -55,6 +55,25 @@ Ws forward_ws(const Shape& s, const delta::Plan& p) {
   return w;
 }
 
+// Workspace of the gradient: [states before chunks | gradients after chunks | pieces,
+// as the forward's | dq and dk by value head, where these share a key head].
+struct GradWs {
+  size_t dstates, seg_n, seg_m, dq, dk, total;
+};
+GradWs grad_ws(const Shape& s, const delta::Plan& p) {
+  const size_t all = round256((size_t)delta::chunk_slots(s.n, s.nseq) * s.state());
+  const Ws f = forward_ws(s, p);
+  GradWs w;
+  w.dstates = all;
+  w.seg_n = 2 * all;
+  w.seg_m = w.seg_n + f.m;
+  w.dq = w.seg_n + f.total;
+  const size_t part = s.hv == s.hk ? 0 : round256((size_t)s.n * s.hv * s.dk * sizeof(float));
+  w.dk = w.dq + part;
+  w.total = w.dk + part;
+  return w;
+}
+
 int check_scale(float scale) {
   if (!std::isfinite(scale)) return fail(VGGT3_EINVAL, "scale = %g", (double)scale);
   return VGGT3_OK;
@@ -120,6 +139,80 @@ int vggt3_gated_delta(const void* q, const void* k, const void* v, const float* 
   a.scale = scale;
   rc = check_hip(delta::launch_forward(a, p, dtype == VGGT3_BF16, static_cast<hipStream_t>(stream)),
                  "gated delta rule launch");
+  return rc ? rc : ok();
+}
+
+size_t vggt3_gated_delta_grad_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int64_t max_seqlen, int32_t n_heads,
+                                              int32_t n_heads_v, int32_t d_k, int32_t d_v, int32_t dtype) {
+  const Shape s{n_tokens, n_seqs, n_heads, n_heads_v, d_k, d_v, dtype};
+  if (check_shape(s) != VGGT3_OK || max_seqlen < 0) return 0;
+  return grad_ws(s, plan_of(s, max_seqlen)).total;
+}
+
+int vggt3_gated_delta_grad(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                           const int32_t* cu_seqlens, int64_t max_seqlen, const float* state, float scale,
+                           const void* d_o, const float* dstate_out, void* dq, void* dk, void* dv, float* dg,
+                           float* dbeta, float* dstate, int64_t n_tokens, int32_t n_seqs, int32_t n_heads,
+                           int32_t n_heads_v, int32_t d_k, int32_t d_v, int32_t dtype, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const Shape s{n_tokens, n_seqs, n_heads, n_heads_v, d_k, d_v, dtype};
+  int rc = check_shape(s);
+  if (!rc) rc = check_seqs(s, cu_seqlens, max_seqlen);
+  if (!rc) rc = check_scale(scale);
+  if (rc) return rc;
+  if (n_tokens > 0) {
+    const void* need[] = {q, k, v, beta, d_o};
+    const char* names[] = {"q", "k", "v", "beta", "d_o"};
+    for (int i = 0; i < 5; ++i)
+      if (need[i] == nullptr) return fail(VGGT3_EINVAL, "%s is NULL", names[i]);
+  }
+  if (dg && !g) return fail(VGGT3_EINVAL, "dg without g");
+  const delta::Plan p = plan_of(s, max_seqlen);
+  const GradWs w = grad_ws(s, p);
+  rc = check_grid(p.pieces * s.hv);
+  if (!rc) rc = check_grid(delta::chunk_slots(n_tokens, n_seqs) * s.hv);
+  if (rc) return rc;
+  if (workspace == nullptr || workspace_bytes < w.total)
+    return fail(VGGT3_EWORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : (size_t)0, w.total);
+  const size_t states = (size_t)n_seqs * s.state();
+  const Region rs[] = {{"q", q, s.keys(), false},
+                       {"k", k, s.keys(), false},
+                       {"v", v, s.values(), false},
+                       {"g", g, s.scalars(), false, 4},
+                       {"beta", beta, s.scalars(), false, 4},
+                       {"cu_seqlens", cu_seqlens, ((size_t)n_seqs + 1) * sizeof(int32_t), false, 4},
+                       {"state", state, states, false},
+                       {"d_o", d_o, s.values(), false},
+                       {"dstate_out", dstate_out, states, false},
+                       {"dq", dq, s.keys(), true},
+                       {"dk", dk, s.keys(), true},
+                       {"dv", dv, s.values(), true},
+                       {"dg", dg, s.scalars(), true, 4},
+                       {"dbeta", dbeta, s.scalars(), true, 4},
+                       {"dstate", dstate, states, true},
+                       {"workspace", workspace, w.total, true}};
+  rc = check_regions(rs, 16, {{8, 14}});  // in place: dstate may be dstate_out
+  if (rc) return rc;
+  char* ws = static_cast<char*>(workspace);
+  delta::Args a{};
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.cu = cu_seqlens; a.state = state;
+  a.dout = d_o; a.dlast = dstate_out; a.dfirst = dstate;
+  a.states = reinterpret_cast<float*>(ws);
+  a.dstates = reinterpret_cast<float*>(ws + w.dstates);
+  a.seg_n = reinterpret_cast<float*>(ws + w.seg_n);
+  a.seg_m = reinterpret_cast<float*>(ws + w.seg_m);
+  a.dq = dq; a.dk_out = dk; a.dv_out = dv; a.dg = dg; a.dbeta = dbeta;
+  if (s.hv != s.hk) {
+    a.dq_part = reinterpret_cast<float*>(ws + w.dq);
+    a.dk_part = reinterpret_cast<float*>(ws + w.dk);
+  }
+  a.n = n_tokens; a.per = p.per; a.nseq = n_seqs; a.hk = n_heads; a.hv = n_heads_v; a.dk = d_k; a.dv = d_v;
+  a.scale = scale;
+  const bool bf16 = dtype == VGGT3_BF16;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  rc = check_hip(delta::launch_states(a, p, bf16, st), "gated delta states launch");
+  if (!rc) rc = check_hip(delta::launch_back(a, p, bf16, st), "gated delta reverse launch");
+  if (!rc) rc = check_hip(delta::launch_grad(a, bf16, st), "gated delta gradient launch");
   return rc ? rc : ok();
 }
 

@@ -20,6 +20,19 @@ struct Args {
   // pieces (segments) of a sequence that are worked on at once
   float* seg_n;  // [pieces][hv][dk][dv]: a piece's last state from none; then its first state
   float* seg_m;  // [pieces][hv][dk][dk]: what it makes of its first state
+  // gradient
+  const void* dout;    // of o
+  const float* dlast;  // of state_out: NULL (zeros) or [nseq][hv][dk][dv]
+  float* dfirst;       // of state
+  float* states;       // [chunks][hv][dk][dv]: the state before each chunk
+  float* dstates;      // the gradient of the state after each chunk
+  void* dq;            // each NULL: not wanted
+  void* dk_out;
+  void* dv_out;
+  float* dg;
+  float* dbeta;
+  float* dq_part;  // [n][hv][dk], where value heads share a key head
+  float* dk_part;
   int64_t n, per;  // per: tokens of a piece
   int nseq, hk, hv, dk, dv;
   float scale;
@@ -49,6 +62,14 @@ struct StepArgs {
 
 hipError_t launch_step(const StepArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_forward(const Args& a, const Plan& p, bool bf16, hipStream_t stream);
+
+// The gradient: the state before every chunk, then the gradient of the state after
+// every chunk (and dfirst), then everything else chunk by chunk. Chunks of sequence
+// b are numbered from cu[b] / 32 + b on.
+inline int64_t chunk_slots(int64_t n, int nseq) { return n / 32 + nseq; }
+hipError_t launch_states(const Args& a, const Plan& p, bool bf16, hipStream_t stream);
+hipError_t launch_back(const Args& a, const Plan& p, bool bf16, hipStream_t stream);
+hipError_t launch_grad(const Args& a, bool bf16, hipStream_t stream);
 
 }  // namespace delta
 }  // namespace vggt3

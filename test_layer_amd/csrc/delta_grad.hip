@@ -1,0 +1,435 @@
+// The gradient of the gated delta rule, chunk by chunk, from the state S before each
+// chunk and the gradient dS of the state after it (delta_scan.hip). With y, u, T, B
+// and the decays of the forward, du, dR of the reverse scan,
+//
+//   dV = dR,      x = du - N'^T dR  (N' = N without its beta),   dbeta_i = x_i . y_i
+//   F = scale D . (dO u^T) (lower),    E = D . (dR u^T) (strictly lower)
+//   dQ = scale G . (dO S^T) + F K
+//   dK = F^T Q + G_end / G . (u dS^T) - G . (dR S^T) - E K - E^T K
+//   dg_t = sum over i >= t of (o_i . dO_i - v_i . dR_i) + <dS, the state after>
+//
+// The last line: G enters o_i as its query's factor, and each token's error as its
+// read key's factor minus its write key's, whose sum is -v_i . dR_i; a whole chunk
+// back from its end, what the later chunks say is in <dS, state>. (One such sum over
+// the whole sequence would lose the small terms; over 32 tokens it does not.)
+//
+// Four waves to a chunk and head. First each forms one of the 32 x 32 operands, then
+// each has a quarter of the value channels (u, du, dR, o and the row sums), then two
+// forms each of F and E, then a quarter of the key channels (dQ, dK).
+#include "delta_chunk.hpp"
+
+namespace vggt3 {
+namespace delta {
+namespace {
+
+constexpr int kWaves = 4;
+
+template <class T, int DK, int DV>
+struct GradShared {
+  static constexpr int kParts = sizeof(T) == 2 ? 2 : 1;  // of y and dR as operands of bf16 results
+  T k[kChunk][kPitch<T, DK>];
+  T q[kChunk][kPitch<T, DK>];
+  T y[kParts][kChunk][kPitch<T, DV>];
+  T dr[kParts][kChunk][kPitch<T, DV>];
+  u32x4 op[5][2 * kOperand<T>];  // T, T^T, B, B^T, N'^T; then F, F^T, -E, -E^T
+  Rows rows;
+  float along[kWaves][kChunk], step[kWaves][kChunk], all[kWaves];
+};
+
+// A tile pair's values as rows of LDS, split into parts.
+template <int PITCH>
+__device__ __forceinline__ void put_tile(uint16_t* to, const f32x4& v0, const f32x4& v1, int part, int col, int q) {
+  f32x4 v[2] = {v0, v1};
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint16_t b = f32_to_bf16_bits(v[it][r]);
+        to[p * part + (16 * it + 4 * q + r) * PITCH + col] = b;
+        v[it][r] -= bf16_bits_to_f32(b);
+      }
+}
+template <int PITCH>
+__device__ __forceinline__ void put_tile(float* to, const f32x4& v0, const f32x4& v1, int, int col, int q) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    to[(4 * q + r) * PITCH + col] = v0[r];
+    to[(16 + 4 * q + r) * PITCH + col] = v1[r];
+  }
+}
+template <int PITCH>
+__device__ __forceinline__ void row_parts(Frag<uint16_t>& f, const uint16_t* from, int part, int row, int col) {
+  f.part[0] = ld_op(from + row * PITCH + col);
+  f.part[1] = ld_op(from + part + row * PITCH + col);
+}
+template <int PITCH>
+__device__ __forceinline__ void row_parts(Frag<float>& f, const float* from, int, int row, int col) {
+  row8(f, from + row * PITCH + col);
+}
+
+// Sum over a row's 16 lanes, in all of them.
+template <int CTRL>
+__device__ __forceinline__ float row_add(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row_sum(float x) {
+  return row_add<0x140>(row_add<0x141>(row_add<0x4E>(row_add<0xB1>(x))));
+}
+
+template <class T, int DK, int DV>
+__global__ __launch_bounds__(64 * kWaves, 1) void grad_kernel(const Args a) {
+  using Sh = GradShared<T, DK, DV>;
+  constexpr int kP = kWhole<T>, kV = DV / 64, kK = DK / 64, kPV = kPitch<T, DV>, kPK = kPitch<T, DK>;
+  __shared__ Sh m;
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int c = lane % 16, q = lane / 16;
+  const int h = blockIdx.x % a.hv;
+  const int64_t slot = blockIdx.x / a.hv;
+  const Piece p = find_piece(a.cu, a.nseq, a.n, kChunk, slot, lane);
+  if (p.seg < 0 || p.len == 0) return;
+  const int kh = h / (a.hv / a.hk), len = p.len;
+  const int64_t ldk = (int64_t)a.hk * DK, ldv = (int64_t)a.hv * DV;
+  const T* dop = static_cast<const T*>(a.dout) + p.first * ldv + h * DV;
+  const float* S0 = a.states + (slot * a.hv + h) * DK * DV;
+  const float* S1 = a.dstates + (slot * a.hv + h) * DK * DV;
+
+  stage<T, DK, 256>(&m.k[0][0], static_cast<const T*>(a.k) + p.first * ldk + kh * DK, ldk, len, threadIdx.x);
+  stage<T, DK, 256>(&m.q[0][0], static_cast<const T*>(a.q) + p.first * ldk + kh * DK, ldk, len, threadIdx.x);
+  const Gates gt = gates(a, p.first, len, h, lane);
+  if (wave == 0) put_rows(m.rows, gt, lane);
+  __syncthreads();
+  {
+    const auto key = [&](Frag<T>& f, int row, int col) { row8(f, &m.k[row + c][col]); };
+    const auto query = [&](Frag<T>& f, int row, int col) { row8(f, &m.q[row + c][col]); };
+    if (wave == 0) {  // T and T^T
+      Tri n{zero4(), zero4(), zero4()};
+#pragma unroll
+      for (int s = 0; s < DK / 32; ++s) {
+        Frag<T> k0, k1;
+        key(k0, 0, 32 * s + 8 * q);
+        key(k1, 16, 32 * s + 8 * q);
+        n.t00 = mm<1, 1>(k0, k0, n.t00);
+        n.t10 = mm<1, 1>(k0, k1, n.t10);
+        n.t11 = mm<1, 1>(k1, k1, n.t11);
+      }
+      decay_tri<false>(n, gt, true, true, 1.0f, lane);
+      Tri t;
+      unit_inverse(n.t00, n.t10, n.t11, t.t00, t.t10, t.t11, reinterpret_cast<float*>(m.op[0]), lane);
+      put_lower<T, kP>(m.op[0], t, lane);
+      t.t00 = turned(t.t00, lane);
+      t.t10 = turned(t.t10, lane);
+      t.t11 = turned(t.t11, lane);
+      put_upper<T, kP>(m.op[1], t, lane);
+    } else if (wave == 1) {  // B: queries by lane
+      Tri w{zero4(), zero4(), zero4()};
+#pragma unroll
+      for (int s = 0; s < DK / 32; ++s) {
+        Frag<T> k0, k1, q0, q1;
+        key(k0, 0, 32 * s + 8 * q);
+        key(k1, 16, 32 * s + 8 * q);
+        query(q0, 0, 32 * s + 8 * q);
+        query(q1, 16, 32 * s + 8 * q);
+        w.t00 = mm<1, 1>(k0, q0, w.t00);
+        w.t10 = mm<1, 1>(k0, q1, w.t10);
+        w.t11 = mm<1, 1>(k1, q1, w.t11);
+      }
+      decay_tri<false>(w, gt, false, false, a.scale, lane);
+      put_lower<T, kP>(m.op[2], w, lane);
+    } else if (wave == 2) {  // B^T: keys by lane
+      Tri w = products<1, 1, T, DK>(query, key, q);
+      decay_tri<true>(w, gt, false, false, a.scale, lane);
+      put_upper<T, kP>(m.op[3], w, lane);
+    } else {  // N'^T
+      Tri w = products<1, 1, T, DK>(key, key, q);
+      decay_tri<true>(w, gt, true, false, 1.0f, lane);
+      put_upper<T, kP>(m.op[4], w, lane);
+    }
+  }
+  __syncthreads();
+
+  // this wave's value channels
+  {
+    const int col = wave * 16 * kV + kV * c;
+    f32x4 V[2][kV], dO[2][kV], ks[2][kV], kd[2][kV], qs[2][kV];
+    load_rows<kV>(V, static_cast<const T*>(a.v) + p.first * ldv + h * DV + col, ldv, len, q);
+    load_rows<kV>(dO, dop + col, ldv, len, q);
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int x = 0; x < kV; ++x) ks[it][x] = kd[it][x] = qs[it][x] = zero4();
+    float both = 0.0f;  // <dS, S>
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s) {
+      f32x4 st[2][kV], ds[2][kV];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float w0[kV], w1[kV];
+          const int64_t at = (int64_t)channel(2 * s + i, 4 * q + r) * DV + col;
+          load_n<kV>(w0, S0 + at);
+          load_n<kV>(w1, S1 + at);
+#pragma unroll
+          for (int x = 0; x < kV; ++x) {
+            st[i][x][r] = w0[x];
+            ds[i][x][r] = w1[x];
+            both += w0[x] * w1[x];
+          }
+        }
+      Frag<T> k0, k1, q0, q1;
+      row8(k0, &m.k[c][32 * s + 8 * q]);
+      row8(k1, &m.k[16 + c][32 * s + 8 * q]);
+      row8(q0, &m.q[c][32 * s + 8 * q]);
+      row8(q1, &m.q[16 + c][32 * s + 8 * q]);
+#pragma unroll
+      for (int x = 0; x < kV; ++x) {
+        Frag<T> f;
+        make<kP>(f, st[0][x], st[1][x]);
+        ks[0][x] = mm<1, kP>(k0, f, ks[0][x]);
+        ks[1][x] = mm<1, kP>(k1, f, ks[1][x]);
+        qs[0][x] = mm<1, kP>(q0, f, qs[0][x]);
+        qs[1][x] = mm<1, kP>(q1, f, qs[1][x]);
+        make<kP>(f, ds[0][x], ds[1][x]);
+        kd[0][x] = mm<1, kP>(k0, f, kd[0][x]);
+        kd[1][x] = mm<1, kP>(k1, f, kd[1][x]);
+      }
+    }
+    f32x4 dec[2], rest[2], bt[2], along[2], step[2];
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      dec[it] = rows4(m.rows.decay, it, q);
+      rest[it] = rows4(m.rows.rest, it, q);
+      bt[it] = rows4(m.rows.beta, it, q);
+      along[it] = step[it] = zero4();
+    }
+    both *= m.rows.total;
+    f32x4 dR[2][kV];
+#pragma unroll
+    for (int x = 0; x < kV; ++x) {
+      Frag<T> f, o0, o1;
+      make<kP>(f, V[0][x] - dec[0] * ks[0][x], V[1][x] - dec[1] * ks[1][x]);
+      get<kP>(o0, m.op[0], lane);
+      get<kP>(o1, m.op[0] + kOperand<T>, lane);
+      const f32x4 y0 = mm<kP, kP>(o0, f, zero4()), y1 = mm<kP, kP>(o1, f, zero4());
+      const f32x4 u0 = y0 * bt[0], u1 = y1 * bt[1];
+      make<kP>(f, u0, u1);
+      get<kP>(o0, m.op[2], lane);
+      get<kP>(o1, m.op[2] + kOperand<T>, lane);
+      along[0] += dO[0][x] * mm<kP, kP>(o0, f, qs[0][x] * (dec[0] * a.scale));
+      along[1] += dO[1][x] * mm<kP, kP>(o1, f, qs[1][x] * (dec[1] * a.scale));
+      make<1>(f, dO[0][x], dO[1][x]);
+      get<kP>(o0, m.op[3], lane);
+      get<kP>(o1, m.op[3] + kOperand<T>, lane);
+      const f32x4 e0 = kd[0][x] * rest[0], e1 = kd[1][x] * rest[1];
+      const f32x4 du0 = mm<kP, 1>(o0, f, e0), du1 = mm<kP, 1>(o1, f, e1);
+      make<kP>(f, du0 * bt[0], du1 * bt[1]);
+      get<kP>(o0, m.op[1], lane);
+      get<kP>(o1, m.op[1] + kOperand<T>, lane);
+      dR[0][x] = mm<kP, kP>(o0, f, zero4());
+      dR[1][x] = mm<kP, kP>(o1, f, zero4());
+      along[0] -= V[0][x] * dR[0][x];
+      along[1] -= V[1][x] * dR[1][x];
+      make<kP>(f, -dR[0][x], -dR[1][x]);
+      get<kP>(o0, m.op[4], lane);
+      get<kP>(o1, m.op[4] + kOperand<T>, lane);
+      step[0] += y0 * mm<kP, kP>(o0, f, du0);
+      step[1] += y1 * mm<kP, kP>(o1, f, du1);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) both += e0[r] * u0[r] + e1[r] * u1[r];
+      put_tile<kPV>(&m.y[0][0][0], y0, y1, kChunk * kPV, col + x, q);
+      put_tile<kPV>(&m.dr[0][0][0], dR[0][x], dR[1][x], kChunk * kPV, col + x, q);
+    }
+    if (a.dv_out) store_rows<kV>(static_cast<T*>(a.dv_out) + p.first * ldv + h * DV + col, dR, ldv, len, q);
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float s0 = row_sum(along[it][r]), s1 = row_sum(step[it][r]);
+        if (c == 0) {
+          m.along[wave][16 * it + 4 * q + r] = s0;
+          m.step[wave][16 * it + 4 * q + r] = s1;
+        }
+      }
+    both = wave_sum(both);
+    if (lane == 0) m.all[wave] = both;
+  }
+  __syncthreads();
+
+  // F and E by row and by column: waves 0 and 1 dO y^T, waves 2 and 3 dR y^T
+  {
+    Tri w{zero4(), zero4(), zero4()};
+    const bool by_row = wave % 2 == 0, of_e = wave >= 2;
+#pragma unroll
+    for (int s = 0; s < DV / 32; ++s) {
+      Frag<T> l0, l1, y0, y1;
+      const int col = 32 * s + 8 * q;
+      row_parts<kPV>(y0, &m.y[0][0][0], kChunk * kPV, c, col);
+      row_parts<kPV>(y1, &m.y[0][0][0], kChunk * kPV, 16 + c, col);
+      if (of_e) {
+        row_parts<kPV>(l0, &m.dr[0][0][0], kChunk * kPV, c, col);
+        row_parts<kPV>(l1, &m.dr[0][0][0], kChunk * kPV, 16 + c, col);
+        if (by_row) {
+          w.t00 = mm<2, 2>(y0, l0, w.t00);
+          w.t10 = mm<2, 2>(y0, l1, w.t10);
+          w.t11 = mm<2, 2>(y1, l1, w.t11);
+        } else {
+          w.t00 = mm<2, 2>(l0, y0, w.t00);
+          w.t10 = mm<2, 2>(l1, y0, w.t10);
+          w.t11 = mm<2, 2>(l1, y1, w.t11);
+        }
+      } else {
+        clear(l0);
+        clear(l1);
+        if (c < len) row8(l0, dop + c * ldv + col);
+        if (16 + c < len) row8(l1, dop + (16 + c) * ldv + col);
+        if (by_row) {
+          w.t00 = mm<2, 1>(y0, l0, w.t00);
+          w.t10 = mm<2, 1>(y0, l1, w.t10);
+          w.t11 = mm<2, 1>(y1, l1, w.t11);
+        } else {
+          w.t00 = mm<1, 2>(l0, y0, w.t00);
+          w.t10 = mm<1, 2>(l1, y0, w.t10);
+          w.t11 = mm<1, 2>(l1, y1, w.t11);
+        }
+      }
+    }
+    const float f = of_e ? -1.0f : a.scale;
+    if (by_row) {
+      decay_tri<false>(w, gt, of_e, true, f, lane);
+      put_lower<T, 2>(m.op[wave], w, lane);
+    } else {
+      decay_tri<true>(w, gt, of_e, true, f, lane);
+      put_upper<T, 2>(m.op[wave], w, lane);
+    }
+  }
+  if (wave == 0 && lane < kChunk) {
+    double x = 0.0;
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      x += m.along[w][lane];
+      s += m.step[w][lane];
+    }
+#pragma unroll
+    for (int off = 1; off < kChunk; off *= 2) {
+      const double down = __shfl_down(x, off, 32);
+      if (lane + off < kChunk) x += down;
+    }
+    const double all = (double)m.all[0] + m.all[1] + m.all[2] + m.all[3];
+    if (lane < len) {
+      if (a.dg) a.dg[(p.first + lane) * a.hv + h] = (float)(x + all);
+      if (a.dbeta) a.dbeta[(p.first + lane) * a.hv + h] = s;
+    }
+  }
+  __syncthreads();
+
+  // this wave's key channels: lane c has channel 16 (kK wave + x) + c
+  if (a.dq == nullptr && a.dk_out == nullptr) return;
+  f32x4 dq[2][kK], ds[2][kK], rs[2][kK];
+#pragma unroll
+  for (int x = 0; x < kK; ++x) {
+#pragma unroll
+    for (int it = 0; it < 2; ++it) dq[it][x] = ds[it][x] = rs[it][x] = zero4();
+    const int64_t row = (int64_t)(16 * (kK * wave + x) + c) * DV;
+#pragma unroll
+    for (int s = 0; s < DV / 32; ++s) {
+      const int col = 32 * s + 8 * q;
+      Frag<T> s0, s1, l;
+      make<2>(s0, *reinterpret_cast<const f32x4*>(S0 + row + col), *reinterpret_cast<const f32x4*>(S0 + row + col + 4));
+      make<2>(s1, *reinterpret_cast<const f32x4*>(S1 + row + col), *reinterpret_cast<const f32x4*>(S1 + row + col + 4));
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        clear(l);
+        if (16 * it + c < len) row8(l, dop + (16 * it + c) * ldv + col);
+        dq[it][x] = mm<1, 2>(l, s0, dq[it][x]);
+        row_parts<kPV>(l, &m.dr[0][0][0], kChunk * kPV, 16 * it + c, col);
+        rs[it][x] = mm<2, 2>(l, s0, rs[it][x]);
+        row_parts<kPV>(l, &m.y[0][0][0], kChunk * kPV, 16 * it + c, col);
+        ds[it][x] = mm<2, 2>(l, s1, ds[it][x]);
+      }
+    }
+    Frag<T> kc, qc;
+    columns<kPK>(kc, &m.k[0][0], 16 * (kK * wave + x), 4, lane);
+    columns<kPK>(qc, &m.q[0][0], 16 * (kK * wave + x), 4, lane);
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      const f32x4 dec = rows4(m.rows.decay, it, q), rest = rows4(m.rows.rest, it, q), bt = rows4(m.rows.beta, it, q);
+      Frag<T> l;
+      get<2>(l, m.op[0] + it * kOperand<T>, lane);
+      dq[it][x] = mm<2, 1>(l, kc, dq[it][x] * (dec * a.scale));
+      f32x4 dk = ds[it][x] * (rest * bt) - rs[it][x] * dec;
+      get<2>(l, m.op[1] + it * kOperand<T>, lane);
+      dk = mm<2, 1>(l, qc, dk);
+      get<2>(l, m.op[2] + it * kOperand<T>, lane);
+      dk = mm<2, 1>(l, kc, dk);
+      get<2>(l, m.op[3] + it * kOperand<T>, lane);
+      ds[it][x] = mm<2, 1>(l, kc, dk);
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < kK; ++x) {
+    const int ch = 16 * (kK * wave + x) + c;
+    f32x4 one[2][1];
+    one[0][0] = dq[0][x];
+    one[1][0] = dq[1][x];
+    if (a.dq_part)
+      store_rows<1>(a.dq_part + (p.first * a.hv + h) * DK + ch, one, (int64_t)a.hv * DK, len, q);
+    else if (a.dq)
+      store_rows<1>(static_cast<T*>(a.dq) + p.first * ldk + kh * DK + ch, one, ldk, len, q);
+    one[0][0] = ds[0][x];
+    one[1][0] = ds[1][x];
+    if (a.dk_part)
+      store_rows<1>(a.dk_part + (p.first * a.hv + h) * DK + ch, one, (int64_t)a.hv * DK, len, q);
+    else if (a.dk_out)
+      store_rows<1>(static_cast<T*>(a.dk_out) + p.first * ldk + kh * DK + ch, one, ldk, len, q);
+  }
+}
+
+// dq, dk of key heads that several value heads share, in the heads' order. Rows of
+// no sequence are left as they are.
+template <class T>
+__global__ __launch_bounds__(256) void group_kernel(const Args a) {
+  const int64_t row = blockIdx.x;
+  bool inside = a.cu == nullptr;
+  for (int b = threadIdx.x; !inside && b < a.nseq; b += 256)
+    inside = row >= bound(a.cu, b, a.n) && row < bound(a.cu, b + 1, a.n);
+  if (!__syncthreads_or(inside)) return;
+  const int group = a.hv / a.hk, width = a.hk * a.dk;
+  const float* from = blockIdx.y ? a.dk_part : a.dq_part;
+  T* to = static_cast<T*>(blockIdx.y ? a.dk_out : a.dq);
+  if (from == nullptr || to == nullptr) return;
+  for (int i = 4 * threadIdx.x; i < width; i += 1024) {
+    const int kh = i / a.dk, ch = i % a.dk;
+    f32x4 s = zero4();
+    for (int g = 0; g < group; ++g)
+      s += *reinterpret_cast<const f32x4*>(from + (row * a.hv + kh * group + g) * a.dk + ch);
+    const float w[4] = {s[0], s[1], s[2], s[3]};
+    store_n<4>(to + row * width + i, w);
+  }
+}
+
+template <class T, int DK, int DV>
+hipError_t run(const Args& a, hipStream_t s) {
+  grad_kernel<T, DK, DV><<<(unsigned)(chunk_slots(a.n, a.nseq) * a.hv), 64 * kWaves, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <class T>
+hipError_t grad_of(const Args& a, hipStream_t s) {
+  hipError_t e = a.dk == 64 ? (a.dv == 64 ? run<T, 64, 64>(a, s) : run<T, 64, 128>(a, s))
+                            : (a.dv == 64 ? run<T, 128, 64>(a, s) : run<T, 128, 128>(a, s));
+  if (e != hipSuccess || a.dq_part == nullptr || (a.dq == nullptr && a.dk_out == nullptr)) return e;
+  group_kernel<T><<<dim3((unsigned)a.n, 2), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_grad(const Args& a, bool bf16, hipStream_t stream) {
+  if (a.n == 0) return hipSuccess;
+  return bf16 ? grad_of<uint16_t>(a, stream) : grad_of<float>(a, stream);
+}
+
+}  // namespace delta
+}  // namespace vggt3

@@ -19,27 +19,31 @@ namespace delta {
 // grows with the chunk.)
 constexpr int kChunk = 32;
 
-// Operand of a 32-deep product. bf16: hi + lo, 16 bits of the value (hi alone where
-// the value is bf16 already); fp32: the value.
+// Operand of a 32-deep product. bf16: 1 to 3 parts of 8 bits each, 3 of them the
+// whole fp32 value (one where the value is bf16 already); fp32: the value.
 template <class T>
 struct Frag;
 template <>
 struct Frag<uint16_t> {
-  bf16x8 hi, lo;
+  bf16x8 part[3];
 };
 template <>
 struct Frag<float> {
   f32x4 a, b;
 };
 
-// c += A B. NA, NB: parts of A and B that count (bf16). Two values of two parts
-// each differ from fp32 ones by the product of their second parts and by what the
-// second parts leave out, 2^-17 relative at most each.
+// c += A B. NA, NB: parts of A and B that count (bf16); products of parts that lie
+// below the last one kept are left out: 2^-16 relative for 2, 2^-24 for 3.
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 mm(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x4 c) {
-  if constexpr (NB == 2) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.hi, b.lo, c, 0, 0, 0);
-  if constexpr (NA == 2) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.lo, b.hi, c, 0, 0, 0);
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.hi, b.hi, c, 0, 0, 0);
+  constexpr int kLast = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+  for (int sum = kLast; sum >= 0; --sum)
+#pragma unroll
+    for (int i = 0; i <= sum; ++i)
+      if (i < NA && sum - i < NB)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.part[i], b.part[sum - i], c, 0, 0, 0);
+  return c;
 }
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 mm(const Frag<float>& a, const Frag<float>& b, f32x4 c) {
@@ -58,48 +62,64 @@ __device__ __forceinline__ f32x4 mm16(const f32x4& a, const f32x4& b, f32x4 c) {
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
-// Two tiles as an operand.
+// Two tiles as an operand of P parts.
+template <int P>
 __device__ __forceinline__ void make(Frag<float>& f, const f32x4& x, const f32x4& y) {
   f.a = x;
   f.b = y;
 }
-__device__ __forceinline__ void make(Frag<uint16_t>& f, const f32x4& x, const f32x4& y) {
-  u32x4 h, l;
+template <int P>
+__device__ __forceinline__ void make(Frag<uint16_t>& f, f32x4 x, f32x4 y) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float p = i < 2 ? x[2 * i] : y[2 * i - 4], q = i < 2 ? x[2 * i + 1] : y[2 * i - 3];
-    h[i] = pack_bf16x2(p, q);
-    l[i] = pack_bf16x2(p - bf16_lo(h[i]), q - bf16_hi(h[i]));
+  for (int p = 0; p < P; ++p) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+      w[2 + i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+    }
+    f.part[p] = as_bf16x8(w);
+    if (p + 1 < P) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[2 * i] -= bf16_lo(w[i]);
+        x[2 * i + 1] -= bf16_hi(w[i]);
+        y[2 * i] -= bf16_lo(w[2 + i]);
+        y[2 * i + 1] -= bf16_hi(w[2 + i]);
+      }
+    }
   }
-  f.hi = as_bf16x8(h);
-  f.lo = as_bf16x8(l);
 }
 
-// Operands through LDS: 2 KB each, 16 bytes a lane twice.
+// Operands through LDS: 16 bytes a lane for each part (fp32: for each half).
+template <int P>
 __device__ __forceinline__ void put(u32x4* at, const Frag<uint16_t>& f, int lane) {
-  at[lane] = as_u32x4(f.hi);
-  at[64 + lane] = as_u32x4(f.lo);
+#pragma unroll
+  for (int p = 0; p < P; ++p) at[64 * p + lane] = as_u32x4(f.part[p]);
 }
+template <int P>
 __device__ __forceinline__ void put(u32x4* at, const Frag<float>& f, int lane) {
   at[lane] = __builtin_bit_cast(u32x4, f.a);
   at[64 + lane] = __builtin_bit_cast(u32x4, f.b);
 }
+template <int P>
 __device__ __forceinline__ void get(Frag<uint16_t>& f, const u32x4* at, int lane) {
-  f.hi = as_bf16x8(at[lane]);
-  f.lo = as_bf16x8(at[64 + lane]);
+#pragma unroll
+  for (int p = 0; p < P; ++p) f.part[p] = as_bf16x8(at[64 * p + lane]);
 }
+template <int P>
 __device__ __forceinline__ void get(Frag<float>& f, const u32x4* at, int lane) {
   f.a = __builtin_bit_cast(f32x4, at[lane]);
   f.b = __builtin_bit_cast(f32x4, at[64 + lane]);
 }
 
 // 8 values of a row, at a 16-byte boundary.
-__device__ __forceinline__ void row8(Frag<uint16_t>& f, const uint16_t* p) { f.hi = ld_op(p); }
+__device__ __forceinline__ void row8(Frag<uint16_t>& f, const uint16_t* p) { f.part[0] = ld_op(p); }
 __device__ __forceinline__ void row8(Frag<float>& f, const float* p) {
   f.a = *reinterpret_cast<const f32x4*>(p);
   f.b = *reinterpret_cast<const f32x4*>(p + 4);
 }
-__device__ __forceinline__ void clear(Frag<uint16_t>& f) { f.hi = as_bf16x8(u32x4{0, 0, 0, 0}); }
+__device__ __forceinline__ void clear(Frag<uint16_t>& f) { f.part[0] = as_bf16x8(u32x4{0, 0, 0, 0}); }
 __device__ __forceinline__ void clear(Frag<float>& f) { f.a = f.b = zero4(); }
 
 // A head's channels are the rows of its state's tiles in an order in which 8
@@ -109,24 +129,30 @@ __device__ __forceinline__ int channel(int tile, int row) {
   return 32 * (tile / 2) + 8 * (row / 4) + 4 * (tile % 2) + row % 4;
 }
 
-// Left operand X^T for tile t of X's channels, over the chunk's tokens, from X
-// [kChunk][pitch] in LDS. bf16: transposing reads, each lane of 16 giving the
-// address of 4 neighbouring channels of one token.
+// X^T as a left operand (or X as a right one) over the chunk's tokens, from X
+// [kChunk][pitch] in LDS: lane c has channel base + step (c / 4) + c % 4. bf16:
+// transposing reads, each lane of 16 giving the address of 4 neighbouring channels
+// of one token.
 template <int PITCH>
-__device__ __forceinline__ void columns(Frag<uint16_t>& f, const uint16_t* x, int tile, int lane) {
+__device__ __forceinline__ void columns(Frag<uint16_t>& f, const uint16_t* x, int base, int step, int lane) {
   const int s = lane % 16, q = lane / 16;
-  const uint16_t* p = x + (4 * q + s / 4) * PITCH + 32 * (tile / 2) + 8 * (s % 4) + 4 * (tile % 2);
-  f.hi = tr_op(p, p + 16 * PITCH);
+  const uint16_t* p = x + (4 * q + s / 4) * PITCH + base + step * (s % 4);
+  f.part[0] = tr_op(p, p + 16 * PITCH);
 }
 template <int PITCH>
-__device__ __forceinline__ void columns(Frag<float>& f, const float* x, int tile, int lane) {
-  const int q = lane / 16;
-  const float* p = x + 4 * q * PITCH + channel(tile, lane % 16);
+__device__ __forceinline__ void columns(Frag<float>& f, const float* x, int base, int step, int lane) {
+  const int c = lane % 16, q = lane / 16;
+  const float* p = x + 4 * q * PITCH + base + step * (c / 4) + c % 4;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     f.a[r] = p[r * PITCH];
     f.b[r] = p[(16 + r) * PITCH];
   }
+}
+// The same for the rows of a state's tile.
+template <int PITCH, class T>
+__device__ __forceinline__ void state_rows(Frag<T>& f, const T* x, int tile, int lane) {
+  columns<PITCH>(f, x, 32 * (tile / 2) + 4 * (tile % 2), 8, lane);
 }
 
 // N neighbouring values <-> fp32 (N = 1, 2 or 4, aligned to N values).

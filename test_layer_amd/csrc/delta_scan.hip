@@ -22,130 +22,70 @@
 // a value-free run that starts from the unit matrix), join_kernel goes through the
 // pieces, and the main pass starts each piece from its own first state. (A
 // sequence's first piece starts from the sequence's first state in both passes.)
-#include "delta.hpp"
-#include "delta_ops.hpp"
+#include "delta_chunk.hpp"
 
 namespace vggt3 {
 namespace delta {
 namespace {
 
-enum Mode { kForward, kSummary };
+// kStates: the state before every chunk, for the gradient (no outputs).
+enum Mode { kForward, kSummary, kStates };
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr double kLog2eD = 1.4426950408889634074;
-
-// What a chunk's columns share, in LDS.
 template <class T, int DK>
 struct Shared {
-  static constexpr int kPitch = DK + 16 / sizeof(T);  // rows 16 bytes apart in the banks
-  T k[kChunk][kPitch];
-  u32x4 t[2][128];   // T, rows 0-15 and 16-31, as operands
-  u32x4 b[2][128];   // the triangle of Q K^T
-  float decay[kChunk], rest[kChunk], beta[kChunk];
-  float total;
-  float scratch[2 * 16 * 20];
+  T k[kChunk][kPitch<T, DK>];
+  u32x4 t[2 * kOperand<T>];  // T
+  u32x4 b[2 * kOperand<T>];  // the triangle of Q K^T
+  Rows rows;
 };
 
 // One wave prepares a chunk: rows first .. first + len - 1, len in 1 .. 32 (rows
 // behind them count as zeros).
 template <class T, int DK, bool QK>
 __device__ __forceinline__ void prepare(Shared<T, DK>& sh, const Args& a, int64_t first, int len, int h, int lane) {
-  constexpr int kSteps = DK / 32, kPiece = 16 / sizeof(T), kPieces = DK / kPiece;
   const int kh = h / (a.hv / a.hk), c = lane % 16, q = lane / 16;
   const int64_t ld = (int64_t)a.hk * DK;
-  const T* kp = static_cast<const T*>(a.k) + first * ld + kh * DK;
-#pragma unroll
-  for (int x = 0; x < kChunk * kPieces / 64; ++x) {
-    const int at = x * 64 + lane, row = at / kPieces, col = at % kPieces * kPiece;
-    u32x4 w = {0, 0, 0, 0};
-    if (row < len) w = ld16(kp + row * ld + col);
-    st16(&sh.k[row][col], w);
-  }
-  // decays in powers of 2, summed in 64 bits: a difference of two sums is right
-  // whatever lies before them. Below 2^-2000 a decay is 0 in either form.
-  const int t = lane % 32;
-  double G = 0.0;
-  float bt = 0.0f;
-  if (t < len) {
-    if (a.g) {
-      const float g = a.g[(first + t) * a.hv + h];
-      G = (g < -2000.0f ? -2000.0f : g) * kLog2eD;
-    }
-    bt = a.beta[(first + t) * a.hv + h];
-  }
-#pragma unroll
-  for (int off = 1; off < kChunk; off *= 2) {
-    const double up = __shfl_up(G, off, 32);
-    if (t >= off) G += up;
-  }
-  const double end = __shfl(G, 31, 32);
-  if (lane < kChunk) {
-    sh.decay[t] = __builtin_amdgcn_exp2f((float)G);
-    sh.rest[t] = __builtin_amdgcn_exp2f((float)(end - G));
-    sh.beta[t] = bt;
-    if (t == 31) sh.total = __builtin_amdgcn_exp2f((float)G);
-  }
+  stage<T, DK, 64>(&sh.k[0][0], static_cast<const T*>(a.k) + first * ld + kh * DK, ld, len, lane);
+  const Gates gt = gates(a, first, len, h, lane);
+  put_rows(sh.rows, gt, lane);
   wave_lds_order();
-  // products with keys as rows and keys or queries as columns: results are left
-  // operands, lane (i, q) holding columns 4q .. 4q+3 of row i
-  f32x4 kk[3], qk[3];
+  // keys as a tile's rows: results by row of N and of Q K^T
+  const auto key = [&](Frag<T>& f, int row, int col) { row8(f, &sh.k[row + c][col]); };
+  const T* qp = static_cast<const T*>(a.q) + first * ld + kh * DK;
+  const auto query = [&](Frag<T>& f, int row, int col) {
+    clear(f);
+    if (row + c < len) row8(f, qp + (row + c) * ld + col);
+  };
+  Tri n{zero4(), zero4(), zero4()}, w = n;
 #pragma unroll
-  for (int x = 0; x < 3; ++x) kk[x] = qk[x] = zero4();
-  const T* qp = static_cast<const T*>(a.q) + first * ld + kh * DK + 8 * q;
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
+  for (int s = 0; s < DK / 32; ++s) {
     Frag<T> k0, k1, q0, q1;
-    row8(k0, &sh.k[c][32 * s + 8 * q]);
-    row8(k1, &sh.k[16 + c][32 * s + 8 * q]);
-    kk[0] = mm<1, 1>(k0, k0, kk[0]);
-    kk[1] = mm<1, 1>(k0, k1, kk[1]);
-    kk[2] = mm<1, 1>(k1, k1, kk[2]);
+    key(k0, 0, 32 * s + 8 * q);
+    key(k1, 16, 32 * s + 8 * q);
+    n.t00 = mm<1, 1>(k0, k0, n.t00);
+    n.t10 = mm<1, 1>(k0, k1, n.t10);
+    n.t11 = mm<1, 1>(k1, k1, n.t11);
     if constexpr (QK) {
-      clear(q0);
-      clear(q1);
-      if (c < len) row8(q0, qp + c * ld + 32 * s);
-      if (16 + c < len) row8(q1, qp + (16 + c) * ld + 32 * s);
-      qk[0] = mm<1, 1>(k0, q0, qk[0]);
-      qk[1] = mm<1, 1>(k0, q1, qk[1]);
-      qk[2] = mm<1, 1>(k1, q1, qk[2]);
+      query(q0, 0, 32 * s + 8 * q);
+      query(q1, 16, 32 * s + 8 * q);
+      w.t00 = mm<1, 1>(k0, q0, w.t00);
+      w.t10 = mm<1, 1>(k0, q1, w.t10);
+      w.t11 = mm<1, 1>(k1, q1, w.t11);
     }
   }
-  // tiles: rows (keys) 0-15 x columns 0-15; 0-15 x 16-31; 16-31 x 16-31
-  const double Gi[2] = {__shfl(G, c, 32), __shfl(G, 16 + c, 32)};
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int j = 4 * q + r;
-    const double G0 = __shfl(G, j, 32), G1 = __shfl(G, 16 + j, 32);
-    const float d0 = __builtin_amdgcn_exp2f((float)(Gi[0] - G0)), d1 = __builtin_amdgcn_exp2f((float)(Gi[1] - G0)),
-                d2 = __builtin_amdgcn_exp2f((float)(Gi[1] - G1));
-    const float b0 = __shfl(bt, j, 32), b1 = __shfl(bt, 16 + j, 32);
-    kk[0][r] = j < c ? kk[0][r] * d0 * b0 : 0.0f;
-    kk[1][r] = kk[1][r] * d1 * b0;
-    kk[2][r] = j < c ? kk[2][r] * d2 * b1 : 0.0f;
-    if constexpr (QK) {
-      qk[0][r] = j <= c ? qk[0][r] * d0 : 0.0f;
-      qk[1][r] = qk[1][r] * d1;
-      qk[2][r] = j <= c ? qk[2][r] * d2 : 0.0f;
-    }
-  }
-  f32x4 t00, t10, t11;
-  unit_inverse(kk[0], kk[1], kk[2], t00, t10, t11, sh.scratch, lane);
-  Frag<T> f;
-  make(f, t00, zero4());
-  put(sh.t[0], f, lane);
-  make(f, t10, t11);
-  put(sh.t[1], f, lane);
+  decay_tri<false>(n, gt, true, true, 1.0f, lane);
+  Tri t;
+  unit_inverse(n.t00, n.t10, n.t11, t.t00, t.t10, t.t11, reinterpret_cast<float*>(sh.t), lane);
+  put_lower<T, kWhole<T>>(sh.t, t, lane);
   if constexpr (QK) {
-    make(f, qk[0], zero4());
-    put(sh.b[0], f, lane);
-    make(f, qk[1], qk[2]);
-    put(sh.b[1], f, lane);
+    decay_tri<false>(w, gt, false, false, a.scale, lane);
+    put_lower<T, 2>(sh.b, w, lane);
   }
 }
 
 template <class T, int DK, int DV, int NCT, int W, int GC, Mode MODE>
 __global__ __launch_bounds__(64 * W, 1) void scan_kernel(const Args a) {
-  constexpr int kTiles = DK / 16, kSteps = DK / 32;
+  constexpr int kTiles = DK / 16, kSteps = DK / 32, kP = kWhole<T>;
   __shared__ Shared<T, DK> sh[GC];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int c = lane % 16, q = lane / 16;
@@ -160,23 +100,15 @@ __global__ __launch_bounds__(64 * W, 1) void scan_kernel(const Args a) {
   if (unit && p.seg == 0) return;  // its first state is known (whole workgroups: DV is a multiple of their columns)
 
   f32x4 S[kTiles][NCT];
-  {
+  if (unit) {
+    unit_state<DK, NCT>(S, col - DV, q);
+  } else {
     const float* from = nullptr;
-    if (MODE == kForward && p.segs > 1)
-      from = a.seg_n + (sid * a.hv + h) * DK * DV;
-    else if (a.state && p.seg == 0 && !unit)
-      from = a.state + ((int64_t)p.b * a.hv + h) * DK * DV;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float w[NCT];
-#pragma unroll
-        for (int x = 0; x < NCT; ++x) w[x] = unit && channel(t, 4 * q + r) == col - DV + x ? 1.0f : 0.0f;
-        if (from) load_n<NCT>(w, from + channel(t, 4 * q + r) * DV + col);
-#pragma unroll
-        for (int x = 0; x < NCT; ++x) S[t][x][r] = w[x];
-      }
+    if (MODE != kSummary && p.segs > 1)
+      from = a.seg_n + (sid * a.hv + h) * DK * DV + col;
+    else if (a.state && p.seg == 0)
+      from = a.state + ((int64_t)p.b * a.hv + h) * DK * DV + col;
+    load_state<DK, NCT>(S, from, DV, q);
   }
 
   const int64_t ldq = (int64_t)a.hk * DK, ldv = (int64_t)a.hv * DV;
@@ -192,17 +124,12 @@ __global__ __launch_bounds__(64 * W, 1) void scan_kernel(const Args a) {
       const Shared<T, DK>& m = sh[i];
       const int64_t first = p.first + (int64_t)(c0 + i) * kChunk;
       const int len = min(kChunk, p.len - (c0 + i) * kChunk);
-      float V[2][4][NCT];
-#pragma unroll
-      for (int it = 0; it < 2; ++it)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * it + 4 * q + r;
-#pragma unroll
-          for (int x = 0; x < NCT; ++x) V[it][r][x] = 0.0f;
-          if (!unit && row < len)
-            load_n<NCT>(V[it][r], static_cast<const T*>(a.v) + (first + row) * ldv + h * DV + col);
-        }
+      if constexpr (MODE == kStates) {
+        const int64_t slot = p.begin / kChunk + p.b + (p.first - p.begin) / kChunk + c0 + i;
+        store_state<DK, NCT>(S, a.states + (slot * a.hv + h) * DK * DV + col, DV, q);
+      }
+      f32x4 V[2][NCT];
+      load_rows<NCT>(V, static_cast<const T*>(a.v) + first * ldv + h * DV + col, ldv, unit ? 0 : len, q);
       Frag<T> qf[2][kSteps];
       if constexpr (MODE == kForward) {
 #pragma unroll
@@ -227,9 +154,9 @@ __global__ __launch_bounds__(64 * W, 1) void scan_kernel(const Args a) {
 #pragma unroll
         for (int x = 0; x < NCT; ++x) {
           Frag<T> f;
-          make(f, S[2 * s][x], S[2 * s + 1][x]);
-          ks[0][x] = mm<1, 2>(k0, f, ks[0][x]);
-          ks[1][x] = mm<1, 2>(k1, f, ks[1][x]);
+          make<kP>(f, S[2 * s][x], S[2 * s + 1][x]);
+          ks[0][x] = mm<1, kP>(k0, f, ks[0][x]);
+          ks[1][x] = mm<1, kP>(k1, f, ks[1][x]);
           if constexpr (MODE == kForward) {
             o[0][x] = mm<1, 2>(qf[0][s], f, o[0][x]);
             o[1][x] = mm<1, 2>(qf[1][s], f, o[1][x]);
@@ -239,86 +166,219 @@ __global__ __launch_bounds__(64 * W, 1) void scan_kernel(const Args a) {
       f32x4 dec[2], rest[2], bt[2];
 #pragma unroll
       for (int it = 0; it < 2; ++it) {
-        dec[it] = *reinterpret_cast<const f32x4*>(&m.decay[16 * it + 4 * q]);
-        rest[it] = *reinterpret_cast<const f32x4*>(&m.rest[16 * it + 4 * q]);
-        bt[it] = *reinterpret_cast<const f32x4*>(&m.beta[16 * it + 4 * q]);
+        dec[it] = rows4(m.rows.decay, it, q);
+        rest[it] = rows4(m.rows.rest, it, q);
+        bt[it] = rows4(m.rows.beta, it, q);
       }
-      const float total = m.total;
+      const float total = m.rows.total;
       Frag<T> t0, t1;
-      get(t0, m.t[0], lane);
-      get(t1, m.t[1], lane);
+      get<kP>(t0, m.t, lane);
+      get<kP>(t1, m.t + kOperand<T>, lane);
 #pragma unroll
       for (int x = 0; x < NCT; ++x) {
-        f32x4 R[2];
-#pragma unroll
-        for (int it = 0; it < 2; ++it)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) R[it][r] = V[it][r][x] - dec[it][r] * ks[it][x][r];
         Frag<T> f;
-        make(f, R[0], R[1]);
-        f32x4 u0 = mm<2, 2>(t0, f, zero4()), u1 = mm<2, 2>(t1, f, zero4());
-        u0 *= bt[0];
-        u1 *= bt[1];
+        make<kP>(f, V[0][x] - dec[0] * ks[0][x], V[1][x] - dec[1] * ks[1][x]);
+        const f32x4 u0 = mm<kP, kP>(t0, f, zero4()) * bt[0], u1 = mm<kP, kP>(t1, f, zero4()) * bt[1];
         if constexpr (MODE == kForward) {
           Frag<T> b0, b1;
-          get(b0, m.b[0], lane);
-          get(b1, m.b[1], lane);
-          make(f, u0, u1);
-          o[0][x] = mm<2, 2>(b0, f, o[0][x] * dec[0]);
-          o[1][x] = mm<2, 2>(b1, f, o[1][x] * dec[1]);
+          get<2>(b0, m.b, lane);
+          get<2>(b1, m.b + kOperand<T>, lane);
+          make<2>(f, u0, u1);
+          o[0][x] = mm<2, 2>(b0, f, o[0][x] * (dec[0] * a.scale));
+          o[1][x] = mm<2, 2>(b1, f, o[1][x] * (dec[1] * a.scale));
         }
-        make(f, u0 * rest[0], u1 * rest[1]);
+        make<kP>(f, u0 * rest[0], u1 * rest[1]);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           Frag<T> kt;
-          columns<Shared<T, DK>::kPitch>(kt, &m.k[0][0], t, lane);
-          S[t][x] = mm<1, 2>(kt, f, S[t][x] * total);
+          state_rows<kPitch<T, DK>>(kt, &m.k[0][0], t, lane);
+          S[t][x] = mm<1, kP>(kt, f, S[t][x] * total);
         }
       }
-      if constexpr (MODE == kForward) {
+      if constexpr (MODE == kForward)
+        store_rows<NCT>(static_cast<T*>(a.o) + first * ldv + h * DV + col, o, ldv, len, q);
+    }
+    __syncthreads();
+  }
+
+  if constexpr (MODE == kForward) {
+    if (a.state_out && p.seg == p.segs - 1)
+      store_state<DK, NCT>(S, a.state_out + ((int64_t)p.b * a.hv + h) * DK * DV + col, DV, q);
+  } else if constexpr (MODE == kSummary) {
+    if (unit)
+      store_state<DK, NCT>(S, a.seg_m + (sid * a.hv + h) * DK * DK + col - DV, DK, q);
+    else
+      store_state<DK, NCT>(S, a.seg_n + (sid * a.hv + h) * DK * DV + col, DV, q);
+  }
+}
+
+// The reverse of the scan, for the gradient. With dS the gradient of the state after a
+// chunk,
+//
+//   du = B^T dO + G_end / G . (K dS),  dR = T^T (beta . du)  (the gradient of V),
+//   dS <- G_end dS + Q^T (scale G . dO) - K^T (G . dR),    B = scale D . Q K^T (lower)
+//
+// by the same columns, with dS in the registers. kBack: dS after every chunk is
+// stored; kBackSummary: what a piece makes of the dS behind it.
+enum BackMode { kBack, kBackSummary };
+
+template <class T, int DK>
+struct BackShared {
+  T k[kChunk][kPitch<T, DK>];
+  T q[kChunk][kPitch<T, DK>];
+  u32x4 tt[2 * kOperand<T>];  // T^T
+  u32x4 bt[2 * kOperand<T>];  // B^T
+  Rows rows;
+};
+
+template <class T, int DK>
+__device__ __forceinline__ void prepare_back(BackShared<T, DK>& sh, const Args& a, int64_t first, int len, int h,
+                                             int lane) {
+  const int kh = h / (a.hv / a.hk), c = lane % 16, q = lane / 16;
+  const int64_t ld = (int64_t)a.hk * DK;
+  stage<T, DK, 64>(&sh.k[0][0], static_cast<const T*>(a.k) + first * ld + kh * DK, ld, len, lane);
+  stage<T, DK, 64>(&sh.q[0][0], static_cast<const T*>(a.q) + first * ld + kh * DK, ld, len, lane);
+  const Gates gt = gates(a, first, len, h, lane);
+  put_rows(sh.rows, gt, lane);
+  wave_lds_order();
+  const auto key = [&](Frag<T>& f, int row, int col) { row8(f, &sh.k[row + c][col]); };
+  const auto query = [&](Frag<T>& f, int row, int col) { row8(f, &sh.q[row + c][col]); };
+  // N by row (keys 16-31 against keys 0-15 turned round: 10 by row is 01 by column)
+  Tri n{zero4(), zero4(), zero4()};
 #pragma unroll
-        for (int it = 0; it < 2; ++it)
+  for (int s = 0; s < DK / 32; ++s) {
+    Frag<T> k0, k1;
+    key(k0, 0, 32 * s + 8 * q);
+    key(k1, 16, 32 * s + 8 * q);
+    n.t00 = mm<1, 1>(k0, k0, n.t00);
+    n.t10 = mm<1, 1>(k0, k1, n.t10);
+    n.t11 = mm<1, 1>(k1, k1, n.t11);
+  }
+  decay_tri<false>(n, gt, true, true, 1.0f, lane);
+  Tri t;
+  unit_inverse(n.t00, n.t10, n.t11, t.t00, t.t10, t.t11, reinterpret_cast<float*>(sh.tt), lane);
+  t.t00 = turned(t.t00, lane);
+  t.t10 = turned(t.t10, lane);
+  t.t11 = turned(t.t11, lane);
+  put_upper<T, kWhole<T>>(sh.tt, t, lane);
+  Tri w = products<1, 1, T, DK>(query, key, q);
+  decay_tri<true>(w, gt, false, false, a.scale, lane);
+  put_upper<T, kWhole<T>>(sh.bt, w, lane);
+}
+
+template <class T, int DK, int DV, int NCT, int W, int GC, BackMode MODE>
+__global__ __launch_bounds__(64 * W, 1) void back_kernel(const Args a) {
+  constexpr int kTiles = DK / 16, kSteps = DK / 32, kP = kWhole<T>;
+  __shared__ BackShared<T, DK> sh[GC];
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int c = lane % 16, q = lane / 16;
+  const int h = blockIdx.x % a.hv;
+  const int64_t sid = blockIdx.x / a.hv;
+  const Piece p = find_piece(a.cu, a.nseq, a.n, a.per, sid, lane);
+  if (p.seg < 0) return;
+  if (MODE == kBackSummary && p.seg == 0) return;  // nothing lies before it
+  const int col = (blockIdx.y * W + wave) * 16 * NCT + NCT * c;
+  const bool unit = MODE == kBackSummary && col >= DV;
+  if (unit && p.seg == p.segs - 1) return;  // the dS behind it is known
+
+  f32x4 S[kTiles][NCT];
+  if (unit) {
+    unit_state<DK, NCT>(S, col - DV, q);
+  } else {
+    const float* from = nullptr;
+    if (MODE == kBack && p.segs > 1)
+      from = a.seg_n + (sid * a.hv + h) * DK * DV + col;
+    else if (a.dlast && p.seg == p.segs - 1)
+      from = a.dlast + ((int64_t)p.b * a.hv + h) * DK * DV + col;
+    load_state<DK, NCT>(S, from, DV, q);
+  }
+
+  const int64_t ldv = (int64_t)a.hv * DV;
+  const int chunks = (p.len + kChunk - 1) / kChunk;
+  for (int c1 = chunks; c1 > 0; c1 -= GC) {  // chunks c1 - 1, c1 - 2, ..
+    if (wave < GC && c1 - 1 - wave >= 0) {
+      const int at = (c1 - 1 - wave) * kChunk;
+      prepare_back<T, DK>(sh[wave], a, p.first + at, min(kChunk, p.len - at), h, lane);
+    }
+    __syncthreads();
+    for (int i = 0; i < GC && c1 - 1 - i >= 0; ++i) {
+      const BackShared<T, DK>& m = sh[i];
+      const int at = (c1 - 1 - i) * kChunk;
+      const int64_t first = p.first + at;
+      const int len = min(kChunk, p.len - at);
+      if constexpr (MODE == kBack) {
+        const int64_t slot = p.begin / kChunk + p.b + (first - p.begin) / kChunk;
+        store_state<DK, NCT>(S, a.dstates + (slot * a.hv + h) * DK * DV + col, DV, q);
+      }
+      f32x4 dO[2][NCT];
+      load_rows<NCT>(dO, static_cast<const T*>(a.dout) + first * ldv + h * DV + col, ldv, unit ? 0 : len, q);
+      f32x4 kd[2][NCT];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = 16 * it + 4 * q + r;
-            float w[NCT];
+      for (int it = 0; it < 2; ++it)
 #pragma unroll
-            for (int x = 0; x < NCT; ++x) w[x] = o[it][x][r] * a.scale;
-            if (row < len) store_n<NCT>(static_cast<T*>(a.o) + (first + row) * ldv + h * DV + col, w);
-          }
+        for (int x = 0; x < NCT; ++x) kd[it][x] = zero4();
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        Frag<T> k0, k1;
+        row8(k0, &m.k[c][32 * s + 8 * q]);
+        row8(k1, &m.k[16 + c][32 * s + 8 * q]);
+#pragma unroll
+        for (int x = 0; x < NCT; ++x) {
+          Frag<T> f;
+          make<kP>(f, S[2 * s][x], S[2 * s + 1][x]);
+          kd[0][x] = mm<1, kP>(k0, f, kd[0][x]);
+          kd[1][x] = mm<1, kP>(k1, f, kd[1][x]);
+        }
+      }
+      f32x4 dec[2], rest[2], bt[2];
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        dec[it] = rows4(m.rows.decay, it, q);
+        rest[it] = rows4(m.rows.rest, it, q);
+        bt[it] = rows4(m.rows.beta, it, q);
+      }
+      const float total = m.rows.total;
+#pragma unroll
+      for (int x = 0; x < NCT; ++x) {
+        Frag<T> f, b0, b1, t0, t1;
+        make<1>(f, dO[0][x], dO[1][x]);
+        get<kP>(b0, m.bt, lane);
+        get<kP>(b1, m.bt + kOperand<T>, lane);
+        const f32x4 du0 = mm<kP, 1>(b0, f, kd[0][x] * rest[0]), du1 = mm<kP, 1>(b1, f, kd[1][x] * rest[1]);
+        make<kP>(f, du0 * bt[0], du1 * bt[1]);
+        get<kP>(t0, m.tt, lane);
+        get<kP>(t1, m.tt + kOperand<T>, lane);
+        const f32x4 dR0 = mm<kP, kP>(t0, f, zero4()), dR1 = mm<kP, kP>(t1, f, zero4());
+        Frag<T> g;
+        make<kP>(f, dO[0][x] * (dec[0] * a.scale), dO[1][x] * (dec[1] * a.scale));
+        make<kP>(g, -dR0 * dec[0], -dR1 * dec[1]);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          Frag<T> kt, qt;
+          state_rows<kPitch<T, DK>>(kt, &m.k[0][0], t, lane);
+          state_rows<kPitch<T, DK>>(qt, &m.q[0][0], t, lane);
+          S[t][x] = mm<1, kP>(kt, g, mm<1, kP>(qt, f, S[t][x] * total));
+        }
       }
     }
     __syncthreads();
   }
 
-  float* to = nullptr;
-  int64_t ld = DV;
-  int at = col;
-  if constexpr (MODE == kForward) {
-    if (a.state_out && p.seg == p.segs - 1) to = a.state_out + ((int64_t)p.b * a.hv + h) * DK * DV;
-  } else if (unit) {
-    to = a.seg_m + (sid * a.hv + h) * DK * DK;
-    ld = DK;
-    at = col - DV;
+  if constexpr (MODE == kBack) {
+    if (a.dfirst && p.seg == 0)
+      store_state<DK, NCT>(S, a.dfirst + ((int64_t)p.b * a.hv + h) * DK * DV + col, DV, q);
   } else {
-    to = a.seg_n + (sid * a.hv + h) * DK * DV;
-  }
-  if (to) {
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float w[NCT];
-#pragma unroll
-        for (int x = 0; x < NCT; ++x) w[x] = S[t][x][r];
-        store_n<NCT>(to + channel(t, 4 * q + r) * ld + at, w);
-      }
+    if (unit)
+      store_state<DK, NCT>(S, a.seg_m + (sid * a.hv + h) * DK * DK + col - DV, DK, q);
+    else
+      store_state<DK, NCT>(S, a.seg_n + (sid * a.hv + h) * DK * DV + col, DV, q);
   }
 }
 
-// First states of a sequence's pieces: S <- M S + R from piece to piece, one wave
-// for 16 columns. In fp32 products for both types: they are few.
-template <int DK, int DV>
+// First states of a sequence's pieces, in seg_n's place: S <- M S + R from piece to
+// piece (BACK: from the last piece to the first), one wave for 16 columns. In fp32
+// products for both types: they are few.
+template <int DK, int DV, bool BACK>
 __global__ __launch_bounds__(64) void join_kernel(const Args a) {
   constexpr int kTiles = DK / 16, kSteps = DK / 32;
   const int lane = threadIdx.x, c = lane % 16, q = lane / 16;
@@ -330,66 +390,85 @@ __global__ __launch_bounds__(64) void join_kernel(const Args a) {
   const int segs = (int)((len + a.per - 1) / a.per);
   if (segs < 2) return;
   const int64_t sid = begin / a.per + b;
-  f32x4 S[kTiles];
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      S[t][r] = a.state ? a.state[(((int64_t)b * a.hv + h) * DK + channel(t, 4 * q + r)) * DV + col] : 0.0f;
-  for (int seg = 0; seg < segs; ++seg) {
+  const float* from = BACK ? a.dlast : a.state;
+  f32x4 S[kTiles][1];
+  load_state<DK, 1>(S, from ? from + ((int64_t)b * a.hv + h) * DK * DV + col : nullptr, DV, q);
+  for (int i = 0; i < segs; ++i) {
+    const int seg = BACK ? segs - 1 - i : i;
     float* np = a.seg_n + ((sid + seg) * a.hv + h) * DK * DV + col;
     const float* mp = a.seg_m + ((sid + seg) * a.hv + h) * DK * DK;
-    f32x4 out[kTiles];
-    const bool more = seg + 1 < segs;
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float* at = np + channel(t, 4 * q + r) * DV;
-        out[t][r] = more ? *at : 0.0f;
-        *at = S[t][r];
-      }
+    f32x4 out[kTiles][1];
+    const bool more = i + 1 < segs;
+    load_state<DK, 1>(out, more ? np : nullptr, DV, q);
+    store_state<DK, 1>(S, np, DV, q);
     if (!more) break;
-    if (seg > 0) {  // the first piece was run from the sequence's own first state
+    if (i > 0) {  // the first piece was run from the given state
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           Frag<float> m, f;
           row8(m, mp + channel(t, c) * DK + 32 * s + 8 * q);
-          make(f, S[2 * s], S[2 * s + 1]);
-          out[t] = mm<1, 1>(m, f, out[t]);
+          make<1>(f, S[2 * s][0], S[2 * s + 1][0]);
+          out[t][0] = mm<1, 1>(m, f, out[t][0]);
         }
       }
     }
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) S[t] = out[t];
+    for (int t = 0; t < kTiles; ++t) S[t][0] = out[t][0];
   }
 }
 
-template <class T, int DK, int DV>
-hipError_t forward(const Args& a, const Plan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)(p.pieces * a.hv), DV / 64);
+template <class T, int DK, int DV, Mode MODE>
+hipError_t run_forward(const Args& a, const Plan& p, hipStream_t stream) {
+  const unsigned x = (unsigned)(p.pieces * a.hv);
   if (p.split) {
-    scan_kernel<T, DK, DV, 1, 4, 2, kSummary><<<dim3(grid.x, (DV + DK) / 64), 256, 0, stream>>>(a);
+    scan_kernel<T, DK, DV, 1, 4, 2, kSummary><<<dim3(x, (DV + DK) / 64), 256, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
-    join_kernel<DK, DV><<<dim3((unsigned)(a.nseq * a.hv), DV / 16), 64, 0, stream>>>(a);
+    join_kernel<DK, DV, false><<<dim3((unsigned)(a.nseq * a.hv), DV / 16), 64, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  scan_kernel<T, DK, DV, 1, 4, 2, kForward><<<grid, 256, 0, stream>>>(a);
+  scan_kernel<T, DK, DV, 1, 4, 2, MODE><<<dim3(x, DV / 64), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
+template <class T, int DK, int DV>
+hipError_t run_back(const Args& a, const Plan& p, hipStream_t stream) {
+  const unsigned x = (unsigned)(p.pieces * a.hv);
+  if (p.split) {
+    back_kernel<T, DK, DV, 1, 4, 2, kBackSummary><<<dim3(x, (DV + DK) / 64), 256, 0, stream>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+    join_kernel<DK, DV, true><<<dim3((unsigned)(a.nseq * a.hv), DV / 16), 64, 0, stream>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  back_kernel<T, DK, DV, 1, 4, 2, kBack><<<dim3(x, DV / 64), 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+enum What { kOutputs, kKeepStates, kReverse };
+
+template <class T, int DK, int DV>
+hipError_t run(const Args& a, const Plan& p, What what, hipStream_t s) {
+  if (what == kOutputs) return run_forward<T, DK, DV, kForward>(a, p, s);
+  if (what == kKeepStates) return run_forward<T, DK, DV, kStates>(a, p, s);
+  return run_back<T, DK, DV>(a, p, s);
+}
 template <class T>
-hipError_t forward_of(const Args& a, const Plan& p, hipStream_t s) {
-  if (a.dk == 64) return a.dv == 64 ? forward<T, 64, 64>(a, p, s) : forward<T, 64, 128>(a, p, s);
-  return a.dv == 64 ? forward<T, 128, 64>(a, p, s) : forward<T, 128, 128>(a, p, s);
+hipError_t run_of(const Args& a, const Plan& p, What what, hipStream_t s) {
+  if (a.dk == 64) return a.dv == 64 ? run<T, 64, 64>(a, p, what, s) : run<T, 64, 128>(a, p, what, s);
+  return a.dv == 64 ? run<T, 128, 64>(a, p, what, s) : run<T, 128, 128>(a, p, what, s);
 }
 
 }  // namespace
 
 hipError_t launch_forward(const Args& a, const Plan& p, bool bf16, hipStream_t stream) {
-  return bf16 ? forward_of<uint16_t>(a, p, stream) : forward_of<float>(a, p, stream);
+  return bf16 ? run_of<uint16_t>(a, p, kOutputs, stream) : run_of<float>(a, p, kOutputs, stream);
+}
+hipError_t launch_states(const Args& a, const Plan& p, bool bf16, hipStream_t stream) {
+  return bf16 ? run_of<uint16_t>(a, p, kKeepStates, stream) : run_of<float>(a, p, kKeepStates, stream);
+}
+hipError_t launch_back(const Args& a, const Plan& p, bool bf16, hipStream_t stream) {
+  return bf16 ? run_of<uint16_t>(a, p, kReverse, stream) : run_of<float>(a, p, kReverse, stream);
 }
 
 // Pieces: as long as about 512 workgroups of 64 columns allow, at least 4 chunks;
