@@ -851,8 +851,15 @@ def block_join_grad(r: torch.Tensor, f: Optional[torch.Tensor] = None, dr: Optio
 NORM_L2 = 3
 
 
+_QK_NORMS = {**_NORMS, "l2": NORM_L2}
+
+
 def _qk_norm_code(kind) -> int:
-    return NORM_L2 if kind == "l2" else _norm_code(kind)
+    if kind is not None and not isinstance(kind, str):
+        return int(kind)
+    if kind not in _QK_NORMS:
+        raise KeyError(f"unknown norm {kind!r}; None, 'none', 'l2', 'rms' or 'layer'")
+    return _QK_NORMS[kind]
 
 
 def _heads_of(name: str, t: torch.Tensor, heads: int, d: Optional[int] = None) -> int:
@@ -870,6 +877,8 @@ def _rows_of(name: str, t: Optional[torch.Tensor]):
         return None, 0
     if t.get_device() < 0:
         raise ValueError("tensors must live on the GPU (HIP device memory)")
+    if t.numel() == 0:
+        return None, t.shape[1]
     if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
         raise ValueError(f"{name}: the channels of a row must be neighbours and rows apart, strides {t.stride()}")
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
@@ -915,6 +924,7 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], n_heads: int, n_hea
     axis turns: with per_axis each axis has channels and a ladder of frequencies
     base^(-j / section) of its own, without it all pairs share one. Pairs are a half apart,
     or neighbours (interleaved). q_out may be q and k_out k."""
+    kind = _qk_norm_code(norm)
     d, hk, sections = _qk_inputs(q, k, n_heads, n_heads_k, pos, sections, dict(q_w=q_w, q_b=q_b, k_w=k_w, k_b=k_b))
     n = q.shape[0]
     if q_out is None:
@@ -929,7 +939,7 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], n_heads: int, n_hea
     pk, sk = _rows_of("k", k)
     dev, (_, _, qw, qb, kw, kb, pp, po, ko) = _pointers(q[:0], None if k is None else k[:0], q_w, q_b, k_w, k_b, pos, q_out,
                                                         k_out)
-    _run("vggt3_qk_norm_rope", dev, pq, sq, pk, sk, _qk_norm_code(norm), qw, qb, kw, kb, float(eps), pp,
+    _run("vggt3_qk_norm_rope", dev, pq, sq, pk, sk, kind, qw, qb, kw, kb, float(eps), pp,
          _sections_ptr(sections), len(sections), float(base), int(bool(per_axis)), int(bool(interleaved)), po, ko, n,
          n_heads, hk, d, _dtype_code(q))
     return q_out, k_out
@@ -962,6 +972,7 @@ def qk_norm_rope_grad(q: torch.Tensor, k: Optional[torch.Tensor], dq_out: torch.
     Gradients of what was given are returned (bias: there were biases, whose values
     do not enter). With `out`, exactly its tensors are written; out.dq may be
     dq_out and out.dk dk_out."""
+    kind = _qk_norm_code(norm)
     d, hk, sections = _qk_inputs(q, k, n_heads, n_heads_k, pos, sections, dict(q_w=q_w, k_w=k_w))
     n = q.shape[0]
     if (k is None) != (dk_out is None):
@@ -987,7 +998,7 @@ def qk_norm_rope_grad(q: torch.Tensor, k: Optional[torch.Tensor], dq_out: torch.
     pk, sk = _rows_of("k", k)
     dev, (_, _, dqo, dko, qw, kw, pp, ws, *grads) = _pointers(q[:0], None if k is None else k[:0], dq_out, dk_out, q_w, k_w,
                                                               pos, workspace, *out)
-    _run("vggt3_qk_norm_rope_grad", dev, pq, sq, pk, sk, dqo, dko, _qk_norm_code(norm), qw, kw, float(eps), pp,
+    _run("vggt3_qk_norm_rope_grad", dev, pq, sq, pk, sk, dqo, dko, kind, qw, kw, float(eps), pp,
          _sections_ptr(sections), len(sections), float(base), int(bool(per_axis)), int(bool(interleaved)), *grads, n, n_heads,
          hk, d, _dtype_code(q), ws, nb)
     return out
