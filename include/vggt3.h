@@ -686,8 +686,7 @@ int vggt3_qk_norm_rope_grad(const void* q, int64_t q_stride, const void* k, int6
  *   state, state_out   float32 [n_seqs][n_heads_v][d_k][d_v]: S before each
  *                sequence (NULL: 0) and after it (NULL: not wanted). state_out may be
  *                state.
- *   workspace    at least vggt3_gated_delta_workspace_bytes(...) bytes (may be NULL when
- *                that is 0).
+ *   workspace    at least vggt3_gated_delta_workspace_bytes(...) bytes.
  * Computed by chunks of 32 tokens (the same values by matrix products): S, decays,
  * sums and the chunk's triangular inverse are fp32 (bf16 dtype: products of fp32 values
  * in three bf16 parts; two for o), o is rounded once. A value that is not finite makes its sequence's
@@ -712,8 +711,8 @@ int vggt3_gated_delta(const void* q, const void* k, const void* v, const float* 
  *                dstate float32, of state (may be dstate_out; may be asked for without a
  *                state). Each may be NULL (not wanted). Rows of no sequence are left as
  *                they are.
- *   workspace    at least vggt3_gated_delta_grad_workspace_bytes(...) bytes: the state
- *                before, and the gradient of the state after, every 32 tokens.
+ *   workspace    at least vggt3_gated_delta_grad_workspace_bytes(...) bytes: for every 32
+ *                tokens, the state before them and the gradient of the state after them.
  * Rounding as in the forward; no atomics, the same bits each time. n_tokens == 0 copies
  * dstate_out to dstate.
  */

@@ -43,35 +43,43 @@ delta::Plan plan_of(const Shape& s, int64_t max_seqlen) {
   return delta::plan(s.n, s.nseq, longest_of(max_seqlen, s.n), s.hv, s.dk, s.dv);
 }
 
-// Workspace of the forward: [a piece's R | a piece's M].
+// Workspace of the forward: [chunks' matrices | a piece's R | a piece's M].
 struct Ws {
-  size_t m, total;
+  size_t seg_n, seg_m, total;
 };
-Ws forward_ws(const Shape& s, const delta::Plan& p) {
-  Ws w{0, 0};
-  if (!p.split) return w;
-  w.m = round256((size_t)p.pieces * s.state());
-  w.total = w.m + round256((size_t)p.pieces * s.hv * s.dk * s.dk * sizeof(float));
+Ws forward_ws(const Shape& s, const delta::Plan& p, bool keep) {
+  Ws w;
+  w.seg_n = round256((size_t)delta::chunk_slots(s.n, s.nseq) * s.hv * delta::matrix_bytes(keep));
+  w.seg_m = w.seg_n + (p.split ? round256((size_t)p.pieces * s.state()) : 0);
+  w.total = w.seg_m + (p.split ? round256((size_t)p.pieces * s.hv * s.dk * s.dk * sizeof(float)) : 0);
   return w;
 }
 
-// Workspace of the gradient: [states before chunks | gradients after chunks | pieces,
-// as the forward's | dq and dk by value head, where these share a key head].
+// Workspace of the gradient: [the forward's | states before chunks | gradients after
+// chunks | dq and dk by value head, where these share a key head].
 struct GradWs {
-  size_t dstates, seg_n, seg_m, dq, dk, total;
+  Ws f;
+  size_t states, dstates, dq, dk, total;
 };
 GradWs grad_ws(const Shape& s, const delta::Plan& p) {
   const size_t all = round256((size_t)delta::chunk_slots(s.n, s.nseq) * s.state());
-  const Ws f = forward_ws(s, p);
   GradWs w;
-  w.dstates = all;
-  w.seg_n = 2 * all;
-  w.seg_m = w.seg_n + f.m;
-  w.dq = w.seg_n + f.total;
+  w.f = forward_ws(s, p, true);
+  w.states = w.f.total;
+  w.dstates = w.states + all;
+  w.dq = w.dstates + all;
   const size_t part = s.hv == s.hk ? 0 : round256((size_t)s.n * s.hv * s.dk * sizeof(float));
   w.dk = w.dq + part;
   w.total = w.dk + part;
   return w;
+}
+
+// The workspace's matrices and pieces.
+void place(delta::Args& a, char* ws, const Ws& w, bool keep) {
+  a.mats = ws;
+  a.keep = keep;
+  a.seg_n = reinterpret_cast<float*>(ws + w.seg_n);
+  a.seg_m = reinterpret_cast<float*>(ws + w.seg_m);
 }
 
 int check_scale(float scale) {
@@ -93,7 +101,7 @@ size_t vggt3_gated_delta_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int64
                                          int32_t n_heads_v, int32_t d_k, int32_t d_v, int32_t dtype) {
   const Shape s{n_tokens, n_seqs, n_heads, n_heads_v, d_k, d_v, dtype};
   if (check_shape(s) != VGGT3_OK || max_seqlen < 0) return 0;
-  return forward_ws(s, plan_of(s, max_seqlen)).total;
+  return forward_ws(s, plan_of(s, max_seqlen), false).total;
 }
 
 int vggt3_gated_delta(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -112,10 +120,11 @@ int vggt3_gated_delta(const void* q, const void* k, const void* v, const float* 
       if (need[i] == nullptr) return fail(VGGT3_EINVAL, "%s is NULL", names[i]);
   }
   const delta::Plan p = plan_of(s, max_seqlen);
-  const Ws w = forward_ws(s, p);
+  const Ws w = forward_ws(s, p, false);
   rc = check_grid(p.pieces * s.hv);
+  if (!rc) rc = check_grid(delta::chunk_slots(n_tokens, n_seqs) * s.hv / 4);
   if (rc) return rc;
-  if (w.total > 0 && (workspace == nullptr || workspace_bytes < w.total))
+  if (workspace == nullptr || workspace_bytes < w.total)
     return fail(VGGT3_EWORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : (size_t)0, w.total);
   const size_t states = (size_t)n_seqs * s.state();
   const Region rs[] = {{"q", q, s.keys(), false},
@@ -127,14 +136,13 @@ int vggt3_gated_delta(const void* q, const void* k, const void* v, const float* 
                        {"state", state, states, false},
                        {"o", o, s.values(), true},
                        {"state_out", state_out, states, true},
-                       {"workspace", w.total ? workspace : nullptr, w.total, true}};
+                       {"workspace", workspace, w.total, true}};
   rc = check_regions(rs, 10, {{6, 8}});  // in place: state_out may be state
   if (rc) return rc;
   delta::Args a{};
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.cu = cu_seqlens; a.state = state;
   a.o = o; a.state_out = state_out;
-  a.seg_n = static_cast<float*>(workspace);
-  a.seg_m = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.m);
+  place(a, static_cast<char*>(workspace), w, false);
   a.n = n_tokens; a.per = p.per; a.nseq = n_seqs; a.hk = n_heads; a.hv = n_heads_v; a.dk = d_k; a.dv = d_v;
   a.scale = scale;
   rc = check_hip(delta::launch_forward(a, p, dtype == VGGT3_BF16, static_cast<hipStream_t>(stream)),
@@ -197,10 +205,9 @@ int vggt3_gated_delta_grad(const void* q, const void* k, const void* v, const fl
   delta::Args a{};
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.cu = cu_seqlens; a.state = state;
   a.dout = d_o; a.dlast = dstate_out; a.dfirst = dstate;
-  a.states = reinterpret_cast<float*>(ws);
+  place(a, ws, w.f, true);
+  a.states = reinterpret_cast<float*>(ws + w.states);
   a.dstates = reinterpret_cast<float*>(ws + w.dstates);
-  a.seg_n = reinterpret_cast<float*>(ws + w.seg_n);
-  a.seg_m = reinterpret_cast<float*>(ws + w.seg_m);
   a.dq = dq; a.dk_out = dk; a.dv_out = dv; a.dg = dg; a.dbeta = dbeta;
   if (s.hv != s.hk) {
     a.dq_part = reinterpret_cast<float*>(ws + w.dq);

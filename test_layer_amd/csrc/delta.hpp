@@ -17,6 +17,8 @@ struct Args {
   const float* state; // NULL (zeros) or [nseq][hv][dk][dv]
   void* o;
   float* state_out;
+  void* mats;  // [chunks][hv]: the chunks' shared matrices
+  int keep;    // those of the gradient among them
   // pieces (segments) of a sequence that are worked on at once
   float* seg_n;  // [pieces][hv][dk][dv]: a piece's last state from none; then its first state
   float* seg_m;  // [pieces][hv][dk][dk]: what it makes of its first state
@@ -40,9 +42,10 @@ struct Args {
 
 // How a call's sequences are cut: pieces of `per` tokens, at most `pieces` in all;
 // split: whether a sequence may have more than one.
+// wide: a wave has 64 columns (32 where d_k is 128) instead of 16.
 struct Plan {
   int64_t per, pieces;
-  bool split;
+  bool split, wide;
 };
 Plan plan(int64_t n, int nseq, int64_t longest, int hv, int dk, int dv);
 
@@ -62,6 +65,9 @@ struct StepArgs {
 
 hipError_t launch_step(const StepArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_forward(const Args& a, const Plan& p, bool bf16, hipStream_t stream);
+
+// Bytes of a chunk's and head's shared matrices (keep: with the gradient's).
+size_t matrix_bytes(bool keep);
 
 // The gradient: the state before every chunk, then the gradient of the state after
 // every chunk (and dfirst), then everything else chunk by chunk. Chunks of sequence

@@ -3,6 +3,8 @@
 // formulas.
 #pragma once
 
+#include <cstddef>
+
 #include "delta.hpp"
 #include "delta_ops.hpp"
 
@@ -171,6 +173,53 @@ __device__ __forceinline__ f32x4 turned(const f32x4& x, int lane) {
   return mm16(x, one, zero4());
 }
 
+// A chunk's shared matrices in memory, as operands: tiles 00, 10, 11 of T and B by row,
+// and for the gradient of their transposes (tiles by column). B of the forward alone is
+// in two bf16 parts (bf16).
+struct Matrices {
+  f32x4 t[3][64];
+  f32x4 b[3][64];
+  Rows rows;
+  float pad[kChunk - 1];
+  f32x4 tt[3][64];  // the gradient's only
+  f32x4 bt[3][64];
+};
+__host__ __device__ constexpr size_t matrices_bytes(bool keep) {
+  return keep ? sizeof(Matrices) : offsetof(Matrices, tt);
+}
+__device__ __forceinline__ Matrices* matrices_of(void* base, int64_t at, bool keep) {
+  return reinterpret_cast<Matrices*>(static_cast<char*>(base) + at * matrices_bytes(keep));
+}
+__device__ __forceinline__ void put_tri(f32x4 (*to)[64], const Tri& m, int lane) {
+  to[0][lane] = m.t00;
+  to[1][lane] = m.t10;
+  to[2][lane] = m.t11;
+}
+// A tile in two bf16 parts, and two of them as an operand.
+template <class T>
+__device__ __forceinline__ u32x4 tile_parts(const f32x4& x) {
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(u32x4, x);
+  } else {
+    const uint32_t a = pack_bf16x2(x[0], x[1]), b = pack_bf16x2(x[2], x[3]);
+    return u32x4{a, b, pack_bf16x2(x[0] - bf16_lo(a), x[1] - bf16_hi(a)), pack_bf16x2(x[2] - bf16_lo(b), x[3] - bf16_hi(b))};
+  }
+}
+template <class T>
+__device__ __forceinline__ void put_tri_parts(f32x4 (*to)[64], const Tri& m, int lane) {
+  to[0][lane] = __builtin_bit_cast(f32x4, tile_parts<T>(m.t00));
+  to[1][lane] = __builtin_bit_cast(f32x4, tile_parts<T>(m.t10));
+  to[2][lane] = __builtin_bit_cast(f32x4, tile_parts<T>(m.t11));
+}
+__device__ __forceinline__ void parts_frag(Frag<uint16_t>& f, const u32x4& x, const u32x4& y) {
+  f.part[0] = as_bf16x8(u32x4{x[0], x[1], y[0], y[1]});
+  f.part[1] = as_bf16x8(u32x4{x[2], x[3], y[2], y[3]});
+}
+__device__ __forceinline__ void parts_frag(Frag<float>& f, const u32x4& x, const u32x4& y) {
+  f.a = __builtin_bit_cast(f32x4, x);
+  f.b = __builtin_bit_cast(f32x4, y);
+}
+
 // The tile of 16 * NCT columns that a lane has NCT of, to and from rows in memory.
 template <int DK, int NCT>
 __device__ __forceinline__ void load_state(f32x4 (*S)[NCT], const float* from, int64_t ld, int q) {
@@ -235,6 +284,10 @@ __device__ __forceinline__ void store_rows(T* to, const f32x4 (*V)[NCT], int64_t
       for (int x = 0; x < NCT; ++x) w[x] = V[it][x][r];
       if (row < len) store_n<NCT>(to + row * ld, w);
     }
+}
+
+__device__ __forceinline__ Tri turned(const Tri& m, int lane) {
+  return Tri{turned(m.t00, lane), turned(m.t10, lane), turned(m.t11, lane)};
 }
 
 }  // namespace delta

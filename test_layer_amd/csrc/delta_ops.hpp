@@ -206,6 +206,89 @@ __device__ __forceinline__ void store_n(float* p, const float* v) {
   }
 }
 
+// Rows of a sequence through buffer descriptors: `len` rows from `base` on, each of D
+// values, `ld` apart. Reads behind the last row give 0 and writes there are dropped, by
+// the descriptor's range check. Offsets are in bytes.
+typedef __amdgpu_buffer_rsrc_t Window;
+template <int D, class T>
+__device__ __forceinline__ Window window(const T* base, int64_t ld, int len) {
+  const int64_t values = len > 0 ? (len - 1) * ld + D : 0;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)(values * (int)sizeof(T)), 0x00020000);
+}
+// 8 values of a row, as they are stored.
+template <class T>
+struct Raw {
+  u32x4 r[sizeof(T) / 2];
+};
+template <class T>
+__device__ __forceinline__ void load_raw(Raw<T>& f, Window w, int off) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    f.r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w, off + 16 * i, 0, 0));
+}
+template <class T>
+__device__ __forceinline__ void put_raw(T* p, const Raw<T>& f) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) st16(p + 16 / sizeof(T) * i, f.r[i]);
+}
+__device__ __forceinline__ void as_frag(Frag<uint16_t>& f, const Raw<uint16_t>& x) { f.part[0] = as_bf16x8(x.r[0]); }
+__device__ __forceinline__ void as_frag(Frag<float>& f, const Raw<float>& x) {
+  f.a = __builtin_bit_cast(f32x4, x.r[0]);
+  f.b = __builtin_bit_cast(f32x4, x.r[1]);
+}
+// N neighbouring values of a row, as they are stored, and as fp32.
+template <class T, int N>
+struct RawN {
+  uint32_t r[(N * sizeof(T) + 3) / 4];
+};
+template <class T, int N>
+__device__ __forceinline__ void load_rawn(RawN<T, N>& f, Window w, int off) {
+  constexpr int kBytes = N * (int)sizeof(T);
+  if constexpr (kBytes == 2) {
+    f.r[0] = __builtin_amdgcn_raw_buffer_load_b16(w, off, 0, 0);
+  } else if constexpr (kBytes == 4) {
+    f.r[0] = __builtin_amdgcn_raw_buffer_load_b32(w, off, 0, 0);
+  } else if constexpr (kBytes == 8) {
+    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(w, off, 0, 0));
+    f.r[0] = x[0];
+    f.r[1] = x[1];
+  } else {
+    const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w, off, 0, 0));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.r[i] = x[i];
+  }
+}
+template <int N>
+__device__ __forceinline__ float value_of(const RawN<uint16_t, N>& f, int i) {
+  return i % 2 ? bf16_hi(f.r[i / 2]) : bf16_lo(f.r[i / 2]);
+}
+template <int N>
+__device__ __forceinline__ float value_of(const RawN<float, N>& f, int i) {
+  return __uint_as_float(f.r[i]);
+}
+template <class T, int N>
+__device__ __forceinline__ void store_rawn(Window w, int off, const float* v) {
+  constexpr int kBytes = N * (int)sizeof(T);
+  uint32_t x[(kBytes + 3) / 4];
+#pragma unroll
+  for (int i = 0; i < (kBytes + 3) / 4; ++i) {
+    if constexpr (sizeof(T) == 4)
+      x[i] = __float_as_uint(v[i]);
+    else if constexpr (N == 1)
+      x[i] = f32_to_bf16_bits(v[0]);
+    else
+      x[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  }
+  if constexpr (kBytes == 2)
+    __builtin_amdgcn_raw_buffer_store_b16((unsigned short)x[0], w, off, 0, 0);
+  else if constexpr (kBytes == 4)
+    __builtin_amdgcn_raw_buffer_store_b32(x[0], w, off, 0, 0);
+  else if constexpr (kBytes == 8)
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{x[0], x[1]}, w, off, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{x[0], x[1], x[2], x[3]}, w, off, 0, 0);
+}
+
 // Between a wave's writes to LDS and its reads of what other lanes wrote: LDS
 // operations of one wave are carried out in order, so only the compiler has to
 // keep it.

@@ -12,10 +12,11 @@
 //
 // A column of S, and of everything that u and O are made of, depends on no other
 // column. So a wave keeps NCT tiles of 16 columns of S in registers over its whole
-// piece of a sequence, and the products chain through its registers (delta_ops.hpp);
-// only K, T and the triangle of Q K^T, which all columns share, pass through LDS.
-// A workgroup takes GC chunks at a time: each of GC waves prepares one chunk's
-// shared matrices by itself, then all waves run through the chunks.
+// piece of a sequence, and the products chain through its registers (delta_ops.hpp).
+// T and the triangle of Q K^T, which all columns share and no state enters, are formed
+// beforehand for all chunks at once (matrices_kernel) and read as operands. A wave
+// works by itself: it asks for the next chunk's rows and operands before it computes,
+// and passes K alone through LDS, for its transpose.
 //
 // Long sequences are cut into pieces that are worked on at once: a first pass finds
 // what each piece makes of its first state (M S + R: the columns of M are those of
@@ -28,65 +29,87 @@ namespace vggt3 {
 namespace delta {
 namespace {
 
-// kStates: the state before every chunk, for the gradient (no outputs).
-enum Mode { kForward, kSummary, kStates };
-
-template <class T, int DK>
-struct Shared {
-  T k[kChunk][kPitch<T, DK>];
-  u32x4 t[2 * kOperand<T>];  // T
-  u32x4 b[2 * kOperand<T>];  // the triangle of Q K^T
-  Rows rows;
-};
-
-// One wave prepares a chunk: rows first .. first + len - 1, len in 1 .. 32 (rows
-// behind them count as zeros).
-template <class T, int DK, bool QK>
-__device__ __forceinline__ void prepare(Shared<T, DK>& sh, const Args& a, int64_t first, int len, int h, int lane) {
-  const int kh = h / (a.hv / a.hk), c = lane % 16, q = lane / 16;
+// One wave to a chunk and head: its shared matrices. KEEP: those of the gradient too.
+template <class T, int DK, bool KEEP>
+__global__ __launch_bounds__(256) void matrices_kernel(const Args a) {
+  __shared__ float scratch[4][2 * 16 * 20];
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int c = lane % 16, q = lane / 16;
+  const int64_t id = (int64_t)blockIdx.x * 4 + wave;
+  const int h = (int)(id % a.hv);
+  const int64_t slot = id / a.hv;
+  const Piece p = find_piece(a.cu, a.nseq, a.n, kChunk, slot, lane);
+  if (p.seg < 0 || p.len == 0) return;
   const int64_t ld = (int64_t)a.hk * DK;
-  stage<T, DK, 64>(&sh.k[0][0], static_cast<const T*>(a.k) + first * ld + kh * DK, ld, len, lane);
-  const Gates gt = gates(a, first, len, h, lane);
-  put_rows(sh.rows, gt, lane);
-  wave_lds_order();
-  // keys as a tile's rows: results by row of N and of Q K^T
-  const auto key = [&](Frag<T>& f, int row, int col) { row8(f, &sh.k[row + c][col]); };
-  const T* qp = static_cast<const T*>(a.q) + first * ld + kh * DK;
-  const auto query = [&](Frag<T>& f, int row, int col) {
-    clear(f);
-    if (row + c < len) row8(f, qp + (row + c) * ld + col);
-  };
-  Tri n{zero4(), zero4(), zero4()}, w = n;
+  const int64_t at = p.first * ld + h / (a.hv / a.hk) * DK;
+  const Window kw = window<DK>(static_cast<const T*>(a.k) + at, ld, p.len);
+  const Window qw = window<DK>(static_cast<const T*>(a.q) + at, ld, p.len);
+  const int off = (int)((c * ld + 8 * q) * (int)sizeof(T)), next = (int)(16 * ld * (int)sizeof(T));
+  Raw<T> kr[2][DK / 32], qr[2][DK / 32];
+#pragma unroll
+  for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      load_raw(kr[it][s], kw, off + it * next + 32 * s * (int)sizeof(T));
+      load_raw(qr[it][s], qw, off + it * next + 32 * s * (int)sizeof(T));
+    }
+  const Gates gt = gates(a, p.first, p.len, h, lane);
+  // keys as a tile's rows: N and Q K^T by row
+  Tri n{zero4(), zero4(), zero4()}, b = n, bt = n;
 #pragma unroll
   for (int s = 0; s < DK / 32; ++s) {
     Frag<T> k0, k1, q0, q1;
-    key(k0, 0, 32 * s + 8 * q);
-    key(k1, 16, 32 * s + 8 * q);
+    as_frag(k0, kr[0][s]);
+    as_frag(k1, kr[1][s]);
+    as_frag(q0, qr[0][s]);
+    as_frag(q1, qr[1][s]);
     n.t00 = mm<1, 1>(k0, k0, n.t00);
     n.t10 = mm<1, 1>(k0, k1, n.t10);
     n.t11 = mm<1, 1>(k1, k1, n.t11);
-    if constexpr (QK) {
-      query(q0, 0, 32 * s + 8 * q);
-      query(q1, 16, 32 * s + 8 * q);
-      w.t00 = mm<1, 1>(k0, q0, w.t00);
-      w.t10 = mm<1, 1>(k0, q1, w.t10);
-      w.t11 = mm<1, 1>(k1, q1, w.t11);
+    b.t00 = mm<1, 1>(k0, q0, b.t00);
+    b.t10 = mm<1, 1>(k0, q1, b.t10);
+    b.t11 = mm<1, 1>(k1, q1, b.t11);
+    if constexpr (KEEP) {
+      bt.t00 = mm<1, 1>(q0, k0, bt.t00);
+      bt.t10 = mm<1, 1>(q1, k0, bt.t10);
+      bt.t11 = mm<1, 1>(q1, k1, bt.t11);
     }
   }
   decay_tri<false>(n, gt, true, true, 1.0f, lane);
+  decay_tri<false>(b, gt, false, false, a.scale, lane);
   Tri t;
-  unit_inverse(n.t00, n.t10, n.t11, t.t00, t.t10, t.t11, reinterpret_cast<float*>(sh.t), lane);
-  put_lower<T, kWhole<T>>(sh.t, t, lane);
-  if constexpr (QK) {
-    decay_tri<false>(w, gt, false, false, a.scale, lane);
-    put_lower<T, 2>(sh.b, w, lane);
+  unit_inverse(n.t00, n.t10, n.t11, t.t00, t.t10, t.t11, scratch[wave], lane);
+  Matrices* m = matrices_of(a.mats, slot * a.hv + h, KEEP);
+  put_tri(m->t, t, lane);
+  if constexpr (KEEP) {
+    put_tri(m->b, b, lane);
+    decay_tri<true>(bt, gt, false, false, a.scale, lane);
+    put_tri(m->bt, bt, lane);
+    put_tri(m->tt, turned(t, lane), lane);
+  } else {
+    put_tri_parts<T>(m->b, b, lane);
   }
+  put_rows(m->rows, gt, lane);
 }
 
-template <class T, int DK, int DV, int NCT, int W, int GC, Mode MODE>
-__global__ __launch_bounds__(64 * W, 1) void scan_kernel(const Args a) {
-  constexpr int kTiles = DK / 16, kSteps = DK / 32, kP = kWhole<T>;
-  __shared__ Shared<T, DK> sh[GC];
+// kStates: the state before every chunk, for the gradient (no outputs).
+enum Mode { kForward, kSummary, kStates };
+
+// What a wave has of a chunk before it computes.
+template <class T, int DK, int NCT, Mode MODE>
+struct Loaded {
+  Raw<T> k[2][DK / 32], q[MODE == kForward ? 2 : 0][DK / 32];
+  RawN<T, NCT> v[2][4];
+  f32x4 t[3];
+  u32x4 b[3];
+  f32x4 decay[2], rest[2], beta[2];
+  float total;
+};
+
+template <class T, int DK, int DV, int NCT, Mode MODE>
+__global__ __launch_bounds__(64 * (4 / NCT), 1) void scan_kernel(const Args a) {
+  constexpr int kTiles = DK / 16, kSteps = DK / 32, kP = kWhole<T>, kW = 4 / NCT, kB = (int)sizeof(T);
+  __shared__ T ks_rows[kW][kChunk * kPitch<T, DK>];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int c = lane % 16, q = lane / 16;
   const int h = blockIdx.x % a.hv;
@@ -95,9 +118,10 @@ __global__ __launch_bounds__(64 * W, 1) void scan_kernel(const Args a) {
   if (p.seg < 0) return;
   if (MODE == kSummary && p.seg == p.segs - 1) return;  // nothing follows it
   // this lane's columns: NCT neighbours
-  const int col = (blockIdx.y * W + wave) * 16 * NCT + NCT * c;
-  const bool unit = MODE == kSummary && col >= DV;
-  if (unit && p.seg == 0) return;  // its first state is known (whole workgroups: DV is a multiple of their columns)
+  const int col = blockIdx.y * 64 + wave * 16 * NCT + NCT * c;
+  const bool unit = MODE == kSummary && blockIdx.y * 64 >= DV;
+  if (unit && p.seg == 0) return;  // its first state is known
+  T* const kt_rows = ks_rows[wave];
 
   f32x4 S[kTiles][NCT];
   if (unit) {
@@ -114,91 +138,138 @@ __global__ __launch_bounds__(64 * W, 1) void scan_kernel(const Args a) {
   const int64_t ldq = (int64_t)a.hk * DK, ldv = (int64_t)a.hv * DV;
   const int kh = h / (a.hv / a.hk);
   const int chunks = (p.len + kChunk - 1) / kChunk;
-  for (int c0 = 0; c0 < chunks; c0 += GC) {
-    if (wave < GC && c0 + wave < chunks) {
-      const int at = (c0 + wave) * kChunk;
-      prepare<T, DK, MODE == kForward>(sh[wave], a, p.first + at, min(kChunk, p.len - at), h, lane);
-    }
-    __syncthreads();
-    for (int i = 0; i < GC && c0 + i < chunks; ++i) {
-      const Shared<T, DK>& m = sh[i];
-      const int64_t first = p.first + (int64_t)(c0 + i) * kChunk;
-      const int len = min(kChunk, p.len - (c0 + i) * kChunk);
-      if constexpr (MODE == kStates) {
-        const int64_t slot = p.begin / kChunk + p.b + (p.first - p.begin) / kChunk + c0 + i;
-        store_state<DK, NCT>(S, a.states + (slot * a.hv + h) * DK * DV + col, DV, q);
-      }
-      f32x4 V[2][NCT];
-      load_rows<NCT>(V, static_cast<const T*>(a.v) + first * ldv + h * DV + col, ldv, unit ? 0 : len, q);
-      Frag<T> qf[2][kSteps];
-      if constexpr (MODE == kForward) {
+  const int64_t slot0 = p.begin / kChunk + p.b + (p.first - p.begin) / kChunk;
+  const int koff = (int)((c * ldq + 8 * q) * kB), knext = (int)(16 * ldq * kB);
+  const int voff = (int)((4 * q * ldv + NCT * c) * kB), vrow = (int)(ldv * kB);
+
+  typedef Loaded<T, DK, NCT, MODE> L;
+  const auto load = [&](L& x, int i) {
+    const int64_t first = p.first + (int64_t)i * kChunk;
+    const int len = min(kChunk, p.len - i * kChunk);
+    const Window kw = window<DK>(static_cast<const T*>(a.k) + first * ldq + kh * DK, ldq, len);
 #pragma unroll
-        for (int it = 0; it < 2; ++it)
+    for (int it = 0; it < 2; ++it)
 #pragma unroll
-          for (int s = 0; s < kSteps; ++s) {
-            clear(qf[it][s]);
-            if (16 * it + c < len)
-              row8(qf[it][s], static_cast<const T*>(a.q) + (first + 16 * it + c) * ldq + kh * DK + 32 * s + 8 * q);
-          }
-      }
-      f32x4 ks[2][NCT], o[2][NCT];
+      for (int s = 0; s < kSteps; ++s) load_raw(x.k[it][s], kw, koff + it * knext + 32 * s * kB);
+    if constexpr (MODE == kForward) {
+      const Window qw = window<DK>(static_cast<const T*>(a.q) + first * ldq + kh * DK, ldq, len);
 #pragma unroll
       for (int it = 0; it < 2; ++it)
 #pragma unroll
-        for (int x = 0; x < NCT; ++x) ks[it][x] = o[it][x] = zero4();
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        Frag<T> k0, k1;
-        row8(k0, &m.k[c][32 * s + 8 * q]);
-        row8(k1, &m.k[16 + c][32 * s + 8 * q]);
-#pragma unroll
-        for (int x = 0; x < NCT; ++x) {
-          Frag<T> f;
-          make<kP>(f, S[2 * s][x], S[2 * s + 1][x]);
-          ks[0][x] = mm<1, kP>(k0, f, ks[0][x]);
-          ks[1][x] = mm<1, kP>(k1, f, ks[1][x]);
-          if constexpr (MODE == kForward) {
-            o[0][x] = mm<1, 2>(qf[0][s], f, o[0][x]);
-            o[1][x] = mm<1, 2>(qf[1][s], f, o[1][x]);
-          }
-        }
-      }
-      f32x4 dec[2], rest[2], bt[2];
-#pragma unroll
-      for (int it = 0; it < 2; ++it) {
-        dec[it] = rows4(m.rows.decay, it, q);
-        rest[it] = rows4(m.rows.rest, it, q);
-        bt[it] = rows4(m.rows.beta, it, q);
-      }
-      const float total = m.rows.total;
-      Frag<T> t0, t1;
-      get<kP>(t0, m.t, lane);
-      get<kP>(t1, m.t + kOperand<T>, lane);
-#pragma unroll
-      for (int x = 0; x < NCT; ++x) {
-        Frag<T> f;
-        make<kP>(f, V[0][x] - dec[0] * ks[0][x], V[1][x] - dec[1] * ks[1][x]);
-        const f32x4 u0 = mm<kP, kP>(t0, f, zero4()) * bt[0], u1 = mm<kP, kP>(t1, f, zero4()) * bt[1];
-        if constexpr (MODE == kForward) {
-          Frag<T> b0, b1;
-          get<2>(b0, m.b, lane);
-          get<2>(b1, m.b + kOperand<T>, lane);
-          make<2>(f, u0, u1);
-          o[0][x] = mm<2, 2>(b0, f, o[0][x] * (dec[0] * a.scale));
-          o[1][x] = mm<2, 2>(b1, f, o[1][x] * (dec[1] * a.scale));
-        }
-        make<kP>(f, u0 * rest[0], u1 * rest[1]);
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          Frag<T> kt;
-          state_rows<kPitch<T, DK>>(kt, &m.k[0][0], t, lane);
-          S[t][x] = mm<1, kP>(kt, f, S[t][x] * total);
-        }
-      }
-      if constexpr (MODE == kForward)
-        store_rows<NCT>(static_cast<T*>(a.o) + first * ldv + h * DV + col, o, ldv, len, q);
+        for (int s = 0; s < kSteps; ++s) load_raw(x.q[it][s], qw, koff + it * knext + 32 * s * kB);
     }
-    __syncthreads();
+    const Window vw = window<16 * NCT>(static_cast<const T*>(a.v) + first * ldv + h * DV + (unit ? 0 : col - NCT * c), ldv,
+                                       unit ? 0 : len);
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) load_rawn(x.v[it][r], vw, voff + (16 * it + r) * vrow);
+    const Matrices* m = matrices_of(a.mats, (slot0 + i) * a.hv + h, a.keep);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      x.t[j] = m->t[j][lane];
+      if constexpr (MODE == kForward) x.b[j] = __builtin_bit_cast(u32x4, m->b[j][lane]);
+    }
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      x.decay[it] = rows4(m->rows.decay, it, q);
+      x.rest[it] = rows4(m->rows.rest, it, q);
+      x.beta[it] = rows4(m->rows.beta, it, q);
+    }
+    x.total = m->rows.total;
+  };
+  const auto compute = [&](const L& x, int i) {
+    if constexpr (MODE == kStates)
+      store_state<DK, NCT>(S, a.states + ((slot0 + i) * a.hv + h) * DK * DV + col, DV, q);
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) put_raw(kt_rows + (16 * it + c) * kPitch<T, DK> + 32 * s + 8 * q, x.k[it][s]);
+    f32x4 ks[2][NCT], o[2][NCT];
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int y = 0; y < NCT; ++y) ks[it][y] = o[it][y] = zero4();
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      Frag<T> k0, k1, q0, q1;
+      as_frag(k0, x.k[0][s]);
+      as_frag(k1, x.k[1][s]);
+      if constexpr (MODE == kForward) {
+        as_frag(q0, x.q[0][s]);
+        as_frag(q1, x.q[1][s]);
+      }
+#pragma unroll
+      for (int y = 0; y < NCT; ++y) {
+        Frag<T> f;
+        make<kP>(f, S[2 * s][y], S[2 * s + 1][y]);
+        ks[0][y] = mm<1, kP>(k0, f, ks[0][y]);
+        ks[1][y] = mm<1, kP>(k1, f, ks[1][y]);
+        if constexpr (MODE == kForward) {
+          o[0][y] = mm<1, 2>(q0, f, o[0][y]);
+          o[1][y] = mm<1, 2>(q1, f, o[1][y]);
+        }
+      }
+    }
+    Frag<T> t0, t1, b0, b1;
+    make<kP>(t0, x.t[0], zero4());
+    make<kP>(t1, x.t[1], x.t[2]);
+    if constexpr (MODE == kForward) {
+      parts_frag(b0, x.b[0], u32x4{0, 0, 0, 0});
+      parts_frag(b1, x.b[1], x.b[2]);
+    }
+    Frag<T> uf[NCT];
+#pragma unroll
+    for (int y = 0; y < NCT; ++y) {
+      f32x4 R[2];
+#pragma unroll
+      for (int it = 0; it < 2; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) R[it][r] = value_of(x.v[it][r], y) - x.decay[it][r] * ks[it][y][r];
+      Frag<T> f;
+      make<kP>(f, R[0], R[1]);
+      const f32x4 u0 = mm<kP, kP>(t0, f, zero4()) * x.beta[0], u1 = mm<kP, kP>(t1, f, zero4()) * x.beta[1];
+      if constexpr (MODE == kForward) {
+        make<2>(f, u0, u1);
+        o[0][y] = mm<2, 2>(b0, f, o[0][y] * (x.decay[0] * a.scale));
+        o[1][y] = mm<2, 2>(b1, f, o[1][y] * (x.decay[1] * a.scale));
+      }
+      make<kP>(uf[y], u0 * x.rest[0], u1 * x.rest[1]);
+    }
+    wave_lds_order();
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      Frag<T> kt;
+      state_rows<kPitch<T, DK>>(kt, (const T*)kt_rows, t, lane);
+#pragma unroll
+      for (int y = 0; y < NCT; ++y) S[t][y] = mm<1, kP>(kt, uf[y], S[t][y] * x.total);
+    }
+    wave_lds_order();
+    if constexpr (MODE == kForward) {
+      const int64_t first = p.first + (int64_t)i * kChunk;
+      const Window ow = window<16 * NCT>(static_cast<const T*>(a.o) + first * ldv + h * DV + col - NCT * c, ldv,
+                                         min(kChunk, p.len - i * kChunk));
+#pragma unroll
+      for (int it = 0; it < 2; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float w[NCT];
+#pragma unroll
+          for (int y = 0; y < NCT; ++y) w[y] = o[it][y][r];
+          store_rawn<T, NCT>(ow, voff + (16 * it + r) * vrow, w);
+        }
+    }
+  };
+  if (chunks > 0) {
+    L x, y;
+    load(x, 0);
+    for (int i = 0; i < chunks; i += 2) {
+      load(y, min(i + 1, chunks - 1));
+      compute(x, i);
+      if (i + 1 >= chunks) break;
+      load(x, min(i + 2, chunks - 1));
+      compute(y, i + 1);
+    }
   }
 
   if constexpr (MODE == kForward) {
@@ -222,54 +293,19 @@ __global__ __launch_bounds__(64 * W, 1) void scan_kernel(const Args a) {
 // stored; kBackSummary: what a piece makes of the dS behind it.
 enum BackMode { kBack, kBackSummary };
 
-template <class T, int DK>
-struct BackShared {
-  T k[kChunk][kPitch<T, DK>];
-  T q[kChunk][kPitch<T, DK>];
-  u32x4 tt[2 * kOperand<T>];  // T^T
-  u32x4 bt[2 * kOperand<T>];  // B^T
-  Rows rows;
+template <class T, int DK, int NCT>
+struct BackLoaded {
+  Raw<T> k[2][DK / 32], q[2][DK / 32];
+  RawN<T, NCT> d[2][4];
+  f32x4 tt[3], bt[3];
+  f32x4 decay[2], rest[2], beta[2];
+  float total;
 };
 
-template <class T, int DK>
-__device__ __forceinline__ void prepare_back(BackShared<T, DK>& sh, const Args& a, int64_t first, int len, int h,
-                                             int lane) {
-  const int kh = h / (a.hv / a.hk), c = lane % 16, q = lane / 16;
-  const int64_t ld = (int64_t)a.hk * DK;
-  stage<T, DK, 64>(&sh.k[0][0], static_cast<const T*>(a.k) + first * ld + kh * DK, ld, len, lane);
-  stage<T, DK, 64>(&sh.q[0][0], static_cast<const T*>(a.q) + first * ld + kh * DK, ld, len, lane);
-  const Gates gt = gates(a, first, len, h, lane);
-  put_rows(sh.rows, gt, lane);
-  wave_lds_order();
-  const auto key = [&](Frag<T>& f, int row, int col) { row8(f, &sh.k[row + c][col]); };
-  const auto query = [&](Frag<T>& f, int row, int col) { row8(f, &sh.q[row + c][col]); };
-  // N by row (keys 16-31 against keys 0-15 turned round: 10 by row is 01 by column)
-  Tri n{zero4(), zero4(), zero4()};
-#pragma unroll
-  for (int s = 0; s < DK / 32; ++s) {
-    Frag<T> k0, k1;
-    key(k0, 0, 32 * s + 8 * q);
-    key(k1, 16, 32 * s + 8 * q);
-    n.t00 = mm<1, 1>(k0, k0, n.t00);
-    n.t10 = mm<1, 1>(k0, k1, n.t10);
-    n.t11 = mm<1, 1>(k1, k1, n.t11);
-  }
-  decay_tri<false>(n, gt, true, true, 1.0f, lane);
-  Tri t;
-  unit_inverse(n.t00, n.t10, n.t11, t.t00, t.t10, t.t11, reinterpret_cast<float*>(sh.tt), lane);
-  t.t00 = turned(t.t00, lane);
-  t.t10 = turned(t.t10, lane);
-  t.t11 = turned(t.t11, lane);
-  put_upper<T, kWhole<T>>(sh.tt, t, lane);
-  Tri w = products<1, 1, T, DK>(query, key, q);
-  decay_tri<true>(w, gt, false, false, a.scale, lane);
-  put_upper<T, kWhole<T>>(sh.bt, w, lane);
-}
-
-template <class T, int DK, int DV, int NCT, int W, int GC, BackMode MODE>
-__global__ __launch_bounds__(64 * W, 1) void back_kernel(const Args a) {
-  constexpr int kTiles = DK / 16, kSteps = DK / 32, kP = kWhole<T>;
-  __shared__ BackShared<T, DK> sh[GC];
+template <class T, int DK, int DV, int NCT, BackMode MODE>
+__global__ __launch_bounds__(64 * (4 / NCT), 1) void back_kernel(const Args a) {
+  constexpr int kTiles = DK / 16, kSteps = DK / 32, kP = kWhole<T>, kW = 4 / NCT, kB = (int)sizeof(T);
+  __shared__ T rows[kW][2][kChunk * kPitch<T, DK>];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int c = lane % 16, q = lane / 16;
   const int h = blockIdx.x % a.hv;
@@ -277,9 +313,11 @@ __global__ __launch_bounds__(64 * W, 1) void back_kernel(const Args a) {
   const Piece p = find_piece(a.cu, a.nseq, a.n, a.per, sid, lane);
   if (p.seg < 0) return;
   if (MODE == kBackSummary && p.seg == 0) return;  // nothing lies before it
-  const int col = (blockIdx.y * W + wave) * 16 * NCT + NCT * c;
-  const bool unit = MODE == kBackSummary && col >= DV;
+  const int col = blockIdx.y * 64 + wave * 16 * NCT + NCT * c;
+  const bool unit = MODE == kBackSummary && blockIdx.y * 64 >= DV;
   if (unit && p.seg == p.segs - 1) return;  // the dS behind it is known
+  T* const kt_rows = rows[wave][0];
+  T* const qt_rows = rows[wave][1];
 
   f32x4 S[kTiles][NCT];
   if (unit) {
@@ -293,75 +331,116 @@ __global__ __launch_bounds__(64 * W, 1) void back_kernel(const Args a) {
     load_state<DK, NCT>(S, from, DV, q);
   }
 
-  const int64_t ldv = (int64_t)a.hv * DV;
+  const int64_t ldq = (int64_t)a.hk * DK, ldv = (int64_t)a.hv * DV;
+  const int kh = h / (a.hv / a.hk);
   const int chunks = (p.len + kChunk - 1) / kChunk;
-  for (int c1 = chunks; c1 > 0; c1 -= GC) {  // chunks c1 - 1, c1 - 2, ..
-    if (wave < GC && c1 - 1 - wave >= 0) {
-      const int at = (c1 - 1 - wave) * kChunk;
-      prepare_back<T, DK>(sh[wave], a, p.first + at, min(kChunk, p.len - at), h, lane);
-    }
-    __syncthreads();
-    for (int i = 0; i < GC && c1 - 1 - i >= 0; ++i) {
-      const BackShared<T, DK>& m = sh[i];
-      const int at = (c1 - 1 - i) * kChunk;
-      const int64_t first = p.first + at;
-      const int len = min(kChunk, p.len - at);
-      if constexpr (MODE == kBack) {
-        const int64_t slot = p.begin / kChunk + p.b + (first - p.begin) / kChunk;
-        store_state<DK, NCT>(S, a.dstates + (slot * a.hv + h) * DK * DV + col, DV, q);
+  const int64_t slot0 = p.begin / kChunk + p.b + (p.first - p.begin) / kChunk;
+  const int koff = (int)((c * ldq + 8 * q) * kB), knext = (int)(16 * ldq * kB);
+  const int voff = (int)((4 * q * ldv + NCT * c) * kB), vrow = (int)(ldv * kB);
+
+  typedef BackLoaded<T, DK, NCT> L;
+  const auto load = [&](L& x, int i) {
+    const int64_t first = p.first + (int64_t)i * kChunk;
+    const int len = min(kChunk, p.len - i * kChunk);
+    const Window kw = window<DK>(static_cast<const T*>(a.k) + first * ldq + kh * DK, ldq, len);
+    const Window qw = window<DK>(static_cast<const T*>(a.q) + first * ldq + kh * DK, ldq, len);
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        load_raw(x.k[it][s], kw, koff + it * knext + 32 * s * kB);
+        load_raw(x.q[it][s], qw, koff + it * knext + 32 * s * kB);
       }
-      f32x4 dO[2][NCT];
-      load_rows<NCT>(dO, static_cast<const T*>(a.dout) + first * ldv + h * DV + col, ldv, unit ? 0 : len, q);
-      f32x4 kd[2][NCT];
+    const Window dw = window<16 * NCT>(static_cast<const T*>(a.dout) + first * ldv + h * DV + (unit ? 0 : col - NCT * c), ldv,
+                                       unit ? 0 : len);
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) load_rawn(x.d[it][r], dw, voff + (16 * it + r) * vrow);
+    const Matrices* m = matrices_of(a.mats, (slot0 + i) * a.hv + h, true);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      x.tt[j] = m->tt[j][lane];
+      x.bt[j] = m->bt[j][lane];
+    }
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      x.decay[it] = rows4(m->rows.decay, it, q);
+      x.rest[it] = rows4(m->rows.rest, it, q);
+      x.beta[it] = rows4(m->rows.beta, it, q);
+    }
+    x.total = m->rows.total;
+  };
+  const auto compute = [&](const L& x, int i) {
+    if constexpr (MODE == kBack)
+      store_state<DK, NCT>(S, a.dstates + ((slot0 + i) * a.hv + h) * DK * DV + col, DV, q);
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        put_raw(kt_rows + (16 * it + c) * kPitch<T, DK> + 32 * s + 8 * q, x.k[it][s]);
+        put_raw(qt_rows + (16 * it + c) * kPitch<T, DK> + 32 * s + 8 * q, x.q[it][s]);
+      }
+    f32x4 kd[2][NCT];
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int y = 0; y < NCT; ++y) kd[it][y] = zero4();
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      Frag<T> k0, k1;
+      as_frag(k0, x.k[0][s]);
+      as_frag(k1, x.k[1][s]);
+#pragma unroll
+      for (int y = 0; y < NCT; ++y) {
+        Frag<T> f;
+        make<kP>(f, S[2 * s][y], S[2 * s + 1][y]);
+        kd[0][y] = mm<1, kP>(k0, f, kd[0][y]);
+        kd[1][y] = mm<1, kP>(k1, f, kd[1][y]);
+      }
+    }
+    Frag<T> t0, t1, b0, b1;
+    make<kP>(t0, x.tt[0], x.tt[1]);
+    make<kP>(t1, zero4(), x.tt[2]);
+    make<kP>(b0, x.bt[0], x.bt[1]);
+    make<kP>(b1, zero4(), x.bt[2]);
+    Frag<T> df[NCT], rf[NCT];
+#pragma unroll
+    for (int y = 0; y < NCT; ++y) {
+      f32x4 dO[2];
 #pragma unroll
       for (int it = 0; it < 2; ++it)
 #pragma unroll
-        for (int x = 0; x < NCT; ++x) kd[it][x] = zero4();
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        Frag<T> k0, k1;
-        row8(k0, &m.k[c][32 * s + 8 * q]);
-        row8(k1, &m.k[16 + c][32 * s + 8 * q]);
-#pragma unroll
-        for (int x = 0; x < NCT; ++x) {
-          Frag<T> f;
-          make<kP>(f, S[2 * s][x], S[2 * s + 1][x]);
-          kd[0][x] = mm<1, kP>(k0, f, kd[0][x]);
-          kd[1][x] = mm<1, kP>(k1, f, kd[1][x]);
-        }
-      }
-      f32x4 dec[2], rest[2], bt[2];
-#pragma unroll
-      for (int it = 0; it < 2; ++it) {
-        dec[it] = rows4(m.rows.decay, it, q);
-        rest[it] = rows4(m.rows.rest, it, q);
-        bt[it] = rows4(m.rows.beta, it, q);
-      }
-      const float total = m.rows.total;
-#pragma unroll
-      for (int x = 0; x < NCT; ++x) {
-        Frag<T> f, b0, b1, t0, t1;
-        make<1>(f, dO[0][x], dO[1][x]);
-        get<kP>(b0, m.bt, lane);
-        get<kP>(b1, m.bt + kOperand<T>, lane);
-        const f32x4 du0 = mm<kP, 1>(b0, f, kd[0][x] * rest[0]), du1 = mm<kP, 1>(b1, f, kd[1][x] * rest[1]);
-        make<kP>(f, du0 * bt[0], du1 * bt[1]);
-        get<kP>(t0, m.tt, lane);
-        get<kP>(t1, m.tt + kOperand<T>, lane);
-        const f32x4 dR0 = mm<kP, kP>(t0, f, zero4()), dR1 = mm<kP, kP>(t1, f, zero4());
-        Frag<T> g;
-        make<kP>(f, dO[0][x] * (dec[0] * a.scale), dO[1][x] * (dec[1] * a.scale));
-        make<kP>(g, -dR0 * dec[0], -dR1 * dec[1]);
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          Frag<T> kt, qt;
-          state_rows<kPitch<T, DK>>(kt, &m.k[0][0], t, lane);
-          state_rows<kPitch<T, DK>>(qt, &m.q[0][0], t, lane);
-          S[t][x] = mm<1, kP>(kt, g, mm<1, kP>(qt, f, S[t][x] * total));
-        }
-      }
+        for (int r = 0; r < 4; ++r) dO[it][r] = value_of(x.d[it][r], y);
+      Frag<T> f;
+      make<1>(f, dO[0], dO[1]);
+      const f32x4 du0 = mm<kP, 1>(b0, f, kd[0][y] * x.rest[0]), du1 = mm<kP, 1>(b1, f, kd[1][y] * x.rest[1]);
+      make<kP>(f, du0 * x.beta[0], du1 * x.beta[1]);
+      const f32x4 dR0 = mm<kP, kP>(t0, f, zero4()), dR1 = mm<kP, kP>(t1, f, zero4());
+      make<kP>(df[y], dO[0] * (x.decay[0] * a.scale), dO[1] * (x.decay[1] * a.scale));
+      make<kP>(rf[y], -dR0 * x.decay[0], -dR1 * x.decay[1]);
     }
-    __syncthreads();
+    wave_lds_order();
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      Frag<T> kt, qt;
+      state_rows<kPitch<T, DK>>(kt, (const T*)kt_rows, t, lane);
+      state_rows<kPitch<T, DK>>(qt, (const T*)qt_rows, t, lane);
+#pragma unroll
+      for (int y = 0; y < NCT; ++y) S[t][y] = mm<1, kP>(kt, rf[y], mm<1, kP>(qt, df[y], S[t][y] * x.total));
+    }
+    wave_lds_order();
+  };
+  if (chunks > 0) {
+    L x, y;
+    load(x, chunks - 1);
+    for (int i = chunks - 1; i >= 0; i -= 2) {
+      load(y, max(i - 1, 0));
+      compute(x, i);
+      if (i < 1) break;
+      load(x, max(i - 2, 0));
+      compute(y, i - 1);
+    }
   }
 
   if constexpr (MODE == kBack) {
@@ -419,39 +498,54 @@ __global__ __launch_bounds__(64) void join_kernel(const Args a) {
   }
 }
 
-template <class T, int DK, int DV, Mode MODE>
+template <class T, int DK, bool KEEP>
+hipError_t run_matrices(const Args& a, hipStream_t stream) {
+  const int64_t waves = chunk_slots(a.n, a.nseq) * a.hv;
+  matrices_kernel<T, DK, KEEP><<<(unsigned)((waves + 3) / 4), 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <class T, int DK, int DV, int NCT, Mode MODE>
 hipError_t run_forward(const Args& a, const Plan& p, hipStream_t stream) {
+  constexpr int kThreads = 64 * (4 / NCT);
   const unsigned x = (unsigned)(p.pieces * a.hv);
+  if (hipError_t e = run_matrices<T, DK, MODE == kStates>(a, stream)) return e;
   if (p.split) {
-    scan_kernel<T, DK, DV, 1, 4, 2, kSummary><<<dim3(x, (DV + DK) / 64), 256, 0, stream>>>(a);
+    scan_kernel<T, DK, DV, NCT, kSummary><<<dim3(x, (DV + DK) / 64), kThreads, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
     join_kernel<DK, DV, false><<<dim3((unsigned)(a.nseq * a.hv), DV / 16), 64, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  scan_kernel<T, DK, DV, 1, 4, 2, MODE><<<dim3(x, DV / 64), 256, 0, stream>>>(a);
+  scan_kernel<T, DK, DV, NCT, MODE><<<dim3(x, DV / 64), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-template <class T, int DK, int DV>
+template <class T, int DK, int DV, int NCT>
 hipError_t run_back(const Args& a, const Plan& p, hipStream_t stream) {
+  constexpr int kThreads = 64 * (4 / NCT);
   const unsigned x = (unsigned)(p.pieces * a.hv);
   if (p.split) {
-    back_kernel<T, DK, DV, 1, 4, 2, kBackSummary><<<dim3(x, (DV + DK) / 64), 256, 0, stream>>>(a);
+    back_kernel<T, DK, DV, NCT, kBackSummary><<<dim3(x, (DV + DK) / 64), kThreads, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
     join_kernel<DK, DV, true><<<dim3((unsigned)(a.nseq * a.hv), DV / 16), 64, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  back_kernel<T, DK, DV, 1, 4, 2, kBack><<<dim3(x, DV / 64), 256, 0, stream>>>(a);
+  back_kernel<T, DK, DV, NCT, kBack><<<dim3(x, DV / 64), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 enum What { kOutputs, kKeepStates, kReverse };
 
+template <class T, int DK, int DV, int NCT>
+hipError_t run_wide(const Args& a, const Plan& p, What what, hipStream_t s) {
+  if (what == kOutputs) return run_forward<T, DK, DV, NCT, kForward>(a, p, s);
+  if (what == kKeepStates) return run_forward<T, DK, DV, NCT, kStates>(a, p, s);
+  return run_back<T, DK, DV, NCT>(a, p, s);
+}
 template <class T, int DK, int DV>
 hipError_t run(const Args& a, const Plan& p, What what, hipStream_t s) {
-  if (what == kOutputs) return run_forward<T, DK, DV, kForward>(a, p, s);
-  if (what == kKeepStates) return run_forward<T, DK, DV, kStates>(a, p, s);
-  return run_back<T, DK, DV>(a, p, s);
+  constexpr int kMost = DK == 64 ? 4 : 2;
+  return p.wide ? run_wide<T, DK, DV, kMost>(a, p, what, s) : run_wide<T, DK, DV, 1>(a, p, what, s);
 }
 template <class T>
 hipError_t run_of(const Args& a, const Plan& p, What what, hipStream_t s) {
@@ -471,13 +565,15 @@ hipError_t launch_back(const Args& a, const Plan& p, bool bf16, hipStream_t stre
   return bf16 ? run_of<uint16_t>(a, p, kReverse, stream) : run_of<float>(a, p, kReverse, stream);
 }
 
-// Pieces: as long as about 512 workgroups of 64 columns allow, at least 4 chunks;
-// one for the whole sequence where that is as much work at once.
+size_t matrix_bytes(bool keep) { return matrices_bytes(keep); }
+
 Plan plan(int64_t n, int nseq, int64_t longest, int hv, int dk, int dv) {
   const int64_t chunks = (n + kChunk - 1) / kChunk, rows = (int64_t)hv * (dv / 64);
-  int64_t each = (chunks * rows + 511) / 512;
-  if (each < 4) each = 4;
   Plan p;
+  p.wide = chunks * rows >= 16384;
+  const int64_t waves = p.wide ? 1024 : 512;
+  int64_t each = (chunks * rows + waves - 1) / waves;
+  if (each < 4) each = 4;
   p.split = longest > each * kChunk;
   p.per = p.split ? each * kChunk : (n / kChunk + 1) * kChunk;
   p.pieces = n / p.per + nseq;
