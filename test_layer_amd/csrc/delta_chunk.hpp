@@ -11,8 +11,6 @@
 namespace vggt3 {
 namespace delta {
 
-constexpr double kLog2eD = 1.4426950408889634074;
-
 // Parts of an operand that holds fp32 values whole, and its 16-byte pieces.
 template <class T>
 constexpr int kWhole = sizeof(T) == 2 ? 3 : 1;
@@ -35,48 +33,61 @@ __device__ __forceinline__ void stage(T* dst, const T* src, int64_t ld, int len,
   }
 }
 
-// Lane t % 32's token: the chunk's decay up to it, as a power of 2 in 64 bits, so that
-// a difference of two is right whatever lies before them; and beta. (Below 2^-2000 a
-// decay is 0 in either form.)
-struct Gates {
-  double G, end;  // end: of the whole chunk
-  float beta;
-};
-__device__ __forceinline__ Gates gates(const Args& a, int64_t first, int len, int h, int lane) {
-  const int t = lane % 32;
-  Gates x{0.0, 0.0, 0.0f};
-  if (t < len) {
-    if (a.g) {
-      const float g = a.g[(first + t) * a.hv + h];
-      x.G = (g < -2000.0f ? -2000.0f : g) * kLog2eD;
-    }
-    x.beta = a.beta[(first + t) * a.hv + h];
-  }
-  if (a.g) {
-#pragma unroll
-    for (int off = 1; off < kChunk; off *= 2) {
-      const double up = __shfl_up(x.G, off, 32);
-      if (t >= off) x.G += up;
-    }
-    x.end = __shfl(x.G, 31, 32);
-  }
-  return x;
-}
-__device__ __forceinline__ float exp2d(double x) { return __builtin_amdgcn_exp2f((float)x); }
-
-// The gates that a chunk's columns use, by token.
+// The gates that a chunk's columns use, by token. Its decay up to a token is
+// 2^(high + low): high a multiple of 2^-6, so that sums and differences of it are
+// exact (at most 32 * 2885 in size), low what that leaves, at most 2^-7 a token. So
+// the decay between two tokens is right whatever lies before them. (Below e^-2000 a
+// token's decay is 0 in either form.)
 struct Rows {
   float decay[kChunk];  // from the chunk's start
   float rest[kChunk];   // to its end
   float beta[kChunk];
-  float total;
+  float high[kChunk];
+  float low[kChunk];
+  float total, pad[3];
 };
-__device__ __forceinline__ void put_rows(Rows& m, const Gates& x, int lane) {
+
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float shifted(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, ROWS, 0xf, false));
+}
+// Sums over the lanes before and with each, in every 32.
+__device__ __forceinline__ float running_sum(float x) {
+  x += shifted<0x111>(x);  // one lane down, within 16; then 2, 4, 8
+  x += shifted<0x112>(x);
+  x += shifted<0x114>(x);
+  x += shifted<0x118>(x);
+  x += shifted<0x142, 0xa>(x);  // the first 16's sum to the second's lanes
+  return x;
+}
+
+__device__ __forceinline__ void put_rows(Rows& m, const Args& a, int64_t first, int len, int h, int lane) {
+  const int t = lane % 32;
+  float high = 0.0f, low = 0.0f, beta = 0.0f;
+  if (t < len) {
+    if (a.g) {
+      float g = a.g[(first + t) * a.hv + h];
+      g = g < -2000.0f ? -2000.0f : g;
+      constexpr float kLog2e = 1.44269502162933349609f, kMore = 1.92596299112661746887e-08f;  // their sum: log2 e
+      const float x = g * kLog2e;
+      high = __builtin_rintf(x * 64.0f) * 0.015625f;
+      low = (x - high) + __builtin_fmaf(g, kMore, __builtin_fmaf(g, kLog2e, -x));
+    }
+    beta = a.beta[(first + t) * a.hv + h];
+  }
+  if (a.g) {
+    high = running_sum(high);
+    low = running_sum(low);
+  }
+  const float end = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, high), 31)),
+              more = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, low), 31));
   if (lane >= kChunk) return;
-  m.decay[lane] = exp2d(x.G);
-  m.rest[lane] = exp2d(x.end - x.G);
-  m.beta[lane] = x.beta;
-  if (lane == 31) m.total = exp2d(x.G);
+  m.decay[lane] = __builtin_amdgcn_exp2f(high + low);
+  m.rest[lane] = __builtin_amdgcn_exp2f((end - high) + (more - low));
+  m.beta[lane] = beta;
+  m.high[lane] = high;
+  m.low[lane] = low;
+  if (lane == 0) m.total = __builtin_amdgcn_exp2f(end + more);
 }
 __device__ __forceinline__ f32x4 rows4(const float* v, int it, int q) {
   return *reinterpret_cast<const f32x4*>(v + 16 * it + 4 * q);
@@ -87,81 +98,58 @@ struct Tri {
   f32x4 t00, t10, t11;
 };
 
-// D_ij x_ij for j < i (strict) or j <= i, 0 elsewhere, times beta_j if `beta`, times f.
-// FORWARD: lane (c, q) holds rows i = 4q + r of columns j = c; otherwise columns
-// 4q + r of rows i = c.
+__device__ __forceinline__ Tri operator*(const Tri& x, const Tri& y) {
+  return Tri{x.t00 * y.t00, x.t10 * y.t10, x.t11 * y.t11};
+}
+
+// The decays D_ij from token j to token i. FORWARD: lane (c, q) has rows i = 4q + r of
+// columns j = c; otherwise columns j = 4q + r of rows i = c. (Above the diagonal:
+// anything.)
 template <bool FORWARD>
-__device__ __forceinline__ void decay_tri(Tri& m, const Gates& x, bool strict, bool beta, float f, int lane) {
+__device__ __forceinline__ Tri decays(const Rows& m, int lane) {
   const int c = lane % 16, q = lane / 16;
-  const double Gc0 = __shfl(x.G, c, 32), Gc1 = __shfl(x.G, 16 + c, 32);
-  const float bc0 = __shfl(x.beta, c, 32), bc1 = __shfl(x.beta, 16 + c, 32);
+  const float hc[2] = {m.high[c], m.high[16 + c]}, lc[2] = {m.low[c], m.low[16 + c]};
+  const f32x4 he[2] = {rows4(m.high, 0, q), rows4(m.high, 1, q)}, le[2] = {rows4(m.low, 0, q), rows4(m.low, 1, q)};
+  Tri d;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    const int e = 4 * q + r;
-    const double Ge0 = __shfl(x.G, e, 32), Ge1 = __shfl(x.G, 16 + e, 32);
-    float d00, d10, d11, b0 = 1.0f, b1 = 1.0f;
-    bool in;
-    if (FORWARD) {
-      d00 = exp2d(Ge0 - Gc0);
-      d10 = exp2d(Ge1 - Gc0);
-      d11 = exp2d(Ge1 - Gc1);
-      in = strict ? c < e : c <= e;
-      if (beta) {
-        b0 = bc0;
-        b1 = bc1;
-      }
-    } else {
-      d00 = exp2d(Gc0 - Ge0);
-      d10 = exp2d(Gc1 - Ge0);
-      d11 = exp2d(Gc1 - Ge1);
-      in = strict ? e < c : e <= c;
-      if (beta) {
-        b0 = __shfl(x.beta, e, 32);
-        b1 = __shfl(x.beta, 16 + e, 32);
-      }
-    }
-    m.t00[r] = in ? m.t00[r] * d00 * b0 * f : 0.0f;
-    m.t10[r] = m.t10[r] * d10 * b0 * f;
-    m.t11[r] = in ? m.t11[r] * d11 * b1 * f : 0.0f;
+    const auto decay = [&](int i, int j) {
+      const float hi = FORWARD ? he[i][r] : hc[i], li = FORWARD ? le[i][r] : lc[i];
+      const float hj = FORWARD ? hc[j] : he[j][r], lj = FORWARD ? lc[j] : le[j][r];
+      return __builtin_amdgcn_exp2f((hi - hj) + (li - lj));
+    };
+    d.t00[r] = decay(0, 0);
+    d.t10[r] = decay(1, 0);
+    d.t11[r] = decay(1, 1);
   }
+  return d;
 }
-
-// Tiles of X Y^T, X and Y [kChunk][pitch] in LDS, where lane (c, q) gets rows 4q + r
-// of X and column c of Y: 00, 10 (rows of X 16-31, columns 0-15 of Y) and 11.
-template <int NX, int NY, class T, int D, class LX, class LY>
-__device__ __forceinline__ Tri products(LX x, LY y, int q) {
-  Tri m{zero4(), zero4(), zero4()};
+// What lies on and above (strict: or on) the diagonal to 0.
+template <bool FORWARD, bool STRICT>
+__device__ __forceinline__ Tri lower(const Tri& m, int lane) {
+  const int c = lane % 16, q = lane / 16;
+  Tri o = m;
 #pragma unroll
-  for (int s = 0; s < D / 32; ++s) {
-    Frag<T> x0, x1, y0, y1;
-    x(x0, 0, 32 * s + 8 * q);
-    x(x1, 16, 32 * s + 8 * q);
-    y(y0, 0, 32 * s + 8 * q);
-    y(y1, 16, 32 * s + 8 * q);
-    m.t00 = mm<NX, NY>(x0, y0, m.t00);
-    m.t10 = mm<NX, NY>(x1, y0, m.t10);
-    m.t11 = mm<NX, NY>(x1, y1, m.t11);
+  for (int r = 0; r < 4; ++r) {
+    const int i = FORWARD ? 4 * q + r : c, j = FORWARD ? c : 4 * q + r;
+    const bool in = STRICT ? j < i : j <= i;
+    o.t00[r] = in ? m.t00[r] : 0.0f;
+    o.t11[r] = in ? m.t11[r] : 0.0f;
   }
-  return m;
+  return o;
 }
 
-// A triangle as a left operand: L from tiles that hold its rows i by lane (columns
-// 4q + r), and L^T from tiles that hold its columns j by lane.
-template <class T, int P>
-__device__ __forceinline__ void put_lower(u32x4* at, const Tri& m, int lane) {
-  Frag<T> f;
-  make<P>(f, m.t00, zero4());
-  put<P>(at, f, lane);
-  make<P>(f, m.t10, m.t11);
-  put<P>(at + kOperand<T>, f, lane);
+// A triangle L as a left operand of its rows (tiles with columns 4q + r of rows c), and
+// L^T as one (tiles with rows 4q + r of columns c).
+template <int P, class T>
+__device__ __forceinline__ void lower_rows(Frag<T> (&f)[2], const Tri& m) {
+  make<P>(f[0], m.t00, zero4());
+  make<P>(f[1], m.t10, m.t11);
 }
-template <class T, int P>
-__device__ __forceinline__ void put_upper(u32x4* at, const Tri& m, int lane) {
-  Frag<T> f;
-  make<P>(f, m.t00, m.t10);
-  put<P>(at, f, lane);
-  make<P>(f, zero4(), m.t11);
-  put<P>(at + kOperand<T>, f, lane);
+template <int P, class T>
+__device__ __forceinline__ void upper_rows(Frag<T> (&f)[2], const Tri& m) {
+  make<P>(f[0], m.t00, m.t10);
+  make<P>(f[1], zero4(), m.t11);
 }
 
 // Tiles by row -> the same tiles by column (and back): a product with the unit
@@ -173,22 +161,24 @@ __device__ __forceinline__ f32x4 turned(const f32x4& x, int lane) {
   return mm16(x, one, zero4());
 }
 
-// A chunk's shared matrices in memory, as operands: tiles 00, 10, 11 of T and B by row,
-// and for the gradient of their transposes (tiles by column). B of the forward alone is
-// in two bf16 parts (bf16).
+// A chunk's shared matrices in memory, tile by tile as lanes hold them: T = (I + N)^-1
+// and B by row, and for the gradient X = (I + beta N')^-1 and B with tiles by column
+// (the operands X^T and B^T). B of the forward alone is in two bf16 parts (bf16).
 struct Matrices {
   f32x4 t[3][64];
   f32x4 b[3][64];
   Rows rows;
-  float pad[kChunk - 1];
-  f32x4 tt[3][64];  // the gradient's only
+  f32x4 x[3][64];  // the gradient's only
   f32x4 bt[3][64];
 };
 __host__ __device__ constexpr size_t matrices_bytes(bool keep) {
-  return keep ? sizeof(Matrices) : offsetof(Matrices, tt);
+  return keep ? sizeof(Matrices) : offsetof(Matrices, x);
 }
 __device__ __forceinline__ Matrices* matrices_of(void* base, int64_t at, bool keep) {
   return reinterpret_cast<Matrices*>(static_cast<char*>(base) + at * matrices_bytes(keep));
+}
+__device__ __forceinline__ Tri get_tri(const f32x4 (*from)[64], int lane) {
+  return Tri{from[0][lane], from[1][lane], from[2][lane]};
 }
 __device__ __forceinline__ void put_tri(f32x4 (*to)[64], const Tri& m, int lane) {
   to[0][lane] = m.t00;

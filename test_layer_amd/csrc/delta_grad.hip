@@ -1,8 +1,8 @@
 // The gradient of the gated delta rule, chunk by chunk, from the state S before each
-// chunk and the gradient dS of the state after it (delta_scan.hip). With y, u, T, B
-// and the decays of the forward, du, dR of the reverse scan,
+// chunk and the gradient dS of the state after it (delta_scan.hip). With the forward's
+// y, u, o and the reverse scan's du, x = X^T du, dR = beta . x,
 //
-//   dV = dR,      x = du - N'^T dR  (N' = N without its beta),   dbeta_i = x_i . y_i
+//   dV = dR,    dbeta_i = x_i . y_i
 //   F = scale D . (dO u^T) (lower),    E = D . (dR u^T) (strictly lower)
 //   dQ = scale G . (dO S^T) + F K
 //   dK = F^T Q + G_end / G . (u dS^T) - G . (dR S^T) - E K - E^T K
@@ -13,9 +13,12 @@
 // back from its end, what the later chunks say is in <dS, state>. (One such sum over
 // the whole sequence would lose the small terms; over 32 tokens it does not.)
 //
-// Four waves to a chunk and head. First each forms one of the 32 x 32 operands, then
-// each has a quarter of the value channels (u, du, dR, o and the row sums), then two
-// forms each of F and E, then a quarter of the key channels (dQ, dK).
+// Four waves to a chunk and head: each has a quarter of the value channels (u, x, o and
+// the row sums, in fp32 values whole), then two forms each of F and E, then a quarter
+// of the key channels (dQ, dK, from operands in two bf16 parts). u and dR change from
+// columns by lane to rows by lane through LDS.
+#include <type_traits>
+
 #include "delta_chunk.hpp"
 
 namespace vggt3 {
@@ -26,13 +29,13 @@ constexpr int kWaves = 4;
 
 template <class T, int DK, int DV>
 struct GradShared {
-  static constexpr int kParts = sizeof(T) == 2 ? 2 : 1;  // of y and dR as operands of bf16 results
+  static constexpr int kParts = sizeof(T) == 2 ? 2 : 1;  // of u and dR
+  static constexpr int kTwo = 128;                       // an operand of two parts, or of fp32 values
   T k[kChunk][kPitch<T, DK>];
   T q[kChunk][kPitch<T, DK>];
-  T y[kParts][kChunk][kPitch<T, DV>];
+  T u[kParts][kChunk][kPitch<T, DV>];
   T dr[kParts][kChunk][kPitch<T, DV>];
-  u32x4 op[5][2 * kOperand<T>];  // T, T^T, B, B^T, N'^T; then F, F^T, -E, -E^T
-  Rows rows;
+  u32x4 op[4][2][kTwo];  // F, F^T, -E, -E^T, 16 rows each
   float along[kWaves][kChunk], step[kWaves][kChunk], all[kWaves];
 };
 
@@ -79,9 +82,9 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 template <class T, int DK, int DV>
-__global__ __launch_bounds__(64 * kWaves, 1) void grad_kernel(const Args a) {
+__global__ __launch_bounds__(64 * kWaves, DK + DV == 128 ? 3 : 1) void grad_kernel(const Args a) {
   using Sh = GradShared<T, DK, DV>;
-  constexpr int kP = kWhole<T>, kV = DV / 64, kK = DK / 64, kPV = kPitch<T, DV>, kPK = kPitch<T, DK>;
+  constexpr int kP = kWhole<T>, kV = DV / 64, kK = DK / 64, kPV = kPitch<T, DV>, kPK = kPitch<T, DK>, kB = (int)sizeof(T);
   __shared__ Sh m;
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int c = lane % 16, q = lane / 16;
@@ -91,75 +94,60 @@ __global__ __launch_bounds__(64 * kWaves, 1) void grad_kernel(const Args a) {
   if (p.seg < 0 || p.len == 0) return;
   const int kh = h / (a.hv / a.hk), len = p.len;
   const int64_t ldk = (int64_t)a.hk * DK, ldv = (int64_t)a.hv * DV;
-  const T* dop = static_cast<const T*>(a.dout) + p.first * ldv + h * DV;
+  const Window kw = window<DK>(static_cast<const T*>(a.k) + p.first * ldk + kh * DK, ldk, len);
+  const Window qw = window<DK>(static_cast<const T*>(a.q) + p.first * ldk + kh * DK, ldk, len);
+  const Window vw = window<DV>(static_cast<const T*>(a.v) + p.first * ldv + h * DV, ldv, len);
+  const Window ow = window<DV>(static_cast<const T*>(a.dout) + p.first * ldv + h * DV, ldv, len);
   const float* S0 = a.states + (slot * a.hv + h) * DK * DV;
   const float* S1 = a.dstates + (slot * a.hv + h) * DK * DV;
+  const Matrices& mat = *matrices_of(a.mats, slot * a.hv + h, true);
+  const int orow = (int)((c * ldv + 8 * q) * kB), onext = (int)(16 * ldv * kB);  // dO by rows
 
-  stage<T, DK, 256>(&m.k[0][0], static_cast<const T*>(a.k) + p.first * ldk + kh * DK, ldk, len, threadIdx.x);
-  stage<T, DK, 256>(&m.q[0][0], static_cast<const T*>(a.q) + p.first * ldk + kh * DK, ldk, len, threadIdx.x);
-  const Gates gt = gates(a, p.first, len, h, lane);
-  if (wave == 0) put_rows(m.rows, gt, lane);
-  __syncthreads();
-  {
-    const auto key = [&](Frag<T>& f, int row, int col) { row8(f, &m.k[row + c][col]); };
-    const auto query = [&](Frag<T>& f, int row, int col) { row8(f, &m.q[row + c][col]); };
-    if (wave == 0) {  // T and T^T
-      Tri n{zero4(), zero4(), zero4()};
+  {  // K and Q to LDS
+    constexpr int kPieces = DK / 8, kEach = kChunk * kPieces / (64 * kWaves);
+    Raw<T> kr[kEach], qr[kEach];
 #pragma unroll
-      for (int s = 0; s < DK / 32; ++s) {
-        Frag<T> k0, k1;
-        key(k0, 0, 32 * s + 8 * q);
-        key(k1, 16, 32 * s + 8 * q);
-        n.t00 = mm<1, 1>(k0, k0, n.t00);
-        n.t10 = mm<1, 1>(k0, k1, n.t10);
-        n.t11 = mm<1, 1>(k1, k1, n.t11);
-      }
-      decay_tri<false>(n, gt, true, true, 1.0f, lane);
-      Tri t;
-      unit_inverse(n.t00, n.t10, n.t11, t.t00, t.t10, t.t11, reinterpret_cast<float*>(m.op[0]), lane);
-      put_lower<T, kP>(m.op[0], t, lane);
-      t.t00 = turned(t.t00, lane);
-      t.t10 = turned(t.t10, lane);
-      t.t11 = turned(t.t11, lane);
-      put_upper<T, kP>(m.op[1], t, lane);
-    } else if (wave == 1) {  // B: queries by lane
-      Tri w{zero4(), zero4(), zero4()};
+    for (int i = 0; i < kEach; ++i) {
+      const int at = i * 64 * kWaves + threadIdx.x, off = (int)((at / kPieces * ldk + at % kPieces * 8) * kB);
+      load_raw(kr[i], kw, off);
+      load_raw(qr[i], qw, off);
+    }
 #pragma unroll
-      for (int s = 0; s < DK / 32; ++s) {
-        Frag<T> k0, k1, q0, q1;
-        key(k0, 0, 32 * s + 8 * q);
-        key(k1, 16, 32 * s + 8 * q);
-        query(q0, 0, 32 * s + 8 * q);
-        query(q1, 16, 32 * s + 8 * q);
-        w.t00 = mm<1, 1>(k0, q0, w.t00);
-        w.t10 = mm<1, 1>(k0, q1, w.t10);
-        w.t11 = mm<1, 1>(k1, q1, w.t11);
-      }
-      decay_tri<false>(w, gt, false, false, a.scale, lane);
-      put_lower<T, kP>(m.op[2], w, lane);
-    } else if (wave == 2) {  // B^T: keys by lane
-      Tri w = products<1, 1, T, DK>(query, key, q);
-      decay_tri<true>(w, gt, false, false, a.scale, lane);
-      put_upper<T, kP>(m.op[3], w, lane);
-    } else {  // N'^T
-      Tri w = products<1, 1, T, DK>(key, key, q);
-      decay_tri<true>(w, gt, true, false, 1.0f, lane);
-      put_upper<T, kP>(m.op[4], w, lane);
+    for (int i = 0; i < kEach; ++i) {
+      const int at = i * 64 * kWaves + threadIdx.x;
+      put_raw(&m.k[at / kPieces][at % kPieces * 8], kr[i]);
+      put_raw(&m.q[at / kPieces][at % kPieces * 8], qr[i]);
     }
   }
-  __syncthreads();
 
   // this wave's value channels
   {
     const int col = wave * 16 * kV + kV * c;
-    f32x4 V[2][kV], dO[2][kV], ks[2][kV], kd[2][kV], qs[2][kV];
-    load_rows<kV>(V, static_cast<const T*>(a.v) + p.first * ldv + h * DV + col, ldv, len, q);
-    load_rows<kV>(dO, dop + col, ldv, len, q);
+    const int voff = (int)((4 * q * ldv + col) * kB), vrow = (int)(ldv * kB);
+    RawN<T, kV> vr[2][4], dr[2][4];
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        load_rawn(vr[it][r], vw, voff + (16 * it + r) * vrow);
+        load_rawn(dr[it][r], ow, voff + (16 * it + r) * vrow);
+      }
+    const Tri t = get_tri(mat.t, lane), b = get_tri(mat.b, lane), bt = get_tri(mat.bt, lane), xt = get_tri(mat.x, lane);
+    f32x4 dec[2], rest[2], beta[2], along[2], step[2];
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      dec[it] = rows4(mat.rows.decay, it, q);
+      rest[it] = rows4(mat.rows.rest, it, q);
+      beta[it] = rows4(mat.rows.beta, it, q);
+      along[it] = step[it] = zero4();
+    }
+    f32x4 ks[2][kV], kd[2][kV], qs[2][kV];
 #pragma unroll
     for (int it = 0; it < 2; ++it)
 #pragma unroll
       for (int x = 0; x < kV; ++x) ks[it][x] = kd[it][x] = qs[it][x] = zero4();
     float both = 0.0f;  // <dS, S>
+    __syncthreads();
 #pragma unroll
     for (int s = 0; s < DK / 32; ++s) {
       f32x4 st[2][kV], ds[2][kV];
@@ -168,7 +156,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void grad_kernel(const Args a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           float w0[kV], w1[kV];
-          const int64_t at = (int64_t)channel(2 * s + i, 4 * q + r) * DV + col;
+          const int at = channel(2 * s + i, 4 * q + r) * DV + col;
           load_n<kV>(w0, S0 + at);
           load_n<kV>(w1, S1 + at);
 #pragma unroll
@@ -196,52 +184,58 @@ __global__ __launch_bounds__(64 * kWaves, 1) void grad_kernel(const Args a) {
         kd[1][x] = mm<1, kP>(k1, f, kd[1][x]);
       }
     }
-    f32x4 dec[2], rest[2], bt[2], along[2], step[2];
-#pragma unroll
-    for (int it = 0; it < 2; ++it) {
-      dec[it] = rows4(m.rows.decay, it, q);
-      rest[it] = rows4(m.rows.rest, it, q);
-      bt[it] = rows4(m.rows.beta, it, q);
-      along[it] = step[it] = zero4();
-    }
-    both *= m.rows.total;
+    both *= mat.rows.total;
+    Frag<T> o[2];
     f32x4 dR[2][kV];
 #pragma unroll
     for (int x = 0; x < kV; ++x) {
-      Frag<T> f, o0, o1;
-      make<kP>(f, V[0][x] - dec[0] * ks[0][x], V[1][x] - dec[1] * ks[1][x]);
-      get<kP>(o0, m.op[0], lane);
-      get<kP>(o1, m.op[0] + kOperand<T>, lane);
-      const f32x4 y0 = mm<kP, kP>(o0, f, zero4()), y1 = mm<kP, kP>(o1, f, zero4());
-      const f32x4 u0 = y0 * bt[0], u1 = y1 * bt[1];
+      f32x4 V[2], dO[2];
+#pragma unroll
+      for (int it = 0; it < 2; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          V[it][r] = value_of(vr[it][r], x);
+          dO[it][r] = value_of(dr[it][r], x);
+        }
+      Frag<T> f;
+      make<kP>(f, V[0] - dec[0] * ks[0][x], V[1] - dec[1] * ks[1][x]);
+      lower_rows<kP>(o, t);
+      const f32x4 y0 = mm<kP, kP>(o[0], f, zero4()), y1 = mm<kP, kP>(o[1], f, zero4());
+      const f32x4 u0 = y0 * beta[0], u1 = y1 * beta[1];
+      put_tile<kPV>(&m.u[0][0][0], u0, u1, kChunk * kPV, col + x, q);
       make<kP>(f, u0, u1);
-      get<kP>(o0, m.op[2], lane);
-      get<kP>(o1, m.op[2] + kOperand<T>, lane);
-      along[0] += dO[0][x] * mm<kP, kP>(o0, f, qs[0][x] * (dec[0] * a.scale));
-      along[1] += dO[1][x] * mm<kP, kP>(o1, f, qs[1][x] * (dec[1] * a.scale));
-      make<1>(f, dO[0][x], dO[1][x]);
-      get<kP>(o0, m.op[3], lane);
-      get<kP>(o1, m.op[3] + kOperand<T>, lane);
+      lower_rows<kP>(o, b);
+      along[0] += dO[0] * mm<kP, kP>(o[0], f, qs[0][x] * (dec[0] * a.scale));
+      along[1] += dO[1] * mm<kP, kP>(o[1], f, qs[1][x] * (dec[1] * a.scale));
+      make<1>(f, dO[0], dO[1]);
+      upper_rows<kP>(o, bt);
       const f32x4 e0 = kd[0][x] * rest[0], e1 = kd[1][x] * rest[1];
-      const f32x4 du0 = mm<kP, 1>(o0, f, e0), du1 = mm<kP, 1>(o1, f, e1);
-      make<kP>(f, du0 * bt[0], du1 * bt[1]);
-      get<kP>(o0, m.op[1], lane);
-      get<kP>(o1, m.op[1] + kOperand<T>, lane);
-      dR[0][x] = mm<kP, kP>(o0, f, zero4());
-      dR[1][x] = mm<kP, kP>(o1, f, zero4());
-      along[0] -= V[0][x] * dR[0][x];
-      along[1] -= V[1][x] * dR[1][x];
-      make<kP>(f, -dR[0][x], -dR[1][x]);
-      get<kP>(o0, m.op[4], lane);
-      get<kP>(o1, m.op[4] + kOperand<T>, lane);
-      step[0] += y0 * mm<kP, kP>(o0, f, du0);
-      step[1] += y1 * mm<kP, kP>(o1, f, du1);
+      const f32x4 du0 = mm<kP, 1>(o[0], f, e0), du1 = mm<kP, 1>(o[1], f, e1);
+      make<kP>(f, du0, du1);
+      upper_rows<kP>(o, xt);
+      const f32x4 x0 = mm<kP, kP>(o[0], f, zero4()), x1 = mm<kP, kP>(o[1], f, zero4());
+      dR[0][x] = x0 * beta[0];
+      dR[1][x] = x1 * beta[1];
+      put_tile<kPV>(&m.dr[0][0][0], dR[0][x], dR[1][x], kChunk * kPV, col + x, q);
+      along[0] -= V[0] * dR[0][x];
+      along[1] -= V[1] * dR[1][x];
+      step[0] += y0 * x0;
+      step[1] += y1 * x1;
 #pragma unroll
       for (int r = 0; r < 4; ++r) both += e0[r] * u0[r] + e1[r] * u1[r];
-      put_tile<kPV>(&m.y[0][0][0], y0, y1, kChunk * kPV, col + x, q);
-      put_tile<kPV>(&m.dr[0][0][0], dR[0][x], dR[1][x], kChunk * kPV, col + x, q);
     }
-    if (a.dv_out) store_rows<kV>(static_cast<T*>(a.dv_out) + p.first * ldv + h * DV + col, dR, ldv, len, q);
+    if (a.dv_out) {
+      const Window dw = window<DV>(static_cast<const T*>(a.dv_out) + p.first * ldv + h * DV, ldv, len);
+#pragma unroll
+      for (int it = 0; it < 2; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float w[kV];
+#pragma unroll
+          for (int x = 0; x < kV; ++x) w[x] = dR[it][x][r];
+          store_rawn<T, kV>(dw, voff + (16 * it + r) * vrow, w);
+        }
+    }
 #pragma unroll
     for (int it = 0; it < 2; ++it)
 #pragma unroll
@@ -257,54 +251,65 @@ __global__ __launch_bounds__(64 * kWaves, 1) void grad_kernel(const Args a) {
   }
   __syncthreads();
 
-  // F and E by row and by column: waves 0 and 1 dO y^T, waves 2 and 3 dR y^T
+  // F and E, rows by lane and columns by lane: waves 0 and 1 dO u^T, waves 2 and 3 dR u^T
   {
     Tri w{zero4(), zero4(), zero4()};
     const bool by_row = wave % 2 == 0, of_e = wave >= 2;
 #pragma unroll
     for (int s = 0; s < DV / 32; ++s) {
-      Frag<T> l0, l1, y0, y1;
+      Frag<T> l0, l1, u0, u1;
       const int col = 32 * s + 8 * q;
-      row_parts<kPV>(y0, &m.y[0][0][0], kChunk * kPV, c, col);
-      row_parts<kPV>(y1, &m.y[0][0][0], kChunk * kPV, 16 + c, col);
+      row_parts<kPV>(u0, &m.u[0][0][0], kChunk * kPV, c, col);
+      row_parts<kPV>(u1, &m.u[0][0][0], kChunk * kPV, 16 + c, col);
       if (of_e) {
         row_parts<kPV>(l0, &m.dr[0][0][0], kChunk * kPV, c, col);
         row_parts<kPV>(l1, &m.dr[0][0][0], kChunk * kPV, 16 + c, col);
         if (by_row) {
-          w.t00 = mm<2, 2>(y0, l0, w.t00);
-          w.t10 = mm<2, 2>(y0, l1, w.t10);
-          w.t11 = mm<2, 2>(y1, l1, w.t11);
+          w.t00 = mm<2, 2>(u0, l0, w.t00);
+          w.t10 = mm<2, 2>(u0, l1, w.t10);
+          w.t11 = mm<2, 2>(u1, l1, w.t11);
         } else {
-          w.t00 = mm<2, 2>(l0, y0, w.t00);
-          w.t10 = mm<2, 2>(l1, y0, w.t10);
-          w.t11 = mm<2, 2>(l1, y1, w.t11);
+          w.t00 = mm<2, 2>(l0, u0, w.t00);
+          w.t10 = mm<2, 2>(l1, u0, w.t10);
+          w.t11 = mm<2, 2>(l1, u1, w.t11);
         }
       } else {
-        clear(l0);
-        clear(l1);
-        if (c < len) row8(l0, dop + c * ldv + col);
-        if (16 + c < len) row8(l1, dop + (16 + c) * ldv + col);
+        Raw<T> r0, r1;
+        load_raw(r0, ow, orow + 32 * s * kB);
+        load_raw(r1, ow, orow + onext + 32 * s * kB);
+        as_frag(l0, r0);
+        as_frag(l1, r1);
         if (by_row) {
-          w.t00 = mm<2, 1>(y0, l0, w.t00);
-          w.t10 = mm<2, 1>(y0, l1, w.t10);
-          w.t11 = mm<2, 1>(y1, l1, w.t11);
+          w.t00 = mm<2, 1>(u0, l0, w.t00);
+          w.t10 = mm<2, 1>(u0, l1, w.t10);
+          w.t11 = mm<2, 1>(u1, l1, w.t11);
         } else {
-          w.t00 = mm<1, 2>(l0, y0, w.t00);
-          w.t10 = mm<1, 2>(l1, y0, w.t10);
-          w.t11 = mm<1, 2>(l1, y1, w.t11);
+          w.t00 = mm<1, 2>(l0, u0, w.t00);
+          w.t10 = mm<1, 2>(l1, u0, w.t10);
+          w.t11 = mm<1, 2>(l1, u1, w.t11);
         }
       }
     }
     const float f = of_e ? -1.0f : a.scale;
+    Frag<T> o[2];
     if (by_row) {
-      decay_tri<false>(w, gt, of_e, true, f, lane);
-      put_lower<T, 2>(m.op[wave], w, lane);
+      w = w * decays<false>(mat.rows, lane);
+      w = of_e ? lower<false, true>(w, lane) : lower<false, false>(w, lane);
     } else {
-      decay_tri<true>(w, gt, of_e, true, f, lane);
-      put_upper<T, 2>(m.op[wave], w, lane);
+      w = w * decays<true>(mat.rows, lane);
+      w = of_e ? lower<true, true>(w, lane) : lower<true, false>(w, lane);
     }
+    w.t00 *= f;
+    w.t10 *= f;
+    w.t11 *= f;
+    if (by_row)
+      lower_rows<2>(o, w);
+    else
+      upper_rows<2>(o, w);
+    put<2>(m.op[wave][0], o[0], lane);
+    put<2>(m.op[wave][1], o[1], lane);
   }
-  if (wave == 0 && lane < kChunk) {
+  if (wave == 3 && lane < kChunk) {
     double x = 0.0;
     float s = 0.0f;
 #pragma unroll
@@ -325,14 +330,15 @@ __global__ __launch_bounds__(64 * kWaves, 1) void grad_kernel(const Args a) {
   }
   __syncthreads();
 
-  // this wave's key channels: lane c has channel 16 (kK wave + x) + c
+  // this wave's key channels: lane c has channels kK wave 16 + kK c and the next
   if (a.dq == nullptr && a.dk_out == nullptr) return;
-  f32x4 dq[2][kK], ds[2][kK], rs[2][kK];
+  f32x4 dq[2][kK], dk[2][kK];
 #pragma unroll
   for (int x = 0; x < kK; ++x) {
+    f32x4 ds[2], rs[2];
 #pragma unroll
-    for (int it = 0; it < 2; ++it) dq[it][x] = ds[it][x] = rs[it][x] = zero4();
-    const int64_t row = (int64_t)(16 * (kK * wave + x) + c) * DV;
+    for (int it = 0; it < 2; ++it) dq[it][x] = ds[it] = rs[it] = zero4();
+    const int row = (16 * kK * wave + kK * c + x) * DV;
 #pragma unroll
     for (int s = 0; s < DV / 32; ++s) {
       const int col = 32 * s + 8 * q;
@@ -341,49 +347,55 @@ __global__ __launch_bounds__(64 * kWaves, 1) void grad_kernel(const Args a) {
       make<2>(s1, *reinterpret_cast<const f32x4*>(S1 + row + col), *reinterpret_cast<const f32x4*>(S1 + row + col + 4));
 #pragma unroll
       for (int it = 0; it < 2; ++it) {
-        clear(l);
-        if (16 * it + c < len) row8(l, dop + (16 * it + c) * ldv + col);
+        Raw<T> r;
+        load_raw(r, ow, orow + it * onext + 32 * s * kB);
+        as_frag(l, r);
         dq[it][x] = mm<1, 2>(l, s0, dq[it][x]);
         row_parts<kPV>(l, &m.dr[0][0][0], kChunk * kPV, 16 * it + c, col);
-        rs[it][x] = mm<2, 2>(l, s0, rs[it][x]);
-        row_parts<kPV>(l, &m.y[0][0][0], kChunk * kPV, 16 * it + c, col);
-        ds[it][x] = mm<2, 2>(l, s1, ds[it][x]);
+        rs[it] = mm<2, 2>(l, s0, rs[it]);
+        row_parts<kPV>(l, &m.u[0][0][0], kChunk * kPV, 16 * it + c, col);
+        ds[it] = mm<2, 2>(l, s1, ds[it]);
       }
     }
     Frag<T> kc, qc;
-    columns<kPK>(kc, &m.k[0][0], 16 * (kK * wave + x), 4, lane);
-    columns<kPK>(qc, &m.q[0][0], 16 * (kK * wave + x), 4, lane);
+    token_columns<kK, kPK>(kc, &m.k[0][0], 16 * kK * wave, x, lane);
+    token_columns<kK, kPK>(qc, &m.q[0][0], 16 * kK * wave, x, lane);
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
-      const f32x4 dec = rows4(m.rows.decay, it, q), rest = rows4(m.rows.rest, it, q), bt = rows4(m.rows.beta, it, q);
+      const f32x4 dec = rows4(mat.rows.decay, it, q), rest = rows4(mat.rows.rest, it, q);
       Frag<T> l;
-      get<2>(l, m.op[0] + it * kOperand<T>, lane);
+      get<2>(l, m.op[0][it], lane);
       dq[it][x] = mm<2, 1>(l, kc, dq[it][x] * (dec * a.scale));
-      f32x4 dk = ds[it][x] * (rest * bt) - rs[it][x] * dec;
-      get<2>(l, m.op[1] + it * kOperand<T>, lane);
-      dk = mm<2, 1>(l, qc, dk);
-      get<2>(l, m.op[2] + it * kOperand<T>, lane);
-      dk = mm<2, 1>(l, kc, dk);
-      get<2>(l, m.op[3] + it * kOperand<T>, lane);
-      ds[it][x] = mm<2, 1>(l, kc, dk);
+      f32x4 d = ds[it] * rest - rs[it] * dec;
+      get<2>(l, m.op[1][it], lane);
+      d = mm<2, 1>(l, qc, d);
+      get<2>(l, m.op[2][it], lane);
+      d = mm<2, 1>(l, kc, d);
+      get<2>(l, m.op[3][it], lane);
+      dk[it][x] = mm<2, 1>(l, kc, d);
     }
   }
+  const int ch = 16 * kK * wave + kK * c;
+  const auto store = [&](auto* to, int64_t ld, const f32x4(*v)[kK]) {
+    using U = std::remove_pointer_t<decltype(to)>;
+    const Window w = window<DK>(to, ld, len);
+    const int off = (int)((4 * q * ld + ch) * (int)sizeof(U)), next = (int)(ld * (int)sizeof(U));
 #pragma unroll
-  for (int x = 0; x < kK; ++x) {
-    const int ch = 16 * (kK * wave + x) + c;
-    f32x4 one[2][1];
-    one[0][0] = dq[0][x];
-    one[1][0] = dq[1][x];
-    if (a.dq_part)
-      store_rows<1>(a.dq_part + (p.first * a.hv + h) * DK + ch, one, (int64_t)a.hv * DK, len, q);
-    else if (a.dq)
-      store_rows<1>(static_cast<T*>(a.dq) + p.first * ldk + kh * DK + ch, one, ldk, len, q);
-    one[0][0] = ds[0][x];
-    one[1][0] = ds[1][x];
-    if (a.dk_part)
-      store_rows<1>(a.dk_part + (p.first * a.hv + h) * DK + ch, one, (int64_t)a.hv * DK, len, q);
-    else if (a.dk_out)
-      store_rows<1>(static_cast<T*>(a.dk_out) + p.first * ldk + kh * DK + ch, one, ldk, len, q);
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float o[kK];
+#pragma unroll
+        for (int x = 0; x < kK; ++x) o[x] = v[it][x][r];
+        store_rawn<U, kK>(w, off + (16 * it + r) * next, o);
+      }
+  };
+  if (a.dq_part) {
+    store(a.dq_part + (p.first * a.hv + h) * DK, (int64_t)a.hv * DK, dq);
+    store(a.dk_part + (p.first * a.hv + h) * DK, (int64_t)a.hv * DK, dk);
+  } else {
+    if (a.dq) store(static_cast<T*>(a.dq) + p.first * ldk + kh * DK, ldk, dq);
+    if (a.dk_out) store(static_cast<T*>(a.dk_out) + p.first * ldk + kh * DK, ldk, dk);
   }
 }
 
@@ -391,7 +403,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void grad_kernel(const Args a) {
 // no sequence are left as they are.
 template <class T>
 __global__ __launch_bounds__(256) void group_kernel(const Args a) {
-  const int64_t row = blockIdx.x;
+  const uint32_t row = blockIdx.x;
   bool inside = a.cu == nullptr;
   for (int b = threadIdx.x; !inside && b < a.nseq; b += 256)
     inside = row >= bound(a.cu, b, a.n) && row < bound(a.cu, b + 1, a.n);
@@ -404,9 +416,9 @@ __global__ __launch_bounds__(256) void group_kernel(const Args a) {
     const int kh = i / a.dk, ch = i % a.dk;
     f32x4 s = zero4();
     for (int g = 0; g < group; ++g)
-      s += *reinterpret_cast<const f32x4*>(from + (row * a.hv + kh * group + g) * a.dk + ch);
+      s += *reinterpret_cast<const f32x4*>(from + ((int64_t)row * a.hv + kh * group + g) * a.dk + ch);
     const float w[4] = {s[0], s[1], s[2], s[3]};
-    store_n<4>(to + row * width + i, w);
+    store_n<4>(to + (int64_t)row * width + i, w);
   }
 }
 

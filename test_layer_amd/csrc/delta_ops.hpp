@@ -62,6 +62,17 @@ __device__ __forceinline__ f32x4 mm16(const f32x4& a, const f32x4& b, f32x4 c) {
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
+// x - (the pair's low or high bf16), in one instruction: the pair's dot product with
+// (-1, -0) or (-0, -1), added to x. What is left of a value that was rounded to bf16
+// is exact in fp32. (With +0 the pair (-1, 0) is folded into the inline constant -1,
+// which the instruction takes as (0, -1).)
+__device__ __forceinline__ float less_lo(float x, uint32_t pair) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, 0x8000bf80u), x, false);
+}
+__device__ __forceinline__ float less_hi(float x, uint32_t pair) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, 0xbf808000u), x, false);
+}
+
 // Two tiles as an operand of P parts.
 template <int P>
 __device__ __forceinline__ void make(Frag<float>& f, const f32x4& x, const f32x4& y) {
@@ -82,10 +93,10 @@ __device__ __forceinline__ void make(Frag<uint16_t>& f, f32x4 x, f32x4 y) {
     if (p + 1 < P) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        x[2 * i] -= bf16_lo(w[i]);
-        x[2 * i + 1] -= bf16_hi(w[i]);
-        y[2 * i] -= bf16_lo(w[2 + i]);
-        y[2 * i + 1] -= bf16_hi(w[2 + i]);
+        x[2 * i] = less_lo(x[2 * i], w[i]);
+        x[2 * i + 1] = less_hi(x[2 * i + 1], w[i]);
+        y[2 * i] = less_lo(y[2 * i], w[2 + i]);
+        y[2 * i + 1] = less_hi(y[2 * i + 1], w[2 + i]);
       }
     }
   }
@@ -129,30 +140,50 @@ __device__ __forceinline__ int channel(int tile, int row) {
   return 32 * (tile / 2) + 8 * (row / 4) + 4 * (tile % 2) + row % 4;
 }
 
-// X^T as a left operand (or X as a right one) over the chunk's tokens, from X
-// [kChunk][pitch] in LDS: lane c has channel base + step (c / 4) + c % 4. bf16:
-// transposing reads, each lane of 16 giving the address of 4 neighbouring channels
-// of one token.
+// X^T as a left operand over the chunk's tokens, for the rows of a state's tile, from X
+// [kChunk][PITCH] in LDS. bf16: transposing reads, each lane of 16 giving the address
+// of 4 neighbouring channels of one token.
 template <int PITCH>
-__device__ __forceinline__ void columns(Frag<uint16_t>& f, const uint16_t* x, int base, int step, int lane) {
+__device__ __forceinline__ void state_rows(Frag<uint16_t>& f, const uint16_t* x, int tile, int lane) {
   const int s = lane % 16, q = lane / 16;
-  const uint16_t* p = x + (4 * q + s / 4) * PITCH + base + step * (s % 4);
+  const uint16_t* p = x + (4 * q + s / 4) * PITCH + channel(tile, 4 * (s % 4));
   f.part[0] = tr_op(p, p + 16 * PITCH);
 }
 template <int PITCH>
-__device__ __forceinline__ void columns(Frag<float>& f, const float* x, int base, int step, int lane) {
-  const int c = lane % 16, q = lane / 16;
-  const float* p = x + 4 * q * PITCH + base + step * (c / 4) + c % 4;
+__device__ __forceinline__ void state_rows(Frag<float>& f, const float* x, int tile, int lane) {
+  const float* p = x + 4 * (lane / 16) * PITCH + channel(tile, lane % 16);
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     f.a[r] = p[r * PITCH];
     f.b[r] = p[(16 + r) * PITCH];
   }
 }
-// The same for the rows of a state's tile.
-template <int PITCH, class T>
-__device__ __forceinline__ void state_rows(Frag<T>& f, const T* x, int tile, int lane) {
-  columns<PITCH>(f, x, 32 * (tile / 2) + 4 * (tile % 2), 8, lane);
+// X as a right operand over the chunk's tokens: lane c has channel base + N c + n.
+template <int N, int PITCH>
+__device__ __forceinline__ void token_columns(Frag<uint16_t>& f, const uint16_t* x, int base, int n, int lane) {
+  const int s = lane % 16, q = lane / 16;
+  if constexpr (N == 1) {
+    const uint16_t* p = x + (4 * q + s / 4) * PITCH + base + 4 * (s % 4);
+    f.part[0] = tr_op(p, p + 16 * PITCH);
+  } else {
+    const uint16_t* p = x + 4 * q * PITCH + base + N * s + n;
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint16_t* r = p + (16 * (i / 2) + 2 * (i % 2)) * PITCH;
+      w[i] = (uint32_t)r[0] | (uint32_t)r[PITCH] << 16;
+    }
+    f.part[0] = as_bf16x8(w);
+  }
+}
+template <int N, int PITCH>
+__device__ __forceinline__ void token_columns(Frag<float>& f, const float* x, int base, int n, int lane) {
+  const float* p = x + 4 * (lane / 16) * PITCH + base + N * (lane % 16) + n;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    f.a[r] = p[r * PITCH];
+    f.b[r] = p[(16 + r) * PITCH];
+  }
 }
 
 // N neighbouring values <-> fp32 (N = 1, 2 or 4, aligned to N values).
@@ -352,45 +383,55 @@ __device__ __forceinline__ void unit_inverse(const f32x4& n00, const f32x4& n10,
   for (int r = 0; r < 4; ++r) t10[r] = -t10[r];
 }
 
-// A sequence's piece: rows first .. first + len - 1, piece `seg` of `segs` of
-// sequence b. Rows and sequence boundaries are held inside [0, n], whatever cu
-// says.
-struct Piece {
-  int64_t first;   // row of its first token
-  int64_t begin;   // row of its sequence's first token
-  int len;         // tokens
-  int b, seg, segs;
-};
+// A value that is the same in all lanes, as the compiler sees it: descriptors and
+// addresses made of it stay in scalar registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
-__device__ __forceinline__ int64_t bound(const int32_t* cu, int64_t i, int64_t n) {
+// Rows are counted in 32 bits (at most 2^31 - 1). A boundary, held inside [0, n]
+// whatever cu says.
+__device__ __forceinline__ uint32_t bound(const int32_t* cu, uint32_t i, uint32_t n) {
   if (cu == nullptr) return i == 0 ? 0 : n;
-  const int64_t v = cu[i];
-  return v < 0 ? 0 : v > n ? n : v;
+  const int32_t v = cu[i];
+  return v < 0 ? 0 : (uint32_t)v > n ? n : (uint32_t)v;
 }
+
+// A sequence's piece: rows first .. first + len - 1, piece `seg` of `segs` of
+// sequence b, whose first row is `begin`. seg < 0: there is no such piece.
+struct Piece {
+  int64_t first, begin;
+  int len, b, seg, segs;
+};
 
 // Piece `sid`: sequence b's pieces of `per` tokens are numbered from
 // cu[b] / per + b on, which leaves room for each sequence's last, shorter piece (an
 // empty sequence has one piece of no tokens). A 64-ary search by the wave.
-__device__ __forceinline__ Piece find_piece(const int32_t* cu, int nseq, int64_t n, int64_t per, int64_t sid, int lane) {
-  int64_t lo = 0, size = nseq;
+__device__ __forceinline__ Piece find_piece(const int32_t* cu, int nseq, int64_t rows, int64_t tokens, int64_t id, int lane) {
+  const uint32_t n = (uint32_t)rows, per = (uint32_t)tokens, sid = (uint32_t)id;
+  uint32_t lo = 0, size = nseq;
   while (size > 1) {
-    const int64_t stride = (size + 63) / 64, at = lo + lane * stride;
+    const uint32_t stride = (size + 63) / 64, at = lo + lane * stride;
     const bool before = lane * stride < size && bound(cu, at, n) / per + at <= sid;
-    const int64_t found = __popcll(__ballot(before));
+    const uint32_t found = __popcll(__ballot(before));
     lo += (found > 0 ? found - 1 : 0) * stride;
     size = size < stride ? size : stride;
-    if (lo + size > nseq) size = nseq - lo;
+    if (lo + size > (uint32_t)nseq) size = nseq - lo;
   }
   Piece p;
-  p.b = __builtin_amdgcn_readfirstlane((int)lo);
-  p.begin = bound(cu, p.b, n);
-  const int64_t end = bound(cu, p.b + 1, n), len = end > p.begin ? end - p.begin : 0;
-  p.seg = (int)(sid - (p.begin / per + p.b));
-  p.segs = len > 0 ? (int)((len + per - 1) / per) : 1;
-  p.first = p.begin + p.seg * per;
-  const int64_t left = len - p.seg * per;
-  p.len = (int)(left < 0 ? 0 : left < per ? left : per);
-  if (p.seg < 0 || p.seg >= p.segs) p.seg = -1;
+  p.b = (int)uniform(lo);
+  const uint32_t begin = uniform(bound(cu, p.b, n)), end = uniform(bound(cu, p.b + 1, n));
+  const uint32_t len = end > begin ? end - begin : 0;
+  p.begin = begin;
+  p.seg = (int)(sid - (begin / per + p.b));
+  p.segs = len > 0 ? (int)(len / per + (len % per != 0)) : 1;
+  if (p.seg < 0 || p.seg >= p.segs) {
+    p.seg = -1;
+    p.first = begin;
+    p.len = 0;
+    return p;
+  }
+  const uint32_t before = (uint32_t)p.seg * per, left = len - before;
+  p.first = begin + before;
+  p.len = (int)(left < per ? left : per);
   return p;
 }
 

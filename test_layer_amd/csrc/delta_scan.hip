@@ -5,7 +5,7 @@
 // by chunks of 32 tokens. With G_i the chunk's decay up to token i, D_ij = G_i / G_j
 // and S the state before the chunk,
 //
-//   N = strict lower triangle of D . (K K^T) . beta_j,    T = (I + N)^-1
+//   N' = strict lower triangle of D . (K K^T),    T = (I + N' beta)^-1
 //   y = T (V - G . (K S)),  u = beta . y
 //   O = scale (G . (Q S) + (lower triangle of D . (Q K^T)) u)
 //   S <- G_end S + K^T (G_end / G . u)
@@ -33,11 +33,11 @@ namespace {
 template <class T, int DK, bool KEEP>
 __global__ __launch_bounds__(256) void matrices_kernel(const Args a) {
   __shared__ float scratch[4][2 * 16 * 20];
+  __shared__ Rows gates[4];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int c = lane % 16, q = lane / 16;
-  const int64_t id = (int64_t)blockIdx.x * 4 + wave;
+  const uint32_t id = blockIdx.x * 4 + wave, slot = id / a.hv;
   const int h = (int)(id % a.hv);
-  const int64_t slot = id / a.hv;
   const Piece p = find_piece(a.cu, a.nseq, a.n, kChunk, slot, lane);
   if (p.seg < 0 || p.len == 0) return;
   const int64_t ld = (int64_t)a.hk * DK;
@@ -53,9 +53,10 @@ __global__ __launch_bounds__(256) void matrices_kernel(const Args a) {
       load_raw(kr[it][s], kw, off + it * next + 32 * s * (int)sizeof(T));
       load_raw(qr[it][s], qw, off + it * next + 32 * s * (int)sizeof(T));
     }
-  const Gates gt = gates(a, p.first, p.len, h, lane);
-  // keys as a tile's rows: N and Q K^T by row
-  Tri n{zero4(), zero4(), zero4()}, b = n, bt = n;
+  Rows& rows = gates[wave];
+  put_rows(rows, a, p.first, p.len, h, lane);
+  // keys as a tile's rows: N' and Q K^T with rows by lane
+  Tri n{zero4(), zero4(), zero4()}, b = n;
 #pragma unroll
   for (int s = 0; s < DK / 32; ++s) {
     Frag<T> k0, k1, q0, q1;
@@ -69,27 +70,39 @@ __global__ __launch_bounds__(256) void matrices_kernel(const Args a) {
     b.t00 = mm<1, 1>(k0, q0, b.t00);
     b.t10 = mm<1, 1>(k0, q1, b.t10);
     b.t11 = mm<1, 1>(k1, q1, b.t11);
-    if constexpr (KEEP) {
-      bt.t00 = mm<1, 1>(q0, k0, bt.t00);
-      bt.t10 = mm<1, 1>(q1, k0, bt.t10);
-      bt.t11 = mm<1, 1>(q1, k1, bt.t11);
-    }
   }
-  decay_tri<false>(n, gt, true, true, 1.0f, lane);
-  decay_tri<false>(b, gt, false, false, a.scale, lane);
+  wave_lds_order();
+  const Tri d = decays<false>(rows, lane);
+  n = lower<false, true>(n * d, lane);
+  b = lower<false, false>(b * d, lane);
+  b.t00 *= a.scale;
+  b.t10 *= a.scale;
+  b.t11 *= a.scale;
+  const f32x4 b0 = rows4(rows.beta, 0, q), b1 = rows4(rows.beta, 1, q);
   Tri t;
-  unit_inverse(n.t00, n.t10, n.t11, t.t00, t.t10, t.t11, scratch[wave], lane);
-  Matrices* m = matrices_of(a.mats, slot * a.hv + h, KEEP);
+  unit_inverse(n.t00 * b0, n.t10 * b0, n.t11 * b1, t.t00, t.t10, t.t11, scratch[wave], lane);
+  Matrices* m = matrices_of(a.mats, (int64_t)slot * a.hv + h, KEEP);
   put_tri(m->t, t, lane);
   if constexpr (KEEP) {
     put_tri(m->b, b, lane);
-    decay_tri<true>(bt, gt, false, false, a.scale, lane);
-    put_tri(m->bt, bt, lane);
-    put_tri(m->tt, turned(t, lane), lane);
+    put_tri(m->bt, turned(b, lane), lane);
+    // X = (I + beta N')^-1 = I - beta (T N'): one inverse serves both sides' scaling
+    n = turned(n, lane);
+    f32x4 one;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) one[r] = 4 * q + r == c ? 1.0f : 0.0f;
+    Tri x;
+    x.t00 = one - b0 * mm16(t.t00, n.t00, zero4());
+    x.t10 = -b1 * mm16(t.t11, n.t10, mm16(t.t10, n.t00, zero4()));
+    x.t11 = one - b1 * mm16(t.t11, n.t11, zero4());
+    put_tri(m->x, x, lane);
   } else {
     put_tri_parts<T>(m->b, b, lane);
   }
-  put_rows(m->rows, gt, lane);
+  const float* from = reinterpret_cast<const float*>(&rows);
+  float* to = reinterpret_cast<float*>(&m->rows);
+#pragma unroll
+  for (int i = lane; i < (int)(sizeof(Rows) / 4); i += 64) to[i] = from[i];
 }
 
 // kStates: the state before every chunk, for the gradient (no outputs).
@@ -107,7 +120,7 @@ struct Loaded {
 };
 
 template <class T, int DK, int DV, int NCT, Mode MODE>
-__global__ __launch_bounds__(64 * (4 / NCT), 1) void scan_kernel(const Args a) {
+__global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_kernel(const Args a) {
   constexpr int kTiles = DK / 16, kSteps = DK / 32, kP = kWhole<T>, kW = 4 / NCT, kB = (int)sizeof(T);
   __shared__ T ks_rows[kW][kChunk * kPitch<T, DK>];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -118,7 +131,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), 1) void scan_kernel(const Args a) {
   if (p.seg < 0) return;
   if (MODE == kSummary && p.seg == p.segs - 1) return;  // nothing follows it
   // this lane's columns: NCT neighbours
-  const int col = blockIdx.y * 64 + wave * 16 * NCT + NCT * c;
+  const int col0 = blockIdx.y * 64 + wave * 16 * NCT, col = col0 + NCT * c;
   const bool unit = MODE == kSummary && blockIdx.y * 64 >= DV;
   if (unit && p.seg == 0) return;  // its first state is known
   T* const kt_rows = ks_rows[wave];
@@ -158,7 +171,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), 1) void scan_kernel(const Args a) {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) load_raw(x.q[it][s], qw, koff + it * knext + 32 * s * kB);
     }
-    const Window vw = window<16 * NCT>(static_cast<const T*>(a.v) + first * ldv + h * DV + (unit ? 0 : col - NCT * c), ldv,
+    const Window vw = window<16 * NCT>(static_cast<const T*>(a.v) + first * ldv + h * DV + (unit ? 0 : col0), ldv,
                                        unit ? 0 : len);
 #pragma unroll
     for (int it = 0; it < 2; ++it)
@@ -247,7 +260,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), 1) void scan_kernel(const Args a) {
     wave_lds_order();
     if constexpr (MODE == kForward) {
       const int64_t first = p.first + (int64_t)i * kChunk;
-      const Window ow = window<16 * NCT>(static_cast<const T*>(a.o) + first * ldv + h * DV + col - NCT * c, ldv,
+      const Window ow = window<16 * NCT>(static_cast<const T*>(a.o) + first * ldv + h * DV + col0, ldv,
                                          min(kChunk, p.len - i * kChunk));
 #pragma unroll
       for (int it = 0; it < 2; ++it)
@@ -286,8 +299,10 @@ __global__ __launch_bounds__(64 * (4 / NCT), 1) void scan_kernel(const Args a) {
 // The reverse of the scan, for the gradient. With dS the gradient of the state after a
 // chunk,
 //
-//   du = B^T dO + G_end / G . (K dS),  dR = T^T (beta . du)  (the gradient of V),
-//   dS <- G_end dS + Q^T (scale G . dO) - K^T (G . dR),    B = scale D . Q K^T (lower)
+//   du = B^T dO + G_end / G . (K dS),  dR = beta . X^T du  (the gradient of V),
+//   dS <- G_end dS + Q^T (scale G . dO) - K^T (G . dR)
+//
+// with B = scale D . Q K^T (lower) and X = (I + beta N')^-1,
 //
 // by the same columns, with dS in the registers. kBack: dS after every chunk is
 // stored; kBackSummary: what a piece makes of the dS behind it.
@@ -297,13 +312,13 @@ template <class T, int DK, int NCT>
 struct BackLoaded {
   Raw<T> k[2][DK / 32], q[2][DK / 32];
   RawN<T, NCT> d[2][4];
-  f32x4 tt[3], bt[3];
+  f32x4 xt[3], bt[3];
   f32x4 decay[2], rest[2], beta[2];
   float total;
 };
 
 template <class T, int DK, int DV, int NCT, BackMode MODE>
-__global__ __launch_bounds__(64 * (4 / NCT), 1) void back_kernel(const Args a) {
+__global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void back_kernel(const Args a) {
   constexpr int kTiles = DK / 16, kSteps = DK / 32, kP = kWhole<T>, kW = 4 / NCT, kB = (int)sizeof(T);
   __shared__ T rows[kW][2][kChunk * kPitch<T, DK>];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -313,7 +328,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), 1) void back_kernel(const Args a) {
   const Piece p = find_piece(a.cu, a.nseq, a.n, a.per, sid, lane);
   if (p.seg < 0) return;
   if (MODE == kBackSummary && p.seg == 0) return;  // nothing lies before it
-  const int col = blockIdx.y * 64 + wave * 16 * NCT + NCT * c;
+  const int col0 = blockIdx.y * 64 + wave * 16 * NCT, col = col0 + NCT * c;
   const bool unit = MODE == kBackSummary && blockIdx.y * 64 >= DV;
   if (unit && p.seg == p.segs - 1) return;  // the dS behind it is known
   T* const kt_rows = rows[wave][0];
@@ -351,7 +366,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), 1) void back_kernel(const Args a) {
         load_raw(x.k[it][s], kw, koff + it * knext + 32 * s * kB);
         load_raw(x.q[it][s], qw, koff + it * knext + 32 * s * kB);
       }
-    const Window dw = window<16 * NCT>(static_cast<const T*>(a.dout) + first * ldv + h * DV + (unit ? 0 : col - NCT * c), ldv,
+    const Window dw = window<16 * NCT>(static_cast<const T*>(a.dout) + first * ldv + h * DV + (unit ? 0 : col0), ldv,
                                        unit ? 0 : len);
 #pragma unroll
     for (int it = 0; it < 2; ++it)
@@ -360,7 +375,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), 1) void back_kernel(const Args a) {
     const Matrices* m = matrices_of(a.mats, (slot0 + i) * a.hv + h, true);
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-      x.tt[j] = m->tt[j][lane];
+      x.xt[j] = m->x[j][lane];
       x.bt[j] = m->bt[j][lane];
     }
 #pragma unroll
@@ -400,8 +415,8 @@ __global__ __launch_bounds__(64 * (4 / NCT), 1) void back_kernel(const Args a) {
       }
     }
     Frag<T> t0, t1, b0, b1;
-    make<kP>(t0, x.tt[0], x.tt[1]);
-    make<kP>(t1, zero4(), x.tt[2]);
+    make<kP>(t0, x.xt[0], x.xt[1]);
+    make<kP>(t1, zero4(), x.xt[2]);
     make<kP>(b0, x.bt[0], x.bt[1]);
     make<kP>(b1, zero4(), x.bt[2]);
     Frag<T> df[NCT], rf[NCT];
@@ -415,8 +430,8 @@ __global__ __launch_bounds__(64 * (4 / NCT), 1) void back_kernel(const Args a) {
       Frag<T> f;
       make<1>(f, dO[0], dO[1]);
       const f32x4 du0 = mm<kP, 1>(b0, f, kd[0][y] * x.rest[0]), du1 = mm<kP, 1>(b1, f, kd[1][y] * x.rest[1]);
-      make<kP>(f, du0 * x.beta[0], du1 * x.beta[1]);
-      const f32x4 dR0 = mm<kP, kP>(t0, f, zero4()), dR1 = mm<kP, kP>(t1, f, zero4());
+      make<kP>(f, du0, du1);
+      const f32x4 dR0 = mm<kP, kP>(t0, f, zero4()) * x.beta[0], dR1 = mm<kP, kP>(t1, f, zero4()) * x.beta[1];
       make<kP>(df[y], dO[0] * (x.decay[0] * a.scale), dO[1] * (x.decay[1] * a.scale));
       make<kP>(rf[y], -dR0 * x.decay[0], -dR1 * x.decay[1]);
     }
@@ -455,46 +470,66 @@ __global__ __launch_bounds__(64 * (4 / NCT), 1) void back_kernel(const Args a) {
 }
 
 // First states of a sequence's pieces, in seg_n's place: S <- M S + R from piece to
-// piece (BACK: from the last piece to the first), one wave for 16 columns. In fp32
-// products for both types: they are few.
+// piece (BACK: from the last piece to the first). One step waits for the one before, so
+// it is cut short: DK / 16 waves share 16 columns, a wave has 16 rows of the products
+// (in fp32 for both types: they are few) and its rows of the next M and R at hand, and
+// the new S goes round through LDS.
 template <int DK, int DV, bool BACK>
-__global__ __launch_bounds__(64) void join_kernel(const Args a) {
-  constexpr int kTiles = DK / 16, kSteps = DK / 32;
-  const int lane = threadIdx.x, c = lane % 16, q = lane / 16;
-  const int h = blockIdx.x % a.hv;
-  const int b = blockIdx.x / a.hv;
+__global__ __launch_bounds__(4 * DK) void join_kernel(const Args a) {
+  constexpr int kSteps = DK / 32;
+  __shared__ f32x4 rows[2][DK / 16][64];
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int c = lane % 16, q = lane / 16;
+  const int h = blockIdx.x % a.hv, b = blockIdx.x / a.hv;
   const int col = blockIdx.y * 16 + c;
-  const int64_t begin = bound(a.cu, b, a.n), end = bound(a.cu, b + 1, a.n);
-  const int64_t len = end > begin ? end - begin : 0;
-  const int segs = (int)((len + a.per - 1) / a.per);
+  const uint32_t n = (uint32_t)a.n, per = (uint32_t)a.per;
+  const uint32_t begin = uniform(bound(a.cu, b, n)), end = uniform(bound(a.cu, b + 1, n));
+  const int segs = end > begin ? (int)((end - begin - 1) / per + 1) : 0;
   if (segs < 2) return;
-  const int64_t sid = begin / a.per + b;
+  const int64_t sid = begin / per + b;
   const float* from = BACK ? a.dlast : a.state;
-  f32x4 S[kTiles][1];
-  load_state<DK, 1>(S, from ? from + ((int64_t)b * a.hv + h) * DK * DV + col : nullptr, DV, q);
-  for (int i = 0; i < segs; ++i) {
-    const int seg = BACK ? segs - 1 - i : i;
-    float* np = a.seg_n + ((sid + seg) * a.hv + h) * DK * DV + col;
-    const float* mp = a.seg_m + ((sid + seg) * a.hv + h) * DK * DK;
-    f32x4 out[kTiles][1];
-    const bool more = i + 1 < segs;
-    load_state<DK, 1>(out, more ? np : nullptr, DV, q);
-    store_state<DK, 1>(S, np, DV, q);
-    if (!more) break;
-    if (i > 0) {  // the first piece was run from the given state
+  const int64_t own = (int64_t)channel(wave, 4 * q) * DV + col;  // its 4 rows are neighbours
+  const int64_t mine = (int64_t)channel(wave, c) * DK + 8 * q;
+  const int64_t nstep = (int64_t)a.hv * DK * DV * (BACK ? -1 : 1), mstep = (int64_t)a.hv * DK * DK * (BACK ? -1 : 1);
+  const int64_t first = sid + (BACK ? segs - 1 : 0);
+  float* np = a.seg_n + (first * a.hv + h) * DK * DV + own;
+  const float* mp = a.seg_m + (first * a.hv + h) * DK * DK + mine;
+  f32x4 S = zero4(), R[2];
+  Frag<float> M[2][kSteps];
+  const auto load = [&](f32x4& R, Frag<float>* M, int i) {
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
+    for (int r = 0; r < 4; ++r) R[r] = np[i * nstep + r * DV];
+    if (i == 0) return;  // the first piece was run from the given state
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          Frag<float> m, f;
-          row8(m, mp + channel(t, c) * DK + 32 * s + 8 * q);
-          make<1>(f, S[2 * s][0], S[2 * s + 1][0]);
-          out[t][0] = mm<1, 1>(m, f, out[t][0]);
-        }
+    for (int s = 0; s < kSteps; ++s) row8(M[s], mp + i * mstep + 32 * s);
+  };
+  if (from) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) S[r] = from[((int64_t)b * a.hv + h) * DK * DV + own + r * DV];
+  }
+  load(R[0], M[0], 0);
+  const auto step = [&](const f32x4& R, const Frag<float>* M, f32x4& Rn, Frag<float>* Mn, int i) {
+    if (i + 2 < segs) load(Rn, Mn, i + 1);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) np[i * nstep + r * DV] = S[r];
+    if (i + 1 == segs) return;
+    if (i > 0) {
+      rows[i & 1][wave][lane] = S;
+      __syncthreads();
+      S = R;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        Frag<float> f;
+        make<1>(f, rows[i & 1][2 * s][lane], rows[i & 1][2 * s + 1][lane]);
+        S = mm<1, 1>(M[s], f, S);
       }
+    } else {
+      S = R;
     }
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) S[t][0] = out[t][0];
+  };
+  for (int i = 0; i < segs; i += 2) {
+    step(R[0], M[0], R[1], M[1], i);
+    if (i + 1 < segs) step(R[1], M[1], R[0], M[0], i + 1);
   }
 }
 
@@ -513,7 +548,7 @@ hipError_t run_forward(const Args& a, const Plan& p, hipStream_t stream) {
   if (p.split) {
     scan_kernel<T, DK, DV, NCT, kSummary><<<dim3(x, (DV + DK) / 64), kThreads, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
-    join_kernel<DK, DV, false><<<dim3((unsigned)(a.nseq * a.hv), DV / 16), 64, 0, stream>>>(a);
+    join_kernel<DK, DV, false><<<dim3((unsigned)(a.nseq * a.hv), DV / 16), 4 * DK, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
   }
   scan_kernel<T, DK, DV, NCT, MODE><<<dim3(x, DV / 64), kThreads, 0, stream>>>(a);
@@ -527,7 +562,7 @@ hipError_t run_back(const Args& a, const Plan& p, hipStream_t stream) {
   if (p.split) {
     back_kernel<T, DK, DV, NCT, kBackSummary><<<dim3(x, (DV + DK) / 64), kThreads, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
-    join_kernel<DK, DV, true><<<dim3((unsigned)(a.nseq * a.hv), DV / 16), 64, 0, stream>>>(a);
+    join_kernel<DK, DV, true><<<dim3((unsigned)(a.nseq * a.hv), DV / 16), 4 * DK, 0, stream>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
   }
   back_kernel<T, DK, DV, NCT, kBack><<<dim3(x, DV / 64), kThreads, 0, stream>>>(a);
@@ -544,8 +579,7 @@ hipError_t run_wide(const Args& a, const Plan& p, What what, hipStream_t s) {
 }
 template <class T, int DK, int DV>
 hipError_t run(const Args& a, const Plan& p, What what, hipStream_t s) {
-  constexpr int kMost = DK == 64 ? 4 : 2;
-  return p.wide ? run_wide<T, DK, DV, kMost>(a, p, what, s) : run_wide<T, DK, DV, 1>(a, p, what, s);
+  return p.wide ? run_wide<T, DK, DV, DK == 64 ? 4 : 2>(a, p, what, s) : run_wide<T, DK, DV, 1>(a, p, what, s);
 }
 template <class T>
 hipError_t run_of(const Args& a, const Plan& p, What what, hipStream_t s) {
