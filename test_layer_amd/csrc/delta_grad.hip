@@ -13,10 +13,11 @@
 // back from its end, what the later chunks say is in <dS, state>. (One such sum over
 // the whole sequence would lose the small terms; over 32 tokens it does not.)
 //
-// Four waves to a chunk and head: each has a quarter of the value channels (u, x, o and
-// the row sums, in fp32 values whole), then two forms each of F and E, then a quarter
-// of the key channels (dQ, dK, from operands in two bf16 parts). u and dR change from
-// columns by lane to rows by lane through LDS.
+// A wave has 64 value channels of a chunk and head, 4 neighbours a lane (u, x, o and the
+// row sums, in fp32 values whole), then F and E, then its share of the key channels
+// (dQ, dK, from operands in two bf16 parts). u and dR change from columns by lane to
+// rows by lane through LDS; the triangles stay in registers. (Four waves of 16 columns
+// to a chunk convert each triangle four times over: 1300 us against 48 views.)
 #include <type_traits>
 
 #include "delta_chunk.hpp"
@@ -25,42 +26,24 @@ namespace vggt3 {
 namespace delta {
 namespace {
 
-constexpr int kWaves = 4;
-
 template <class T, int DK, int DV>
 struct GradShared {
   static constexpr int kParts = sizeof(T) == 2 ? 2 : 1;  // of u and dR
-  static constexpr int kTwo = 128;                       // an operand of two parts, or of fp32 values
   T k[kChunk][kPitch<T, DK>];
   T q[kChunk][kPitch<T, DK>];
   T u[kParts][kChunk][kPitch<T, DV>];
   T dr[kParts][kChunk][kPitch<T, DV>];
-  u32x4 op[4][2][kTwo];  // F, F^T, -E, -E^T, 16 rows each
-  float along[kWaves][kChunk], step[kWaves][kChunk], all[kWaves];
+  float along[DV / 64][kChunk], step[DV / 64][kChunk], all[DV / 64];
 };
 
-// A tile pair's values as rows of LDS, split into parts.
-template <int PITCH>
-__device__ __forceinline__ void put_tile(uint16_t* to, const f32x4& v0, const f32x4& v1, int part, int col, int q) {
-  f32x4 v[2] = {v0, v1};
-#pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int it = 0; it < 2; ++it)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint16_t b = f32_to_bf16_bits(v[it][r]);
-        to[p * part + (16 * it + 4 * q + r) * PITCH + col] = b;
-        v[it][r] -= bf16_bits_to_f32(b);
-      }
+// 4 neighbouring values of a row to LDS, split into two parts (bf16).
+__device__ __forceinline__ void put_four(uint16_t* to, int part, const float* v) {
+  const uint32_t a = pack_bf16x2(v[0], v[1]), b = pack_bf16x2(v[2], v[3]);
+  st8(to, u32x2{a, b});
+  st8(to + part, u32x2{pack_bf16x2(less_lo(v[0], a), less_hi(v[1], a)), pack_bf16x2(less_lo(v[2], b), less_hi(v[3], b))});
 }
-template <int PITCH>
-__device__ __forceinline__ void put_tile(float* to, const f32x4& v0, const f32x4& v1, int, int col, int q) {
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    to[(4 * q + r) * PITCH + col] = v0[r];
-    to[(16 + 4 * q + r) * PITCH + col] = v1[r];
-  }
+__device__ __forceinline__ void put_four(float* to, int, const float* v) {
+  *reinterpret_cast<f32x4*>(to) = f32x4{v[0], v[1], v[2], v[3]};
 }
 template <int PITCH>
 __device__ __forceinline__ void row_parts(Frag<uint16_t>& f, const uint16_t* from, int part, int row, int col) {
@@ -81,10 +64,25 @@ __device__ __forceinline__ float row_sum(float x) {
   return row_add<0x140>(row_add<0x141>(row_add<0x4E>(row_add<0xB1>(x))));
 }
 
+// A value that the compiler takes as a new one: what was made of it before is made
+// again, instead of being held in registers until then.
+__device__ __forceinline__ void anew(uint32_t& x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void anew(f32x4& x) { asm volatile("" : "+v"(x)); }
+
+// Between the waves of a workgroup, or a wave's own LDS accesses.
+template <int W>
+__device__ __forceinline__ void meet() {
+  if constexpr (W == 1)
+    wave_lds_order();
+  else
+    __syncthreads();
+}
+
 template <class T, int DK, int DV>
-__global__ __launch_bounds__(64 * kWaves, DK + DV == 128 ? 3 : 1) void grad_kernel(const Args a) {
+__global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
   using Sh = GradShared<T, DK, DV>;
-  constexpr int kP = kWhole<T>, kV = DV / 64, kK = DK / 64, kPV = kPitch<T, DV>, kPK = kPitch<T, DK>, kB = (int)sizeof(T);
+  constexpr int kW = DV / 64, kP = kWhole<T>, kPV = kPitch<T, DV>, kPK = kPitch<T, DK>, kB = (int)sizeof(T);
+  constexpr int kPart = kChunk * kPV, kS = DK / 32;
   __shared__ Sh m;
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int c = lane % 16, q = lane / 16;
@@ -101,30 +99,82 @@ __global__ __launch_bounds__(64 * kWaves, DK + DV == 128 ? 3 : 1) void grad_kern
   const float* S0 = a.states + (slot * a.hv + h) * DK * DV;
   const float* S1 = a.dstates + (slot * a.hv + h) * DK * DV;
   const Matrices& mat = *matrices_of(a.mats, slot * a.hv + h, true);
-  const int orow = (int)((c * ldv + 8 * q) * kB), onext = (int)(16 * ldv * kB);  // dO by rows
+  const int krow = (int)((c * ldk + 8 * q) * kB), knext = (int)(16 * ldk * kB);
+  const int orow = (int)((c * ldv + 8 * q) * kB), onext = (int)(16 * ldv * kB);
+  const int col = wave * 64 + 4 * c;
+  const int voff = (int)((4 * q * ldv + col) * kB), vrow = (int)(ldv * kB);
 
-  {  // K and Q to LDS
-    constexpr int kPieces = DK / 8, kEach = kChunk * kPieces / (64 * kWaves);
-    Raw<T> kr[kEach], qr[kEach];
+  Raw<T> kr[2][kS], qr[2][kS];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int at = i * 64 * kWaves + threadIdx.x, off = (int)((at / kPieces * ldk + at % kPieces * 8) * kB);
-      load_raw(kr[i], kw, off);
-      load_raw(qr[i], qw, off);
-    }
+  for (int it = 0; it < 2; ++it)
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int at = i * 64 * kWaves + threadIdx.x;
-      put_raw(&m.k[at / kPieces][at % kPieces * 8], kr[i]);
-      put_raw(&m.q[at / kPieces][at % kPieces * 8], qr[i]);
+    for (int s = 0; s < kS; ++s) {
+      load_raw(kr[it][s], kw, krow + it * knext + 32 * s * kB);
+      load_raw(qr[it][s], qw, krow + it * knext + 32 * s * kB);
     }
+  f32x4 dec[2], rest[2], beta[2];
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    dec[it] = rows4(mat.rows.decay, it, q);
+    rest[it] = rows4(mat.rows.rest, it, q);
+    beta[it] = rows4(mat.rows.beta, it, q);
   }
+#pragma unroll
+  for (int it = 0; it < 2; ++it)
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+      if (s % kW != wave) continue;
+      put_raw(&m.k[16 * it + c][32 * s + 8 * q], kr[it][s]);
+      put_raw(&m.q[16 * it + c][32 * s + 8 * q], qr[it][s]);
+    }
+  // 128 key channels of them by rows would take 64 registers: they come from LDS again
+  constexpr bool kAgain = DK > 64;
+  if constexpr (kAgain) meet<kW>();
+  const auto rows_of = [&](Frag<T>& f0, Frag<T>& f1, const Raw<T>(*r)[kS], const T* from, int s) {
+    if constexpr (!kAgain) {
+      as_frag(f0, r[0][s]);
+      as_frag(f1, r[1][s]);
+    } else {
+      row8(f0, from + c * kPK + 32 * s + 8 * q);
+      row8(f1, from + (16 + c) * kPK + 32 * s + 8 * q);
+    }
+  };
 
-  // this wave's value channels
+  // this wave's value channels: u and o, then x and dR
+  RawN<T, 4> vr[2][4], dr[2][4];
+  f32x4 y[2][4], dR[2][4];
+  f32x4 along[2] = {zero4(), zero4()}, step[2] = {zero4(), zero4()};
+  float both = 0.0f;  // <dS, S>
   {
-    const int col = wave * 16 * kV + kV * c;
-    const int voff = (int)((4 * q * ldv + col) * kB), vrow = (int)(ldv * kB);
-    RawN<T, kV> vr[2][4], dr[2][4];
+    f32x4 ks[2][4], qs[2][4];
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) ks[it][x] = qs[it][x] = zero4();
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+      f32x4 st[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x4 w = *reinterpret_cast<const f32x4*>(S0 + channel(2 * s + i, 4 * q + r) * DV + col);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) st[i][x][r] = w[x];
+        }
+      Frag<T> k0, k1, q0, q1;
+      rows_of(k0, k1, kr, &m.k[0][0], s);
+      rows_of(q0, q1, qr, &m.q[0][0], s);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        Frag<T> f;
+        make<kP>(f, st[0][x], st[1][x]);
+        ks[0][x] = mm<1, kP>(k0, f, ks[0][x]);
+        ks[1][x] = mm<1, kP>(k1, f, ks[1][x]);
+        qs[0][x] = mm<1, kP>(q0, f, qs[0][x]);
+        qs[1][x] = mm<1, kP>(q1, f, qs[1][x]);
+      }
+    }
 #pragma unroll
     for (int it = 0; it < 2; ++it)
 #pragma unroll
@@ -132,63 +182,11 @@ __global__ __launch_bounds__(64 * kWaves, DK + DV == 128 ? 3 : 1) void grad_kern
         load_rawn(vr[it][r], vw, voff + (16 * it + r) * vrow);
         load_rawn(dr[it][r], ow, voff + (16 * it + r) * vrow);
       }
-    const Tri t = get_tri(mat.t, lane), b = get_tri(mat.b, lane), bt = get_tri(mat.bt, lane), xt = get_tri(mat.x, lane);
-    f32x4 dec[2], rest[2], beta[2], along[2], step[2];
+    Frag<T> tf[2], bf[2];
+    lower_rows<kP>(tf, get_tri(mat.t, lane));
+    lower_rows<kP>(bf, get_tri(mat.b, lane));
 #pragma unroll
-    for (int it = 0; it < 2; ++it) {
-      dec[it] = rows4(mat.rows.decay, it, q);
-      rest[it] = rows4(mat.rows.rest, it, q);
-      beta[it] = rows4(mat.rows.beta, it, q);
-      along[it] = step[it] = zero4();
-    }
-    f32x4 ks[2][kV], kd[2][kV], qs[2][kV];
-#pragma unroll
-    for (int it = 0; it < 2; ++it)
-#pragma unroll
-      for (int x = 0; x < kV; ++x) ks[it][x] = kd[it][x] = qs[it][x] = zero4();
-    float both = 0.0f;  // <dS, S>
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < DK / 32; ++s) {
-      f32x4 st[2][kV], ds[2][kV];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float w0[kV], w1[kV];
-          const int at = channel(2 * s + i, 4 * q + r) * DV + col;
-          load_n<kV>(w0, S0 + at);
-          load_n<kV>(w1, S1 + at);
-#pragma unroll
-          for (int x = 0; x < kV; ++x) {
-            st[i][x][r] = w0[x];
-            ds[i][x][r] = w1[x];
-            both += w0[x] * w1[x];
-          }
-        }
-      Frag<T> k0, k1, q0, q1;
-      row8(k0, &m.k[c][32 * s + 8 * q]);
-      row8(k1, &m.k[16 + c][32 * s + 8 * q]);
-      row8(q0, &m.q[c][32 * s + 8 * q]);
-      row8(q1, &m.q[16 + c][32 * s + 8 * q]);
-#pragma unroll
-      for (int x = 0; x < kV; ++x) {
-        Frag<T> f;
-        make<kP>(f, st[0][x], st[1][x]);
-        ks[0][x] = mm<1, kP>(k0, f, ks[0][x]);
-        ks[1][x] = mm<1, kP>(k1, f, ks[1][x]);
-        qs[0][x] = mm<1, kP>(q0, f, qs[0][x]);
-        qs[1][x] = mm<1, kP>(q1, f, qs[1][x]);
-        make<kP>(f, ds[0][x], ds[1][x]);
-        kd[0][x] = mm<1, kP>(k0, f, kd[0][x]);
-        kd[1][x] = mm<1, kP>(k1, f, kd[1][x]);
-      }
-    }
-    both *= mat.rows.total;
-    Frag<T> o[2];
-    f32x4 dR[2][kV];
-#pragma unroll
-    for (int x = 0; x < kV; ++x) {
+    for (int x = 0; x < 4; ++x) {
       f32x4 V[2], dO[2];
 #pragma unroll
       for (int it = 0; it < 2; ++it)
@@ -199,204 +197,287 @@ __global__ __launch_bounds__(64 * kWaves, DK + DV == 128 ? 3 : 1) void grad_kern
         }
       Frag<T> f;
       make<kP>(f, V[0] - dec[0] * ks[0][x], V[1] - dec[1] * ks[1][x]);
-      lower_rows<kP>(o, t);
-      const f32x4 y0 = mm<kP, kP>(o[0], f, zero4()), y1 = mm<kP, kP>(o[1], f, zero4());
-      const f32x4 u0 = y0 * beta[0], u1 = y1 * beta[1];
-      put_tile<kPV>(&m.u[0][0][0], u0, u1, kChunk * kPV, col + x, q);
-      make<kP>(f, u0, u1);
-      lower_rows<kP>(o, b);
-      along[0] += dO[0] * mm<kP, kP>(o[0], f, qs[0][x] * (dec[0] * a.scale));
-      along[1] += dO[1] * mm<kP, kP>(o[1], f, qs[1][x] * (dec[1] * a.scale));
-      make<1>(f, dO[0], dO[1]);
-      upper_rows<kP>(o, bt);
-      const f32x4 e0 = kd[0][x] * rest[0], e1 = kd[1][x] * rest[1];
-      const f32x4 du0 = mm<kP, 1>(o[0], f, e0), du1 = mm<kP, 1>(o[1], f, e1);
-      make<kP>(f, du0, du1);
-      upper_rows<kP>(o, xt);
-      const f32x4 x0 = mm<kP, kP>(o[0], f, zero4()), x1 = mm<kP, kP>(o[1], f, zero4());
-      dR[0][x] = x0 * beta[0];
-      dR[1][x] = x1 * beta[1];
-      put_tile<kPV>(&m.dr[0][0][0], dR[0][x], dR[1][x], kChunk * kPV, col + x, q);
-      along[0] -= V[0] * dR[0][x];
-      along[1] -= V[1] * dR[1][x];
-      step[0] += y0 * x0;
-      step[1] += y1 * x1;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) both += e0[r] * u0[r] + e1[r] * u1[r];
+      y[0][x] = mm<kP, kP>(tf[0], f, zero4());
+      y[1][x] = mm<kP, kP>(tf[1], f, zero4());
+      make<kP>(f, y[0][x] * beta[0], y[1][x] * beta[1]);
+      along[0] += dO[0] * mm<kP, kP>(bf[0], f, qs[0][x] * (dec[0] * a.scale));
+      along[1] += dO[1] * mm<kP, kP>(bf[1], f, qs[1][x] * (dec[1] * a.scale));
     }
-    if (a.dv_out) {
-      const Window dw = window<DV>(static_cast<const T*>(a.dv_out) + p.first * ldv + h * DV, ldv, len);
+  }
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    anew(beta[it]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T); ++i) {
+        anew(vr[it][r].r[i]);
+        anew(dr[it][r].r[i]);
+      }
+  }
+  {
+    f32x4 kd[2][4];
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) kd[it][x] = zero4();
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+      f32x4 ds[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x4 w = *reinterpret_cast<const f32x4*>(S1 + channel(2 * s + i, 4 * q + r) * DV + col);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) ds[i][x][r] = w[x];
+        }
+      Frag<T> k0, k1;
+      rows_of(k0, k1, kr, &m.k[0][0], s);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        Frag<T> f;
+        make<kP>(f, ds[0][x], ds[1][x]);
+        kd[0][x] = mm<1, kP>(k0, f, kd[0][x]);
+        kd[1][x] = mm<1, kP>(k1, f, kd[1][x]);
+      }
+    }
+    Frag<T> btf[2], xf[2];
+    upper_rows<kP>(btf, get_tri(mat.bt, lane));
+    upper_rows<kP>(xf, get_tri(mat.x, lane));
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      f32x4 V[2], dO[2];
 #pragma unroll
       for (int it = 0; it < 2; ++it)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float w[kV];
-#pragma unroll
-          for (int x = 0; x < kV; ++x) w[x] = dR[it][x][r];
-          store_rawn<T, kV>(dw, voff + (16 * it + r) * vrow, w);
+          V[it][r] = value_of(vr[it][r], x);
+          dO[it][r] = value_of(dr[it][r], x);
         }
+      Frag<T> f;
+      make<1>(f, dO[0], dO[1]);
+      const f32x4 e0 = kd[0][x] * rest[0], e1 = kd[1][x] * rest[1];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) both += e0[r] * (y[0][x][r] * beta[0][r]) + e1[r] * (y[1][x][r] * beta[1][r]);
+      const f32x4 du0 = mm<kP, 1>(btf[0], f, e0), du1 = mm<kP, 1>(btf[1], f, e1);
+      make<kP>(f, du0, du1);
+      const f32x4 x0 = mm<kP, kP>(xf[0], f, zero4()), x1 = mm<kP, kP>(xf[1], f, zero4());
+      step[0] += y[0][x] * x0;
+      step[1] += y[1][x] * x1;
+      dR[0][x] = x0 * beta[0];
+      dR[1][x] = x1 * beta[1];
+      along[0] -= V[0] * dR[0][x];
+      along[1] -= V[1] * dR[1][x];
     }
+  }
+  anew(beta[0]);
+  anew(beta[1]);
+  {
+    const Window dw = window<DV>(static_cast<const T*>(a.dv_out) + p.first * ldv + h * DV, ldv, a.dv_out ? len : 0);
 #pragma unroll
     for (int it = 0; it < 2; ++it)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float s0 = row_sum(along[it][r]), s1 = row_sum(step[it][r]);
-        if (c == 0) {
-          m.along[wave][16 * it + 4 * q + r] = s0;
-          m.step[wave][16 * it + 4 * q + r] = s1;
-        }
+        const float w[4] = {y[it][0][r] * beta[it][r], y[it][1][r] * beta[it][r], y[it][2][r] * beta[it][r],
+                            y[it][3][r] * beta[it][r]};
+        const float z[4] = {dR[it][0][r], dR[it][1][r], dR[it][2][r], dR[it][3][r]};
+        put_four(&m.u[0][16 * it + 4 * q + r][col], kPart, w);
+        put_four(&m.dr[0][16 * it + 4 * q + r][col], kPart, z);
+        store_rawn<T, 4>(dw, voff + (16 * it + r) * vrow, z);
       }
-    both = wave_sum(both);
-    if (lane == 0) m.all[wave] = both;
   }
-  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < 2; ++it)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float s0 = row_sum(along[it][r]), s1 = row_sum(step[it][r]);
+      if (c == 0) {
+        m.along[wave][16 * it + 4 * q + r] = s0;
+        m.step[wave][16 * it + 4 * q + r] = s1;
+      }
+    }
+  meet<kW>();
 
-  // F and E, rows by lane and columns by lane: waves 0 and 1 dO u^T, waves 2 and 3 dR u^T
-  {
-    Tri w{zero4(), zero4(), zero4()};
-    const bool by_row = wave % 2 == 0, of_e = wave >= 2;
+  // F = dO u^T and E = dR u^T, with rows by lane (as F, -E) and columns by lane (F^T, -E^T)
+  Frag<T> ff[2], ft[2], ef[2], et[2];
+  const auto triangles = [&]() {
+    Tri f{zero4(), zero4(), zero4()}, g = f, e = f, d = f;
 #pragma unroll
     for (int s = 0; s < DV / 32; ++s) {
-      Frag<T> l0, l1, u0, u1;
-      const int col = 32 * s + 8 * q;
-      row_parts<kPV>(u0, &m.u[0][0][0], kChunk * kPV, c, col);
-      row_parts<kPV>(u1, &m.u[0][0][0], kChunk * kPV, 16 + c, col);
-      if (of_e) {
-        row_parts<kPV>(l0, &m.dr[0][0][0], kChunk * kPV, c, col);
-        row_parts<kPV>(l1, &m.dr[0][0][0], kChunk * kPV, 16 + c, col);
-        if (by_row) {
-          w.t00 = mm<2, 2>(u0, l0, w.t00);
-          w.t10 = mm<2, 2>(u0, l1, w.t10);
-          w.t11 = mm<2, 2>(u1, l1, w.t11);
-        } else {
-          w.t00 = mm<2, 2>(l0, u0, w.t00);
-          w.t10 = mm<2, 2>(l1, u0, w.t10);
-          w.t11 = mm<2, 2>(l1, u1, w.t11);
-        }
-      } else {
-        Raw<T> r0, r1;
-        load_raw(r0, ow, orow + 32 * s * kB);
-        load_raw(r1, ow, orow + onext + 32 * s * kB);
-        as_frag(l0, r0);
-        as_frag(l1, r1);
-        if (by_row) {
-          w.t00 = mm<2, 1>(u0, l0, w.t00);
-          w.t10 = mm<2, 1>(u0, l1, w.t10);
-          w.t11 = mm<2, 1>(u1, l1, w.t11);
-        } else {
-          w.t00 = mm<1, 2>(l0, u0, w.t00);
-          w.t10 = mm<1, 2>(l1, u0, w.t10);
-          w.t11 = mm<1, 2>(l1, u1, w.t11);
+      Frag<T> r0, r1, u0, u1, o0, o1;
+      const int at = 32 * s + 8 * q;
+      row_parts<kPV>(u0, &m.u[0][0][0], kPart, c, at);
+      row_parts<kPV>(u1, &m.u[0][0][0], kPart, 16 + c, at);
+      row_parts<kPV>(r0, &m.dr[0][0][0], kPart, c, at);
+      row_parts<kPV>(r1, &m.dr[0][0][0], kPart, 16 + c, at);
+      Raw<T> w0, w1;
+      load_raw(w0, ow, orow + 32 * s * kB);
+      load_raw(w1, ow, orow + onext + 32 * s * kB);
+      as_frag(o0, w0);
+      as_frag(o1, w1);
+      f.t00 = mm<2, 1>(u0, o0, f.t00);
+      f.t10 = mm<2, 1>(u0, o1, f.t10);
+      f.t11 = mm<2, 1>(u1, o1, f.t11);
+      g.t00 = mm<1, 2>(o0, u0, g.t00);
+      g.t10 = mm<1, 2>(o1, u0, g.t10);
+      g.t11 = mm<1, 2>(o1, u1, g.t11);
+      e.t00 = mm<2, 2>(u0, r0, e.t00);
+      e.t10 = mm<2, 2>(u0, r1, e.t10);
+      e.t11 = mm<2, 2>(u1, r1, e.t11);
+      d.t00 = mm<2, 2>(r0, u0, d.t00);
+      d.t10 = mm<2, 2>(r1, u0, d.t10);
+      d.t11 = mm<2, 2>(r1, u1, d.t11);
+    }
+    Tri w = decays<false>(mat.rows, lane);
+    e = lower<false, true>(e * w, lane);
+    const f32x4 one = {1.0f, 1.0f, 1.0f, 1.0f}, sc = one * a.scale;
+    f = lower<false, false>(f * w, lane);
+    lower_rows<2>(ff, f * Tri{sc, sc, sc});
+    lower_rows<2>(ef, e * Tri{-one, -one, -one});
+    w = decays<true>(mat.rows, lane);
+    d = lower<true, true>(d * w, lane);
+    g = lower<true, false>(g * w, lane);
+    upper_rows<2>(ft, g * Tri{sc, sc, sc});
+    upper_rows<2>(et, d * Tri{-one, -one, -one});
+  };
+
+  // this wave's key channels, kN neighbours a lane at a time
+  constexpr int kEach = DK / kW, kN = kEach / 16 < 4 ? kEach / 16 : 4;
+  float apart = 0.0f;  // <dS, S before the chunk>, by rows
+  f32x4 dq[2][kN], dk[2][kN];
+  // what S and dS have of them
+  const auto by_states = [&](int base) {
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int x = 0; x < kN; ++x) dq[it][x] = dk[it][x] = zero4();
+    const int row = (base + kN * c) * DV + 8 * q;
+    const auto eight = [&](f32x4* w, const float* from, int x, int s) {
+      const float* at = from + row + x * DV + 32 * s;
+      w[0] = *reinterpret_cast<const f32x4*>(at);
+      w[1] = *reinterpret_cast<const f32x4*>(at + 4);
+    };
+#pragma unroll
+    for (int s = 0; s < DV / 32; ++s) {
+      Frag<T> o[2], r[2];
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        Raw<T> w;
+        load_raw(w, ow, orow + it * onext + 32 * s * kB);
+        as_frag(o[it], w);
+        row_parts<kPV>(r[it], &m.dr[0][0][0], kPart, 16 * it + c, 32 * s + 8 * q);
+      }
+#pragma unroll
+      for (int x = 0; x < kN; ++x) {
+        f32x4 w[2];
+        eight(w, S0, x, s);
+        Frag<T> f;
+        make<2>(f, w[0], w[1]);
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+          dq[it][x] = mm<1, 2>(o[it], f, dq[it][x]);
+          dk[it][x] = mm<2, 2>(r[it], f, dk[it][x]);
         }
       }
     }
-    const float f = of_e ? -1.0f : a.scale;
-    Frag<T> o[2];
-    if (by_row) {
-      w = w * decays<false>(mat.rows, lane);
-      w = of_e ? lower<false, true>(w, lane) : lower<false, false>(w, lane);
-    } else {
-      w = w * decays<true>(mat.rows, lane);
-      w = of_e ? lower<true, true>(w, lane) : lower<true, false>(w, lane);
+    f32x4 us[2][kN];
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int x = 0; x < kN; ++x) us[it][x] = zero4();
+#pragma unroll
+    for (int s = 0; s < DV / 32; ++s) {
+      Frag<T> u[2];
+#pragma unroll
+      for (int it = 0; it < 2; ++it) row_parts<kPV>(u[it], &m.u[0][0][0], kPart, 16 * it + c, 32 * s + 8 * q);
+#pragma unroll
+      for (int x = 0; x < kN; ++x) {
+        f32x4 w[2], z[2];
+        eight(w, S1, x, s);
+        eight(z, S0, x, s);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) apart += w[0][r] * z[0][r] + w[1][r] * z[1][r];
+        Frag<T> f;
+        make<2>(f, w[0], w[1]);
+#pragma unroll
+        for (int it = 0; it < 2; ++it) us[it][x] = mm<2, 2>(u[it], f, us[it][x]);
+      }
     }
-    w.t00 *= f;
-    w.t10 *= f;
-    w.t11 *= f;
-    if (by_row)
-      lower_rows<2>(o, w);
-    else
-      upper_rows<2>(o, w);
-    put<2>(m.op[wave][0], o[0], lane);
-    put<2>(m.op[wave][1], o[1], lane);
+#pragma unroll
+    for (int x = 0; x < kN; ++x)
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        dq[it][x] *= dec[it] * a.scale;
+        dk[it][x] = us[it][x] * rest[it] - dk[it][x] * dec[it];
+      }
+  };
+  // what the chunk's own keys and queries have
+  const auto by_tokens = [&](int base) {
+#pragma unroll
+    for (int x = 0; x < kN; ++x) {
+      Frag<T> kc, qc;
+      token_columns<kN, kPK>(kc, &m.k[0][0], base, x, lane);
+      token_columns<kN, kPK>(qc, &m.q[0][0], base, x, lane);
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        dq[it][x] = mm<2, 1>(ff[it], kc, dq[it][x]);
+        dk[it][x] = mm<2, 1>(ft[it], qc, dk[it][x]);
+        dk[it][x] = mm<2, 1>(ef[it], kc, dk[it][x]);
+        dk[it][x] = mm<2, 1>(et[it], kc, dk[it][x]);
+      }
+    }
+    const auto store = [&](auto* to, int64_t ld, const f32x4(*v)[kN]) {
+      using U = std::remove_pointer_t<decltype(to)>;
+      const Window w = window<DK>(to, ld, len);
+      const int off = (int)((4 * q * ld + base + kN * c) * (int)sizeof(U)), next = (int)(ld * (int)sizeof(U));
+#pragma unroll
+      for (int it = 0; it < 2; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float z[kN];
+#pragma unroll
+          for (int x = 0; x < kN; ++x) z[x] = v[it][x][r];
+          store_rawn<U, kN>(w, off + (16 * it + r) * next, z);
+        }
+    };
+    if (a.dq_part) {
+      store(a.dq_part + (p.first * a.hv + h) * DK, (int64_t)a.hv * DK, dq);
+      store(a.dk_part + (p.first * a.hv + h) * DK, (int64_t)a.hv * DK, dk);
+    } else {
+      if (a.dq) store(static_cast<T*>(a.dq) + p.first * ldk + kh * DK, ldk, dq);
+      if (a.dk_out) store(static_cast<T*>(a.dk_out) + p.first * ldk + kh * DK, ldk, dk);
+    }
+  };
+  triangles();
+#pragma unroll 1
+  for (int base = wave * kEach; base < (wave + 1) * kEach; base += 16 * kN) {
+    by_states(base);
+    by_tokens(base);
   }
-  if (wave == 3 && lane < kChunk) {
-    double x = 0.0;
+  both = wave_sum(both + apart * mat.rows.total);
+  if (lane == 0) m.all[wave] = both;
+  meet<kW>();
+  if (wave == 0 && lane < kChunk) {
+    double x = 0.0, all = 0.0;
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < kW; ++w) {
       x += m.along[w][lane];
       s += m.step[w][lane];
+      all += m.all[w];
     }
 #pragma unroll
     for (int off = 1; off < kChunk; off *= 2) {
       const double down = __shfl_down(x, off, 32);
       if (lane + off < kChunk) x += down;
     }
-    const double all = (double)m.all[0] + m.all[1] + m.all[2] + m.all[3];
     if (lane < len) {
       if (a.dg) a.dg[(p.first + lane) * a.hv + h] = (float)(x + all);
       if (a.dbeta) a.dbeta[(p.first + lane) * a.hv + h] = s;
     }
   }
-  __syncthreads();
 
-  // this wave's key channels: lane c has channels kK wave 16 + kK c and the next
-  if (a.dq == nullptr && a.dk_out == nullptr) return;
-  f32x4 dq[2][kK], dk[2][kK];
-#pragma unroll
-  for (int x = 0; x < kK; ++x) {
-    f32x4 ds[2], rs[2];
-#pragma unroll
-    for (int it = 0; it < 2; ++it) dq[it][x] = ds[it] = rs[it] = zero4();
-    const int row = (16 * kK * wave + kK * c + x) * DV;
-#pragma unroll
-    for (int s = 0; s < DV / 32; ++s) {
-      const int col = 32 * s + 8 * q;
-      Frag<T> s0, s1, l;
-      make<2>(s0, *reinterpret_cast<const f32x4*>(S0 + row + col), *reinterpret_cast<const f32x4*>(S0 + row + col + 4));
-      make<2>(s1, *reinterpret_cast<const f32x4*>(S1 + row + col), *reinterpret_cast<const f32x4*>(S1 + row + col + 4));
-#pragma unroll
-      for (int it = 0; it < 2; ++it) {
-        Raw<T> r;
-        load_raw(r, ow, orow + it * onext + 32 * s * kB);
-        as_frag(l, r);
-        dq[it][x] = mm<1, 2>(l, s0, dq[it][x]);
-        row_parts<kPV>(l, &m.dr[0][0][0], kChunk * kPV, 16 * it + c, col);
-        rs[it] = mm<2, 2>(l, s0, rs[it]);
-        row_parts<kPV>(l, &m.u[0][0][0], kChunk * kPV, 16 * it + c, col);
-        ds[it] = mm<2, 2>(l, s1, ds[it]);
-      }
-    }
-    Frag<T> kc, qc;
-    token_columns<kK, kPK>(kc, &m.k[0][0], 16 * kK * wave, x, lane);
-    token_columns<kK, kPK>(qc, &m.q[0][0], 16 * kK * wave, x, lane);
-#pragma unroll
-    for (int it = 0; it < 2; ++it) {
-      const f32x4 dec = rows4(mat.rows.decay, it, q), rest = rows4(mat.rows.rest, it, q);
-      Frag<T> l;
-      get<2>(l, m.op[0][it], lane);
-      dq[it][x] = mm<2, 1>(l, kc, dq[it][x] * (dec * a.scale));
-      f32x4 d = ds[it] * rest - rs[it] * dec;
-      get<2>(l, m.op[1][it], lane);
-      d = mm<2, 1>(l, qc, d);
-      get<2>(l, m.op[2][it], lane);
-      d = mm<2, 1>(l, kc, d);
-      get<2>(l, m.op[3][it], lane);
-      dk[it][x] = mm<2, 1>(l, kc, d);
-    }
-  }
-  const int ch = 16 * kK * wave + kK * c;
-  const auto store = [&](auto* to, int64_t ld, const f32x4(*v)[kK]) {
-    using U = std::remove_pointer_t<decltype(to)>;
-    const Window w = window<DK>(to, ld, len);
-    const int off = (int)((4 * q * ld + ch) * (int)sizeof(U)), next = (int)(ld * (int)sizeof(U));
-#pragma unroll
-    for (int it = 0; it < 2; ++it)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float o[kK];
-#pragma unroll
-        for (int x = 0; x < kK; ++x) o[x] = v[it][x][r];
-        store_rawn<U, kK>(w, off + (16 * it + r) * next, o);
-      }
-  };
-  if (a.dq_part) {
-    store(a.dq_part + (p.first * a.hv + h) * DK, (int64_t)a.hv * DK, dq);
-    store(a.dk_part + (p.first * a.hv + h) * DK, (int64_t)a.hv * DK, dk);
-  } else {
-    if (a.dq) store(static_cast<T*>(a.dq) + p.first * ldk + kh * DK, ldk, dq);
-    if (a.dk_out) store(static_cast<T*>(a.dk_out) + p.first * ldk + kh * DK, ldk, dk);
-  }
 }
 
 // dq, dk of key heads that several value heads share, in the heads' order. Rows of
@@ -424,7 +505,7 @@ __global__ __launch_bounds__(256) void group_kernel(const Args a) {
 
 template <class T, int DK, int DV>
 hipError_t run(const Args& a, hipStream_t s) {
-  grad_kernel<T, DK, DV><<<(unsigned)(chunk_slots(a.n, a.nseq) * a.hv), 64 * kWaves, 0, s>>>(a);
+  grad_kernel<T, DK, DV><<<(unsigned)(chunk_slots(a.n, a.nseq) * a.hv), DV, 0, s>>>(a);
   return hipGetLastError();
 }
 template <class T>

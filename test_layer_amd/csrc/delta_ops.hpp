@@ -158,15 +158,17 @@ __device__ __forceinline__ void state_rows(Frag<float>& f, const float* x, int t
     f.b[r] = p[(16 + r) * PITCH];
   }
 }
-// X as a right operand over the chunk's tokens: lane c has channel base + N c + n.
+// X as a right operand over the chunk's tokens: lane c has channel base + N c + n (of N
+// neighbours). bf16: N = 1 by transposing reads; otherwise value by value, since a
+// lane's channels are not neighbours of the next lane's.
 template <int N, int PITCH>
 __device__ __forceinline__ void token_columns(Frag<uint16_t>& f, const uint16_t* x, int base, int n, int lane) {
-  const int s = lane % 16, q = lane / 16;
+  const int c = lane % 16, q = lane / 16;
   if constexpr (N == 1) {
-    const uint16_t* p = x + (4 * q + s / 4) * PITCH + base + 4 * (s % 4);
+    const uint16_t* p = x + (4 * q + c / 4) * PITCH + base + 4 * (c % 4);
     f.part[0] = tr_op(p, p + 16 * PITCH);
   } else {
-    const uint16_t* p = x + 4 * q * PITCH + base + N * s + n;
+    const uint16_t* p = x + 4 * q * PITCH + base + N * c + n;
     u32x4 w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -404,21 +406,36 @@ struct Piece {
 
 // Piece `sid`: sequence b's pieces of `per` tokens are numbered from
 // cu[b] / per + b on, which leaves room for each sequence's last, shorter piece (an
-// empty sequence has one piece of no tokens). A 64-ary search by the wave.
+// empty sequence has one piece of no tokens). Up to 63 sequences are looked at at once,
+// a boundary a lane, in one trip to memory; more by a 64-ary search.
 __device__ __forceinline__ Piece find_piece(const int32_t* cu, int nseq, int64_t rows, int64_t tokens, int64_t id, int lane) {
   const uint32_t n = (uint32_t)rows, per = (uint32_t)tokens, sid = (uint32_t)id;
-  uint32_t lo = 0, size = nseq;
-  while (size > 1) {
-    const uint32_t stride = (size + 63) / 64, at = lo + lane * stride;
-    const bool before = lane * stride < size && bound(cu, at, n) / per + at <= sid;
-    const uint32_t found = __popcll(__ballot(before));
-    lo += (found > 0 ? found - 1 : 0) * stride;
-    size = size < stride ? size : stride;
-    if (lo + size > (uint32_t)nseq) size = nseq - lo;
-  }
   Piece p;
-  p.b = (int)uniform(lo);
-  const uint32_t begin = uniform(bound(cu, p.b, n)), end = uniform(bound(cu, p.b + 1, n));
+  uint32_t begin, end;
+  if (cu == nullptr) {
+    p.b = 0;
+    begin = 0;
+    end = n;
+  } else if (nseq < 64) {
+    const uint32_t at = lane < nseq ? lane : nseq, v = bound(cu, at, n);
+    const uint32_t found = __popcll(__ballot(lane < nseq && v / per + at <= sid));
+    p.b = (int)uniform(found > 0 ? found - 1 : 0);
+    begin = __builtin_amdgcn_readlane(v, p.b);
+    end = __builtin_amdgcn_readlane(v, p.b + 1);
+  } else {
+    uint32_t lo = 0, size = nseq;
+    while (size > 1) {
+      const uint32_t stride = (size + 63) / 64, at = lo + lane * stride;
+      const bool before = lane * stride < size && bound(cu, at, n) / per + at <= sid;
+      const uint32_t found = __popcll(__ballot(before));
+      lo += (found > 0 ? found - 1 : 0) * stride;
+      size = size < stride ? size : stride;
+      if (lo + size > (uint32_t)nseq) size = nseq - lo;
+    }
+    p.b = (int)uniform(lo);
+    begin = uniform(bound(cu, p.b, n));
+    end = uniform(bound(cu, p.b + 1, n));
+  }
   const uint32_t len = end > begin ? end - begin : 0;
   p.begin = begin;
   p.seg = (int)(sid - (begin / per + p.b));

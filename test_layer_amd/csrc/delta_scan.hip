@@ -601,6 +601,9 @@ hipError_t launch_back(const Args& a, const Plan& p, bool bf16, hipStream_t stre
 
 size_t matrix_bytes(bool keep) { return matrices_bytes(keep); }
 
+// Pieces as long as fill the GPU with waves (a wave a SIMD where they are wide, two
+// with their few registers otherwise), at least 4 chunks, and only where sequences are
+// much longer than that: a cut costs a pass over all pieces, with d_k more columns.
 Plan plan(int64_t n, int nseq, int64_t longest, int hv, int dk, int dv) {
   const int64_t chunks = (n + kChunk - 1) / kChunk, rows = (int64_t)hv * (dv / 64);
   Plan p;
@@ -608,7 +611,7 @@ Plan plan(int64_t n, int nseq, int64_t longest, int hv, int dk, int dv) {
   const int64_t waves = p.wide ? 1024 : 512;
   int64_t each = (chunks * rows + waves - 1) / waves;
   if (each < 4) each = 4;
-  p.split = longest > each * kChunk;
+  p.split = longest > each * kChunk * 5 / 2;
   p.per = p.split ? each * kChunk : (n / kChunk + 1) * kChunk;
   p.pieces = n / p.per + nseq;
   return p;

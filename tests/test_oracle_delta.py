@@ -88,6 +88,9 @@ def _find(cu, n, per, sid):
     """A lane-for-lane model of the kernels' search for piece sid: (sequence, piece or -1, first row, rows)."""
     nseq = len(cu) - 1
     lo, size = 0, nseq
+    if nseq < 64:  # a boundary a lane
+        lo = max(sum(_bound(cu, i, n) // per + i <= sid for i in range(nseq)) - 1, 0)
+        size = 1
     while size > 1:
         stride = (size + 63) // 64
         before = [lane * stride < size and _bound(cu, lo + lane * stride, n) // per + lo + lane * stride <= sid
