@@ -10,7 +10,7 @@
 // heads, so a lane's 4 pairs keep their angles over the token's heads and their
 // frequencies and weights over all tokens. A lane holds both channels of 4 pairs:
 // no channel moves between lanes, and the norm's sums over a head are a few DPP
-// steps over 4 to 16 lanes. Angles are formed in 64 bits (in 32 a position of a
+// steps over 8 to 64 lanes. Angles are formed in 64 bits (in 32 a position of a
 // million is off by 0.06 of a radian) and reduced to a turn before the sine, one
 // pair a lane, and handed to the lanes that hold the pair.
 #include "qk.hpp"
@@ -217,10 +217,10 @@ __device__ __forceinline__ Vec vec_of(const float* w, const Pairs& p, float none
 }
 
 // The norm's statistic: x <- x - mean (layer), and the factor of x.
-template <int LANES>
+template <int LANES, int NORM>
 __device__ __forceinline__ float normalise(const Args& a, float* f, float* s, const Pairs& p) {
   const float inv_d = 1.0f / a.d;
-  if (a.norm == kLayer) {
+  if constexpr (NORM == kLayer) {
     float m = 0.0f;
 #pragma unroll
     for (int v = 0; v < 4; ++v) m += f[v] + s[v];
@@ -235,36 +235,56 @@ __device__ __forceinline__ float normalise(const Args& a, float* f, float* s, co
 #pragma unroll
   for (int v = 0; v < 4; ++v) x += f[v] * f[v] + s[v] * s[v];
   x = head_sum<LANES>(x);
-  if (a.norm == kL2) return 1.0f / fmaxf(sqrtf(x), a.eps);
+  if constexpr (NORM == kL2) return 1.0f / fmaxf(sqrtf(x), a.eps);
   return __builtin_amdgcn_rsqf(x * inv_d + a.eps);
 }
 
-template <class T, int LANES, Access A>
+// Norms with weights and biases.
+template <int NORM>
+constexpr bool kAffine = NORM == kRms || NORM == kLayer;
+
+// A wave's token: its heads, kHeads at a time, q's and then k's. The next heads' rows
+// are asked for before the current ones are computed.
+template <class T, int LANES, Access A, int NORM>
 __global__ __launch_bounds__(256) void forward_kernel(const Args a) {
-  const int lane = threadIdx.x % 64, head = lane / LANES;
   constexpr int kHeads = 64 / LANES;
+  const int lane = threadIdx.x % 64, head = lane / LANES;
   const Pairs p = pairs_of<A>(a, lane % LANES);
   const Rotation<LANES> rot(a, lane);
   const bool live = p.first[0] >= 0;  // lanes behind a head's end
-  for (int64_t token = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; token < a.n; token += (int64_t)gridDim.x * 4) {
+  Vec w[2], b[2];
+  if constexpr (kAffine<NORM>) {
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      w[side] = vec_of(a.s[side].w, p, 1.0f);
+      b[side] = vec_of(a.s[side].b, p, 0.0f);
+    }
+  }
+  const int64_t step = (int64_t)gridDim.x * 4;
+  for (int64_t token = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; token < a.n; token += step) {
     const Angles t = rot.at(a, token, lane % LANES);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const Side& sd = a.s[side];
       if (sd.heads == 0) continue;
-      const Vec w = vec_of(sd.w, p, 1.0f), b = vec_of(sd.b, p, 0.0f);
       const T* x = static_cast<const T*>(sd.x) + token * sd.ld;
       T* y = static_cast<T*>(sd.y) + token * sd.heads * a.d;
-      for (int h = head; h < (sd.heads + kHeads - 1) / kHeads * kHeads; h += kHeads) {
-        const bool here = h < sd.heads && live;
-        float f[4] = {0, 0, 0, 0}, s[4] = {0, 0, 0, 0};
-        if (here) load8<A>(f, s, x + (int64_t)h * a.d, p);
-        if (a.norm != kNone) {
-          const float r = normalise<LANES>(a, f, s, p);
+      float f[4] = {0, 0, 0, 0}, s[4] = {0, 0, 0, 0};
+      if (head < sd.heads && live) load8<A>(f, s, x + head * a.d, p);
+      for (int h = head;;) {
+        const bool here = h < sd.heads && live, more = h - head + kHeads < sd.heads;
+        float nf[4] = {0, 0, 0, 0}, ns[4] = {0, 0, 0, 0};
+        if (more && h + kHeads < sd.heads && live) load8<A>(nf, ns, x + (h + kHeads) * a.d, p);
+        if constexpr (NORM != kNone) {
+          const float r = normalise<LANES, NORM>(a, f, s, p);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            f[v] = f[v] * r * w.f[v] + b.f[v];
-            s[v] = s[v] * r * w.s[v] + b.s[v];
+            f[v] *= r;
+            s[v] *= r;
+            if constexpr (kAffine<NORM>) {
+              f[v] = f[v] * w[side].f[v] + b[side].f[v];
+              s[v] = s[v] * w[side].s[v] + b[side].s[v];
+            }
           }
         }
 #pragma unroll
@@ -273,7 +293,14 @@ __global__ __launch_bounds__(256) void forward_kernel(const Args a) {
           s[v] = s[v] * t.c[v] + f[v] * t.s[v];
           f[v] = m;
         }
-        if (here) store8<A>(y + (int64_t)h * a.d, f, s, p);
+        if (here) store8<A>(y + h * a.d, f, s, p);
+        if (!more) break;
+        h += kHeads;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          f[v] = nf[v];
+          s[v] = ns[v];
+        }
       }
     }
   }
@@ -284,7 +311,7 @@ __global__ __launch_bounds__(256) void forward_kernel(const Args a) {
 //   L2     dx = r (e - xhat sum(e xhat)), or e / eps where |x| < eps.
 // The sums over rows are a lane's own registers until the end, then a workgroup's
 // through LDS in a fixed order, and sum_kernel's.
-template <class T, int LANES, Access A>
+template <class T, int LANES, Access A, int NORM>
 __global__ __launch_bounds__(256) void grad_kernel(const Args a) {
   constexpr int kHeads = 64 / LANES;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, head = lane / LANES;
@@ -296,6 +323,11 @@ __global__ __launch_bounds__(256) void grad_kernel(const Args a) {
   for (int side = 0; side < 2; ++side)
 #pragma unroll
     for (int v = 0; v < 8; ++v) dw[side][v] = db[side][v] = 0.0f;
+  Vec ws[2];
+  if constexpr (kAffine<NORM>) {
+    ws[0] = vec_of(a.s[0].w, p, 1.0f);
+    ws[1] = vec_of(a.s[1].w, p, 1.0f);
+  }
   const float inv_d = 1.0f / a.d;
   for (int64_t token = (int64_t)blockIdx.x * 4 + wave; token < a.n; token += (int64_t)gridDim.x * 4) {
     const Angles t = rot.at(a, token, lane % LANES);
@@ -303,16 +335,29 @@ __global__ __launch_bounds__(256) void grad_kernel(const Args a) {
     for (int side = 0; side < 2; ++side) {
       const Side& sd = a.s[side];
       if (sd.heads == 0) continue;
-      const Vec w = vec_of(sd.w, p, 1.0f);
+      const Vec& w = ws[side];
       const T* x = static_cast<const T*>(sd.x) + token * sd.ld;
       const T* dy = static_cast<const T*>(sd.dy) + token * sd.heads * a.d;
       T* dx = static_cast<T*>(sd.y) + token * sd.heads * a.d;
-      for (int h = head; h < (sd.heads + kHeads - 1) / kHeads * kHeads; h += kHeads) {
-        const bool here = h < sd.heads && live;
-        float f[4] = {0, 0, 0, 0}, s[4] = {0, 0, 0, 0}, ef[4] = {0, 0, 0, 0}, es[4] = {0, 0, 0, 0};
-        if (here) {
-          if (a.norm != kNone) load8<A>(f, s, x + (int64_t)h * a.d, p);
-          load8<A>(ef, es, dy + (int64_t)h * a.d, p);
+      float xf[4] = {0, 0, 0, 0}, xs[4] = {0, 0, 0, 0}, yf[4] = {0, 0, 0, 0}, ys[4] = {0, 0, 0, 0};
+      if (head < sd.heads && live) {
+        if constexpr (NORM != kNone) load8<A>(xf, xs, x + head * a.d, p);
+        load8<A>(yf, ys, dy + head * a.d, p);
+      }
+      for (int h = head;;) {
+        const bool here = h < sd.heads && live, more = h - head + kHeads < sd.heads;
+        float f[4], s[4], ef[4], es[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          f[v] = xf[v];
+          s[v] = xs[v];
+          ef[v] = yf[v];
+          es[v] = ys[v];
+          xf[v] = xs[v] = yf[v] = ys[v] = 0.0f;
+        }
+        if (more && h + kHeads < sd.heads && live) {
+          if constexpr (NORM != kNone) load8<A>(xf, xs, x + (h + kHeads) * a.d, p);
+          load8<A>(yf, ys, dy + (h + kHeads) * a.d, p);
         }
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -320,36 +365,43 @@ __global__ __launch_bounds__(256) void grad_kernel(const Args a) {
           es[v] = es[v] * t.c[v] - ef[v] * t.s[v];
           ef[v] = m;
         }
-        if (a.norm != kNone) {
-          const float r = normalise<LANES>(a, f, s, p);
-          const bool clamped = a.norm == kL2 && r >= 1.0f / a.eps;
+        if constexpr (NORM != kNone) {
+          const float r = normalise<LANES, NORM>(a, f, s, p);
+          const bool clamped = NORM == kL2 && r >= 1.0f / a.eps;
           float along = 0.0f, mean = 0.0f;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             f[v] *= r;
             s[v] *= r;
-            if (here) {
+            if (kAffine<NORM> && a.part && here) {
               db[side][v] += ef[v];
               db[side][4 + v] += es[v];
               dw[side][v] += ef[v] * f[v];
               dw[side][4 + v] += es[v] * s[v];
             }
-            ef[v] *= w.f[v];
-            es[v] *= w.s[v];
+            if constexpr (kAffine<NORM>) {
+              ef[v] *= w.f[v];
+              es[v] *= w.s[v];
+            }
             along += ef[v] * f[v] + es[v] * s[v];
             mean += ef[v] + es[v];
           }
           along = head_sum<LANES>(along);
-          if (a.norm != kL2) along *= inv_d;
+          if constexpr (NORM != kL2) along *= inv_d;
           if (clamped) along = 0.0f;
-          mean = a.norm == kLayer ? head_sum<LANES>(mean) * inv_d : 0.0f;
+          if constexpr (NORM == kLayer)
+            mean = head_sum<LANES>(mean) * inv_d;
+          else
+            mean = 0.0f;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             ef[v] = (ef[v] - f[v] * along - mean) * r;
             es[v] = (es[v] - s[v] * along - mean) * r;
           }
         }
-        if (here && sd.y) store8<A>(dx + (int64_t)h * a.d, ef, es, p);
+        if (here && sd.y) store8<A>(dx + h * a.d, ef, es, p);
+        if (!more) break;
+        h += kHeads;
       }
     }
   }
@@ -387,8 +439,10 @@ __global__ __launch_bounds__(256) void sum_kernel(const float* part, int blocks,
   float* out = o.out[vec];
   if (out == nullptr) return;
   float x = 0.0f;
-  if (ch < d)
+  if (ch < d) {
+#pragma unroll 8
     for (int b = r; b < blocks; b += 16) x += part[((int64_t)b * 4 + vec) * d + ch];
+  }
   s[r][c] = x;
   __syncthreads();
   if (r == 0 && ch < d) {
@@ -420,23 +474,32 @@ Access access(const Args& a, size_t value) {
   return run == 4 ? kFours : run == 2 ? kTwos : kSingle;
 }
 
-template <class T, int LANES, Access A, bool GRAD>
+template <class T, int LANES, Access A, int NORM, bool GRAD>
 void run(const Args& a, int blocks, hipStream_t s) {
   if (GRAD)
-    grad_kernel<T, LANES, A><<<blocks, 256, 0, s>>>(a);
+    grad_kernel<T, LANES, A, NORM><<<blocks, 256, 0, s>>>(a);
   else
-    forward_kernel<T, LANES, A><<<blocks, 256, 0, s>>>(a);
+    forward_kernel<T, LANES, A, NORM><<<blocks, 256, 0, s>>>(a);
+}
+template <class T, int LANES, Access A, bool GRAD>
+void by_norm(const Args& a, int blocks, hipStream_t s) {
+  if (a.norm == kNone)
+    run<T, LANES, A, kNone, GRAD>(a, blocks, s);
+  else if (a.norm == kL2)
+    run<T, LANES, A, kL2, GRAD>(a, blocks, s);
+  else if (a.norm == kRms)
+    run<T, LANES, A, kRms, GRAD>(a, blocks, s);
+  else
+    run<T, LANES, A, kLayer, GRAD>(a, blocks, s);
 }
 template <class T, Access A, bool GRAD>
 void by_lanes(const Args& a, int blocks, hipStream_t s) {
-  if (a.d <= 32)
-    run<T, 4, A, GRAD>(a, blocks, s);
-  else if (a.d <= 64)
-    run<T, 8, A, GRAD>(a, blocks, s);
+  if (a.d <= 64)
+    by_norm<T, 8, A, GRAD>(a, blocks, s);
   else if (a.d <= 128)
-    run<T, 16, A, GRAD>(a, blocks, s);
+    by_norm<T, 16, A, GRAD>(a, blocks, s);
   else
-    run<T, 64, A, GRAD>(a, blocks, s);
+    by_norm<T, 64, A, GRAD>(a, blocks, s);
 }
 template <class T, bool GRAD>
 void by_access(const Args& a, int blocks, hipStream_t s) {
@@ -465,7 +528,7 @@ hipError_t launch_forward(const Args& a, bool bf16, hipStream_t stream) {
 
 int grad_blocks(int64_t n) {
   const int64_t units = (n + 3) / 4;
-  return (int)(units < 1024 ? units : 1024);
+  return (int)(units < 768 ? units : 768);  // three waves a SIMD, as their registers allow
 }
 
 hipError_t launch_grad(const Args& a, float* const* out, bool bf16, hipStream_t stream) {
