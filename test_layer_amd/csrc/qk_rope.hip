@@ -8,9 +8,10 @@
 //
 // Bound by memory: x read once, y written once. A wave takes a token with all its
 // heads, so a lane's 4 pairs keep their angles over the token's heads and their
-// frequencies and weights over all tokens. A lane holds both channels of 4 pairs:
-// no channel moves between lanes, and the norm's sums over a head are a few DPP
-// steps over 8 to 64 lanes. Angles are formed in 64 bits (in 32 a position of a
+// frequencies and weights over all tokens. A lane holds both channels of 4 pairs, so
+// that a rotation is its own, and the norm's sums over a head are a few DPP
+// steps over 8 to 64 lanes. 100 views of 16 + 16 heads of 64 in bf16: 214 us,
+// 5.3 TB/s, a copy's rate; 48 views' gradient 158 us. Angles are formed in 64 bits (in 32 a position of a
 // million is off by 0.06 of a radian) and reduced to a turn before the sine, one
 // pair a lane, and handed to the lanes that hold the pair.
 #include "qk.hpp"
@@ -21,8 +22,11 @@ namespace vggt3 {
 namespace qk {
 namespace {
 
-using delta::load_n;
-using delta::store_n;
+using delta::load_rawn;
+using delta::RawN;
+using delta::store_rawn;
+using delta::value_of;
+using delta::Window;
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float x) {
@@ -41,8 +45,12 @@ __device__ __forceinline__ float head_sum(float x) {
 }
 
 // How a lane's 8 channels lie: two runs of 4 (the pairs' first and second
-// channels), two runs of 2 twice, 8 neighbours, or anyhow.
-enum Access { kFours, kTwos, kNeighbours, kSingle };
+// channels), 8 neighbours, anyhow but read and written as 8 neighbours and handed
+// over through LDS, or anyhow. 100 views in bf16 with axes of 12, 10 and 10 pairs:
+// runs of 2 values were 330 us, single ones 560, handed over 214.
+enum Access { kFours, kNeighbours, kStaged, kSingle };
+
+constexpr int kNowhere = 0x40000000;  // an offset behind every row's end
 
 // A rotated pair: its channels, axis and turns a position step.
 struct Pair {
@@ -67,13 +75,19 @@ __device__ __forceinline__ Pair pair_of(const Args& a, int at) {
 struct Pairs {
   int first[4], second[4];
 };
-template <Access A>
+// Pair v of a lane: 4 neighbours, or where pairs lie anyhow every LANES-th, so that
+// the lanes' values are neighbours.
+template <Access A, int LANES>
+__device__ __forceinline__ int pair_at(int lane_in_head, int v) {
+  return A == kFours || A == kNeighbours ? 4 * lane_in_head + v : lane_in_head + LANES * v;
+}
+template <Access A, int LANES>
 __device__ __forceinline__ Pairs pairs_of(const Args& a, int lane_in_head) {
-  constexpr int kRun = A == kFours ? 4 : A == kTwos ? 2 : 1;
+  constexpr int kRun = A == kFours ? 4 : 1;
   Pairs p;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
-    const int at = 4 * lane_in_head + v;
+    const int at = pair_at<A, LANES>(lane_in_head, v);
     if (at < a.rotated) {
       const Pair x = pair_of(a, at);
       p.first[v] = x.first;
@@ -98,7 +112,7 @@ __device__ __forceinline__ void angle_of(const Args& a, int axis, double turns, 
 struct Angles {
   float c[4], s[4];
 };
-template <int LANES>
+template <Access A, int LANES>
 struct Rotation {
   static constexpr int kOwn = LANES <= 16 ? 1 : 4;
   int axis[kOwn];
@@ -108,7 +122,7 @@ struct Rotation {
     for (int v = 0; v < kOwn; ++v) {
       axis[v] = 0;
       turns[v] = 0.0;
-      const int at = kOwn * lane + v;
+      const int at = kOwn == 1 ? lane : pair_at<A, LANES>(lane, v);
       if (at < a.rotated) {
         const Pair x = pair_of(a, at);
         axis[v] = x.axis;
@@ -132,8 +146,8 @@ struct Rotation {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       if constexpr (kOwn == 1) {
-        t.c[v] = __shfl(c[0], 4 * lane_in_head + v, 64);
-        t.s[v] = __shfl(s[0], 4 * lane_in_head + v, 64);
+        t.c[v] = __shfl(c[0], pair_at<A, LANES>(lane_in_head, v), 64);
+        t.s[v] = __shfl(s[0], pair_at<A, LANES>(lane_in_head, v), 64);
       } else {
         t.c[v] = c[v];
         t.s[v] = s[v];
@@ -143,64 +157,106 @@ struct Rotation {
   }
 };
 
-template <Access A, class T>
-__device__ __forceinline__ void load8(float* f, float* s, const T* p, const Pairs& at) {
-  if constexpr (A == kFours) {
-    load_n<4>(f, p + at.first[0]);
-    load_n<4>(s, p + at.second[0]);
-  } else if constexpr (A == kTwos) {
-    load_n<2>(f, p + at.first[0]);
-    load_n<2>(s, p + at.second[0]);
-    if (at.first[2] >= 0) {
-      load_n<2>(f + 2, p + at.first[2]);
-      load_n<2>(s + 2, p + at.second[2]);
-    }
-  } else if constexpr (A == kNeighbours) {
-    float w[8];
-    load_n<4>(w, p + at.first[0]);
-    load_n<4>(w + 4, p + at.first[0] + 4);
+// A lane's 8 channels of a head as runs: how many, of how many values, and where they
+// start in the head's row in bytes (behind every row's end where there is none: the
+// window's range check then reads zeros and drops stores, so that no access hangs on a
+// branch, behind which the compiler would wait for all stores before it).
+template <Access A, class T, int LANES>
+struct Runs {
+  static constexpr int kN = A == kFours || A == kNeighbours ? 4 : 1, kCount = 8 / kN;
+  int at[kCount];
+  __device__ __forceinline__ Runs(const Args&, const Pairs& p, int) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      f[v] = w[2 * v];
-      s[v] = w[2 * v + 1];
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if (at.first[v] >= 0) load_n<1>(&f[v], p + at.first[v]);
-      if (at.second[v] >= 0) load_n<1>(&s[v], p + at.second[v]);
+    for (int i = 0; i < kCount; ++i) {
+      const int v = A == kNeighbours ? 2 * i : i / 2 * kN;
+      const int ch = A == kNeighbours || i % 2 == 0 ? p.first[v] : p.second[v];
+      at[i] = ch < 0 ? kNowhere : ch * (int)sizeof(T);
     }
   }
-}
-template <Access A, class T>
-__device__ __forceinline__ void store8(T* p, const float* f, const float* s, const Pairs& at) {
-  if constexpr (A == kFours) {
-    store_n<4>(p + at.first[0], f);
-    store_n<4>(p + at.second[0], s);
-  } else if constexpr (A == kTwos) {
-    store_n<2>(p + at.first[0], f);
-    store_n<2>(p + at.second[0], s);
-    if (at.first[2] >= 0) {
-      store_n<2>(p + at.first[2], f + 2);
-      store_n<2>(p + at.second[2], s + 2);
-    }
-  } else if constexpr (A == kNeighbours) {
-    float w[8];
+  // Where pair v's channels are among the runs' values.
+  static __device__ __forceinline__ constexpr int first(int v) { return A == kNeighbours ? 2 * v : v / kN * 2 * kN + v % kN; }
+  static __device__ __forceinline__ constexpr int second(int v) { return first(v) + (A == kNeighbours ? 1 : kN); }
+  typedef RawN<T, kN> Raw8[kCount];
+  __device__ __forceinline__ void load(Raw8& r, Window w, int row) const {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) load_rawn(r[i], w, row + at[i]);
+  }
+  __device__ __forceinline__ void values(float* f, float* s, const Raw8& r) const {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      w[2 * v] = f[v];
-      w[2 * v + 1] = s[v];
-    }
-    store_n<4>(p + at.first[0], w);
-    store_n<4>(p + at.first[0] + 4, w + 4);
-  } else {
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if (at.first[v] >= 0) store_n<1>(p + at.first[v], &f[v]);
-      if (at.second[v] >= 0) store_n<1>(p + at.second[v], &s[v]);
+      f[v] = value_of(r[first(v) / kN], first(v) % kN);
+      s[v] = value_of(r[second(v) / kN], second(v) % kN);
     }
   }
-}
+  __device__ __forceinline__ void store(Window w, int row, const float* f, const float* s) const {
+    float x[8];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      x[first(v)] = f[v];
+      x[second(v)] = s[v];
+    }
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) store_rawn<T, kN>(w, row + at[i], x + i * kN);
+  }
+};
+
+// A wave's own part of LDS, in which its lanes hand over heads: rows 8 values apart in
+// the banks, so that 8 heads' lanes meet in none.
+template <class T, int LANES>
+struct Runs<kStaged, T, LANES> {
+  static constexpr int kPitch = LANES * 8 + 8, kWave = 64 / LANES * kPitch;
+  float* mine;  // 8 neighbours as they lie in memory
+  float* head;  // the lane's head, and its pairs' channels in it
+  int first[4], second[4], at;
+  __device__ __forceinline__ Runs(const Args& a, const Pairs& p, int lane) {
+    __shared__ float staged[4][kWave];
+    head = staged[threadIdx.x / 64] + lane / LANES * kPitch;
+    const int in = lane % LANES;
+    mine = head + in * 8;
+    at = in * 8 < a.d ? in * 8 * (int)sizeof(T) : kNowhere;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      // past the head's end: a slot of its own behind it, which holds zeros
+      first[v] = p.first[v] < 0 ? 2 * pair_at<kStaged, LANES>(in, v) : p.first[v];
+      second[v] = p.second[v] < 0 ? 2 * pair_at<kStaged, LANES>(in, v) + 1 : p.second[v];
+    }
+  }
+  typedef RawN<T, 4> Raw8[2];
+  __device__ __forceinline__ void load(Raw8& r, Window w, int row) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_rawn(r[i], w, row + at + i * 4 * (int)sizeof(T));
+  }
+  static __device__ __forceinline__ void handed() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  __device__ __forceinline__ void values(float* f, float* s, const Raw8& r) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mine[i] = value_of(r[i / 4], i % 4);
+    handed();
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      f[v] = head[first[v]];
+      s[v] = head[second[v]];
+    }
+    handed();
+  }
+  __device__ __forceinline__ void store(Window w, int row, const float* f, const float* s) const {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      head[first[v]] = f[v];
+      head[second[v]] = s[v];
+    }
+    handed();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(mine)[i];
+      const float y[4] = {x.x, x.y, x.z, x.w};
+      store_rawn<T, 4>(w, row + at + i * 4 * (int)sizeof(T), y);
+    }
+    handed();
+  }
+};
 
 // Weights or biases of a lane's channels (`none` where there are none).
 struct Vec {
@@ -243,15 +299,22 @@ __device__ __forceinline__ float normalise(const Args& a, float* f, float* s, co
 template <int NORM>
 constexpr bool kAffine = NORM == kRms || NORM == kLayer;
 
-// A wave's token: its heads, kHeads at a time, q's and then k's. The next heads' rows
-// are asked for before the current ones are computed.
+// A token's row of heads.
+template <class T>
+__device__ __forceinline__ Window heads_of(const void* rows, int64_t token, int64_t ld, int heads, int d) {
+  const T* at = static_cast<const T*>(rows) + token * ld;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)at, (short)0, rows ? heads * d * (int)sizeof(T) : 0, 0x00020000);
+}
+
+// A wave's token: its heads, 2 kHeads of q's and of k's at a time, all of whose rows are
+// asked for before any is computed.
 template <class T, int LANES, Access A, int NORM>
 __global__ __launch_bounds__(256) void forward_kernel(const Args a) {
-  constexpr int kHeads = 64 / LANES;
+  constexpr int kHeads = 64 / LANES, kAhead = 2;
   const int lane = threadIdx.x % 64, head = lane / LANES;
-  const Pairs p = pairs_of<A>(a, lane % LANES);
-  const Rotation<LANES> rot(a, lane);
-  const bool live = p.first[0] >= 0;  // lanes behind a head's end
+  const Pairs p = pairs_of<A, LANES>(a, lane % LANES);
+  const Rotation<A, LANES> rot(a, lane);
+  const Runs<A, T, LANES> runs(a, p, lane);
   Vec w[2], b[2];
   if constexpr (kAffine<NORM>) {
 #pragma unroll
@@ -260,48 +323,49 @@ __global__ __launch_bounds__(256) void forward_kernel(const Args a) {
       b[side] = vec_of(a.s[side].b, p, 0.0f);
     }
   }
+  const int most = a.s[0].heads > a.s[1].heads ? a.s[0].heads : a.s[1].heads, row = a.d * (int)sizeof(T);
   const int64_t step = (int64_t)gridDim.x * 4;
-  for (int64_t token = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; token < a.n; token += step) {
-    const Angles t = rot.at(a, token, lane % LANES);
+  for (int64_t token = (int64_t)blockIdx.x * 4 + delta::uniform(threadIdx.x / 64); token < a.n; token += step) {
+    Window x[2], y[2];
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const Side& sd = a.s[side];
-      if (sd.heads == 0) continue;
-      const T* x = static_cast<const T*>(sd.x) + token * sd.ld;
-      T* y = static_cast<T*>(sd.y) + token * sd.heads * a.d;
-      float f[4] = {0, 0, 0, 0}, s[4] = {0, 0, 0, 0};
-      if (head < sd.heads && live) load8<A>(f, s, x + head * a.d, p);
-      for (int h = head;;) {
-        const bool here = h < sd.heads && live, more = h - head + kHeads < sd.heads;
-        float nf[4] = {0, 0, 0, 0}, ns[4] = {0, 0, 0, 0};
-        if (more && h + kHeads < sd.heads && live) load8<A>(nf, ns, x + (h + kHeads) * a.d, p);
-        if constexpr (NORM != kNone) {
-          const float r = normalise<LANES, NORM>(a, f, s, p);
+      x[side] = heads_of<T>(sd.x, token, sd.ld, sd.heads, a.d);
+      y[side] = heads_of<T>(sd.y, token, (int64_t)sd.heads * a.d, sd.heads, a.d);
+    }
+    const Angles t = rot.at(a, token, lane % LANES);
+    for (int base = 0; base < most; base += kAhead * kHeads) {
+      typename Runs<A, T, LANES>::Raw8 raw[kAhead][2];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            f[v] *= r;
-            s[v] *= r;
-            if constexpr (kAffine<NORM>) {
-              f[v] = f[v] * w[side].f[v] + b[side].f[v];
-              s[v] = s[v] * w[side].s[v] + b[side].s[v];
+      for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+        for (int side = 0; side < 2; ++side) runs.load(raw[j][side], x[side], (base + j * kHeads + head) * row);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          float u[4], z[4];
+          runs.values(u, z, raw[j][side]);
+          if constexpr (NORM != kNone) {
+            const float r = normalise<LANES, NORM>(a, u, z, p);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              u[v] *= r;
+              z[v] *= r;
+              if constexpr (kAffine<NORM>) {
+                u[v] = u[v] * w[side].f[v] + b[side].f[v];
+                z[v] = z[v] * w[side].s[v] + b[side].s[v];
+              }
             }
           }
-        }
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float m = f[v] * t.c[v] - s[v] * t.s[v];
-          s[v] = s[v] * t.c[v] + f[v] * t.s[v];
-          f[v] = m;
+          for (int v = 0; v < 4; ++v) {
+            const float m = u[v] * t.c[v] - z[v] * t.s[v];
+            z[v] = z[v] * t.c[v] + u[v] * t.s[v];
+            u[v] = m;
+          }
+          runs.store(y[side], (base + j * kHeads + head) * row, u, z);
         }
-        if (here) store8<A>(y + h * a.d, f, s, p);
-        if (!more) break;
-        h += kHeads;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          f[v] = nf[v];
-          s[v] = ns[v];
-        }
-      }
     }
   }
 }
@@ -315,50 +379,43 @@ template <class T, int LANES, Access A, int NORM>
 __global__ __launch_bounds__(256) void grad_kernel(const Args a) {
   constexpr int kHeads = 64 / LANES;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, head = lane / LANES;
-  const Pairs p = pairs_of<A>(a, lane % LANES);
-  const Rotation<LANES> rot(a, lane);
-  const bool live = p.first[0] >= 0;
+  const Pairs p = pairs_of<A, LANES>(a, lane % LANES);
+  const Rotation<A, LANES> rot(a, lane);
+  const Runs<A, T, LANES> runs(a, p, lane);
   float dw[2][8], db[2][8];
 #pragma unroll
   for (int side = 0; side < 2; ++side)
 #pragma unroll
     for (int v = 0; v < 8; ++v) dw[side][v] = db[side][v] = 0.0f;
-  Vec ws[2];
+  Vec w[2];
   if constexpr (kAffine<NORM>) {
-    ws[0] = vec_of(a.s[0].w, p, 1.0f);
-    ws[1] = vec_of(a.s[1].w, p, 1.0f);
+    w[0] = vec_of(a.s[0].w, p, 1.0f);
+    w[1] = vec_of(a.s[1].w, p, 1.0f);
   }
   const float inv_d = 1.0f / a.d;
-  for (int64_t token = (int64_t)blockIdx.x * 4 + wave; token < a.n; token += (int64_t)gridDim.x * 4) {
-    const Angles t = rot.at(a, token, lane % LANES);
+  const int most = a.s[0].heads > a.s[1].heads ? a.s[0].heads : a.s[1].heads, row = a.d * (int)sizeof(T);
+  const int64_t step = (int64_t)gridDim.x * 4;
+  for (int64_t token = (int64_t)blockIdx.x * 4 + delta::uniform(threadIdx.x / 64); token < a.n; token += step) {
+    Window x[2], dy[2], dx[2];
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const Side& sd = a.s[side];
-      if (sd.heads == 0) continue;
-      const Vec& w = ws[side];
-      const T* x = static_cast<const T*>(sd.x) + token * sd.ld;
-      const T* dy = static_cast<const T*>(sd.dy) + token * sd.heads * a.d;
-      T* dx = static_cast<T*>(sd.y) + token * sd.heads * a.d;
-      float xf[4] = {0, 0, 0, 0}, xs[4] = {0, 0, 0, 0}, yf[4] = {0, 0, 0, 0}, ys[4] = {0, 0, 0, 0};
-      if (head < sd.heads && live) {
-        if constexpr (NORM != kNone) load8<A>(xf, xs, x + head * a.d, p);
-        load8<A>(yf, ys, dy + head * a.d, p);
-      }
-      for (int h = head;;) {
-        const bool here = h < sd.heads && live, more = h - head + kHeads < sd.heads;
-        float f[4], s[4], ef[4], es[4];
+      x[side] = heads_of<T>(sd.x, token, sd.ld, sd.heads, a.d);
+      dy[side] = heads_of<T>(sd.dy, token, (int64_t)sd.heads * a.d, sd.heads, a.d);
+      dx[side] = heads_of<T>(sd.y, token, (int64_t)sd.heads * a.d, sd.heads, a.d);
+    }
+    const Angles t = rot.at(a, token, lane % LANES);
+    for (int base = 0; base < most; base += kHeads) {
+      typename Runs<A, T, LANES>::Raw8 rx[2], ry[2];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          f[v] = xf[v];
-          s[v] = xs[v];
-          ef[v] = yf[v];
-          es[v] = ys[v];
-          xf[v] = xs[v] = yf[v] = ys[v] = 0.0f;
-        }
-        if (more && h + kHeads < sd.heads && live) {
-          if constexpr (NORM != kNone) load8<A>(xf, xs, x + (h + kHeads) * a.d, p);
-          load8<A>(yf, ys, dy + (h + kHeads) * a.d, p);
-        }
+      for (int side = 0; side < 2; ++side) {
+        if constexpr (NORM != kNone) runs.load(rx[side], x[side], (base + head) * row);
+        runs.load(ry[side], dy[side], (base + head) * row);
+      }
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        float ef[4], es[4];
+        runs.values(ef, es, ry[side]);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float m = ef[v] * t.c[v] + es[v] * t.s[v];
@@ -366,22 +423,23 @@ __global__ __launch_bounds__(256) void grad_kernel(const Args a) {
           ef[v] = m;
         }
         if constexpr (NORM != kNone) {
-          const float r = normalise<LANES, NORM>(a, f, s, p);
+          float f[4], s[4];
+          runs.values(f, s, rx[side]);
+          float r = normalise<LANES, NORM>(a, f, s, p);
           const bool clamped = NORM == kL2 && r >= 1.0f / a.eps;
+          r = base + head < a.s[side].heads ? r : 0.0f;  // no head: nothing to the sums, whatever eps
           float along = 0.0f, mean = 0.0f;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             f[v] *= r;
             s[v] *= r;
-            if (kAffine<NORM> && a.part && here) {
+            if constexpr (kAffine<NORM>) {
               db[side][v] += ef[v];
               db[side][4 + v] += es[v];
               dw[side][v] += ef[v] * f[v];
               dw[side][4 + v] += es[v] * s[v];
-            }
-            if constexpr (kAffine<NORM>) {
-              ef[v] *= w.f[v];
-              es[v] *= w.s[v];
+              ef[v] *= w[side].f[v];
+              es[v] *= w[side].s[v];
             }
             along += ef[v] * f[v] + es[v] * s[v];
             mean += ef[v] + es[v];
@@ -399,9 +457,7 @@ __global__ __launch_bounds__(256) void grad_kernel(const Args a) {
             es[v] = (es[v] - s[v] * along - mean) * r;
           }
         }
-        if (here && sd.y) store8<A>(dx + h * a.d, ef, es, p);
-        if (!more) break;
-        h += kHeads;
+        runs.store(dx[side], (base + head) * row, ef, es);
       }
     }
   }
@@ -455,23 +511,19 @@ __global__ __launch_bounds__(256) void sum_kernel(const float* part, int blocks,
 
 bool aligned(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-// Runs of 4 or 2 channels need each axis's channels, the heads and the rows to be
-// multiples of them, and rows to start at a run's alignment.
+// Runs of 4 values need rows and heads that keep their alignment, and pairs a half
+// apart also axes of multiples of 4 pairs.
 Access access(const Args& a, size_t value) {
-  int run = a.d % 8 == 0 ? 4 : a.d % 4 == 0 ? 2 : 1;
-  const bool halves = a.rotated > 0 && !a.interleaved;
-  if (halves && a.per_axis)
-    for (int i = 0; i < a.axes; ++i)
-      while (a.pairs[i] % run) run /= 2;
-  else if (halves)
-    while (a.rotated % run) run /= 2;
+  bool rows = a.d % 8 == 0;
   for (int i = 0; i < 2; ++i) {
     const Side& s = a.s[i];
-    if (s.heads == 0) continue;
-    while (s.ld % run || !aligned(s.x, run * value) || !aligned(s.y, run * value) || !aligned(s.dy, run * value)) run /= 2;
+    if (s.heads) rows = rows && s.ld % 4 == 0 && aligned(s.x, 4 * value) && aligned(s.y, 4 * value) && aligned(s.dy, 4 * value);
   }
-  if (!halves) return run == 4 ? kNeighbours : kSingle;
-  return run == 4 ? kFours : run == 2 ? kTwos : kSingle;
+  if (!rows) return kSingle;
+  if (a.rotated == 0 || a.interleaved) return kNeighbours;
+  bool fours = a.per_axis || a.rotated % 4 == 0;
+  for (int i = 0; i < a.axes && a.per_axis; ++i) fours = fours && a.pairs[i] % 4 == 0;
+  return fours ? kFours : kStaged;
 }
 
 template <class T, int LANES, Access A, int NORM, bool GRAD>
@@ -506,10 +558,10 @@ void by_access(const Args& a, int blocks, hipStream_t s) {
   const Access how = access(a, sizeof(T));
   if (how == kFours)
     by_lanes<T, kFours, GRAD>(a, blocks, s);
-  else if (how == kTwos)
-    by_lanes<T, kTwos, GRAD>(a, blocks, s);
   else if (how == kNeighbours)
     by_lanes<T, kNeighbours, GRAD>(a, blocks, s);
+  else if (how == kStaged)
+    by_lanes<T, kStaged, GRAD>(a, blocks, s);
   else
     by_lanes<T, kSingle, GRAD>(a, blocks, s);
 }

@@ -156,19 +156,18 @@ def test_odd_heads(d, norm, dtype):
 
 
 def test_slices_of_a_projection():
-    # q and k as columns of one wider tensor, at offsets that are and are not multiples of 16 bytes
+    # q and k as columns of one wider tensor, at offsets that are and are not multiples of 16 bytes (other accesses, and
+    # another order of a head's sums)
     for off in (0, 8, 2, 1):
         c = _case(50, 4, 2, 64, "bf16", "rms", (16, 16), True, False, seed=off)
         wide = torch.randn(50, 1000, device="cuda").bfloat16()
         q, k = wide[:, off:off + 256], wide[:, 300 + off:300 + off + 128]
         q.copy_(c["q"])
         k.copy_(c["k"])
-        a, b = _forward(c)
         c2 = dict(c, q=q, k=k)
-        a2, b2 = _forward(c2)
-        assert torch.equal(a, a2) and torch.equal(b, b2) and a2.is_contiguous()
-        g, g2 = _grad(c), _grad(c2)
-        assert all(torch.equal(x, y) for x, y in zip(g, g2) if x is not None)
+        a, b = _check(c2)
+        assert a.is_contiguous() and b.is_contiguous()
+        _check_grad(c2)
     with pytest.raises(ValueError, match="neighbours"):
         _forward(dict(c, q=torch.randn(256, 50, device="cuda").bfloat16().t()))
     with pytest.raises(ValueError, match="apart"):
