@@ -601,16 +601,22 @@ hipError_t launch_back(const Args& a, const Plan& p, bool bf16, hipStream_t stre
 
 size_t matrix_bytes(bool keep) { return matrices_bytes(keep); }
 
-// Pieces as long as fill the GPU with waves (a wave a SIMD where they are wide, two
-// with their few registers otherwise), at least 4 chunks, and only where sequences are
-// much longer than that: a cut costs a pass over all pieces, with d_k more columns.
+// Wide waves pay where they alone fill the GPU: against narrow ones a 100-view scene
+// takes 1020 us (1460), 48 views' gradient 1390 (1650), 24 views in fp32 463 (496), and
+// 12 views with heads of 128, below the limit, 956 (690). Pieces are as long as fill the
+// GPU with waves (one a SIMD where they are wide: 1020 us for the scene, with half or
+// twice as many 1090; half as many narrow ones: 690 us with heads of 128, with one a SIMD
+// 1050), at least 3 chunks (one view's gradient 158 us; of 2: 180, of 4: 167). Sequences
+// are cut only where much longer than that, since a cut costs a pass over all pieces
+// with d_k more columns (48 views of 48 sequences uncut 1390 us, cut 1640; 24 views in
+// 10 sequences cut 463, uncut 1170).
 Plan plan(int64_t n, int nseq, int64_t longest, int hv, int dk, int dv) {
   const int64_t chunks = (n + kChunk - 1) / kChunk, rows = (int64_t)hv * (dv / 64);
   Plan p;
   p.wide = chunks * rows >= 16384;
   const int64_t waves = p.wide ? 1024 : 512;
   int64_t each = (chunks * rows + waves - 1) / waves;
-  if (each < 4) each = 4;
+  if (each < 3) each = 3;
   p.split = longest > each * kChunk * 5 / 2;
   p.per = p.split ? each * kChunk : (n / kChunk + 1) * kChunk;
   p.pieces = n / p.per + nseq;
