@@ -11,27 +11,12 @@
 namespace vggt3 {
 namespace delta {
 
-// Parts of an operand that holds fp32 values whole, and its 16-byte pieces.
+// Parts of an operand that holds fp32 values whole.
 template <class T>
 constexpr int kWhole = sizeof(T) == 2 ? 3 : 1;
-template <class T>
-constexpr int kOperand = 64 * (sizeof(T) == 2 ? 3 : 2);
 // Rows of D values in LDS, 16 bytes apart in the banks.
 template <class T, int D>
 constexpr int kPitch = D + 16 / (int)sizeof(T);
-
-// Rows 0 .. len - 1 of src, `ld` apart, to LDS, zeros behind them, by COUNT threads.
-template <class T, int D, int COUNT>
-__device__ __forceinline__ void stage(T* dst, const T* src, int64_t ld, int len, int thread) {
-  constexpr int kPiece = 16 / sizeof(T), kPieces = D / kPiece;
-#pragma unroll
-  for (int x = 0; x < kChunk * kPieces / COUNT; ++x) {
-    const int at = x * COUNT + thread, row = at / kPieces, col = at % kPieces * kPiece;
-    u32x4 w = {0, 0, 0, 0};
-    if (row < len) w = ld16(src + row * ld + col);
-    st16(dst + row * kPitch<T, D> + col, w);
-  }
-}
 
 // The gates that a chunk's columns use, by token. Its decay up to a token is
 // 2^(high + low): high a multiple of 2^-6, so that sums and differences of it are
@@ -246,36 +231,6 @@ __device__ __forceinline__ void unit_state(f32x4 (*S)[NCT], int col, int q) {
 #pragma unroll
       for (int x = 0; x < NCT; ++x) S[t][x][r] = channel(t, 4 * q + r) == col + x ? 1.0f : 0.0f;
 }
-// Rows of a chunk's values, 0 behind its end.
-template <int NCT, class T>
-__device__ __forceinline__ void load_rows(f32x4 (*V)[NCT], const T* from, int64_t ld, int len, int q) {
-#pragma unroll
-  for (int it = 0; it < 2; ++it)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * it + 4 * q + r;
-      float w[NCT];
-#pragma unroll
-      for (int x = 0; x < NCT; ++x) w[x] = 0.0f;
-      if (row < len) load_n<NCT>(w, from + row * ld);
-#pragma unroll
-      for (int x = 0; x < NCT; ++x) V[it][x][r] = w[x];
-    }
-}
-template <int NCT, class T>
-__device__ __forceinline__ void store_rows(T* to, const f32x4 (*V)[NCT], int64_t ld, int len, int q) {
-#pragma unroll
-  for (int it = 0; it < 2; ++it)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * it + 4 * q + r;
-      float w[NCT];
-#pragma unroll
-      for (int x = 0; x < NCT; ++x) w[x] = V[it][x][r];
-      if (row < len) store_n<NCT>(to + row * ld, w);
-    }
-}
-
 __device__ __forceinline__ Tri turned(const Tri& m, int lane) {
   return Tri{turned(m.t00, lane), turned(m.t10, lane), turned(m.t11, lane)};
 }

@@ -16,8 +16,15 @@
 // A wave has 64 value channels of a chunk and head, 4 neighbours a lane (u, x, o and the
 // row sums, in fp32 values whole), then F and E, then its share of the key channels
 // (dQ, dK, from operands in two bf16 parts). u and dR change from columns by lane to
-// rows by lane through LDS; the triangles stay in registers. (Four waves of 16 columns
-// to a chunk convert each triangle four times over: 1300 us against 48 views.)
+// rows by lane through LDS; the triangles stay in registers.
+//
+// 48 views (65,952 tokens), 16 heads of 64 x 64 in bf16: 785 us, where four waves of 16
+// columns, which convert each triangle four times over, took 1300. The wave fills a
+// SIMD's registers, so nothing runs while it waits: S and dS are read once by columns
+// and once by rows, and of the second reading half comes from memory again (3.1 GB
+// fetched, 2.0 needed). Turning both in LDS instead saves that but takes 1070 us (its
+// writes and conflicts, and 45 registers spilled), asking for the next chunk's lines
+// ahead 950 (the L2 has no room for them).
 #include <type_traits>
 
 #include "delta_chunk.hpp"
@@ -477,29 +484,29 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
       if (a.dbeta) a.dbeta[(p.first + lane) * a.hv + h] = s;
     }
   }
-
 }
 
 // dq, dk of key heads that several value heads share, in the heads' order. Rows of
 // no sequence are left as they are.
 template <class T>
 __global__ __launch_bounds__(256) void group_kernel(const Args a) {
-  const uint32_t row = blockIdx.x;
-  bool inside = a.cu == nullptr;
-  for (int b = threadIdx.x; !inside && b < a.nseq; b += 256)
-    inside = row >= bound(a.cu, b, a.n) && row < bound(a.cu, b + 1, a.n);
-  if (!__syncthreads_or(inside)) return;
   const int group = a.hv / a.hk, width = a.hk * a.dk;
   const float* from = blockIdx.y ? a.dk_part : a.dq_part;
   T* to = static_cast<T*>(blockIdx.y ? a.dk_out : a.dq);
-  if (from == nullptr || to == nullptr) return;
-  for (int i = 4 * threadIdx.x; i < width; i += 1024) {
-    const int kh = i / a.dk, ch = i % a.dk;
-    f32x4 s = zero4();
-    for (int g = 0; g < group; ++g)
-      s += *reinterpret_cast<const f32x4*>(from + ((int64_t)row * a.hv + kh * group + g) * a.dk + ch);
-    const float w[4] = {s[0], s[1], s[2], s[3]};
-    store_n<4>(to + (int64_t)row * width + i, w);
+  if (to == nullptr) return;
+  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+    bool inside = a.cu == nullptr;
+    for (int b = threadIdx.x; !inside && b < a.nseq; b += 256)
+      inside = row >= bound(a.cu, b, a.n) && row < bound(a.cu, b + 1, a.n);
+    if (!__syncthreads_or(inside)) continue;
+    for (int i = 4 * threadIdx.x; i < width; i += 1024) {
+      const int kh = i / a.dk, ch = i % a.dk;
+      f32x4 s = zero4();
+      for (int g = 0; g < group; ++g)
+        s += *reinterpret_cast<const f32x4*>(from + (row * a.hv + kh * group + g) * a.dk + ch);
+      const float w[4] = {s[0], s[1], s[2], s[3]};
+      store_n<4>(to + row * width + i, w);
+    }
   }
 }
 
@@ -513,7 +520,7 @@ hipError_t grad_of(const Args& a, hipStream_t s) {
   hipError_t e = a.dk == 64 ? (a.dv == 64 ? run<T, 64, 64>(a, s) : run<T, 64, 128>(a, s))
                             : (a.dv == 64 ? run<T, 128, 64>(a, s) : run<T, 128, 128>(a, s));
   if (e != hipSuccess || a.dq_part == nullptr || (a.dq == nullptr && a.dk_out == nullptr)) return e;
-  group_kernel<T><<<dim3((unsigned)a.n, 2), 256, 0, s>>>(a);
+  group_kernel<T><<<dim3((unsigned)(a.n < 65536 ? a.n : 65536), 2), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -102,36 +102,12 @@ __device__ __forceinline__ void make(Frag<uint16_t>& f, f32x4 x, f32x4 y) {
   }
 }
 
-// Operands through LDS: 16 bytes a lane for each part (fp32: for each half).
-template <int P>
-__device__ __forceinline__ void put(u32x4* at, const Frag<uint16_t>& f, int lane) {
-#pragma unroll
-  for (int p = 0; p < P; ++p) at[64 * p + lane] = as_u32x4(f.part[p]);
-}
-template <int P>
-__device__ __forceinline__ void put(u32x4* at, const Frag<float>& f, int lane) {
-  at[lane] = __builtin_bit_cast(u32x4, f.a);
-  at[64 + lane] = __builtin_bit_cast(u32x4, f.b);
-}
-template <int P>
-__device__ __forceinline__ void get(Frag<uint16_t>& f, const u32x4* at, int lane) {
-#pragma unroll
-  for (int p = 0; p < P; ++p) f.part[p] = as_bf16x8(at[64 * p + lane]);
-}
-template <int P>
-__device__ __forceinline__ void get(Frag<float>& f, const u32x4* at, int lane) {
-  f.a = __builtin_bit_cast(f32x4, at[lane]);
-  f.b = __builtin_bit_cast(f32x4, at[64 + lane]);
-}
-
 // 8 values of a row, at a 16-byte boundary.
 __device__ __forceinline__ void row8(Frag<uint16_t>& f, const uint16_t* p) { f.part[0] = ld_op(p); }
 __device__ __forceinline__ void row8(Frag<float>& f, const float* p) {
   f.a = *reinterpret_cast<const f32x4*>(p);
   f.b = *reinterpret_cast<const f32x4*>(p + 4);
 }
-__device__ __forceinline__ void clear(Frag<uint16_t>& f) { f.part[0] = as_bf16x8(u32x4{0, 0, 0, 0}); }
-__device__ __forceinline__ void clear(Frag<float>& f) { f.a = f.b = zero4(); }
 
 // A head's channels are the rows of its state's tiles in an order in which 8
 // neighbours are an operand's 8 elements: row p of tile t is channel
@@ -159,24 +135,18 @@ __device__ __forceinline__ void state_rows(Frag<float>& f, const float* x, int t
   }
 }
 // X as a right operand over the chunk's tokens: lane c has channel base + N c + n (of N
-// neighbours). bf16: N = 1 by transposing reads; otherwise value by value, since a
-// lane's channels are not neighbours of the next lane's.
+// neighbours). bf16: value by value, since a lane's channels are not neighbours of the
+// next lane's.
 template <int N, int PITCH>
 __device__ __forceinline__ void token_columns(Frag<uint16_t>& f, const uint16_t* x, int base, int n, int lane) {
-  const int c = lane % 16, q = lane / 16;
-  if constexpr (N == 1) {
-    const uint16_t* p = x + (4 * q + c / 4) * PITCH + base + 4 * (c % 4);
-    f.part[0] = tr_op(p, p + 16 * PITCH);
-  } else {
-    const uint16_t* p = x + 4 * q * PITCH + base + N * c + n;
-    u32x4 w;
+  const uint16_t* p = x + 4 * (lane / 16) * PITCH + base + N * (lane % 16) + n;
+  u32x4 w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint16_t* r = p + (16 * (i / 2) + 2 * (i % 2)) * PITCH;
-      w[i] = (uint32_t)r[0] | (uint32_t)r[PITCH] << 16;
-    }
-    f.part[0] = as_bf16x8(w);
+  for (int i = 0; i < 4; ++i) {
+    const uint16_t* r = p + (16 * (i / 2) + 2 * (i % 2)) * PITCH;
+    w[i] = (uint32_t)r[0] | (uint32_t)r[PITCH] << 16;
   }
+  f.part[0] = as_bf16x8(w);
 }
 template <int N, int PITCH>
 __device__ __forceinline__ void token_columns(Frag<float>& f, const float* x, int base, int n, int lane) {

@@ -23,6 +23,14 @@
 // a value-free run that starts from the unit matrix), join_kernel goes through the
 // pieces, and the main pass starts each piece from its own first state. (A
 // sequence's first piece starts from the sequence's first state in both passes.)
+//
+// 100 views (137,400 tokens) as one sequence, 16 heads of 64 x 64 in bf16: 183 us for
+// the matrices (1.06 GB, 5.8 TB/s: memory), 460 to 540 for the summary, 55 for the join,
+// 370 for the main pass. The scans are bound by vector instructions: fp32 values are cut
+// into 3 bf16 parts before each product (48 views' states: 34 million vector
+// instructions of 4 cycles, 4.8 million products of 16), and with one wave a SIMD, whose
+// registers 64 columns of S fill, neither hides the other. Two waves a SIMD of 32
+// columns, interleaved products, or S held in parts were not faster.
 #include "delta_chunk.hpp"
 
 namespace vggt3 {

@@ -6,7 +6,8 @@
 // so one pass over S gives both sums over its rows, S^T k and S^T q, and the pass
 // that stores S' needs none. Bound by the state, read once and written once. A
 // workgroup holds 64 columns of one head's state in registers, 4 columns and every
-// 16th row a thread (16 bytes a load, 256 contiguous a row).
+// 16th row a thread (16 bytes a load, 256 contiguous a row). 256 streams of 16 heads of
+// 64 x 64: 24.7 us, 5.5 TB/s, a copy's rate; one stream 9 us, a call's host time.
 #include "delta.hpp"
 #include "delta_ops.hpp"
 

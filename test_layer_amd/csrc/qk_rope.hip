@@ -11,9 +11,9 @@
 // frequencies and weights over all tokens. A lane holds both channels of 4 pairs, so
 // that a rotation is its own, and the norm's sums over a head are a few DPP
 // steps over 8 to 64 lanes. 100 views of 16 + 16 heads of 64 in bf16: 214 us,
-// 5.3 TB/s, a copy's rate; 48 views' gradient 158 us. Angles are formed in 64 bits (in 32 a position of a
-// million is off by 0.06 of a radian) and reduced to a turn before the sine, one
-// pair a lane, and handed to the lanes that hold the pair.
+// 5.3 TB/s, a copy's rate; 48 views' gradient 158 us. Angles are formed in 64 bits (in
+// 32 a position of a million is off by 0.06 of a radian) and reduced to a turn before the
+// sine, one pair a lane, and handed to the lanes that hold the pair.
 #include "qk.hpp"
 
 #include "delta_ops.hpp"

@@ -184,7 +184,8 @@ def test_forward_without_gate_or_state(gate, state, dtype):
     _check_forward(_case([70, 40], 3, 1, 64, 64, dtype, gate, state, 5))
 
 
-# Sequences long enough to be cut into pieces (of 4 chunks = 128 tokens at these sizes), with piece ends inside a chunk.
+# Sequences long enough to be cut into pieces (of 3 chunks = 96 tokens at these sizes, where longer than 240), with piece ends
+# inside a chunk.
 LONG = [[129], [128], [700], [300, 0, 1, 513, 40], [1374]]
 
 
@@ -221,6 +222,48 @@ def test_grad_in_pieces(lens, dk, dv, dtype):
 @pytest.mark.parametrize("gate,state", [(False, True), (True, False), (False, False)])
 def test_grad_without_gate_or_state(gate, state, dtype):
     _check_grad(_case([150, 40], 2, 3, 64, 64, dtype, gate, state, 6), 0.5)
+
+
+def _copies(c, times):
+    """The case with its heads `times` over."""
+    def t(x, heads):
+        return None if x is None else x.reshape(len(x), heads, -1).repeat(1, times, 1).flatten(1)
+
+    hk, (hv, dk, dv) = c["heads"], c["dims"]
+    m = dict(c, heads=hk * times, dims=(hv * times, dk, dv))
+    for name, heads in (("q", hk), ("k", hk), ("v", hv), ("do", hv), ("g", hv), ("beta", hv)):
+        m[name] = t(c[name], heads)
+    for name in ("state", "dstate"):
+        m[name] = None if c[name] is None else c[name].repeat(1, times, 1, 1)
+    return m
+
+
+# Enough chunks x heads for waves of 64 columns (32 where d_k is 128), with sequences that are cut and that are not.
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("lens", [[1450, 5, 0, 700], [1050, 1051]], ids=str)
+def test_many_heads_in_wide_waves(lens, dk, dv, dtype, monkeypatch):
+    one = _case(lens, 1, 2 if dk != dv else 1, dk, dv, dtype, seed=dk + dv)
+    times = 256 * 64 // dv // one["dims"][0]
+    many = _copies(one, times)
+    n, (hv, _, _), hk = one["n"], one["dims"], 1
+
+    def first(x, heads):  # every copy's bits are the first one's
+        if x.dim() == 4:
+            y = x.reshape(len(x), times, heads, dk, dv)
+        else:
+            y = x.reshape(n, times, heads, -1)
+        assert torch.equal(y, y[:, :1].expand_as(y))
+        return y[:, 0].contiguous() if x.dim() == 4 else y[:, 0].flatten(1)
+
+    o, S = _forward(many)
+    got = _grad(many)
+    heads = dict(dq=hk, dk=hk, dv=hv, dg=hv, dbeta=hv, dstate=hv)
+    monkeypatch.setattr(tla, "gated_delta", lambda *a, **k: (first(o, hv), first(S, hv)))
+    monkeypatch.setattr(tla, "gated_delta_grad",
+                        lambda *a, **k: tla.GatedDeltaGrads(*[first(t, heads[name]) for name, t in got._asdict().items()]))
+    _check_forward(one)
+    _check_grad(one)
 
 
 def test_many_heads_and_a_whole_view():
