@@ -628,8 +628,9 @@ int vggt3_block_join_grad(const void* r, const void* f, const void* gate, int64_
  *               first 2 * sum channels, pairs to axes in their order.
  *   interleaved != 0: pair j is channels 2j and 2j + 1 (of its axis's channels, or of
  *               all); 0: channels j and size + j.
- * All arithmetic but the angles is fp32; every output is rounded once. d_head at most 512, of any
- * count (sections and heads that are multiples of 4 channels are faster).
+ * All arithmetic but the angles is fp32; every output is rounded once. d_head at most
+ * 512, of any count (multiples of 8, with rows that start at multiples of 4 values, are
+ * faster).
  * n_tokens == 0 is a no-op.
  */
 enum { VGGT3_NORM_L2 = 3 };
@@ -679,8 +680,8 @@ int vggt3_qk_norm_rope_grad(const void* q, int64_t q_stride, const void* k, int6
  *   cu_seqlens   NULL (one sequence) or DEVICE int32 [n_seqs + 1]: sequence b is rows
  *                cu[b] .. cu[b + 1] - 1, empty ones included. Rows of no sequence are
  *                neither read nor written. (Boundaries outside 0 .. n_tokens count as
- *                the nearer of the two, a sequence that ends before it begins as empty; sequences
- *                must not share rows.)
+ *                the nearer of the two, a sequence that ends before it begins as empty;
+ *                sequences must not share rows.)
  *   max_seqlen   the longest sequence's length, or 0 if unknown. Only how the work is
  *                cut depends on it: a wrong one costs time, not results beyond rounding.
  *   state, state_out   float32 [n_seqs][n_heads_v][d_k][d_v]: S before each
@@ -689,9 +690,9 @@ int vggt3_qk_norm_rope_grad(const void* q, int64_t q_stride, const void* k, int6
  *   workspace    at least vggt3_gated_delta_workspace_bytes(...) bytes.
  * Computed by chunks of 32 tokens (the same values by matrix products): S, decays,
  * sums and the chunk's triangular inverse are fp32 (bf16 dtype: products of fp32 values
- * in three bf16 parts; two for o), o is rounded once. A value that is not finite makes its sequence's
- * results not finite from its chunk on, other sequences' not at all. Heads of 64 or
- * 128 each way. The results are the same bits each time. Outputs and the workspace must
+ * in three bf16 parts; two for o), o is rounded once. A value that is not finite may
+ * make its head's results in its sequence not finite from its chunk on, others' not at
+ * all. Heads of 64 or 128 each way. The results are the same bits each time. Outputs and the workspace must
  * not overlap anything else. n_tokens == 0 copies state to state_out.
  */
 size_t vggt3_gated_delta_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int64_t max_seqlen, int32_t n_heads,

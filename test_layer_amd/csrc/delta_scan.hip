@@ -480,11 +480,12 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void back_k
 // First states of a sequence's pieces, in seg_n's place: S <- M S + R from piece to
 // piece (BACK: from the last piece to the first). One step waits for the one before, so
 // it is cut short: DK / 16 waves share 16 columns, a wave has 16 rows of the products
-// (in fp32 for both types: they are few) and its rows of the next M and R at hand, and
-// the new S goes round through LDS.
+// (in fp32 for both types: they are few) and its rows of the next 4 pieces' M and R at
+// hand, and the new S goes round through LDS. 64 pieces 54 us (the next piece's alone:
+// 60), most of it the 16 products one after the other.
 template <int DK, int DV, bool BACK>
 __global__ __launch_bounds__(4 * DK) void join_kernel(const Args a) {
-  constexpr int kSteps = DK / 32;
+  constexpr int kSteps = DK / 32, kAhead = 4;
   __shared__ f32x4 rows[2][DK / 16][64];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int c = lane % 16, q = lane / 16;
@@ -502,42 +503,56 @@ __global__ __launch_bounds__(4 * DK) void join_kernel(const Args a) {
   const int64_t first = sid + (BACK ? segs - 1 : 0);
   float* np = a.seg_n + (first * a.hv + h) * DK * DV + own;
   const float* mp = a.seg_m + (first * a.hv + h) * DK * DK + mine;
-  f32x4 S = zero4(), R[2];
-  Frag<float> M[2][kSteps];
+  f32x4 S = zero4(), R[kAhead];
+  Frag<float> M[kAhead][kSteps];
   const auto load = [&](f32x4& R, Frag<float>* M, int i) {
+    i = min(i, segs - 1);  // (behind the last piece: anything)
 #pragma unroll
     for (int r = 0; r < 4; ++r) R[r] = np[i * nstep + r * DV];
-    if (i == 0) return;  // the first piece was run from the given state
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) row8(M[s], mp + i * mstep + 32 * s);
+  };
+  const auto store = [&](int i) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) np[i * nstep + r * DV] = S[r];
+  };
+  const auto step = [&](const f32x4& R, const Frag<float>* M, int i) {
+    rows[i & 1][wave][lane] = S;
+    __syncthreads();
+    S = R;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      Frag<float> f;
+      make<1>(f, rows[i & 1][2 * s][lane], rows[i & 1][2 * s + 1][lane]);
+      S = mm<1, 1>(M[s], f, S);
+    }
   };
   if (from) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) S[r] = from[((int64_t)b * a.hv + h) * DK * DV + own + r * DV];
   }
-  load(R[0], M[0], 0);
-  const auto step = [&](const f32x4& R, const Frag<float>* M, f32x4& Rn, Frag<float>* Mn, int i) {
-    if (i + 2 < segs) load(Rn, Mn, i + 1);
+  // the first piece was run from the given state
+  f32x4 next;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) np[i * nstep + r * DV] = S[r];
-    if (i + 1 == segs) return;
-    if (i > 0) {
-      rows[i & 1][wave][lane] = S;
-      __syncthreads();
-      S = R;
+  for (int r = 0; r < 4; ++r) next[r] = np[r * DV];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        Frag<float> f;
-        make<1>(f, rows[i & 1][2 * s][lane], rows[i & 1][2 * s + 1][lane]);
-        S = mm<1, 1>(M[s], f, S);
-      }
-    } else {
-      S = R;
+  for (int j = 0; j < kAhead; ++j) load(R[j], M[j], 1 + j);
+  store(0);
+  S = next;
+  int i = 1;
+  for (; i + kAhead < segs; i += kAhead) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      store(i + j);
+      step(R[j], M[j], i + j);
+      load(R[j], M[j], i + j + kAhead);
     }
-  };
-  for (int i = 0; i < segs; i += 2) {
-    step(R[0], M[0], R[1], M[1], i);
-    if (i + 1 < segs) step(R[1], M[1], R[0], M[0], i + 1);
+  }
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    if (i + j >= segs) break;
+    store(i + j);
+    if (i + j + 1 < segs) step(R[j], M[j], i + j);
   }
 }
 

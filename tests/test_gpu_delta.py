@@ -271,6 +271,27 @@ def test_many_heads_and_a_whole_view():
     _check_grad(_case([400, 333], 16, 1, 64, 64, "bf16", seed=2))
 
 
+def test_shared_heads_over_many_rows():
+    # a shared key head's gradients are the sums, in their order, of those of as many key heads of the same rows
+    c = _case([40000, 0, 26001], 1, 2, 64, 64, "f32", seed=7, behind=5)
+    got = _grad(c)
+    apart = _grad(dict(c, q=c["q"].repeat(1, 2), k=c["k"].repeat(1, 2), heads=2))
+    n = c["n"]
+    for name in ("dq", "dk"):
+        a = getattr(apart, name)[:n]
+        assert torch.equal(getattr(got, name)[:n], a[:, :64] + a[:, 64:]), name
+    assert torch.equal(got.dv[:n], apart.dv[:n]) and torch.equal(got.dbeta[:n], apart.dbeta[:n])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_thousands_of_sequences(dtype):
+    lens = np.random.default_rng(8).integers(0, 3, 5000).tolist()
+    lens[4100] = 70
+    c = _case(lens, 1, 1, 64, 64, dtype, state=False, seed=8)
+    _check_forward(c)
+    _check_grad(c)
+
+
 def test_a_head_is_its_own():
     c = _case([200, 77], 3, 2, 64, 64, "bf16", seed=3)
     o, S = _forward(c)
