@@ -877,11 +877,19 @@ def _rows_of(name: str, t: Optional[torch.Tensor]):
         return None, 0
     if t.get_device() < 0:
         raise ValueError("tensors must live on the GPU (HIP device memory)")
+    if t.is_contiguous():
+        return (t.data_ptr() if t.numel() else None), t.shape[1]
     if t.numel() == 0:
         return None, t.shape[1]
     if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
         raise ValueError(f"{name}: the channels of a row must be neighbours and rows apart, strides {t.stride()}")
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _check_gpu(dev: int, *ts) -> None:
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors live on different devices: cuda:{dev} and cuda:{t.get_device()}")
 
 
 def _qk_inputs(q, k, n_heads, n_heads_k, pos, sections, weights):
@@ -894,15 +902,16 @@ def _qk_inputs(q, k, n_heads, n_heads_k, pos, sections, weights):
         if k.shape[0] != q.shape[0] or k.dtype != q.dtype:
             raise ValueError(f"k {tuple(k.shape)} {k.dtype} does not match q {tuple(q.shape)} {q.dtype}")
         _heads_of("k", k, hk, d)
-    sections = tuple(int(c) for c in sections)
+    sections = tuple(map(int, sections))
     if bool(sections) != (pos is not None):
         raise ValueError("pos and sections go together")
     if pos is not None and (pos.dtype != torch.int32 or tuple(pos.shape) != (q.shape[0], len(sections))):
         raise ValueError(f"pos {tuple(pos.shape)} {pos.dtype}, {(q.shape[0], len(sections))} int32 expected")
     for name, w in weights.items():
-        _check_f32(name, w, d)
-        if w is not None and k is None and name.startswith("k"):
-            raise ValueError(f"{name} without k")
+        if w is not None:
+            _check_f32(name, w, d)
+            if k is None and name.startswith("k"):
+                raise ValueError(f"{name} without k")
     return d, hk, sections
 
 
@@ -937,8 +946,8 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], n_heads: int, n_hea
     _check_same("k_out", k_out, k, "k")
     pq, sq = _rows_of("q", q)
     pk, sk = _rows_of("k", k)
-    dev, (_, _, qw, qb, kw, kb, pp, po, ko) = _pointers(q[:0], None if k is None else k[:0], q_w, q_b, k_w, k_b, pos, q_out,
-                                                        k_out)
+    dev, (qw, qb, kw, kb, pp, po, ko) = _pointers(q_w, q_b, k_w, k_b, pos, q_out, k_out)
+    _check_gpu(dev, q, k)
     _run("vggt3_qk_norm_rope", dev, pq, sq, pk, sk, kind, qw, qb, kw, kb, float(eps), pp,
          _sections_ptr(sections), len(sections), float(base), int(bool(per_axis)), int(bool(interleaved)), po, ko, n,
          n_heads, hk, d, _dtype_code(q))
@@ -996,8 +1005,8 @@ def qk_norm_rope_grad(q: torch.Tensor, k: Optional[torch.Tensor], dq_out: torch.
     workspace, nb = _ws(workspace, need, q.device)
     pq, sq = _rows_of("q", q)
     pk, sk = _rows_of("k", k)
-    dev, (_, _, dqo, dko, qw, kw, pp, ws, *grads) = _pointers(q[:0], None if k is None else k[:0], dq_out, dk_out, q_w, k_w,
-                                                              pos, workspace, *out)
+    dev, (dqo, dko, qw, kw, pp, ws, *grads) = _pointers(dq_out, dk_out, q_w, k_w, pos, workspace, *out)
+    _check_gpu(dev, q, k)
     _run("vggt3_qk_norm_rope_grad", dev, pq, sq, pk, sk, dqo, dko, kind, qw, kw, float(eps), pp,
          _sections_ptr(sections), len(sections), float(base), int(bool(per_axis)), int(bool(interleaved)), *grads, n, n_heads,
          hk, d, _dtype_code(q), ws, nb)
