@@ -15,7 +15,7 @@
 // piece of a sequence, and the products chain through its registers (delta_ops.hpp).
 // T and the triangle of Q K^T, which all columns share and no state enters, are formed
 // beforehand for all chunks at once (matrices_kernel) and read as operands. A wave
-// works by itself: it asks for the next chunk's rows and operands before it computes,
+// works by itself: it asks for the next chunk's rows and operands while it computes,
 // and passes K alone through LDS, for its transpose.
 //
 // Long sequences are cut into pieces that are worked on at once: a first pass finds
@@ -130,6 +130,11 @@ struct Loaded {
 template <class T, int DK, int DV, int NCT, Mode MODE>
 __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_kernel(const Args a) {
   constexpr int kTiles = DK / 16, kSteps = DK / 32, kP = kWhole<T>, kW = 4 / NCT, kB = (int)sizeof(T);
+  // The next chunk's rows into the registers that this one's leave, half a chunk ahead, or
+  // whole chunks in two sets by turns: the one is half the code and registers (48 views'
+  // states 256 us, 261 by turns; 24 views in fp32 220 + 201, 224 + 206), the other further
+  // ahead (a scene's two passes in bf16 538 + 388 us, 574 + 416 in one set).
+  constexpr bool kOnce = sizeof(T) == 4 || MODE == kStates;
   __shared__ T ks_rows[kW][kChunk * kPitch<T, DK>];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int c = lane % 16, q = lane / 16;
@@ -164,7 +169,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
   const int voff = (int)((4 * q * ldv + NCT * c) * kB), vrow = (int)(ldv * kB);
 
   typedef Loaded<T, DK, NCT, MODE> L;
-  const auto load = [&](L& x, int i) {
+  const auto load_keys = [&](L& x, int i) {
     const int64_t first = p.first + (int64_t)i * kChunk;
     const int len = min(kChunk, p.len - i * kChunk);
     const Window kw = window<DK>(static_cast<const T*>(a.k) + first * ldq + kh * DK, ldq, len);
@@ -179,6 +184,10 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) load_raw(x.q[it][s], qw, koff + it * knext + 32 * s * kB);
     }
+  };
+  const auto load_rest = [&](L& x, int i) {
+    const int64_t first = p.first + (int64_t)i * kChunk;
+    const int len = min(kChunk, p.len - i * kChunk);
     const Window vw = window<16 * NCT>(static_cast<const T*>(a.v) + first * ldv + h * DV + (unit ? 0 : col0), ldv,
                                        unit ? 0 : len);
 #pragma unroll
@@ -199,7 +208,12 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
     }
     x.total = m->rows.total;
   };
-  const auto compute = [&](const L& x, int i) {
+  const auto load = [&](L& x, int i) {
+    load_keys(x, i);
+    load_rest(x, i);
+  };
+  const auto compute = [&](L& x, int i) {
+    const int next = min(i + 1, chunks - 1);
     if constexpr (MODE == kStates)
       store_state<DK, NCT>(S, a.states + ((slot0 + i) * a.hv + h) * DK * DV + col, DV, q);
 #pragma unroll
@@ -232,6 +246,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
         }
       }
     }
+    if constexpr (kOnce) load_keys(x, next);
     Frag<T> t0, t1, b0, b1;
     make<kP>(t0, x.t[0], zero4());
     make<kP>(t1, x.t[1], x.t[2]);
@@ -257,13 +272,15 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
       }
       make<kP>(uf[y], u0 * x.rest[0], u1 * x.rest[1]);
     }
+    const float total = x.total;
+    if constexpr (kOnce) load_rest(x, next);
     wave_lds_order();
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
       Frag<T> kt;
       state_rows<kPitch<T, DK>>(kt, (const T*)kt_rows, t, lane);
 #pragma unroll
-      for (int y = 0; y < NCT; ++y) S[t][y] = mm<1, kP>(kt, uf[y], S[t][y] * x.total);
+      for (int y = 0; y < NCT; ++y) S[t][y] = mm<1, kP>(kt, uf[y], S[t][y] * total);
     }
     wave_lds_order();
     if constexpr (MODE == kForward) {
@@ -281,7 +298,11 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
         }
     }
   };
-  if (chunks > 0) {
+  if (kOnce && chunks > 0) {
+    L x;
+    load(x, 0);
+    for (int i = 0; i < chunks; ++i) compute(x, i);
+  } else if (chunks > 0) {
     L x, y;
     load(x, 0);
     for (int i = 0; i < chunks; i += 2) {
@@ -362,7 +383,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void back_k
   const int voff = (int)((4 * q * ldv + NCT * c) * kB), vrow = (int)(ldv * kB);
 
   typedef BackLoaded<T, DK, NCT> L;
-  const auto load = [&](L& x, int i) {
+  const auto load_keys = [&](L& x, int i) {
     const int64_t first = p.first + (int64_t)i * kChunk;
     const int len = min(kChunk, p.len - i * kChunk);
     const Window kw = window<DK>(static_cast<const T*>(a.k) + first * ldq + kh * DK, ldq, len);
@@ -374,6 +395,10 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void back_k
         load_raw(x.k[it][s], kw, koff + it * knext + 32 * s * kB);
         load_raw(x.q[it][s], qw, koff + it * knext + 32 * s * kB);
       }
+  };
+  const auto load_rest = [&](L& x, int i) {
+    const int64_t first = p.first + (int64_t)i * kChunk;
+    const int len = min(kChunk, p.len - i * kChunk);
     const Window dw = window<16 * NCT>(static_cast<const T*>(a.dout) + first * ldv + h * DV + (unit ? 0 : col0), ldv,
                                        unit ? 0 : len);
 #pragma unroll
@@ -394,7 +419,8 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void back_k
     }
     x.total = m->rows.total;
   };
-  const auto compute = [&](const L& x, int i) {
+  const auto compute = [&](L& x, int i) {
+    const int next = max(i - 1, 0);
     if constexpr (MODE == kBack)
       store_state<DK, NCT>(S, a.dstates + ((slot0 + i) * a.hv + h) * DK * DV + col, DV, q);
 #pragma unroll
@@ -422,6 +448,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void back_k
         kd[1][y] = mm<1, kP>(k1, f, kd[1][y]);
       }
     }
+    load_keys(x, next);
     Frag<T> t0, t1, b0, b1;
     make<kP>(t0, x.xt[0], x.xt[1]);
     make<kP>(t1, zero4(), x.xt[2]);
@@ -443,6 +470,8 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void back_k
       make<kP>(df[y], dO[0] * (x.decay[0] * a.scale), dO[1] * (x.decay[1] * a.scale));
       make<kP>(rf[y], -dR0 * x.decay[0], -dR1 * x.decay[1]);
     }
+    const float total = x.total;
+    load_rest(x, next);
     wave_lds_order();
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
@@ -450,20 +479,17 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void back_k
       state_rows<kPitch<T, DK>>(kt, (const T*)kt_rows, t, lane);
       state_rows<kPitch<T, DK>>(qt, (const T*)qt_rows, t, lane);
 #pragma unroll
-      for (int y = 0; y < NCT; ++y) S[t][y] = mm<1, kP>(kt, rf[y], mm<1, kP>(qt, df[y], S[t][y] * x.total));
+      for (int y = 0; y < NCT; ++y) S[t][y] = mm<1, kP>(kt, rf[y], mm<1, kP>(qt, df[y], S[t][y] * total));
     }
     wave_lds_order();
   };
+  // the next chunk's rows into the registers that this one's leave (one view in fp32 26 +
+  // 18 us; by turns in two sets, with twice the code for the first to read, 33 + 31)
   if (chunks > 0) {
-    L x, y;
-    load(x, chunks - 1);
-    for (int i = chunks - 1; i >= 0; i -= 2) {
-      load(y, max(i - 1, 0));
-      compute(x, i);
-      if (i < 1) break;
-      load(x, max(i - 2, 0));
-      compute(y, i - 1);
-    }
+    L x;
+    load_keys(x, chunks - 1);
+    load_rest(x, chunks - 1);
+    for (int i = chunks - 1; i >= 0; --i) compute(x, i);
   }
 
   if constexpr (MODE == kBack) {
