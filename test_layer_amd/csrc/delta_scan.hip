@@ -25,7 +25,7 @@
 // sequence's first piece starts from the sequence's first state in both passes.)
 //
 // 100 views (137,400 tokens) as one sequence, 16 heads of 64 x 64 in bf16: 183 us for
-// the matrices (1.06 GB, 5.8 TB/s: memory), 460 to 540 for the summary, 55 for the join,
+// the matrices (1.06 GB, 5.8 TB/s: memory), 460 to 540 for the summary, 53 for the join,
 // 370 for the main pass. The scans are bound by vector instructions: fp32 values are cut
 // into 3 bf16 parts before each product (48 views' states: 34 million vector
 // instructions of 4 cycles, 4.8 million products of 16), and with one wave a SIMD, whose
@@ -506,12 +506,12 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void back_k
 // First states of a sequence's pieces, in seg_n's place: S <- M S + R from piece to
 // piece (BACK: from the last piece to the first). One step waits for the one before, so
 // it is cut short: DK / 16 waves share 16 columns, a wave has 16 rows of the products
-// (in fp32 for both types: they are few) and its rows of the next 4 pieces' M and R at
-// hand, and the new S goes round through LDS. 64 pieces 54 us (the next piece's alone:
-// 60), most of it the 16 products one after the other.
+// (in fp32 for both types: they are few) and its rows of the next 2 pieces' M and R at
+// hand, and the new S goes round through LDS. 64 pieces 53 us, 15 pieces 10.7 (4 at
+// hand: 54 and 12), most of it the 16 products one after the other.
 template <int DK, int DV, bool BACK>
 __global__ __launch_bounds__(4 * DK) void join_kernel(const Args a) {
-  constexpr int kSteps = DK / 32, kAhead = 4;
+  constexpr int kSteps = DK / 32, kAhead = 2;
   __shared__ f32x4 rows[2][DK / 16][64];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int c = lane % 16, q = lane / 16;
@@ -651,14 +651,14 @@ hipError_t launch_back(const Args& a, const Plan& p, bool bf16, hipStream_t stre
 size_t matrix_bytes(bool keep) { return matrices_bytes(keep); }
 
 // Wide waves pay where they alone fill the GPU: against narrow ones a 100-view scene
-// takes 1020 us (1460), 48 views' gradient 1390 (1650), 24 views in fp32 463 (496), and
-// 12 views with heads of 128, below the limit, 956 (690). Pieces are as long as fill the
+// takes 1020 us (1460), 48 views' gradient 1370 (1620), 24 views in fp32 461 (540), and
+// 12 views with heads of 128, below the limit, 926 (645). Pieces are as long as fill the
 // GPU with waves (one a SIMD where they are wide: 1020 us for the scene, with half or
-// twice as many 1090; half as many narrow ones: 690 us with heads of 128, with one a SIMD
-// 1050), at least 3 chunks (one view's gradient 158 us; of 2: 180, of 4: 167). Sequences
+// twice as many 1090; half as many narrow ones: 645 us with heads of 128, with one a SIMD
+// 1010), at least 3 chunks (one view's gradient 138 us; of 2: 160, of 4: 146). Sequences
 // are cut only where much longer than that, since a cut costs a pass over all pieces
-// with d_k more columns (48 views of 48 sequences uncut 1390 us, cut 1640; 24 views in
-// 10 sequences cut 463, uncut 1170).
+// with d_k more columns (48 views of 48 sequences uncut 1370 us, cut 1645; 24 views in
+// 10 sequences cut 461, uncut 1170).
 Plan plan(int64_t n, int nseq, int64_t longest, int hv, int dk, int dv) {
   const int64_t chunks = (n + kChunk - 1) / kChunk, rows = (int64_t)hv * (dv / 64);
   Plan p;
