@@ -650,25 +650,31 @@ hipError_t launch_back(const Args& a, const Plan& p, bool bf16, hipStream_t stre
 
 size_t matrix_bytes(bool keep) { return matrices_bytes(keep); }
 
-// Wide waves pay where they alone fill the GPU: against narrow ones a 100-view scene
-// takes 1020 us (1460), 48 views' gradient 1370 (1620), 24 views in fp32 461 (540), and
-// 12 views with heads of 128, below the limit, 926 (645). Pieces are as long as fill the
-// GPU with waves (one a SIMD where they are wide: 1020 us for the scene, with half or
-// twice as many 1090; half as many narrow ones: 645 us with heads of 128, with one a SIMD
-// 1010), at least 3 chunks (one view's gradient 138 us; of 2: 160, of 4: 146). Sequences
-// are cut only where much longer than that, since a cut costs a pass over all pieces
-// with d_k more columns (48 views of 48 sequences uncut 1370 us, cut 1645; 24 views in
-// 10 sequences cut 461, uncut 1170).
+// Wide waves pay where they alone fill the GPU: against narrow ones a 100-view scene takes
+// 1020 us (1460), 48 views' gradient 1370 (1620), 24 views in fp32 461 (540), and 12
+// views with heads of 128, below the limit, 926 (645). Where narrow ones need no cut,
+// they have to fill half of it (32 sequences of 1374 tokens, 16 heads: 228 us, their
+// gradient 904, narrow 283 and 1010; 24 of them 315 and 983, narrow 246 and 861).
+// Pieces are as long as fill the GPU with waves (one a SIMD where they are wide: 1020 us
+// for the scene, with half or twice as many 1090; half as many narrow ones: 645 us with
+// heads of 128, with one a SIMD 1010), at least 3 chunks (one view's gradient 138 us; of
+// 2: 160, of 4: 146). Sequences are cut only where much longer than that, since a cut
+// costs a pass over all pieces with d_k more columns (48 views of 48 sequences uncut
+// 1370 us, cut 1645; 24 views in 10 sequences cut 461, uncut 1170).
 Plan plan(int64_t n, int nseq, int64_t longest, int hv, int dk, int dv) {
   const int64_t chunks = (n + kChunk - 1) / kChunk, rows = (int64_t)hv * (dv / 64);
   Plan p;
-  p.wide = chunks * rows >= 16384;
-  const int64_t waves = p.wide ? 1024 : 512;
-  int64_t each = (chunks * rows + waves - 1) / waves;
-  if (each < 3) each = 3;
-  p.split = longest > each * kChunk * 5 / 2;
-  p.per = p.split ? each * kChunk : (n / kChunk + 1) * kChunk;
-  p.pieces = n / p.per + nseq;
+  const auto cut = [&](bool wide) {
+    const int64_t waves = wide ? 1024 : 512;
+    int64_t each = (chunks * rows + waves - 1) / waves;
+    if (each < 3) each = 3;
+    p.wide = wide;
+    p.split = longest > each * kChunk * 5 / 2;
+    p.per = p.split ? each * kChunk : (n / kChunk + 1) * kChunk;
+    p.pieces = n / p.per + nseq;
+  };
+  cut(false);
+  if (chunks * rows >= 16384 && (p.split || nseq * rows >= 512)) cut(true);
   return p;
 }
 
