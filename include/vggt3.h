@@ -690,7 +690,7 @@ int vggt3_qk_norm_rope_grad(const void* q, int64_t q_stride, const void* k, int6
  *   workspace    at least vggt3_gated_delta_workspace_bytes(...) bytes.
  * Computed by chunks of 32 tokens (the same values by matrix products): S, decays,
  * sums and the chunk's triangular inverse are fp32 (bf16 dtype: products of fp32 values
- * in three bf16 parts; two for o), o is rounded once. A value that is not finite may
+ * in three bf16 parts, the whole value), o is rounded once. A value that is not finite may
  * make its head's results in its sequence not finite from its chunk on, others' not at
  * all. Heads of 64 or 128 each way. The results are the same bits each time. Outputs and the workspace must
  * not overlap anything else. n_tokens == 0 copies state to state_out.

@@ -148,7 +148,7 @@ __device__ __forceinline__ f32x4 turned(const f32x4& x, int lane) {
 
 // A chunk's shared matrices in memory, tile by tile as lanes hold them: T = (I + N)^-1
 // and B by row, and for the gradient X = (I + beta N')^-1 and B with tiles by column
-// (the operands X^T and B^T). B of the forward alone is in two bf16 parts (bf16).
+// (the operands X^T and B^T).
 struct Matrices {
   f32x4 t[3][64];
   f32x4 b[3][64];
@@ -170,31 +170,6 @@ __device__ __forceinline__ void put_tri(f32x4 (*to)[64], const Tri& m, int lane)
   to[1][lane] = m.t10;
   to[2][lane] = m.t11;
 }
-// A tile in two bf16 parts, and two of them as an operand.
-template <class T>
-__device__ __forceinline__ u32x4 tile_parts(const f32x4& x) {
-  if constexpr (sizeof(T) == 4) {
-    return __builtin_bit_cast(u32x4, x);
-  } else {
-    const uint32_t a = pack_bf16x2(x[0], x[1]), b = pack_bf16x2(x[2], x[3]);
-    return u32x4{a, b, pack_bf16x2(x[0] - bf16_lo(a), x[1] - bf16_hi(a)), pack_bf16x2(x[2] - bf16_lo(b), x[3] - bf16_hi(b))};
-  }
-}
-template <class T>
-__device__ __forceinline__ void put_tri_parts(f32x4 (*to)[64], const Tri& m, int lane) {
-  to[0][lane] = __builtin_bit_cast(f32x4, tile_parts<T>(m.t00));
-  to[1][lane] = __builtin_bit_cast(f32x4, tile_parts<T>(m.t10));
-  to[2][lane] = __builtin_bit_cast(f32x4, tile_parts<T>(m.t11));
-}
-__device__ __forceinline__ void parts_frag(Frag<uint16_t>& f, const u32x4& x, const u32x4& y) {
-  f.part[0] = as_bf16x8(u32x4{x[0], x[1], y[0], y[1]});
-  f.part[1] = as_bf16x8(u32x4{x[2], x[3], y[2], y[3]});
-}
-__device__ __forceinline__ void parts_frag(Frag<float>& f, const u32x4& x, const u32x4& y) {
-  f.a = __builtin_bit_cast(f32x4, x);
-  f.b = __builtin_bit_cast(f32x4, y);
-}
-
 // The tile of 16 * NCT columns that a lane has NCT of, to and from rows in memory.
 template <int DK, int NCT>
 __device__ __forceinline__ void load_state(f32x4 (*S)[NCT], const float* from, int64_t ld, int q) {

@@ -91,8 +91,8 @@ __global__ __launch_bounds__(256) void matrices_kernel(const Args a) {
   unit_inverse(n.t00 * b0, n.t10 * b0, n.t11 * b1, t.t00, t.t10, t.t11, scratch[wave], lane);
   Matrices* m = matrices_of(a.mats, (int64_t)slot * a.hv + h, KEEP);
   put_tri(m->t, t, lane);
+  put_tri(m->b, b, lane);
   if constexpr (KEEP) {
-    put_tri(m->b, b, lane);
     put_tri(m->bt, turned(b, lane), lane);
     // X = (I + beta N')^-1 = I - beta (T N'): one inverse serves both sides' scaling
     n = turned(n, lane);
@@ -104,8 +104,6 @@ __global__ __launch_bounds__(256) void matrices_kernel(const Args a) {
     x.t10 = -b1 * mm16(t.t11, n.t10, mm16(t.t10, n.t00, zero4()));
     x.t11 = one - b1 * mm16(t.t11, n.t11, zero4());
     put_tri(m->x, x, lane);
-  } else {
-    put_tri_parts<T>(m->b, b, lane);
   }
   const float* from = reinterpret_cast<const float*>(&rows);
   float* to = reinterpret_cast<float*>(&m->rows);
@@ -121,8 +119,7 @@ template <class T, int DK, int NCT, Mode MODE>
 struct Loaded {
   Raw<T> k[2][DK / 32], q[MODE == kForward ? 2 : 0][DK / 32];
   RawN<T, NCT> v[2][4];
-  f32x4 t[3];
-  u32x4 b[3];
+  f32x4 t[3], b[3];
   f32x4 decay[2], rest[2], beta[2];
   float total;
 };
@@ -198,7 +195,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
       x.t[j] = m->t[j][lane];
-      if constexpr (MODE == kForward) x.b[j] = __builtin_bit_cast(u32x4, m->b[j][lane]);
+      if constexpr (MODE == kForward) x.b[j] = m->b[j][lane];
     }
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
@@ -241,8 +238,8 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
         ks[0][y] = mm<1, kP>(k0, f, ks[0][y]);
         ks[1][y] = mm<1, kP>(k1, f, ks[1][y]);
         if constexpr (MODE == kForward) {
-          o[0][y] = mm<1, 2>(q0, f, o[0][y]);
-          o[1][y] = mm<1, 2>(q1, f, o[1][y]);
+          o[0][y] = mm<1, kP>(q0, f, o[0][y]);
+          o[1][y] = mm<1, kP>(q1, f, o[1][y]);
         }
       }
     }
@@ -251,8 +248,8 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
     make<kP>(t0, x.t[0], zero4());
     make<kP>(t1, x.t[1], x.t[2]);
     if constexpr (MODE == kForward) {
-      parts_frag(b0, x.b[0], u32x4{0, 0, 0, 0});
-      parts_frag(b1, x.b[1], x.b[2]);
+      make<kP>(b0, x.b[0], zero4());
+      make<kP>(b1, x.b[1], x.b[2]);
     }
     Frag<T> uf[NCT];
 #pragma unroll
@@ -266,9 +263,9 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
       make<kP>(f, R[0], R[1]);
       const f32x4 u0 = mm<kP, kP>(t0, f, zero4()) * x.beta[0], u1 = mm<kP, kP>(t1, f, zero4()) * x.beta[1];
       if constexpr (MODE == kForward) {
-        make<2>(f, u0, u1);
-        o[0][y] = mm<2, 2>(b0, f, o[0][y] * (x.decay[0] * a.scale));
-        o[1][y] = mm<2, 2>(b1, f, o[1][y] * (x.decay[1] * a.scale));
+        make<kP>(f, u0, u1);
+        o[0][y] = mm<kP, kP>(b0, f, o[0][y] * (x.decay[0] * a.scale));
+        o[1][y] = mm<kP, kP>(b1, f, o[1][y] * (x.decay[1] * a.scale));
       }
       make<kP>(uf[y], u0 * x.rest[0], u1 * x.rest[1]);
     }
