@@ -14,9 +14,10 @@
 // the whole sequence would lose the small terms; over 32 tokens it does not.)
 //
 // A wave has 64 value channels of a chunk and head, 4 neighbours a lane (u, x, o and the
-// row sums, in fp32 values whole), then F and E, then its share of the key channels
-// (dQ, dK, from operands in two bf16 parts). u and dR change from columns by lane to
-// rows by lane through LDS; the triangles stay in registers.
+// row sums), then F and E, then its share of the key channels (dQ, dK). In bf16 all
+// fp32 operands are whole, in three parts (in two: 48 views' chunks 785 us for 900, but
+// more last bits of dQ and dK differ than an order of sums explains). u and dR change
+// from columns by lane to rows by lane through LDS; the triangles stay in registers.
 //
 // 48 views (65,952 tokens), 16 heads of 64 x 64 in bf16: 785 us, where four waves of 16
 // columns, which convert each triangle four times over, took 1300. The wave fills a
@@ -35,7 +36,7 @@ namespace {
 
 template <class T, int DK, int DV>
 struct GradShared {
-  static constexpr int kParts = sizeof(T) == 2 ? 2 : 1;  // of u and dR
+  static constexpr int kParts = kWhole<T>;  // of u and dR
   T k[kChunk][kPitch<T, DK>];
   T q[kChunk][kPitch<T, DK>];
   T u[kParts][kChunk][kPitch<T, DV>];
@@ -43,19 +44,26 @@ struct GradShared {
   float along[DV / 64][kChunk], step[DV / 64][kChunk], all[DV / 64];
 };
 
-// 4 neighbouring values of a row to LDS, split into two parts (bf16).
+// 4 neighbouring values of a row to LDS, split into three parts (bf16).
 __device__ __forceinline__ void put_four(uint16_t* to, int part, const float* v) {
-  const uint32_t a = pack_bf16x2(v[0], v[1]), b = pack_bf16x2(v[2], v[3]);
-  st8(to, u32x2{a, b});
-  st8(to + part, u32x2{pack_bf16x2(less_lo(v[0], a), less_hi(v[1], a)), pack_bf16x2(less_lo(v[2], b), less_hi(v[3], b))});
+  float x[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    const uint32_t a = pack_bf16x2(x[0], x[1]), b = pack_bf16x2(x[2], x[3]);
+    st8(to + p * part, u32x2{a, b});
+    x[0] = less_lo(x[0], a);
+    x[1] = less_hi(x[1], a);
+    x[2] = less_lo(x[2], b);
+    x[3] = less_hi(x[3], b);
+  }
 }
 __device__ __forceinline__ void put_four(float* to, int, const float* v) {
   *reinterpret_cast<f32x4*>(to) = f32x4{v[0], v[1], v[2], v[3]};
 }
 template <int PITCH>
 __device__ __forceinline__ void row_parts(Frag<uint16_t>& f, const uint16_t* from, int part, int row, int col) {
-  f.part[0] = ld_op(from + row * PITCH + col);
-  f.part[1] = ld_op(from + part + row * PITCH + col);
+#pragma unroll
+  for (int p = 0; p < 3; ++p) f.part[p] = ld_op(from + p * part + row * PITCH + col);
 }
 template <int PITCH>
 __device__ __forceinline__ void row_parts(Frag<float>& f, const float* from, int, int row, int col) {
@@ -323,30 +331,30 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
       load_raw(w1, ow, orow + onext + 32 * s * kB);
       as_frag(o0, w0);
       as_frag(o1, w1);
-      f.t00 = mm<2, 1>(u0, o0, f.t00);
-      f.t10 = mm<2, 1>(u0, o1, f.t10);
-      f.t11 = mm<2, 1>(u1, o1, f.t11);
-      g.t00 = mm<1, 2>(o0, u0, g.t00);
-      g.t10 = mm<1, 2>(o1, u0, g.t10);
-      g.t11 = mm<1, 2>(o1, u1, g.t11);
-      e.t00 = mm<2, 2>(u0, r0, e.t00);
-      e.t10 = mm<2, 2>(u0, r1, e.t10);
-      e.t11 = mm<2, 2>(u1, r1, e.t11);
-      d.t00 = mm<2, 2>(r0, u0, d.t00);
-      d.t10 = mm<2, 2>(r1, u0, d.t10);
-      d.t11 = mm<2, 2>(r1, u1, d.t11);
+      f.t00 = mm<kP, 1>(u0, o0, f.t00);
+      f.t10 = mm<kP, 1>(u0, o1, f.t10);
+      f.t11 = mm<kP, 1>(u1, o1, f.t11);
+      g.t00 = mm<1, kP>(o0, u0, g.t00);
+      g.t10 = mm<1, kP>(o1, u0, g.t10);
+      g.t11 = mm<1, kP>(o1, u1, g.t11);
+      e.t00 = mm<kP, kP>(u0, r0, e.t00);
+      e.t10 = mm<kP, kP>(u0, r1, e.t10);
+      e.t11 = mm<kP, kP>(u1, r1, e.t11);
+      d.t00 = mm<kP, kP>(r0, u0, d.t00);
+      d.t10 = mm<kP, kP>(r1, u0, d.t10);
+      d.t11 = mm<kP, kP>(r1, u1, d.t11);
     }
     Tri w = decays<false>(mat.rows, lane);
     e = lower<false, true>(e * w, lane);
     const f32x4 one = {1.0f, 1.0f, 1.0f, 1.0f}, sc = one * a.scale;
     f = lower<false, false>(f * w, lane);
-    lower_rows<2>(ff, f * Tri{sc, sc, sc});
-    lower_rows<2>(ef, e * Tri{-one, -one, -one});
+    lower_rows<kP>(ff, f * Tri{sc, sc, sc});
+    lower_rows<kP>(ef, e * Tri{-one, -one, -one});
     w = decays<true>(mat.rows, lane);
     d = lower<true, true>(d * w, lane);
     g = lower<true, false>(g * w, lane);
-    upper_rows<2>(ft, g * Tri{sc, sc, sc});
-    upper_rows<2>(et, d * Tri{-one, -one, -one});
+    upper_rows<kP>(ft, g * Tri{sc, sc, sc});
+    upper_rows<kP>(et, d * Tri{-one, -one, -one});
   };
 
   // this wave's key channels, kN neighbours a lane at a time
@@ -380,11 +388,11 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
         f32x4 w[2];
         eight(w, S0, x, s);
         Frag<T> f;
-        make<2>(f, w[0], w[1]);
+        make<kP>(f, w[0], w[1]);
 #pragma unroll
         for (int it = 0; it < 2; ++it) {
-          dq[it][x] = mm<1, 2>(o[it], f, dq[it][x]);
-          dk[it][x] = mm<2, 2>(r[it], f, dk[it][x]);
+          dq[it][x] = mm<1, kP>(o[it], f, dq[it][x]);
+          dk[it][x] = mm<kP, kP>(r[it], f, dk[it][x]);
         }
       }
     }
@@ -406,9 +414,9 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) apart += w[0][r] * z[0][r] + w[1][r] * z[1][r];
         Frag<T> f;
-        make<2>(f, w[0], w[1]);
+        make<kP>(f, w[0], w[1]);
 #pragma unroll
-        for (int it = 0; it < 2; ++it) us[it][x] = mm<2, 2>(u[it], f, us[it][x]);
+        for (int it = 0; it < 2; ++it) us[it][x] = mm<kP, kP>(u[it], f, us[it][x]);
       }
     }
 #pragma unroll
@@ -428,10 +436,10 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
       token_columns<kN, kPK>(qc, &m.q[0][0], base, x, lane);
 #pragma unroll
       for (int it = 0; it < 2; ++it) {
-        dq[it][x] = mm<2, 1>(ff[it], kc, dq[it][x]);
-        dk[it][x] = mm<2, 1>(ft[it], qc, dk[it][x]);
-        dk[it][x] = mm<2, 1>(ef[it], kc, dk[it][x]);
-        dk[it][x] = mm<2, 1>(et[it], kc, dk[it][x]);
+        dq[it][x] = mm<kP, 1>(ff[it], kc, dq[it][x]);
+        dk[it][x] = mm<kP, 1>(ft[it], qc, dk[it][x]);
+        dk[it][x] = mm<kP, 1>(ef[it], kc, dk[it][x]);
+        dk[it][x] = mm<kP, 1>(et[it], kc, dk[it][x]);
       }
     }
     const auto store = [&](auto* to, int64_t ld, const f32x4(*v)[kN]) {

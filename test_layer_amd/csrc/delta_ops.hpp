@@ -19,8 +19,8 @@ namespace delta {
 // grows with the chunk.)
 constexpr int kChunk = 32;
 
-// Operand of a 32-deep product. bf16: 1 to 3 parts of 8 bits each, 3 of them the
-// whole fp32 value (one where the value is bf16 already); fp32: the value.
+// Operand of a 32-deep product. bf16: 3 parts of 8 bits each, the whole fp32 value, or
+// one where the value is bf16 already; fp32: the value.
 template <class T>
 struct Frag;
 template <>
@@ -32,8 +32,8 @@ struct Frag<float> {
   f32x4 a, b;
 };
 
-// c += A B. NA, NB: parts of A and B that count (bf16); products of parts that lie
-// below the last one kept are left out: 2^-16 relative for 2, 2^-24 for 3.
+// c += A B. NA, NB: parts of A and B (bf16, 1 or 3); products of parts that lie below the
+// last one kept are left out: 2^-24 relative.
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 mm(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x4 c) {
   constexpr int kLast = (NA > NB ? NA : NB) - 1;

@@ -85,3 +85,82 @@ def test_reads_of_nearly_equal_decays(dk, dv):
     want = torch.zeros(n, heads, dtype=torch.float64)
     want[2:] = g[2:].double().exp() * -torch.expm1(g[1:-1].double())
     _near(o.view(n, heads, dv), want.cuda()[..., None].expand(n, heads, dv))
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("n,heads", [(40, 2), (700, 1), (33000, 16)])
+def test_gradients_by_nearly_equal_columns(n, heads, dk, dv):
+    # no keys: dq = S dO and dk = dS u, with dO and u = v a column 2i minus column 2i + 1
+    (a, b), (c, d) = (_neighbours((1, heads, dk, dv // 2), s) for s in (4, 5))
+    state, dstate = (torch.stack(x, 4).reshape(1, heads, dk, dv) for x in ((a, b), (c, d)))
+    i = torch.arange(n) % (dv // 2)
+    v = _hot(n, heads, dv, (2 * i, 1.0), (2 * i + 1, -1.0)).flatten(1)
+    none = torch.zeros(n, heads * dk, dtype=BF, device="cuda")
+    got = tla.gated_delta_grad(none, none, v, None, torch.ones(n, heads, device="cuda"), v, heads, dstate=dstate, state=state)
+    at = i.cuda()
+    _near(got.dq, (a.double() - b.double())[0, :, :, at].permute(2, 0, 1).flatten(1))
+    _near(got.dk, (c.double() - d.double())[0, :, :, at].permute(2, 0, 1).flatten(1))
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_key_gradients_by_nearly_equal_reads(dk, dv):
+    # one token a sequence, key and query of channel 0, whose state is 0: dR = dO, so dk = -S dO and dq = S dO
+    heads, n = 2, dv // 2
+    a, b = _neighbours((n, heads, dk, dv // 2), 6)
+    a[:, :, 0] = b[:, :, 0] = 0
+    state = torch.stack([a, b], 4).reshape(n, heads, dk, dv)
+    i = torch.arange(n)
+    k = _hot(n, heads, dk, (0 * i, 1.0)).flatten(1)
+    do = _hot(n, heads, dv, (2 * i, 1.0), (2 * i + 1, -1.0)).flatten(1)
+    got = tla.gated_delta_grad(k, k.clone(), torch.zeros_like(do), None, torch.ones(n, heads, device="cuda"), do, heads, state=state,
+                               cu_seqlens=torch.arange(n + 1, dtype=torch.int32, device="cuda"), max_seqlen=1)
+    at = i.cuda()
+    want = (a.double() - b.double())[at, :, :, at].flatten(1)
+    _near(got.dq, want)
+    _near(got.dk, -want)
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_gradients_by_nearly_equal_tokens(dk, dv):
+    # three tokens in turn: key e_i with u = beta; key -e_i with u = beta + delta (a full step on v = delta, of which the
+    # first left -beta); a key and query of its own with dO = one channel, whose F and E with the two before, and with all
+    # pairs before these, are beta and beta + delta: dq = -delta at their channels, dk = delta
+    turns, heads = 30, 2
+    n = 3 * turns
+    a, b = _neighbours((turns, heads), 7)
+    beta = torch.ones(n, heads, device="cuda")
+    beta[0::3] = b / 2
+    delta = (a - b) / 2  # 1 to 200 times 2^-24: values of bf16 too
+    v = torch.zeros(n, heads, dv, dtype=BF, device="cuda")
+    v[0::3] = 1.0
+    v[1::3] = delta.to(BF)[..., None]
+    i = torch.arange(turns)
+    k = torch.zeros(n, heads, dk, dtype=BF, device="cuda")
+    k[0::3], k[1::3] = _hot(turns, heads, dk, (i, 1.0)), _hot(turns, heads, dk, (i, -1.0))
+    q = torch.zeros_like(k)
+    q[2::3] = k[2::3] = _hot(turns, heads, dk, (dk - 1 - i, 1.0))
+    do = torch.zeros_like(v)
+    do[2::3] = _hot(turns, heads, dv, (i, 1.0))
+    got = tla.gated_delta_grad(q.flatten(1), k.flatten(1), v.flatten(1), None, beta, do.flatten(1), heads)
+    want = torch.zeros(turns, heads, dk, dtype=torch.float64, device="cuda")
+    want[:, :, :turns] = delta.double().T[None] * (i[None, :] <= i[:, None]).cuda()[:, None]
+    _near(got.dq.view(n, heads, dk)[2::3], -want)
+    _near(got.dk.view(n, heads, dk)[2::3], want)
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_gradients_by_nearly_equal_queries(dk, dv):
+    # no keys: dk = F^T q, the last two tokens' queries e_0 and -e_0 and their F beta and (1 + 2^-15) beta
+    n, heads = 64, 2
+    b = _neighbours((n, heads), 8)[0] / 2
+    v = torch.ones(n, heads, dv, dtype=BF, device="cuda")
+    v[..., 1] = 2.0 ** -8 + 2.0 ** -15
+    q, do = torch.zeros(n, heads, dk, dtype=BF, device="cuda"), torch.zeros_like(v)
+    q[n - 2, :, 0], q[n - 1, :, 0] = 1.0, -1.0
+    do[n - 2:, :, 0] = torch.tensor([1.0, 1 - 2.0 ** -8], dtype=BF, device="cuda")[:, None]
+    do[n - 1, :, 1] = 1.0
+    got = tla.gated_delta_grad(q.flatten(1), torch.zeros_like(q).flatten(1), v.flatten(1), None, b, do.flatten(1), heads)
+    want = torch.zeros(n, heads, dk, dtype=torch.float64, device="cuda")
+    want[:, :, 0] = -b.double() * 2.0 ** -15
+    want[n - 1, :, 0] -= b[n - 1].double()
+    _near(got.dk.view(n, heads, dk), want)
