@@ -6,14 +6,17 @@
 //   F = scale D . (dO u^T) (lower),    E = D . (dR u^T) (strictly lower)
 //   dQ = scale G . (dO S^T) + F K
 //   dK = F^T Q + G_end / G . (u dS^T) - G . (dR S^T) - E K - E^T K
-//   dg_t = sum over i >= t of (o_i . dO_i - v_i . dR_i) + <dS, the state after>
+//   dg_t = sum over i >= t of A_i + over j < t of C_j + over i >= t > j of W_ij + G_end <dS, S>
+//   A_i = G_i (scale q_i S . dO_i - k_i S . dR_i),  C_j = G_end / G_j  k_j dS . u_j
+//   W = B . (dO u^T) - E . (K K^T) (strictly lower)
 //
-// The last line: G enters o_i as its query's factor, and each token's error as its
-// read key's factor minus its write key's, whose sum is -v_i . dR_i; a whole chunk
-// back from its end, what the later chunks say is in <dS, state>. (One such sum over
-// the whole sequence would lose the small terms; over 32 tokens it does not.)
+// The last lines: token t's decay is a factor of what crosses it, from the state or a
+// token j < t to a token i >= t or the state behind. Every term has it as a factor, so
+// dg is right however small the decay makes it. (o_i . dO_i - v_i . dR_i summed over i >= t
+// is the same value by terms without that factor, which must cancel: nothing of dg is left
+// where e^g is 2^-24.)
 //
-// A wave has 64 value channels of a chunk and head, 4 neighbours a lane (u, x, o and the
+// A wave has 64 value channels of a chunk and head, 4 neighbours a lane (u, x and the
 // row sums), then F and E, then its share of the key channels (dQ, dK). In bf16 all
 // fp32 operands are whole, in three parts (in two: 48 views' chunks 785 us for 900, but
 // more last bits of dQ and dK differ than an order of sums explains). u and dR change
@@ -41,7 +44,7 @@ struct GradShared {
   T q[kChunk][kPitch<T, DK>];
   T u[kParts][kChunk][kPitch<T, DV>];
   T dr[kParts][kChunk][kPitch<T, DV>];
-  float along[DV / 64][kChunk], step[DV / 64][kChunk], all[DV / 64];
+  float in[DV / 64][kChunk], out[DV / 64][kChunk], step[DV / 64][kChunk], all[DV / 64];  // A, C, dbeta and <dS, S>
 };
 
 // 4 neighbouring values of a row to LDS, split into three parts (bf16).
@@ -77,6 +80,33 @@ __device__ __forceinline__ float row_add(float x) {
 }
 __device__ __forceinline__ float row_sum(float x) {
   return row_add<0x140>(row_add<0x141>(row_add<0x4E>(row_add<0xB1>(x))));
+}
+
+// The sums of a strict triangle's values over i >= t > j, in lanes t < 32: over its columns
+// by a product with a triangle of ones, then over its rows.
+__device__ __forceinline__ float crossing(const Tri& w, int lane) {
+  const int c = lane % 16, q = lane / 16;
+  f32x4 before, one;  // j < t, and all j
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    before[r] = 4 * q + r < c ? 1.0f : 0.0f;
+    one[r] = 1.0f;
+  }
+  const f32x4 m00 = mm16(w.t00, before, zero4()), m10 = mm16(w.t10, before, zero4());
+  const f32x4 m11 = mm16(w.t11, before, mm16(w.t10, one, zero4()));
+  float x = 0.0f, y = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const bool from = 4 * q + r >= c;
+    x += (from ? m00[r] : 0.0f) + m10[r];
+    y += from ? m11[r] : 0.0f;
+  }
+#pragma unroll
+  for (int off = 16; off < 64; off *= 2) {
+    x += __shfl_xor(x, off, 64);
+    y += __shfl_xor(y, off, 64);
+  }
+  return q == 0 ? x : y;
 }
 
 // A value that the compiler takes as a new one: what was made of it before is made
@@ -155,13 +185,12 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
     }
   };
 
-  // this wave's value channels: u and o, then x and dR
+  // this wave's value channels: u, then x and dR
   RawN<T, 4> vr[2][4], dr[2][4];
-  f32x4 y[2][4], dR[2][4];
-  f32x4 along[2] = {zero4(), zero4()}, step[2] = {zero4(), zero4()};
-  float both = 0.0f;  // <dS, S>
+  f32x4 y[2][4], dR[2][4], ks[2][4];  // ks: G . (K S)
+  f32x4 in[2] = {zero4(), zero4()}, out[2] = {zero4(), zero4()}, step[2] = {zero4(), zero4()};
   {
-    f32x4 ks[2][4], qs[2][4];
+    f32x4 qs[2][4];
 #pragma unroll
     for (int it = 0; it < 2; ++it)
 #pragma unroll
@@ -197,9 +226,8 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
         load_rawn(vr[it][r], vw, voff + (16 * it + r) * vrow);
         load_rawn(dr[it][r], ow, voff + (16 * it + r) * vrow);
       }
-    Frag<T> tf[2], bf[2];
+    Frag<T> tf[2];
     lower_rows<kP>(tf, get_tri(mat.t, lane));
-    lower_rows<kP>(bf, get_tri(mat.b, lane));
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       f32x4 V[2], dO[2];
@@ -211,12 +239,13 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
           dO[it][r] = value_of(dr[it][r], x);
         }
       Frag<T> f;
-      make<kP>(f, V[0] - dec[0] * ks[0][x], V[1] - dec[1] * ks[1][x]);
+      ks[0][x] *= dec[0];
+      ks[1][x] *= dec[1];
+      make<kP>(f, V[0] - ks[0][x], V[1] - ks[1][x]);
       y[0][x] = mm<kP, kP>(tf[0], f, zero4());
       y[1][x] = mm<kP, kP>(tf[1], f, zero4());
-      make<kP>(f, y[0][x] * beta[0], y[1][x] * beta[1]);
-      along[0] += dO[0] * mm<kP, kP>(bf[0], f, qs[0][x] * (dec[0] * a.scale));
-      along[1] += dO[1] * mm<kP, kP>(bf[1], f, qs[1][x] * (dec[1] * a.scale));
+      in[0] += dO[0] * (qs[0][x] * (dec[0] * a.scale));
+      in[1] += dO[1] * (qs[1][x] * (dec[1] * a.scale));
     }
   }
 #pragma unroll
@@ -225,10 +254,7 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T); ++i) {
-        anew(vr[it][r].r[i]);
-        anew(dr[it][r].r[i]);
-      }
+      for (int i = 0; i < (int)sizeof(T); ++i) anew(dr[it][r].r[i]);
   }
   {
     f32x4 kd[2][4];
@@ -262,19 +288,16 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
     upper_rows<kP>(xf, get_tri(mat.x, lane));
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      f32x4 V[2], dO[2];
+      f32x4 dO[2];
 #pragma unroll
       for (int it = 0; it < 2; ++it)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          V[it][r] = value_of(vr[it][r], x);
-          dO[it][r] = value_of(dr[it][r], x);
-        }
+        for (int r = 0; r < 4; ++r) dO[it][r] = value_of(dr[it][r], x);
       Frag<T> f;
       make<1>(f, dO[0], dO[1]);
       const f32x4 e0 = kd[0][x] * rest[0], e1 = kd[1][x] * rest[1];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) both += e0[r] * (y[0][x][r] * beta[0][r]) + e1[r] * (y[1][x][r] * beta[1][r]);
+      out[0] += e0 * (y[0][x] * beta[0]);
+      out[1] += e1 * (y[1][x] * beta[1]);
       const f32x4 du0 = mm<kP, 1>(btf[0], f, e0), du1 = mm<kP, 1>(btf[1], f, e1);
       make<kP>(f, du0, du1);
       const f32x4 x0 = mm<kP, kP>(xf[0], f, zero4()), x1 = mm<kP, kP>(xf[1], f, zero4());
@@ -282,8 +305,8 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
       step[1] += y[1][x] * x1;
       dR[0][x] = x0 * beta[0];
       dR[1][x] = x1 * beta[1];
-      along[0] -= V[0] * dR[0][x];
-      along[1] -= V[1] * dR[1][x];
+      in[0] -= ks[0][x] * dR[0][x];
+      in[1] -= ks[1][x] * dR[1][x];
     }
   }
   anew(beta[0]);
@@ -306,16 +329,18 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
   for (int it = 0; it < 2; ++it)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float s0 = row_sum(along[it][r]), s1 = row_sum(step[it][r]);
+      const float s0 = row_sum(in[it][r]), s1 = row_sum(out[it][r]), s2 = row_sum(step[it][r]);
       if (c == 0) {
-        m.along[wave][16 * it + 4 * q + r] = s0;
-        m.step[wave][16 * it + 4 * q + r] = s1;
+        m.in[wave][16 * it + 4 * q + r] = s0;
+        m.out[wave][16 * it + 4 * q + r] = s1;
+        m.step[wave][16 * it + 4 * q + r] = s2;
       }
     }
   meet<kW>();
 
   // F = dO u^T and E = dR u^T, with rows by lane (as F, -E) and columns by lane (F^T, -E^T)
   Frag<T> ff[2], ft[2], ef[2], et[2];
+  float between = 0.0f;  // lane t < 32: W's sum over i >= t > j
   const auto triangles = [&]() {
     Tri f{zero4(), zero4(), zero4()}, g = f, e = f, d = f;
 #pragma unroll
@@ -346,6 +371,21 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
     }
     Tri w = decays<false>(mat.rows, lane);
     e = lower<false, true>(e * w, lane);
+    {
+      Tri kk{zero4(), zero4(), zero4()};
+#pragma unroll
+      for (int s = 0; s < kS; ++s) {
+        Frag<T> k0, k1;
+        row8(k0, &m.k[c][32 * s + 8 * q]);
+        row8(k1, &m.k[16 + c][32 * s + 8 * q]);
+        kk.t00 = mm<1, 1>(k0, k0, kk.t00);
+        kk.t10 = mm<1, 1>(k0, k1, kk.t10);
+        kk.t11 = mm<1, 1>(k1, k1, kk.t11);
+      }
+      kk = e * kk;
+      const Tri o = lower<false, true>(f * get_tri(mat.b, lane), lane);
+      between = crossing(Tri{o.t00 - kk.t00, o.t10 - kk.t10, o.t11 - kk.t11}, lane);
+    }
     const f32x4 one = {1.0f, 1.0f, 1.0f, 1.0f}, sc = one * a.scale;
     f = lower<false, false>(f * w, lane);
     lower_rows<kP>(ff, f * Tri{sc, sc, sc});
@@ -470,25 +510,29 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
     by_states(base);
     by_tokens(base);
   }
-  both = wave_sum(both + apart * mat.rows.total);
-  if (lane == 0) m.all[wave] = both;
+  apart = wave_sum(apart * mat.rows.total);
+  if (lane == 0) m.all[wave] = apart;
   meet<kW>();
   if (wave == 0 && lane < kChunk) {
-    double x = 0.0, all = 0.0;
-    float s = 0.0f;
+    float x = 0.0f, y = 0.0f, s = 0.0f, all = 0.0f;
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
-      x += m.along[w][lane];
+      x += m.in[w][lane];
+      y += m.out[w][lane];
       s += m.step[w][lane];
       all += m.all[w];
     }
+    // A from each token on, C before it
 #pragma unroll
     for (int off = 1; off < kChunk; off *= 2) {
-      const double down = __shfl_down(x, off, 32);
+      const float down = __shfl_down(x, off, 32), up = __shfl_up(y, off, 32);
       if (lane + off < kChunk) x += down;
+      if (lane >= off) y += up;
     }
+    y = __shfl_up(y, 1, 32);
+    if (lane == 0) y = 0.0f;
     if (lane < len) {
-      if (a.dg) a.dg[(p.first + lane) * a.hv + h] = (float)(x + all);
+      if (a.dg) a.dg[(p.first + lane) * a.hv + h] = (x + y) + (between + all);
       if (a.dbeta) a.dbeta[(p.first + lane) * a.hv + h] = s;
     }
   }
