@@ -681,7 +681,8 @@ int vggt3_qk_norm_rope_grad(const void* q, int64_t q_stride, const void* k, int6
  *                cu[b] .. cu[b + 1] - 1, empty ones included. Rows of no sequence are
  *                neither read nor written. (Boundaries outside 0 .. n_tokens count as
  *                the nearer of the two, a sequence that ends before it begins as empty;
- *                sequences must not share rows.)
+ *                their rows may lie in any order, but sequences must not share rows:
+ *                results of those that do are undefined.)
  *   max_seqlen   the longest sequence's length, or 0 if unknown. Only how the work is
  *                cut depends on it: a wrong one costs time, not results beyond rounding.
  *   state, state_out   float32 [n_seqs][n_heads_v][d_k][d_v]: S before each

@@ -43,15 +43,17 @@ delta::Plan plan_of(const Shape& s, int64_t max_seqlen) {
   return delta::plan(s.n, s.nseq, longest_of(max_seqlen, s.n), s.hv, s.dk, s.dv);
 }
 
-// Workspace of the forward: [chunks' matrices | a piece's R | a piece's M].
+// Workspace of the forward: [chunks' matrices | a piece's R | a piece's M | many sequences'
+// first pieces and chunks].
 struct Ws {
-  size_t seg_n, seg_m, total;
+  size_t seg_n, seg_m, cuts, total;
 };
 Ws forward_ws(const Shape& s, const delta::Plan& p, bool keep) {
   Ws w;
   w.seg_n = round256((size_t)delta::chunk_slots(s.n, s.nseq) * s.hv * delta::matrix_bytes(keep));
   w.seg_m = w.seg_n + (p.split ? round256((size_t)p.pieces * s.state()) : 0);
-  w.total = w.seg_m + (p.split ? round256((size_t)p.pieces * s.hv * s.dk * s.dk * sizeof(float)) : 0);
+  w.cuts = w.seg_m + (p.split ? round256((size_t)p.pieces * s.hv * s.dk * s.dk * sizeof(float)) : 0);
+  w.total = w.cuts + (delta::needs_cuts(true, s.nseq) ? round256(2 * (size_t)s.nseq * sizeof(uint32_t)) : 0);
   return w;
 }
 
@@ -74,12 +76,15 @@ GradWs grad_ws(const Shape& s, const delta::Plan& p) {
   return w;
 }
 
-// The workspace's matrices and pieces.
-void place(delta::Args& a, char* ws, const Ws& w, bool keep) {
+// The workspace's matrices and pieces, and the cut.
+void place(delta::Args& a, char* ws, const Ws& w, const delta::Plan& p, bool keep) {
   a.mats = ws;
   a.keep = keep;
   a.seg_n = reinterpret_cast<float*>(ws + w.seg_n);
   a.seg_m = reinterpret_cast<float*>(ws + w.seg_m);
+  a.cuts = delta::needs_cuts(a.cu != nullptr, a.nseq) ? reinterpret_cast<uint32_t*>(ws + w.cuts) : nullptr;
+  a.per = p.per;
+  a.pieces = p.pieces;
 }
 
 int check_scale(float scale) {
@@ -142,9 +147,9 @@ int vggt3_gated_delta(const void* q, const void* k, const void* v, const float* 
   delta::Args a{};
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.cu = cu_seqlens; a.state = state;
   a.o = o; a.state_out = state_out;
-  place(a, static_cast<char*>(workspace), w, false);
-  a.n = n_tokens; a.per = p.per; a.nseq = n_seqs; a.hk = n_heads; a.hv = n_heads_v; a.dk = d_k; a.dv = d_v;
+  a.n = n_tokens; a.nseq = n_seqs; a.hk = n_heads; a.hv = n_heads_v; a.dk = d_k; a.dv = d_v;
   a.scale = scale;
+  place(a, static_cast<char*>(workspace), w, p, false);
   rc = check_hip(delta::launch_forward(a, p, dtype == VGGT3_BF16, static_cast<hipStream_t>(stream)),
                  "gated delta rule launch");
   return rc ? rc : ok();
@@ -205,7 +210,6 @@ int vggt3_gated_delta_grad(const void* q, const void* k, const void* v, const fl
   delta::Args a{};
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.cu = cu_seqlens; a.state = state;
   a.dout = d_o; a.dlast = dstate_out; a.dfirst = dstate;
-  place(a, ws, w.f, true);
   a.states = reinterpret_cast<float*>(ws + w.states);
   a.dstates = reinterpret_cast<float*>(ws + w.dstates);
   a.dq = dq; a.dk_out = dk; a.dv_out = dv; a.dg = dg; a.dbeta = dbeta;
@@ -213,8 +217,9 @@ int vggt3_gated_delta_grad(const void* q, const void* k, const void* v, const fl
     a.dq_part = reinterpret_cast<float*>(ws + w.dq);
     a.dk_part = reinterpret_cast<float*>(ws + w.dk);
   }
-  a.n = n_tokens; a.per = p.per; a.nseq = n_seqs; a.hk = n_heads; a.hv = n_heads_v; a.dk = d_k; a.dv = d_v;
+  a.n = n_tokens; a.nseq = n_seqs; a.hk = n_heads; a.hv = n_heads_v; a.dk = d_k; a.dv = d_v;
   a.scale = scale;
+  place(a, ws, w.f, p, true);
   const bool bf16 = dtype == VGGT3_BF16;
   hipStream_t st = static_cast<hipStream_t>(stream);
   rc = check_hip(delta::launch_states(a, p, bf16, st), "gated delta states launch");

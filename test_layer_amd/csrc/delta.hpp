@@ -35,7 +35,8 @@ struct Args {
   float* dbeta;
   float* dq_part;  // [n][hv][dk], where value heads share a key head
   float* dk_part;
-  int64_t n, per;  // per: tokens of a piece
+  uint32_t* cuts;  // NULL or [2][nseq]: the first piece of each sequence, its first chunk
+  int64_t n, per, pieces;  // per: tokens of a piece; pieces: room for
   int nseq, hk, hv, dk, dv;
   float scale;
 };
@@ -69,10 +70,14 @@ hipError_t launch_forward(const Args& a, const Plan& p, bool bf16, hipStream_t s
 // Bytes of a chunk's and head's shared matrices (keep: with the gradient's).
 size_t matrix_bytes(bool keep);
 
+// More sequences than a wave looks at by itself: their pieces' numbers are written down
+// beforehand (a launch more: 64 sequences of a token 21 us, 26 with it).
+inline bool needs_cuts(bool cu, int nseq) { return cu && nseq >= 256; }
+
 // The gradient: the state before every chunk, then the gradient of the state after
-// every chunk (and dfirst), then everything else chunk by chunk. Chunks of sequence
-// b are numbered from cu[b] / 32 + b on.
-inline int64_t chunk_slots(int64_t n, int nseq) { return n / 32 + nseq; }
+// every chunk (and dfirst), then everything else chunk by chunk. A sequence has a chunk
+// and a piece at least; where sequences share no rows, their numbers are below these.
+__host__ __device__ constexpr int64_t chunk_slots(int64_t n, int nseq) { return n / 32 + nseq; }
 hipError_t launch_states(const Args& a, const Plan& p, bool bf16, hipStream_t stream);
 hipError_t launch_back(const Args& a, const Plan& p, bool bf16, hipStream_t stream);
 hipError_t launch_grad(const Args& a, bool bf16, hipStream_t stream);

@@ -133,7 +133,7 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
   const int c = lane % 16, q = lane / 16;
   const int h = blockIdx.x % a.hv;
   const int64_t slot = blockIdx.x / a.hv;
-  const Piece p = find_piece(a.cu, a.nseq, a.n, kChunk, slot, lane);
+  const Piece p = find_piece(a, kChunk, slot, lane);
   if (p.seg < 0 || p.len == 0) return;
   const int kh = h / (a.hv / a.hk), len = p.len;
   const int64_t ldk = (int64_t)a.hk * DK, ldv = (int64_t)a.hv * DV;

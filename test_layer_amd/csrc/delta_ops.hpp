@@ -10,6 +10,7 @@
 #pragma once
 
 #include "bf16_ops.hpp"
+#include "delta.hpp"
 
 namespace vggt3 {
 namespace delta {
@@ -367,58 +368,161 @@ __device__ __forceinline__ uint32_t bound(const int32_t* cu, uint32_t i, uint32_
   return v < 0 ? 0 : (uint32_t)v > n ? n : (uint32_t)v;
 }
 
+// Sums over the lanes before and with each.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ uint32_t lanes_down(uint32_t x) {
+  return x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ uint32_t running_count(uint32_t x) {
+  x = lanes_down<0x111>(x);  // one lane down, within 16; then 2, 4, 8
+  x = lanes_down<0x112>(x);
+  x = lanes_down<0x114>(x);
+  x = lanes_down<0x118>(x);
+  x = lanes_down<0x142, 0xa>(x);  // every first 16's sum to the second's lanes
+  return lanes_down<0x143, 0xc>(x);  // the first 32's to the others
+}
+
+// Pieces of `per` tokens that a sequence has; an empty one has one of no tokens.
+__device__ __forceinline__ uint32_t pieces_of(uint32_t begin, uint32_t end, uint32_t per) {
+  return end > begin ? (end - begin - 1) / per + 1 : 1;
+}
+
+// A sequence: its rows begin .. end - 1, and the numbers of its first piece and chunk.
+// They rise from sequence to sequence, whatever the order of their rows.
+struct Sequence {
+  uint32_t begin, end, piece, chunk;
+  int b;
+};
+// Fewer than 64 K sequences, K neighbours a lane. Where no boundary is below the one
+// before it, begin / per + b leaves room for every sequence's last, shorter piece; pieces
+// are counted otherwise. (Counting always would do, but pieces are a wave each and start in
+// the order of their numbers: 10 ragged sequences of 24 views in fp32 463 us, counted 557,
+// where the last ones wait for longer pieces.)
+template <int K>
+struct Lanes {
+  uint32_t at[K + 1], piece[K], chunk[K];
+};
+template <int K>
+__device__ __forceinline__ Lanes<K> lanes_of(const Args& a, uint32_t per, int lane) {
+  Lanes<K> s;
+  bool back = false;
+#pragma unroll
+  for (int i = 0; i <= K; ++i) s.at[i] = bound(a.cu, min(K * lane + i, a.nseq), (uint32_t)a.n);
+#pragma unroll
+  for (int i = 0; i < K; ++i) back = back || s.at[i + 1] < s.at[i];
+  if (!__ballot(back)) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      s.piece[i] = s.at[i] / per + K * lane + i;
+      s.chunk[i] = s.at[i] / kChunk + K * lane + i;
+    }
+    return s;
+  }
+  uint32_t pieces = 0, chunks = 0;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    s.piece[i] = pieces;
+    s.chunk[i] = chunks;
+    if (K * lane + i < a.nseq) {
+      pieces += pieces_of(s.at[i], s.at[i + 1], per);
+      chunks += pieces_of(s.at[i], s.at[i + 1], kChunk);
+    }
+  }
+  pieces = running_count(pieces) - pieces;
+  chunks = running_count(chunks) - chunks;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    s.piece[i] += pieces;
+    s.chunk[i] += chunks;
+  }
+  return s;
+}
+template <int K>
+__device__ __forceinline__ Sequence sequence_of(const Lanes<K>& s, int b) {
+  Lanes<1> x{{s.at[0], s.at[1]}, {s.piece[0]}, {s.chunk[0]}};
+#pragma unroll
+  for (int i = 1; i < K; ++i)
+    if (b % K == i) x = Lanes<1>{{s.at[i], s.at[i + 1]}, {s.piece[i]}, {s.chunk[i]}};
+  Sequence o;
+  o.begin = __builtin_amdgcn_readlane(x.at[0], b / K);
+  o.end = __builtin_amdgcn_readlane(x.at[1], b / K);
+  o.piece = __builtin_amdgcn_readlane(x.piece[0], b / K);
+  o.chunk = __builtin_amdgcn_readlane(x.chunk[0], b / K);
+  o.b = b;
+  return o;
+}
+// The sequence whose pieces include `sid`, or the last that begins before it.
+template <int K>
+__device__ __forceinline__ Sequence sequence_with(const Args& a, uint32_t per, uint32_t sid, int lane) {
+  const Lanes<K> s = lanes_of<K>(a, per, lane);
+  int found = 0;
+#pragma unroll
+  for (int i = 0; i < K; ++i) found += __popcll(__ballot(K * lane + i < a.nseq && s.piece[i] <= sid));
+  return sequence_of(s, (int)uniform(found > 0 ? found - 1 : 0));
+}
+__device__ __forceinline__ Sequence noted_sequence(const Args& a, uint32_t per, int b) {
+  Sequence s;
+  s.begin = uniform(bound(a.cu, b, (uint32_t)a.n));
+  s.end = uniform(bound(a.cu, b + 1, (uint32_t)a.n));
+  s.chunk = uniform(a.cuts[a.nseq + b]);
+  s.piece = per == kChunk ? s.chunk : uniform(a.cuts[b]);
+  s.b = b;
+  return s;
+}
+__device__ __forceinline__ Sequence sequence(const Args& a, uint32_t per, int b, int lane) {
+  if (a.cu == nullptr) return Sequence{0, (uint32_t)a.n, 0, 0, 0};
+  if (a.cuts) return noted_sequence(a, per, b);
+  return a.nseq < 64 ? sequence_of(lanes_of<1>(a, per, lane), b) : sequence_of(lanes_of<4>(a, per, lane), b);
+}
+
 // A sequence's piece: rows first .. first + len - 1, piece `seg` of `segs` of
-// sequence b, whose first row is `begin`. seg < 0: there is no such piece.
+// sequence b, whose chunks are numbered from `slot` on. seg < 0: there is no such piece.
 struct Piece {
-  int64_t first, begin;
+  int64_t first, slot;
   int len, b, seg, segs;
 };
 
-// Piece `sid`: sequence b's pieces of `per` tokens are numbered from
-// cu[b] / per + b on, which leaves room for each sequence's last, shorter piece (an
-// empty sequence has one piece of no tokens). Up to 63 sequences are looked at at once,
-// a boundary a lane, in one trip to memory; more by a 64-ary search.
-__device__ __forceinline__ Piece find_piece(const int32_t* cu, int nseq, int64_t rows, int64_t tokens, int64_t id, int lane) {
-  const uint32_t n = (uint32_t)rows, per = (uint32_t)tokens, sid = (uint32_t)id;
-  Piece p;
-  uint32_t begin, end;
-  if (cu == nullptr) {
-    p.b = 0;
-    begin = 0;
-    end = n;
-  } else if (nseq < 64) {
-    const uint32_t at = lane < nseq ? lane : nseq, v = bound(cu, at, n);
-    const uint32_t found = __popcll(__ballot(lane < nseq && v / per + at <= sid));
-    p.b = (int)uniform(found > 0 ? found - 1 : 0);
-    begin = __builtin_amdgcn_readlane(v, p.b);
-    end = __builtin_amdgcn_readlane(v, p.b + 1);
+// Piece `sid` of `tokens` tokens each. Up to 255 sequences are looked at at once, in one
+// trip to memory; more by a 64-ary search in their noted numbers. (Where
+// sequences share rows, against the rule, there may be more chunks than room for them:
+// those are left out.)
+__device__ __forceinline__ Piece find_piece(const Args& a, int64_t tokens, int64_t id, int lane) {
+  const uint32_t per = (uint32_t)tokens, sid = (uint32_t)id;
+  Sequence s;
+  if (a.cu == nullptr) {
+    s = Sequence{0, (uint32_t)a.n, 0, 0, 0};
+  } else if (a.cuts == nullptr) {
+    s = a.nseq < 64 ? sequence_with<1>(a, per, sid, lane) : sequence_with<4>(a, per, sid, lane);
   } else {
-    uint32_t lo = 0, size = nseq;
+    const uint32_t* first = per == kChunk ? a.cuts + a.nseq : a.cuts;
+    uint32_t lo = 0, size = a.nseq;
     while (size > 1) {
       const uint32_t stride = (size + 63) / 64, at = lo + lane * stride;
-      const bool before = lane * stride < size && bound(cu, at, n) / per + at <= sid;
+      const bool before = lane * stride < size && first[at] <= sid;
       const uint32_t found = __popcll(__ballot(before));
       lo += (found > 0 ? found - 1 : 0) * stride;
       size = size < stride ? size : stride;
-      if (lo + size > (uint32_t)nseq) size = nseq - lo;
+      if (lo + size > (uint32_t)a.nseq) size = a.nseq - lo;
     }
-    p.b = (int)uniform(lo);
-    begin = uniform(bound(cu, p.b, n));
-    end = uniform(bound(cu, p.b + 1, n));
+    s = noted_sequence(a, per, (int)uniform(lo));
   }
-  const uint32_t len = end > begin ? end - begin : 0;
-  p.begin = begin;
-  p.seg = (int)(sid - (begin / per + p.b));
-  p.segs = len > 0 ? (int)(len / per + (len % per != 0)) : 1;
-  if (p.seg < 0 || p.seg >= p.segs) {
+  const uint32_t len = s.end > s.begin ? s.end - s.begin : 0;
+  Piece p;
+  p.b = s.b;
+  p.seg = sid < s.piece ? -1 : (int)(sid - s.piece);
+  p.segs = (int)pieces_of(s.begin, s.end, per);
+  const uint32_t before = (uint32_t)p.seg * per;
+  p.slot = (int64_t)s.chunk + before / kChunk;
+  const int64_t room = chunk_slots(a.n, a.nseq) - p.slot;
+  if (p.seg < 0 || p.seg >= p.segs || room < 1) {
     p.seg = -1;
-    p.first = begin;
+    p.first = s.begin;
     p.len = 0;
     return p;
   }
-  const uint32_t before = (uint32_t)p.seg * per, left = len - before;
-  p.first = begin + before;
-  p.len = (int)(left < per ? left : per);
+  const uint32_t left = len - before, some = left < per ? left : per;
+  p.first = (int64_t)s.begin + before;
+  p.len = (int)(some < room * kChunk ? some : room * kChunk);
   return p;
 }
 

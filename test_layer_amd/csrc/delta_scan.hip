@@ -46,7 +46,7 @@ __global__ __launch_bounds__(256) void matrices_kernel(const Args a) {
   const int c = lane % 16, q = lane / 16;
   const uint32_t id = blockIdx.x * 4 + wave, slot = id / a.hv;
   const int h = (int)(id % a.hv);
-  const Piece p = find_piece(a.cu, a.nseq, a.n, kChunk, slot, lane);
+  const Piece p = find_piece(a, kChunk, slot, lane);
   if (p.seg < 0 || p.len == 0) return;
   const int64_t ld = (int64_t)a.hk * DK;
   const int64_t at = p.first * ld + h / (a.hv / a.hk) * DK;
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
   const int c = lane % 16, q = lane / 16;
   const int h = blockIdx.x % a.hv;
   const int64_t sid = blockIdx.x / a.hv;
-  const Piece p = find_piece(a.cu, a.nseq, a.n, a.per, sid, lane);
+  const Piece p = find_piece(a, a.per, sid, lane);
   if (p.seg < 0) return;
   if (MODE == kSummary && p.seg == p.segs - 1) return;  // nothing follows it
   // this lane's columns: NCT neighbours
@@ -161,7 +161,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void scan_k
   const int64_t ldq = (int64_t)a.hk * DK, ldv = (int64_t)a.hv * DV;
   const int kh = h / (a.hv / a.hk);
   const int chunks = (p.len + kChunk - 1) / kChunk;
-  const int64_t slot0 = p.begin / kChunk + p.b + (p.first - p.begin) / kChunk;
+  const int64_t slot0 = p.slot;
   const int koff = (int)((c * ldq + 8 * q) * kB), knext = (int)(16 * ldq * kB);
   const int voff = (int)((4 * q * ldv + NCT * c) * kB), vrow = (int)(ldv * kB);
 
@@ -351,7 +351,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void back_k
   const int c = lane % 16, q = lane / 16;
   const int h = blockIdx.x % a.hv;
   const int64_t sid = blockIdx.x / a.hv;
-  const Piece p = find_piece(a.cu, a.nseq, a.n, a.per, sid, lane);
+  const Piece p = find_piece(a, a.per, sid, lane);
   if (p.seg < 0) return;
   if (MODE == kBackSummary && p.seg == 0) return;  // nothing lies before it
   const int col0 = blockIdx.y * 64 + wave * 16 * NCT, col = col0 + NCT * c;
@@ -375,7 +375,7 @@ __global__ __launch_bounds__(64 * (4 / NCT), DK * NCT <= 64 ? 2 : 1) void back_k
   const int64_t ldq = (int64_t)a.hk * DK, ldv = (int64_t)a.hv * DV;
   const int kh = h / (a.hv / a.hk);
   const int chunks = (p.len + kChunk - 1) / kChunk;
-  const int64_t slot0 = p.begin / kChunk + p.b + (p.first - p.begin) / kChunk;
+  const int64_t slot0 = p.slot;
   const int koff = (int)((c * ldq + 8 * q) * kB), knext = (int)(16 * ldq * kB);
   const int voff = (int)((4 * q * ldv + NCT * c) * kB), vrow = (int)(ldv * kB);
 
@@ -514,11 +514,10 @@ __global__ __launch_bounds__(4 * DK) void join_kernel(const Args a) {
   const int c = lane % 16, q = lane / 16;
   const int h = blockIdx.x % a.hv, b = blockIdx.x / a.hv;
   const int col = blockIdx.y * 16 + c;
-  const uint32_t n = (uint32_t)a.n, per = (uint32_t)a.per;
-  const uint32_t begin = uniform(bound(a.cu, b, n)), end = uniform(bound(a.cu, b + 1, n));
-  const int segs = end > begin ? (int)((end - begin - 1) / per + 1) : 0;
-  if (segs < 2) return;
-  const int64_t sid = begin / per + b;
+  const Sequence seq = sequence(a, (uint32_t)a.per, b, lane);
+  const int segs = (int)pieces_of(seq.begin, seq.end, (uint32_t)a.per);
+  const int64_t sid = seq.piece;
+  if (segs < 2 || sid + segs > a.pieces) return;
   const float* from = BACK ? a.dlast : a.state;
   const int64_t own = (int64_t)channel(wave, 4 * q) * DV + col;  // its 4 rows are neighbours
   const int64_t mine = (int64_t)channel(wave, c) * DK + 8 * q;
@@ -579,6 +578,54 @@ __global__ __launch_bounds__(4 * DK) void join_kernel(const Args a) {
   }
 }
 
+// The first pieces and chunks of many sequences: 4 sequences a thread, 4096 a turn.
+// (Counts past the room there is, of sequences that share rows, stay at it.)
+__global__ __launch_bounds__(1024) void cuts_kernel(const Args a) {
+  __shared__ uint64_t sums[2][2][16];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const uint32_t n = (uint32_t)a.n, per = (uint32_t)a.per;
+  const uint64_t room[2] = {(uint64_t)a.pieces, (uint64_t)chunk_slots(a.n, a.nseq)};
+  uint64_t before[2] = {0, 0};
+  for (int64_t base = 0, turn = 0; base < a.nseq; base += 4096, turn ^= 1) {
+    const int64_t b = base + 4 * threadIdx.x;
+    uint32_t v[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = b + i <= a.nseq ? bound(a.cu, (uint32_t)(b + i), n) : 0;
+    uint64_t count[2][4], all[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      all[j] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        count[j][i] = b + i < a.nseq ? pieces_of(v[i], v[i + 1], j == 0 ? per : (uint32_t)kChunk) : 0;
+        all[j] += count[j][i];
+      }
+      uint64_t x = all[j];
+#pragma unroll
+      for (int off = 1; off < 64; off *= 2) {
+        const uint64_t y = __shfl_up(x, off, 64);
+        if (lane >= off) x += y;
+      }
+      if (lane == 63) sums[turn][j][wave] = x;
+      all[j] = x - all[j];  // of the lanes before
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint64_t at = before[j] + all[j];
+      for (int w = 0; w < 16; ++w) {
+        if (w < wave) at += sums[turn][j][w];
+        before[j] += sums[turn][j][w];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (b + i < a.nseq) a.cuts[j * (int64_t)a.nseq + b + i] = (uint32_t)(at < room[j] ? at : room[j]);
+        at += count[j][i];
+      }
+    }
+  }
+}
+
 template <class T, int DK, bool KEEP>
 hipError_t run_matrices(const Args& a, hipStream_t stream) {
   const int64_t waves = chunk_slots(a.n, a.nseq) * a.hv;
@@ -590,6 +637,10 @@ template <class T, int DK, int DV, int NCT, Mode MODE>
 hipError_t run_forward(const Args& a, const Plan& p, hipStream_t stream) {
   constexpr int kThreads = 64 * (4 / NCT);
   const unsigned x = (unsigned)(p.pieces * a.hv);
+  if (a.cuts) {
+    cuts_kernel<<<1, 1024, 0, stream>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
   if (hipError_t e = run_matrices<T, DK, MODE == kStates>(a, stream)) return e;
   if (p.split) {
     scan_kernel<T, DK, DV, NCT, kSummary><<<dim3(x, (DV + DK) / 64), kThreads, 0, stream>>>(a);
