@@ -538,27 +538,23 @@ __global__ __launch_bounds__(DV, 1) void grad_kernel(const Args a) {
   }
 }
 
-// dq, dk of key heads that several value heads share, in the heads' order. Rows of
-// no sequence are left as they are.
+// dq, dk of key heads that several value heads share, in the heads' order, a chunk's rows
+// a workgroup. Rows of no sequence are of no chunk.
 template <class T>
 __global__ __launch_bounds__(256) void group_kernel(const Args a) {
+  const Piece p = find_piece(a, kChunk, blockIdx.x, threadIdx.x % 64);
   const int group = a.hv / a.hk, width = a.hk * a.dk;
   const float* from = blockIdx.y ? a.dk_part : a.dq_part;
   T* to = static_cast<T*>(blockIdx.y ? a.dk_out : a.dq);
-  if (to == nullptr) return;
-  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
-    bool inside = a.cu == nullptr;
-    for (int b = threadIdx.x; !inside && b < a.nseq; b += 256)
-      inside = row >= bound(a.cu, b, a.n) && row < bound(a.cu, b + 1, a.n);
-    if (!__syncthreads_or(inside)) continue;
-    for (int i = 4 * threadIdx.x; i < width; i += 1024) {
-      const int kh = i / a.dk, ch = i % a.dk;
-      f32x4 s = zero4();
-      for (int g = 0; g < group; ++g)
-        s += *reinterpret_cast<const f32x4*>(from + (row * a.hv + kh * group + g) * a.dk + ch);
-      const float w[4] = {s[0], s[1], s[2], s[3]};
-      store_n<4>(to + row * width + i, w);
-    }
+  if (p.seg < 0 || to == nullptr) return;
+  for (int at = 4 * threadIdx.x; at < p.len * width; at += 1024) {
+    const int64_t row = p.first + at / width;
+    const int i = at % width, kh = i / a.dk, ch = i % a.dk;
+    f32x4 s = zero4();
+    for (int g = 0; g < group; ++g)
+      s += *reinterpret_cast<const f32x4*>(from + (row * a.hv + kh * group + g) * a.dk + ch);
+    const float w[4] = {s[0], s[1], s[2], s[3]};
+    store_n<4>(to + row * width + i, w);
   }
 }
 
@@ -572,7 +568,7 @@ hipError_t grad_of(const Args& a, hipStream_t s) {
   hipError_t e = a.dk == 64 ? (a.dv == 64 ? run<T, 64, 64>(a, s) : run<T, 64, 128>(a, s))
                             : (a.dv == 64 ? run<T, 128, 64>(a, s) : run<T, 128, 128>(a, s));
   if (e != hipSuccess || a.dq_part == nullptr || (a.dq == nullptr && a.dk_out == nullptr)) return e;
-  group_kernel<T><<<dim3((unsigned)(a.n < 65536 ? a.n : 65536), 2), 256, 0, s>>>(a);
+  group_kernel<T><<<dim3((unsigned)chunk_slots(a.n, a.nseq), 2), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -75,3 +75,15 @@ def test_the_same_sequences_in_both_orders(lens, dtype):
         for x, y in zip(a, b):
             assert torch.isfinite(x).all()
             assert torch.equal(x, y if x.dim() == 2 else y[turn])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_heads_in_many_sequences(dtype):
+    # a shared key head's gradients in more sequences than a workgroup has threads, and rows of no sequence behind them
+    lens = np.random.default_rng(9).integers(0, 4, 3000).tolist()
+    lens[1234], lens[2999] = 100, 33
+    c = _case(lens, 1, 2, 64, 64, dtype, state=False, seed=9, behind=40)
+    out = tla.GatedDeltaGrads(*(torch.full_like(c[x], 5.0) for x in ("q", "k", "v", "g", "beta")))
+    got = _check_grad(c, out=out)
+    for x in got[:5]:
+        assert (x[c["n"]:] == 5.0).all()
