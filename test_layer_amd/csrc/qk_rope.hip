@@ -291,7 +291,10 @@ __device__ __forceinline__ float normalise(const Args& a, float* f, float* s, co
 #pragma unroll
   for (int v = 0; v < 4; ++v) x += f[v] * f[v] + s[v] * s[v];
   x = head_sum<LANES>(x);
-  if constexpr (NORM == kL2) return 1.0f / fmaxf(sqrtf(x), a.eps);
+  if constexpr (NORM == kL2) {
+    const float length = sqrtf(x);
+    return 1.0f / (length < a.eps ? a.eps : length);  // (the larger one, and NaN of a length that is)
+  }
   return __builtin_amdgcn_rsqf(x * inv_d + a.eps);
 }
 
