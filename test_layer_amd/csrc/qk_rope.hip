@@ -74,6 +74,7 @@ __device__ __forceinline__ Pair pair_of(const Args& a, int at) {
 // rotated are paired so that they lie as the others do.
 struct Pairs {
   int first[4], second[4];
+  bool turned[4];
 };
 // Pair v of a lane: 4 neighbours, or where pairs lie anyhow every LANES-th, so that
 // the lanes' values are neighbours.
@@ -88,7 +89,8 @@ __device__ __forceinline__ Pairs pairs_of(const Args& a, int lane_in_head) {
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int at = pair_at<A, LANES>(lane_in_head, v);
-    if (at < a.rotated) {
+    p.turned[v] = at < a.rotated;
+    if (p.turned[v]) {
       const Pair x = pair_of(a, at);
       p.first[v] = x.first;
       p.second[v] = x.second;
@@ -156,6 +158,14 @@ struct Rotation {
     return t;
   }
 };
+
+// A pair rotated. Channels that are not have nothing to do with the one that they are
+// paired with: 0 times it would be NaN where it is Inf or NaN.
+__device__ __forceinline__ void turn(bool turned, float c, float s, float& a, float& b) {
+  const float x = a * c - b * s, y = b * c + a * s;
+  a = turned ? x : a;
+  b = turned ? y : b;
+}
 
 // A lane's 8 channels of a head as runs: how many, of how many values, and where they
 // start in the head's row in bytes (behind every row's end where there is none: the
@@ -362,11 +372,7 @@ __global__ __launch_bounds__(256) void forward_kernel(const Args a) {
             }
           }
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float m = u[v] * t.c[v] - z[v] * t.s[v];
-            z[v] = z[v] * t.c[v] + u[v] * t.s[v];
-            u[v] = m;
-          }
+          for (int v = 0; v < 4; ++v) turn(p.turned[v], t.c[v], t.s[v], u[v], z[v]);
           runs.store(y[side], (base + j * kHeads + head) * row, u, z);
         }
     }
@@ -420,11 +426,7 @@ __global__ __launch_bounds__(256) void grad_kernel(const Args a) {
         float ef[4], es[4];
         runs.values(ef, es, ry[side]);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float m = ef[v] * t.c[v] + es[v] * t.s[v];
-          es[v] = es[v] * t.c[v] - ef[v] * t.s[v];
-          ef[v] = m;
-        }
+        for (int v = 0; v < 4; ++v) turn(p.turned[v], t.c[v], -t.s[v], ef[v], es[v]);
         if constexpr (NORM != kNone) {
           float f[4], s[4];
           runs.values(f, s, rx[side]);

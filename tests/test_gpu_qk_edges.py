@@ -38,3 +38,57 @@ def test_length_of_a_head_with_nan(d, sections, interleaved, dtype):
         for got, want in ((tla.qk_norm_rope(bad, None, heads, **rest)[0], y),
                           (tla.qk_norm_rope_grad(bad, None, dy, None, heads, **rest).dq, g)):
             assert torch.isnan(got[spoilt]).all() and torch.equal(got[~spoilt], want[~spoilt])
+
+
+def _partners(d, sections, interleaved):
+    """The channels that each channel's result is made of, axis by axis (per_axis)."""
+    of = {ch: {ch} for ch in range(d)}
+    off = 0
+    for c in sections:
+        for j in range(c):
+            a, b = (off + 2 * j, off + 2 * j + 1) if interleaved else (off + j, off + j + c)
+            of[a] = of[b] = {a, b}
+        off += 2 * c
+    return of
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,sections,interleaved", [s for s in SHAPES if s[1]], ids=str)
+def test_channels_that_are_not_rotated_are_their_own(d, sections, interleaved, dtype):
+    # no norm: a value that is not finite spoils its pair's channels, and of channels that are not rotated itself alone
+    n = 5
+    x, dy = (_randn(n, d, seed=s, dtype=DT[dtype]) for s in (4, 5))
+    rest = dict(norm=None, pos=_pos(n, sections) * 2 + 1, sections=sections, interleaved=interleaved)
+    y, _ = tla.qk_norm_rope(x, None, 1, **rest)
+    g = tla.qk_norm_rope_grad(x, None, dy, None, 1, **rest).dq
+    of = _partners(d, sections, interleaved)
+    for ch in range(d):
+        bad_x, bad_dy = x.clone(), dy.clone()
+        bad_x[2, ch], bad_dy[2, ch] = float("inf"), float("nan")
+        mine = torch.tensor([ch in of[c] for c in range(d)]).cuda()
+        for got, want in ((tla.qk_norm_rope(bad_x, None, 1, **rest)[0], y),
+                          (tla.qk_norm_rope_grad(x, None, bad_dy, None, 1, **rest).dq, g)):
+            assert torch.equal(got[2, ~mine], want[2, ~mine]) and not torch.isfinite(got[2, mine]).any(), ch
+            assert torch.equal(got[[0, 1, 3, 4]], want[[0, 1, 3, 4]])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 63, 128, 104, 200, 7])
+def test_norms_alone_leave_channels_to_themselves(d, dtype):
+    # no rotation: an infinite value is NaN after an L2 norm, and the others 0; an infinite weight or bias is its own channel's
+    n = 5
+    x = _randn(n, d, seed=6, dtype=DT[dtype])
+    w, b = _randn(d, seed=7), _randn(d, seed=8)
+    rest = dict(norm="rms", eps=1e-6)
+    y, _ = tla.qk_norm_rope(x, None, 1, q_w=w, q_b=b, **rest)
+    for ch in range(d):
+        bad = x.clone()
+        bad[1, ch] = float("inf")
+        got, _ = tla.qk_norm_rope(bad, None, 1, norm="l2")
+        others = torch.arange(d, device="cuda") != ch
+        assert torch.isnan(got[1, ch]) and (got[1, others] == 0).all()
+        for name in ("q_w", "q_b"):
+            v = dict(q_w=w.clone(), q_b=b.clone())
+            v[name][ch] = float("inf")
+            got, _ = tla.qk_norm_rope(x, None, 1, **v, **rest)
+            assert torch.equal(got[:, others], y[:, others]) and torch.isinf(got[:, ch]).all()
