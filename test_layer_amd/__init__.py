@@ -851,12 +851,19 @@ def block_join_grad(r: torch.Tensor, f: Optional[torch.Tensor] = None, dr: Optio
 NORM_L2 = 3
 
 
+def _int32(name: str, x) -> int:
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7FFFFFFF:  # ctypes would pass on its low 32 bits
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
 _QK_NORMS = {**_NORMS, "l2": NORM_L2}
 
 
 def _qk_norm_code(kind) -> int:
     if kind is not None and not isinstance(kind, str):
-        return int(kind)
+        return _int32("norm", kind)
     if kind not in _QK_NORMS:
         raise KeyError(f"unknown norm {kind!r}; None, 'none', 'l2', 'rms' or 'layer'")
     return _QK_NORMS[kind]
@@ -894,15 +901,17 @@ def _check_gpu(dev: int, *ts) -> None:
 
 def _qk_inputs(q, k, n_heads, n_heads_k, pos, sections, weights):
     _check_tokens("q", q)
+    _check_width("q", q.shape[1])
     d = _heads_of("q", q, n_heads)
     hk = 0
     if k is not None:
         _check_tokens("k", k)
+        _check_width("k", k.shape[1])
         hk = n_heads if n_heads_k is None else n_heads_k
         if k.shape[0] != q.shape[0] or k.dtype != q.dtype:
             raise ValueError(f"k {tuple(k.shape)} {k.dtype} does not match q {tuple(q.shape)} {q.dtype}")
         _heads_of("k", k, hk, d)
-    sections = tuple(map(int, sections))
+    sections = tuple(_int32("sections", c) for c in sections)
     if bool(sections) != (pos is not None):
         raise ValueError("pos and sections go together")
     if pos is not None and (pos.dtype != torch.int32 or tuple(pos.shape) != (q.shape[0], len(sections))):
@@ -1022,6 +1031,8 @@ def _delta_inputs(q, k, v, g, beta, n_heads):
     _check_tokens("q", q)
     _check_same("k", k, q, "q")
     _check_tokens("v", v)
+    _check_width("q", q.shape[1])
+    _check_width("v", v.shape[1])
     n, dk = q.shape[0], _heads_of("q", q, n_heads)
     if v.shape[0] != n or v.dtype != q.dtype:
         raise ValueError(f"v {tuple(v.shape)} {v.dtype} does not match q {tuple(q.shape)} {q.dtype}")
