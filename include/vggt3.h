@@ -618,7 +618,8 @@ int vggt3_block_join_grad(const void* r, const void* f, const void* gate, int64_
  *               n_heads_k = 0: no keys. q_out, k_out have no gaps; q_out may be q
  *               and k_out k (in place) where these have none either.
  *   q_w .. k_b  NULL (1 / 0) or float32 [d_head] (RMS and layer norm).
- *   pos         int32 [n_tokens][n_axes], any values (angles are formed in 64 bits).
+ *   pos         int32 [n_tokens][n_axes], any values: angles are formed in two doubles and
+ *               right to an fp32 rounding of a part of a turn at all of them.
  *   sections    HOST int32 [n_axes]: pairs that each axis rotates, 1 or more; twice
  *               their sum at most d_head. Channels behind them are not rotated. 0
  *               axes: no rotation (pos and sections may be NULL).

@@ -68,7 +68,17 @@ qk::Args args_of(const Call& c, int32_t per_axis, int32_t interleaved) {
   }
   a.per_axis = per_axis != 0;
   a.interleaved = interleaved != 0;
-  a.log2_base = c.axes > 0 ? std::log2(c.base) : 0.0;
+  for (int i = 0; i < c.axes; ++i) {
+    const int size = a.per_axis ? c.sections[i] : a.rotated;
+    if (i > 0 && size == (a.per_axis ? c.sections[i - 1] : a.rotated)) {
+      a.step[i][0] = a.step[i - 1][0];
+      a.step[i][1] = a.step[i - 1][1];
+      continue;
+    }
+    const long double step = std::pow((long double)c.base, -1.0L / size);  // 64 bits: the two doubles hold them
+    a.step[i][0] = (double)step;
+    a.step[i][1] = (double)(step - a.step[i][0]);
+  }
   a.eps = c.eps;
   return a;
 }

@@ -33,7 +33,7 @@ struct Args {
   int rotated;          // their sum
   int per_axis;         // each axis has channels and a ladder of frequencies of its own
   int interleaved;      // pairs are neighbours; otherwise a half apart
-  double log2_base;
+  double step[kMaxAxes][2];  // base^(-1 / size) of each axis's ladder, in two doubles
   float eps;
 };
 

@@ -11,9 +11,10 @@
 // frequencies and weights over all tokens. A lane holds both channels of 4 pairs, so
 // that a rotation is its own, and the norm's sums over a head are a few DPP
 // steps over 8 to 64 lanes. 100 views of 16 + 16 heads of 64 in bf16: 214 us,
-// 5.3 TB/s, a copy's rate; 48 views' gradient 158 us. Angles are formed in 64 bits (in
-// 32 a position of a million is off by 0.06 of a radian) and reduced to a turn before the
-// sine, one pair a lane, and handed to the lanes that hold the pair.
+// 5.3 TB/s, a copy's rate; 48 views' gradient 158 us. Angles are formed in two doubles (in
+// one a position of 2^31 is off by 6 u, in 32 bits one of a million by 0.06 of a radian) and
+// reduced to a turn before the sine, one pair a lane, and handed to the lanes that hold the
+// pair.
 #include "qk.hpp"
 
 #include "delta_ops.hpp"
@@ -52,10 +53,25 @@ enum Access { kFours, kNeighbours, kStaged, kSingle };
 
 constexpr int kNowhere = 0x40000000;  // an offset behind every row's end
 
+// A value in two doubles, to about 100 bits. (Products and their roundings' rests must not
+// be contracted: the rest would count twice.)
+struct Two {
+  double hi, lo;
+};
+__device__ __forceinline__ Two operator*(const Two& x, const Two& y) {
+#pragma clang fp contract(off)
+  const double p = x.hi * y.hi;
+  const double e = fma(x.hi, y.lo, fma(x.lo, y.hi, fma(x.hi, y.hi, -p)));
+  Two z;
+  z.hi = p + e;
+  z.lo = e - (z.hi - p);
+  return z;
+}
+
 // A rotated pair: its channels, axis and turns a position step.
 struct Pair {
   int first, second, axis;
-  double turns;
+  Two turns;
 };
 __device__ __forceinline__ Pair pair_of(const Args& a, int at) {
   Pair p;
@@ -66,7 +82,12 @@ __device__ __forceinline__ Pair pair_of(const Args& a, int at) {
   p.first = off + (a.interleaved ? 2 * j : j);
   p.second = a.interleaved ? p.first + 1 : p.first + size;
   p.axis = axis;
-  p.turns = exp2(-a.log2_base * j / size) * 0.15915494309189533577;
+  p.turns = Two{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
+  Two step{a.step[axis][0], a.step[axis][1]};
+  for (int k = j; k > 0; k /= 2) {
+    if (k % 2) p.turns = p.turns * step;
+    if (k > 1) step = step * step;
+  }
   return p;
 }
 
@@ -103,10 +124,11 @@ __device__ __forceinline__ Pairs pairs_of(const Args& a, int lane_in_head) {
   return p;
 }
 
-__device__ __forceinline__ void angle_of(const Args& a, int axis, double turns, int64_t token, float& c, float& s) {
-  double x = a.pos[token * a.axes + axis] * turns;
-  x -= rint(x);
-  sincospif(2.0f * (float)x, &s, &c);
+__device__ __forceinline__ void angle_of(const Args& a, int axis, const Two& turns, int64_t token, float& c, float& s) {
+#pragma clang fp contract(off)
+  const double at = a.pos[token * a.axes + axis], x = at * turns.hi;
+  const double rest = fma(at, turns.lo, fma(at, turns.hi, -x));
+  sincospif(2.0f * (float)((x - rint(x)) + rest), &s, &c);
 }
 
 // The sines and cosines of a lane's 4 pairs at a token. Heads of up to 128 channels
@@ -118,12 +140,12 @@ template <Access A, int LANES>
 struct Rotation {
   static constexpr int kOwn = LANES <= 16 ? 1 : 4;
   int axis[kOwn];
-  double turns[kOwn];
+  Two turns[kOwn];
   __device__ __forceinline__ Rotation(const Args& a, int lane) {
 #pragma unroll
     for (int v = 0; v < kOwn; ++v) {
       axis[v] = 0;
-      turns[v] = 0.0;
+      turns[v] = Two{0.0, 0.0};
       const int at = kOwn == 1 ? lane : pair_at<A, LANES>(lane, v);
       if (at < a.rotated) {
         const Pair x = pair_of(a, at);

@@ -1,4 +1,8 @@
 """The query/key preparation and its gradient where values are not finite and where positions are far, on the GPU."""
+import math
+import random
+from decimal import Context, Decimal, localcontext
+
 import pytest
 import torch
 
@@ -92,3 +96,54 @@ def test_norms_alone_leave_channels_to_themselves(d, dtype):
             v[name][ch] = float("inf")
             got, _ = tla.qk_norm_rope(x, None, 1, **v, **rest)
             assert torch.equal(got[:, others], y[:, others]) and torch.isinf(got[:, ch]).all()
+
+
+TURN = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+def _turns(base, j, size):
+    """Turns a position step of pair j, to 60 digits."""
+    with localcontext(Context(prec=60)):
+        return (-Decimal(base).ln() * j / size).exp() / TURN
+
+
+@pytest.mark.parametrize("base", [1.0, 50.0, 100.0, 10000.0, 0.5])
+@pytest.mark.parametrize("d,sections,per_axis", [(64, (16, 16), True), (64, (12, 10, 10), True), (128, (40, 24), False), (512, (256,), True)],
+                         ids=str)
+def test_angles_of_far_positions(d, sections, per_axis, base):
+    # a rotated (1, 0) is (cos, sin) of the angle. Reduced to a part of a turn, that is rounded once to fp32 (2 pi 2^-26 =
+    # 1.6 u), sine and cosine by u each and the product with 1 not at all: 4 u, at any position. (Those taken here are the
+    # ones of many where one double's rounding of the pairs' turns shows most.)
+    axes = len(sections)
+    r = random.Random(d + axes)
+    rows = [[-2 ** 31] * axes, [2 ** 31 - 1] * axes]
+    sizes = [c if per_axis else sum(sections) for c in sections]
+    before = [0 if per_axis else sum(sections[:a]) for a in range(axes)]
+    turns = [[_turns(base, before[a] + j, sizes[a]) for j in range(c)] for a, c in enumerate(sections)]
+
+    def worst(t, count):
+        seen = [r.randrange(2 ** 30, 2 ** 31) * r.choice((1, -1)) for _ in range(count)]
+        return max(seen, key=lambda p: abs(Decimal(float(t) * p) - t * p))
+
+    with localcontext(Context(prec=60)):
+        for i in range(60):
+            rows.append([worst(turns[a][i % min(c, 6)], 50) for a, c in enumerate(sections)])
+        for i in range(20):
+            rows.append([r.randrange(-2 ** (i + 11), 2 ** (i + 11)) for _ in sections])
+        want_cos, want_sin = [], []
+        for row in rows:
+            t = [(p * x) % 1 for p, ts in zip(row, turns) for x in ts]
+            want_cos.append([math.cos(float(x * TURN)) for x in t])
+            want_sin.append([math.sin(float(x * TURN)) for x in t])
+    n, pairs = len(rows), sum(sections)
+    x = torch.zeros(n, d)
+    x[:, 0:2 * pairs:2] = 1.0
+    x = x.cuda()
+    rest = dict(norm=None, pos=torch.tensor(rows, dtype=torch.int32).cuda(), sections=sections, base=base, per_axis=per_axis,
+                interleaved=True)
+    y = tla.qk_norm_rope(x, None, 1, **rest)[0].double().cpu()[:, :2 * pairs]
+    g = tla.qk_norm_rope_grad(x, None, x, None, 1, **rest).dq.double().cpu()[:, :2 * pairs]
+    cos, sin = torch.tensor(want_cos, dtype=torch.float64), torch.tensor(want_sin, dtype=torch.float64)
+    for got, c, s in ((y, cos, sin), (g, cos, -sin)):
+        assert (got[:, 0::2] - c).abs().max() <= 4 * 2.0 ** -24
+        assert (got[:, 1::2] - s).abs().max() <= 4 * 2.0 ** -24
