@@ -21,8 +21,9 @@ constexpr int kPitch = D + 16 / (int)sizeof(T);
 // The gates that a chunk's columns use, by token. Its decay up to a token is
 // 2^(high + low): high a multiple of 2^-6, so that sums and differences of it are
 // exact (at most 32 * 2885 in size), low what that leaves, at most 2^-7 a token. So
-// the decay between two tokens is right whatever lies before them. (Below e^-2000 a
-// token's decay is 0 in either form.)
+// the decay between two tokens is right whatever lies before them, and by a power of 2
+// each, since their sum's rounding would show in it: 11 u at e^-20 (u = 2^-24), 44 u at
+// e^-80. (Below e^-2000 a token's decay is 0 in either form.)
 struct Rows {
   float decay[kChunk];  // from the chunk's start
   float rest[kChunk];   // to its end
@@ -46,7 +47,12 @@ __device__ __forceinline__ float running_sum(float x) {
   return x;
 }
 
+__device__ __forceinline__ float power(float high, float low) {
+  return __builtin_amdgcn_exp2f(high) * __builtin_amdgcn_exp2f(low);
+}
+
 __device__ __forceinline__ void put_rows(Rows& m, const Args& a, int64_t first, int len, int h, int lane) {
+#pragma clang fp contract(off)  // (g log2 e - high would have the product's rest, which low has by itself)
   const int t = lane % 32;
   float high = 0.0f, low = 0.0f, beta = 0.0f;
   if (t < len) {
@@ -56,7 +62,7 @@ __device__ __forceinline__ void put_rows(Rows& m, const Args& a, int64_t first, 
       constexpr float kLog2e = 1.44269502162933349609f, kMore = 1.92596299112661746887e-08f;  // their sum: log2 e
       const float x = g * kLog2e;
       high = __builtin_rintf(x * 64.0f) * 0.015625f;
-      low = (x - high) + __builtin_fmaf(g, kMore, __builtin_fmaf(g, kLog2e, -x));
+      low = __builtin_fmaf(g, kMore, __builtin_fmaf(g, kLog2e, -x)) + (x - high);  // (x - high is exact)
     }
     beta = a.beta[(first + t) * a.hv + h];
   }
@@ -67,12 +73,12 @@ __device__ __forceinline__ void put_rows(Rows& m, const Args& a, int64_t first, 
   const float end = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, high), 31)),
               more = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, low), 31));
   if (lane >= kChunk) return;
-  m.decay[lane] = __builtin_amdgcn_exp2f(high + low);
-  m.rest[lane] = __builtin_amdgcn_exp2f((end - high) + (more - low));
+  m.decay[lane] = power(high, low);
+  m.rest[lane] = power(end - high, more - low);
   m.beta[lane] = beta;
   m.high[lane] = high;
   m.low[lane] = low;
-  if (lane == 0) m.total = __builtin_amdgcn_exp2f(end + more);
+  if (lane == 0) m.total = power(end, more);
 }
 __device__ __forceinline__ f32x4 rows4(const float* v, int it, int q) {
   return *reinterpret_cast<const f32x4*>(v + 16 * it + 4 * q);
@@ -101,7 +107,7 @@ __device__ __forceinline__ Tri decays(const Rows& m, int lane) {
     const auto decay = [&](int i, int j) {
       const float hi = FORWARD ? he[i][r] : hc[i], li = FORWARD ? le[i][r] : lc[i];
       const float hj = FORWARD ? hc[j] : he[j][r], lj = FORWARD ? lc[j] : le[j][r];
-      return __builtin_amdgcn_exp2f((hi - hj) + (li - lj));
+      return power(hi - hj, li - lj);
     };
     d.t00[r] = decay(0, 0);
     d.t10[r] = decay(1, 0);

@@ -92,3 +92,25 @@ def test_strong_decays_among_weak_ones(dk, dv, dtype):
     c = _case([120, 50], dk, dv, dtype, [every(2, -20.0), every(7, -30.0), every(32, -12.0), every(5, -1e4), every(3, -float("inf"))], 3)
     got, _ = _check(c, dk, dv)
     assert (got[2::3, 4][:39] == 0).all()  # a token that forgets everything: 0, not what is left of a difference
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [0.3, 3.0, 20.0, 80.0])
+@pytest.mark.parametrize("n", [2, 32, 45])
+def test_decays_between_two_tokens(n, size, dtype):
+    # key 0 at a full step, read n - 1 tokens later, and the state: the decays of all tokens between, spread over 512 heads.
+    # A decay is two exps of 2 u and their product; up to 45 logarithms add in two floats (the lower ones below 2^-7 a token:
+    # 1 u in all), and a chunk's end is one more product: 8 u of the value at every size
+    heads = 512
+    g = torch.zeros(n, heads)
+    g[1:] = -torch.rand(n - 1, heads, generator=torch.Generator().manual_seed(n)) * size / (n - 1)
+    q, k = torch.zeros(n, heads, 64), torch.zeros(n, heads, 64)
+    q[-1, :, 0] = 1.0
+    k[torch.arange(n), :, torch.arange(n)] = 1.0
+    rows = [x.flatten(1).to(DT[dtype]).cuda() for x in (q, k, torch.ones(n, heads, 64))]
+    o, state = tla.gated_delta(*rows, g.cuda(), torch.ones(n, heads, device="cuda"), heads)
+    want = torch.exp(g.double().sum(0))
+    # bf16: a value below 2^-110 has parts below 2^-126, the least normal number, which count as 0: 2^-126 for each of two
+    half, least = (2.0 ** -8, 2.0 ** -125) if dtype == "bf16" else (0.0, 0.0)
+    assert ((state[0, :, 0, 0].double().cpu() - want).abs() <= 8 * U * want + least).all()
+    assert ((o.view(n, heads, 64)[-1, :, 0].double().cpu() - want).abs() <= (8 * U + half) * want + least).all()
