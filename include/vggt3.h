@@ -684,8 +684,9 @@ int vggt3_qk_norm_rope_grad(const void* q, int64_t q_stride, const void* k, int6
  *                the nearer of the two, a sequence that ends before it begins as empty;
  *                their rows may lie in any order, but sequences must not share rows:
  *                results of those that do are undefined.)
- *   max_seqlen   the longest sequence's length, or 0 if unknown. Only how the work is
- *                cut depends on it: a wrong one costs time, not results beyond rounding.
+ *   max_seqlen   the longest sequence's length, or 0 if unknown (then as long as all
+ *                rows). Only how the work is cut depends on it: a wrong one costs time, not
+ *                results beyond rounding.
  *   state, state_out   float32 [n_seqs][n_heads_v][d_k][d_v]: S before each
  *                sequence (NULL: 0) and after it (NULL: not wanted). state_out may be
  *                state.

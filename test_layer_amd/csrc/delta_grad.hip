@@ -18,17 +18,18 @@
 //
 // A wave has 64 value channels of a chunk and head, 4 neighbours a lane (u, x and the
 // row sums), then F and E, then its share of the key channels (dQ, dK). In bf16 all
-// fp32 operands are whole, in three parts (in two: 48 views' chunks 785 us for 900, but
+// fp32 operands are whole, in three parts (in two: 48 views' chunks 803 us for 928, but
 // more last bits of dQ and dK differ than an order of sums explains). u and dR change
 // from columns by lane to rows by lane through LDS; the triangles stay in registers.
 //
-// 48 views (65,952 tokens), 16 heads of 64 x 64 in bf16: 785 us, where four waves of 16
-// columns, which convert each triangle four times over, took 1300. The wave fills a
-// SIMD's registers, so nothing runs while it waits: S and dS are read once by columns
-// and once by rows, and of the second reading half comes from memory again (3.1 GB
-// fetched, 2.0 needed). Turning both in LDS instead saves that but takes 1070 us (its
-// writes and conflicts, and 45 registers spilled), asking for the next chunk's lines
-// ahead 950 (the L2 has no room for them).
+// 48 views (65,952 tokens), 16 heads of 64 x 64 in bf16: 888 to 928 us. The wave fills a
+// SIMD's registers, so nothing runs while it waits: 39% of its cycles are instructions (33%
+// vector), 13% wait to issue behind a product, 48% wait for memory and LDS. S and dS are read
+// once by columns and once by rows, and of the second reading half comes from memory again
+// (3.2 GB fetched, 2.0 needed; 0.47 written). With operands in two parts, 785 us: turning both
+// in LDS instead saves that but took 1070 (its writes and conflicts, and 45 registers spilled),
+// asking for the next chunk's lines ahead 950 (the L2 has no room for them), four waves of 16
+// columns, which convert each triangle four times over, 1300.
 #include <type_traits>
 
 #include "delta_chunk.hpp"

@@ -24,13 +24,14 @@
 // pieces, and the main pass starts each piece from its own first state. (A
 // sequence's first piece starts from the sequence's first state in both passes.)
 //
-// 100 views (137,400 tokens) as one sequence, 16 heads of 64 x 64 in bf16: 183 us for
-// the matrices (1.06 GB, 5.8 TB/s: memory), 460 to 540 for the summary, 53 for the join,
-// 370 for the main pass. The scans are bound by vector instructions: fp32 values are cut
-// into 3 bf16 parts before each product (48 views' states: 34 million vector
-// instructions of 4 cycles, 4.8 million products of 16), and with one wave a SIMD, whose
-// registers 64 columns of S fill, neither hides the other. Two waves a SIMD of 32
-// columns, interleaved products, or S held in parts were not faster.
+// 100 views (137,400 tokens) as one sequence, 16 heads of 64 x 64 in bf16: 179 to 202 us
+// for the matrices (1.1 GB: memory), 453 to 541 for the summary, 52 for the join, 367 to
+// 427 for the main pass. One wave a SIMD, whose registers 64 columns of S fill, so a wave's
+// waiting is the SIMD's. Its cycles, by counters: 59% (main pass) and 65% (summary) vector
+// instructions, most of which cut fp32 values into 3 bf16 parts before each product, 6 and 7%
+// others, 24 and 20% waiting to issue behind a product that is not done, 11 and 8% waiting for
+// memory and LDS. (48 views' states: 54, 6, 16 and 24%, on 768 waves for 1024 SIMDs.) Two
+// waves a SIMD of 32 columns, interleaved products, or S held in parts were not faster.
 #include "delta_chunk.hpp"
 
 namespace vggt3 {
@@ -699,16 +700,16 @@ hipError_t launch_back(const Args& a, const Plan& p, bool bf16, hipStream_t stre
 size_t matrix_bytes(bool keep) { return matrices_bytes(keep); }
 
 // Wide waves pay where they alone fill the GPU: against narrow ones a 100-view scene takes
-// 1020 us (1460), 48 views' gradient 1370 (1620), 24 views in fp32 461 (540), and 12
-// views with heads of 128, below the limit, 926 (645). Where narrow ones need no cut,
-// they have to fill half of it (32 sequences of 1374 tokens, 16 heads: 228 us, their
-// gradient 904, narrow 283 and 1010; 24 of them 315 and 983, narrow 246 and 861).
-// Pieces are as long as fill the GPU with waves (one a SIMD where they are wide: 1020 us
-// for the scene, with half or twice as many 1090; half as many narrow ones: 645 us with
-// heads of 128, with one a SIMD 1010), at least 3 chunks (one view's gradient 138 us; of
-// 2: 160, of 4: 146). Sequences are cut only where much longer than that, since a cut
-// costs a pass over all pieces with d_k more columns (48 views of 48 sequences uncut
-// 1370 us, cut 1645; 24 views in 10 sequences cut 461, uncut 1170).
+// 1025 us (1467), 48 views' gradient 1520 (1762), 24 views in fp32 462 (549), and 12
+// views with heads of 128, below the limit, 978 (698). Where narrow ones need no cut,
+// they have to fill half of it (32 sequences of 1374 tokens, 16 heads: 302 us, their
+// gradient 1100, narrow 313 and 1196; 24 of them 300 and 1053, narrow 276 and 993).
+// Pieces are as long as fill the GPU with waves (one a SIMD where they are wide: 1025 us
+// for the scene, with half as many 1166, with twice as many 1085; half as many narrow
+// ones: 698 us with heads of 128, with one a SIMD 1095), at least 3 chunks (one view's
+// gradient 141 us; of 2: 164, of 4: 149). Sequences are cut only where much longer than
+// that, since a cut costs a pass over all pieces with d_k more columns (48 views of 48
+// sequences uncut 1520 us, cut 1796; 24 views in 10 sequences cut 462, uncut 529).
 Plan plan(int64_t n, int nseq, int64_t longest, int hv, int dk, int dv) {
   const int64_t chunks = (n + kChunk - 1) / kChunk, rows = (int64_t)hv * (dv / 64);
   Plan p;

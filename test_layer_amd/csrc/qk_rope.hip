@@ -11,7 +11,7 @@
 // frequencies and weights over all tokens. A lane holds both channels of 4 pairs, so
 // that a rotation is its own, and the norm's sums over a head are a few DPP
 // steps over 8 to 64 lanes. 100 views of 16 + 16 heads of 64 in bf16: 214 us,
-// 5.3 TB/s, a copy's rate; 48 views' gradient 158 us. Angles are formed in two doubles (in
+// 5.3 TB/s, a copy's rate; 48 views' gradient 154 us. Angles are formed in two doubles (in
 // one a position of 2^31 is off by 6 u, in 32 bits one of a million by 0.06 of a radian) and
 // reduced to a turn before the sine, one pair a lane, and handed to the lanes that hold the
 // pair.
