@@ -87,3 +87,37 @@ def test_shared_heads_in_many_sequences(dtype):
     got = _check_grad(c, out=out)
     for x in got[:5]:
         assert (x[c["n"]:] == 5.0).all()
+
+
+@pytest.mark.parametrize("nseq", [40, 100, 300])
+def test_boundaries_that_change_between_replays(nseq):
+    # a captured call whose boundaries' tensor gets other values, in order and not: numbers are counted anew each time
+    n = 900
+    c = _ordered([0] * nseq + [n], n, 1, 2, 64, 64, "f32", 4)
+    r = np.random.default_rng(nseq)
+
+    def order(turn):
+        ends = np.sort(r.integers(0, n + 1, nseq // 2 + 1))
+        cu = np.concatenate([[x, y] for x, y in zip(ends, ends[1:])][::-1 if turn % 2 else 1])
+        return torch.tensor(np.concatenate([cu, np.repeat(cu[-1], nseq + 1 - len(cu))]), dtype=torch.int32)
+
+    def run():
+        args = (c["q"], c["k"], c["v"], c["g"], c["beta"])
+        kw = dict(state=c["state"], cu_seqlens=c["cu"])
+        o = torch.zeros_like(c["v"])
+        out = tla.GatedDeltaGrads(*(torch.zeros_like(c[x]) for x in ("q", "k", "v", "g", "beta")), torch.empty_like(c["state"]))
+        o, s = tla.gated_delta(*args, 1, out=o, **kw)
+        return o, s, *tla.gated_delta_grad(*args, c["do"], 1, dstate=c["dstate"], out=out, **kw)
+
+    c["cu"].copy_(order(0))
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run()
+    for turn in range(5):
+        c["cu"].copy_(order(turn))
+        g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, run()):
+            assert torch.isfinite(x).all() and torch.equal(x, y), turn
