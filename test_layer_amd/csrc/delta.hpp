@@ -71,12 +71,12 @@ hipError_t launch_forward(const Args& a, const Plan& p, bool bf16, hipStream_t s
 size_t matrix_bytes(bool keep);
 
 // More sequences than a wave looks at by itself: their pieces' numbers are written down
-// beforehand (a launch more: 64 sequences of a token 21 us, 26 with it).
+// beforehand, a launch more (64 sequences of a token 23 us, with it 26).
 inline bool needs_cuts(bool cu, int nseq) { return cu && nseq >= 256; }
 
 // The gradient: the state before every chunk, then the gradient of the state after
 // every chunk (and dfirst), then everything else chunk by chunk. A sequence has a chunk
-// and a piece at least; where sequences share no rows, their numbers are below these.
+// and a piece at least; where sequences share no rows, chunks' numbers are below this.
 __host__ __device__ constexpr int64_t chunk_slots(int64_t n, int nseq) { return n / 32 + nseq; }
 hipError_t launch_states(const Args& a, const Plan& p, bool bf16, hipStream_t stream);
 hipError_t launch_back(const Args& a, const Plan& p, bool bf16, hipStream_t stream);

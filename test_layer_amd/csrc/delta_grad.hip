@@ -1,6 +1,6 @@
 // The gradient of the gated delta rule, chunk by chunk, from the state S before each
 // chunk and the gradient dS of the state after it (delta_scan.hip). With the forward's
-// y, u, o and the reverse scan's du, x = X^T du, dR = beta . x,
+// y, u and the reverse scan's du, x = X^T du, dR = beta . x,
 //
 //   dV = dR,    dbeta_i = x_i . y_i
 //   F = scale D . (dO u^T) (lower),    E = D . (dR u^T) (strictly lower)
